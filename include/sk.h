@@ -315,6 +315,129 @@ sk_status sk_gemm_rmsnorm_nvfp4_static(const void *x, const void *w, const void 
                                        uint8_t *a, uint8_t *a_sf, void *z_out, int m, int n,
                                        int k, int splits, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The routed experts between the pooler and the unpooler, with 8-bit integer
+ * weights and activations. No counterpart on the pages (there the experts are
+ * another package's): int8 codes carry one FP32 scale per row -- per token of
+ * an activation, per output feature ("channel") of a weight -- and every sum of
+ * products of codes is exact, in 32-bit integers.
+ * ------------------------------------------------------------------------ */
+
+/* Types of sk_route's logits. */
+#define SK_TYPE_BF16 0
+#define SK_TYPE_FP32 1
+
+/* Scores of sk_route. */
+#define SK_SCORE_SOFTMAX 0
+#define SK_SCORE_SIGMOID 1
+
+#define SK_MAX_EXPERTS 1024 /* experts of a layer */
+#define SK_MAX_GROUPS 32    /* groups of experts */
+#define SK_MAX_TOP_K 16     /* experts per token */
+
+/*
+ * sk_route -- routing to experts. For each of m token rows, with a = the row of
+ * logits [n_experts]:
+ *   an expert may be chosen unless its logit is -inf or NaN, or its selection
+ *   value v (below) is -inf or NaN
+ *   score    softmax: p = exp(a - max a) / sum exp(a - max a), over the logits
+ *            that are not -inf or NaN (several +inf share the whole);
+ *            sigmoid: p = 1 / (1 + exp(-a))
+ *   v        bias NULL: a itself (p grows with a); else p + bias
+ *   groups   n_groups > 1: experts [g n_experts / n_groups, ...) form group g;
+ *            its value is the largest v in it (bias NULL) or the sum of its two
+ *            largest (of its one, where only one may be chosen). The
+ *            topk_groups best groups keep their experts, the others' cannot be
+ *            chosen.
+ *   choice   the top_k largest v, largest first; equal values go to the lower
+ *            index, of experts and of groups
+ *   weights  w[j] = p of choice j (without the bias); with renormalize
+ *            w[j] / sum w (0 where the sum is 0); times `scale`
+ * Where fewer than top_k experts may be chosen, the remaining ids are -1 and
+ * their weights 0: a row of -inf logits routes to nobody.
+ * The order is that of values computed in FP64 (p + bias, sums of two); the
+ * weights are FP32.
+ *   logits      BF16 or FP32 [m, n_experts] (logits_type SK_TYPE_*), aligned to
+ *               its element size
+ *   bias        FP32 [n_experts] or NULL
+ *   ids         int32 [m, top_k];  weights FP32 [m, top_k]; 4-byte aligned
+ *   m >= 1; 1 <= n_experts <= 1024; 1 <= n_groups <= 32 dividing n_experts;
+ *   1 <= topk_groups <= n_groups; 1 <= top_k <= 16 and at most
+ *   topk_groups * n_experts / n_groups; score SK_SCORE_*; scale finite.
+ */
+sk_status sk_route(const void *logits, int logits_type, const float *bias, int32_t *ids,
+                   float *weights, int m, int n_experts, int n_groups, int topk_groups, int top_k,
+                   int score, int renormalize, float scale, void *stream);
+
+/*
+ * sk_int8_quantize -- int8 codes and one FP32 scale per row of a BF16 [m, n]:
+ *   amax[i] = max_j |z[i, j]|;  scale[i] = amax / 127  (IEEE FP32)
+ *   q[i, j] = round to nearest even of 127 z[i, j] / amax[i], exactly
+ * A row of zeros has scale 0 and codes 0. A row that holds an Inf or NaN has
+ * scale NaN and codes 0, so that every product with it is NaN.
+ *   z BF16 [m, n], q int8 [m, n], scale FP32 [m];  1 <= m, 16 <= n <= 131056,
+ *   n % 16 == 0; z and q 16-byte, scale 4-byte aligned.
+ * It makes both operands of sk_gemm_int8 and sk_experts_int8: m token rows, or
+ * the rows of a weight (then `scale` is per output feature). A later call on
+ * the stream may read q as its weight at once.
+ */
+sk_status sk_int8_quantize(const void *z, int8_t *q, float *scale, int m, int n, void *stream);
+
+/*
+ * sk_gemm_int8 -- y[m, n] = bf16_rn( (sum_k xq[m, k] wq[n, k]) * x_scale[m] * w_scale[n] )
+ * with the sum exact in 32-bit integers (any codes, -128 included); the two
+ * FP32 products follow in that order, then one rounding to BF16.
+ *   xq int8 [m, k], x_scale FP32 [m], wq int8 [n, k], w_scale FP32 [n],
+ *   y BF16 [m, n];  1 <= m <= 16, n >= 1, k % 16 == 0, 16 <= k <= 131056
+ *   (a sum of k products of magnitude up to 2^14 fits 31 bits);
+ *   xq, wq, y 16-byte aligned, the scales 4-byte aligned.
+ *   splits  0 (automatic), 1, 2, 4 or 8 slices of K. Results do not depend on
+ *           it: integer sums have no order.
+ * wq is read before the kernel ahead in the stream completes, like the weights
+ * of the other GEMMs; xq and both scales after it.
+ */
+sk_status sk_gemm_int8(const int8_t *xq, const float *x_scale, const int8_t *wq,
+                       const float *w_scale, void *y, int m, int n, int k, int splits,
+                       void *stream);
+
+/* Why (m, n, k, splits) has no int8 GEMM launch, or SK_OK (host-only). */
+sk_status sk_gemm_int8_supported(int m, int n, int k, int splits);
+
+/* Size in bytes of the workspace sk_experts_int8 needs: FP32 activations and
+   their codes and scales [m top_k, inter], and FP32 outputs [m top_k, hidden].
+   0 for sizes that the call rejects. */
+size_t sk_experts_int8_workspace(int m, int top_k, int hidden, int inter);
+
+/*
+ * sk_experts_int8 -- the routed experts. For token i and its choice j of expert
+ * e = ids[i, j]:
+ *   h    = (sum_k xq[i, k] w13[e, :, k]) * x_scale[i] * s13[e, :]      [2 inter]
+ *   act  = silu(h[0 : inter]) * h[inter : 2 inter]                  (FP32)
+ *   (hq, hs) = int8 codes and scale of the row act, as sk_int8_quantize's
+ *          (its quotient in FP32)
+ *   o    = (sum_k hq[k] w2[e, :, k]) * hs * s2[e, :]                   [hidden]
+ *   y[i] = bf16_rn( sum over j, in order, of weights[i, j] * o )      (FP32 sum)
+ * A choice whose id is not in [0, n_experts) is left out (a masked choice, a
+ * padded token: a token without choices gets zeros). An expert named twice by
+ * a token counts with both weights.
+ *   xq int8 [m, hidden], x_scale FP32 [m]
+ *   w13 int8 [n_experts, 2 inter, hidden]: inter gate rows, then inter up rows;
+ *   s13 FP32 [n_experts, 2 inter]
+ *   w2 int8 [n_experts, hidden, inter], s2 FP32 [n_experts, hidden]
+ *   ids int32 [m, top_k], weights FP32 [m, top_k] (as sk_route's)
+ *   y BF16 [m, hidden]
+ *   workspace: at least sk_experts_int8_workspace(...) bytes, 256-byte aligned,
+ *   in any state; scratch for this call alone (calls that may run at the same
+ *   time need one each)
+ *   1 <= m <= 16, 1 <= n_experts <= 1024, 1 <= top_k <= 16, hidden and inter
+ *   multiples of 16 in [16, 131056]; codes and y 16-byte, the rest 4-byte aligned.
+ * Only the weights of experts that some token names are read.
+ */
+sk_status sk_experts_int8(const int8_t *xq, const float *x_scale, const int8_t *w13,
+                          const float *s13, const int8_t *w2, const float *s2, const int32_t *ids,
+                          const float *weights, void *y, void *workspace, size_t workspace_bytes,
+                          int m, int n_experts, int top_k, int hidden, int inter, void *stream);
+
 /*
  * sk_wait_probe -- diagnostic of the bounded-wait path: launches one CTA that
  * waits on an mbarrier that nothing completes, through the same bounded wait

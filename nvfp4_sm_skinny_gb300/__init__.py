@@ -81,6 +81,12 @@ def lib() -> ctypes.CDLL:
             "sk_gemm_nvfp4w_bf16": ([vp, vp, vp, vp, vp, i, i, i, i, vp], i),
             "sk_gemm_nvfp4w_supported": ([i, i, i, i], i),
             "sk_gemm_nvfp4w_splits": ([i, i, i, i], i),
+            "sk_route": ([vp, i, vp, vp, vp, i, i, i, i, i, i, i, f, vp], i),
+            "sk_int8_quantize": ([vp, vp, vp, i, i, vp], i),
+            "sk_gemm_int8": ([vp, vp, vp, vp, vp, i, i, i, i, vp], i),
+            "sk_gemm_int8_supported": ([i, i, i, i], i),
+            "sk_experts_int8_workspace": ([i, i, i, i], sz),
+            "sk_experts_int8": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, i, i, i, i, i, vp], i),
             "sk_device_status": ([ctypes.POINTER(ctypes.c_uint32), i], i),
             "sk_convert_probe": ([i, vp, vp, i, vp], i),
             "sk_wait_probe": ([ctypes.c_uint, vp], i),
@@ -389,6 +395,144 @@ def gemm_nvfp4w(x, wq, wsf, w_scale, out=None, splits: int = 0, stream=None):
     _check(lib().sk_gemm_nvfp4w_bf16(_ptr(x), _ptr(wq), _ptr(wsf), _ptr(w_scale), _ptr(out), m, n,
                                      k, splits, _stream(stream)))
     return out
+
+
+# ------------------------------------------------ int8 and routed experts ----
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _launch_on(stream, *tensors):
+    """The raw stream handle of a call on ``stream`` (the current one if None);
+    refuses tensors that are not on its device, where the kernels would run."""
+    dev = tensors[0].device
+    for t in tensors[1:]:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {t.device} and {dev}: needs all of them on one device")
+    if stream is None:
+        if dev.index != torch.cuda.current_device():
+            raise ValueError(f"tensors on {dev}: needs that device to be the current one "
+                             f"(cuda:{torch.cuda.current_device()})")
+        return torch.cuda.current_stream().cuda_stream
+    if stream.device != dev or dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {dev}, a stream of {stream.device}: needs both on the current "
+                         f"device (cuda:{torch.cuda.current_device()})")
+    return stream.cuda_stream
+
+
+def _new(shape, dtype, device, stream):
+    """An output of a call on ``stream``, from that stream's memory."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def route(logits, top_k: int, bias=None, n_groups: int = 1, topk_groups: int = 1,
+          score: str = "softmax", renormalize: bool = True, scale: float = 1.0, ids=None,
+          weights=None, stream=None):
+    """(ids int32 [m, top_k], weights FP32 [m, top_k]): the experts of each row
+    of logits [m, n_experts] (BF16 or FP32), best first, ties to the lower
+    index; ``bias`` (FP32 [n_experts]) is added to the scores for the choice
+    only; ids are -1 where nothing is left to choose (sk_route)."""
+    m, n = logits.shape
+    if logits.dtype != torch.bfloat16:
+        _need(logits, torch.float32, (m, n), "logits")
+    else:
+        _need(logits, torch.bfloat16, (m, n), "logits")
+    if score not in SCORES:
+        raise ValueError(f"score: {score!r}, needs one of {sorted(SCORES)}")
+    if bias is not None:
+        _need(bias, torch.float32, (n,), "bias")
+    if ids is None:
+        ids = _new((m, top_k), torch.int32, logits.device, stream)
+    if weights is None:
+        weights = _new((m, top_k), torch.float32, logits.device, stream)
+    _need(ids, torch.int32, (m, top_k), "ids")
+    _need(weights, torch.float32, (m, top_k), "weights")
+    s = _launch_on(stream, logits, bias, ids, weights)
+    _check(lib().sk_route(logits.data_ptr(), 1 if logits.dtype == torch.float32 else 0,
+                          None if bias is None else bias.data_ptr(), ids.data_ptr(),
+                          weights.data_ptr(), m, n, n_groups, topk_groups, top_k, SCORES[score],
+                          1 if renormalize else 0, scale, s))
+    return ids, weights
+
+
+def int8_quantize(z, q=None, scale=None, stream=None):
+    """(q int8 [m, n], scale FP32 [m]): int8 codes of BF16 z [m, n], one scale
+    per row (amax / 127): m token rows, or the output features of a weight."""
+    m, n = z.shape
+    _need(z, torch.bfloat16, (m, n), "z")
+    if q is None:
+        q = _new((m, n), torch.int8, z.device, stream)
+    if scale is None:
+        scale = _new((m,), torch.float32, z.device, stream)
+    _need(q, torch.int8, (m, n), "q")
+    _need(scale, torch.float32, (m,), "scale")
+    s = _launch_on(stream, z, q, scale)
+    _check(lib().sk_int8_quantize(z.data_ptr(), q.data_ptr(), scale.data_ptr(), m, n, s))
+    return q, scale
+
+
+def gemm_int8_supported(m: int, n: int, k: int, splits: int = 0) -> str | None:
+    """None if the int8 GEMM has a launch for the shape, else why."""
+    st = lib().sk_gemm_int8_supported(m, n, k, splits)
+    return None if st == SK_OK else last_error()
+
+
+def gemm_int8(xq, x_scale, wq, w_scale, out=None, splits: int = 0, stream=None):
+    """out[m, n] = bf16((xq[m, k] @ wq[n, k]^T) * x_scale[m] * w_scale[n]): int8
+    codes, an exact integer sum, FP32 scales per token and output feature."""
+    m, k = xq.shape
+    n = wq.shape[0]
+    _need(xq, torch.int8, (m, k), "xq")
+    _need(x_scale, torch.float32, (m,), "x_scale")
+    _need(wq, torch.int8, (n, k), "wq")
+    _need(w_scale, torch.float32, (n,), "w_scale")
+    if out is None:
+        out = _new((m, n), torch.bfloat16, xq.device, stream)
+    _need(out, torch.bfloat16, (m, n), "out")
+    s = _launch_on(stream, xq, x_scale, wq, w_scale, out)
+    _check(lib().sk_gemm_int8(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(),
+                              out.data_ptr(), m, n, k, splits, s))
+    return out
+
+
+def experts_int8_workspace(m: int, top_k: int, hidden: int, inter: int) -> int:
+    return int(lib().sk_experts_int8_workspace(m, top_k, hidden, inter))
+
+
+def experts_int8(xq, x_scale, w13, s13, w2, s2, ids, weights, out=None, workspace=None,
+                 stream=None):
+    """(out BF16 [m, hidden], workspace): the routed experts of each token,
+    out = sum_j weights[:, j] * w2[e](silu(gate[e](x)) * up[e](x)), e = ids[:, j],
+    with int8 codes: xq [m, hidden], w13 [n_experts, 2 inter, hidden] (gate rows,
+    then up rows), w2 [n_experts, hidden, inter], their scales x_scale [m], s13
+    [n_experts, 2 inter], s2 [n_experts, hidden]; ids and weights as from
+    ``route``, ids outside 0..n_experts-1 left out (sk_experts_int8)."""
+    m, hidden = xq.shape
+    n_experts, _, inter = w2.shape
+    top_k = ids.shape[1]
+    _need(xq, torch.int8, (m, hidden), "xq")
+    _need(x_scale, torch.float32, (m,), "x_scale")
+    _need(w13, torch.int8, (n_experts, 2 * inter, hidden), "w13")
+    _need(s13, torch.float32, (n_experts, 2 * inter), "s13")
+    _need(w2, torch.int8, (n_experts, hidden, inter), "w2")
+    _need(s2, torch.float32, (n_experts, hidden), "s2")
+    _need(ids, torch.int32, (m, top_k), "ids")
+    _need(weights, torch.float32, (m, top_k), "weights")
+    if out is None:
+        out = _new((m, hidden), torch.bfloat16, xq.device, stream)
+    _need(out, torch.bfloat16, (m, hidden), "out")
+    if workspace is None:
+        workspace = _new((experts_int8_workspace(m, top_k, hidden, inter),), torch.uint8, xq.device,
+                         stream)
+    _need(workspace, torch.uint8, (workspace.numel(),), "workspace")
+    s = _launch_on(stream, xq, x_scale, w13, s13, w2, s2, ids, weights, out, workspace)
+    _check(lib().sk_experts_int8(
+        xq.data_ptr(), x_scale.data_ptr(), w13.data_ptr(), s13.data_ptr(), w2.data_ptr(),
+        s2.data_ptr(), ids.data_ptr(), weights.data_ptr(), out.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), m, n_experts, top_k, hidden, inter, s))
+    return out, workspace
 
 
 # ----------------------------------------------------------- diagnostics ----

@@ -1,6 +1,6 @@
 """Builds libsk.so in-tree with nvcc for sm_103a (GB300).
 
-Two translation units compiled in parallel (host front end, device kernels),
+Translation units compiled in parallel (host front ends, device kernels),
 linked into ``nvfp4_sm_skinny_gb300/libsk.so`` with the static CUDA runtime, so
 the library depends only on the driver at run time. No CMake, no JIT.
 """
@@ -19,7 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsk.so")
 
-SOURCES = ["sk_api.cu", "sk_kernels.cu", "sk_static_scratch.cu"]
+SOURCES = ["sk_api.cu", "sk_kernels.cu", "sk_static_scratch.cu", "sk_experts_api.cu",
+           "sk_experts.cu"]
 HEADERS = ["sk_internal.h", "sk_ptx.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

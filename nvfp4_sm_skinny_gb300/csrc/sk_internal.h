@@ -203,6 +203,53 @@ cudaError_t launch_wait_probe(uint64_t limit_ns, cudaStream_t stream);
 
 cudaError_t read_device_status(uint32_t *out, bool clear);
 
+// ------------------------------------------------ the int8 routed experts
+// Routing, one row of logits per token (sk_route).
+struct RouteArgs {
+  const void *logits;
+  const float *bias;  // or null
+  int32_t *ids;
+  float *weights;
+  int m, n_experts, n_groups, topk_groups, top_k;
+  bool fp32;     // type of the logits: FP32 or BF16
+  bool sigmoid;  // scores: sigmoid or softmax
+  bool renormalize;
+  float scale;
+};
+cudaError_t launch_route(const RouteArgs &a, cudaStream_t stream, bool pdl);
+
+cudaError_t launch_int8_quantize(const uint16_t *z, int8_t *q, float *scale, int m, int n,
+                                 cudaStream_t stream, bool pdl);
+
+// The int8 GEMM (sk_gemm_int8).
+struct Int8GemmArgs {
+  const int8_t *xq, *wq;
+  const float *x_scale, *w_scale;
+  uint16_t *y;
+  int m, n, k, splits;
+};
+cudaError_t launch_gemm_int8(const Int8GemmArgs &a, cudaStream_t stream, bool pdl);
+
+// The routed experts (sk_experts_int8); act, hq, hs and o are parts of the
+// caller's workspace, one row per choice.
+struct ExpertsArgs {
+  const int8_t *xq;
+  const float *x_scale;
+  const int8_t *w13;
+  const float *s13;
+  const int8_t *w2;
+  const float *s2;
+  const int32_t *ids;
+  const float *weights;
+  uint16_t *y;
+  float *act;  // [m top_k, inter]
+  int8_t *hq;  // [m top_k, inter]
+  float *hs;   // [m top_k]
+  float *o;    // [m top_k, hidden]
+  int m, n_experts, top_k, hidden, inter;
+};
+cudaError_t launch_experts_int8(const ExpertsArgs &a, cudaStream_t stream, bool pdl);
+
 // The current device, checked to be compute capability 10.3, set up.
 sk_status checked_device(DeviceInfo *info, int *device);
 bool pdl_on();

@@ -1,0 +1,121 @@
+"""Host-side checks of the int8 routed experts' entry points: every refusal
+comes before any CUDA call, with a status and a message (no GPU)."""
+import ctypes
+
+import pytest
+import torch
+
+P = 1 << 20  # an aligned address that nothing reads
+vp = ctypes.c_void_p
+
+
+@pytest.fixture(scope="module")
+def sk():
+    from nvfp4_sm_skinny_gb300 import build
+
+    build.build()
+    import nvfp4_sm_skinny_gb300 as sk
+
+    return sk
+
+
+ROUTE = dict(logits=P, logits_type=1, bias=P, ids=P, weights=P, m=4, n_experts=64, n_groups=8,
+             topk_groups=4, top_k=8, score=1, renormalize=1, scale=1.0, stream=None)
+
+
+@pytest.mark.parametrize("change,word", [
+    (dict(logits_type=2), "logits_type"), (dict(score=2), "score"), (dict(m=0), "m=0"),
+    (dict(m=-3), "m=-3"), (dict(n_experts=0), "n_experts"), (dict(n_experts=1032), "n_experts"),
+    (dict(n_groups=0), "n_groups"), (dict(n_groups=7), "n_groups"), (dict(n_groups=64), "n_groups"),
+    (dict(topk_groups=0), "topk_groups"), (dict(topk_groups=9), "topk_groups"),
+    (dict(top_k=0), "top_k"), (dict(top_k=17), "top_k"), (dict(topk_groups=1, top_k=9), "top_k"),
+    (dict(scale=float("nan")), "scale"), (dict(scale=float("inf")), "scale"),
+    (dict(logits=None), "logits"), (dict(logits=P + 2), "logits"), (dict(bias=P + 2), "bias"),
+    (dict(ids=None), "ids"), (dict(weights=P + 1), "weights"),
+])
+def test_route_refusals(sk, change, word):
+    assert sk.lib().sk_route(*{**ROUTE, **change}.values()) == 1
+    assert word in sk.last_error()
+
+
+@pytest.mark.parametrize("z,q,scale,m,n,word", [
+    (P, P, P, 0, 64, "m=0"), (P, P, P, 1, 0, "n=0"), (P, P, P, 1, 24, "n=24"),
+    (P, P, P, 1, 131072, "n=131072"), (None, P, P, 1, 64, "z"), (P + 8, P, P, 1, 64, "z"),
+    (P, P + 4, P, 1, 64, "q"), (P, P, P + 2, 1, 64, "scale"), (P, P, None, 1, 64, "scale"),
+])
+def test_quantize_refusals(sk, z, q, scale, m, n, word):
+    assert sk.lib().sk_int8_quantize(z, q, scale, m, n, None) == 1
+    assert word in sk.last_error()
+
+
+GEMM = dict(xq=P, x_scale=P, wq=P, w_scale=P, y=P, m=1, n=128, k=256, splits=0, stream=None)
+
+
+@pytest.mark.parametrize("change,status,word", [
+    (dict(m=0), 1, "m=0"), (dict(m=17), 1, "m=17"), (dict(n=0), 1, "n=0"), (dict(k=0), 1, "k=0"),
+    (dict(k=24), 1, "k=24"), (dict(k=131072), 1, "k=131072"), (dict(splits=3), 2, "split"),
+    (dict(splits=16), 2, "split"), (dict(xq=None), 1, "xq"), (dict(wq=P + 8), 1, "wq"),
+    (dict(y=P + 2), 1, "y "), (dict(x_scale=P + 2), 1, "x_scale"), (dict(w_scale=None), 1, "w_scale"),
+])
+def test_gemm_refusals(sk, change, status, word):
+    a = {**GEMM, **change}
+    assert sk.lib().sk_gemm_int8(*a.values()) == status
+    assert word in sk.last_error()
+    if set(change) & {"m", "n", "k", "splits"}:
+        assert sk.lib().sk_gemm_int8_supported(a["m"], a["n"], a["k"], a["splits"]) == status
+        assert word in sk.gemm_int8_supported(a["m"], a["n"], a["k"], a["splits"])
+
+
+def test_gemm_supported(sk):
+    for shape in ((1, 1, 16, 0), (16, 8192, 8192, 8), (5, 4100, 2064, 2), (16, 17, 131056, 0)):
+        assert sk.gemm_int8_supported(*shape) is None
+
+
+EXPERTS = dict(xq=P, x_scale=P, w13=P, s13=P, w2=P, s2=P, ids=P, weights=P, y=P, workspace=P,
+               workspace_bytes=1 << 30, m=2, n_experts=8, top_k=2, hidden=64, inter=32, stream=None)
+
+
+@pytest.mark.parametrize("change,status,word", [
+    (dict(m=0), 1, "m=0"), (dict(m=17), 1, "m=17"), (dict(n_experts=0), 1, "n_experts"),
+    (dict(n_experts=1025), 1, "n_experts"), (dict(top_k=0), 1, "top_k"), (dict(top_k=17), 1, "top_k"),
+    (dict(hidden=40), 1, "hidden"), (dict(inter=8), 1, "inter"), (dict(inter=131072), 1, "inter"),
+    (dict(w13=None), 1, "w13"), (dict(w2=P + 8), 1, "w2"), (dict(ids=P + 2), 1, "ids"),
+    (dict(workspace=P + 16), 1, "workspace"), (dict(workspace_bytes=1024), 4, "workspace"),
+])
+def test_experts_refusals(sk, change, status, word):
+    assert sk.lib().sk_experts_int8(*{**EXPERTS, **change}.values()) == status
+    assert word in sk.last_error()
+
+
+def test_experts_workspace(sk):
+    # act and codes and scales of every choice, outputs of every choice
+    assert sk.experts_int8_workspace(3, 2, 64, 32) == 6 * 32 * 4 + 256 + 256 + 6 * 64 * 4
+    assert sk.experts_int8_workspace(16, 16, 131056, 131056) > 1 << 27
+    assert sk.experts_int8_workspace(17, 2, 64, 32) == 0 and "m=17" in sk.last_error()
+
+
+def test_valid_calls_without_gpu_report_a_device_error(sk):
+    if torch.cuda.is_available():
+        pytest.skip("a CUDA device is present")
+    L = sk.lib()
+    for st in (L.sk_route(*ROUTE.values()), L.sk_int8_quantize(P, P, P, 1, 64, None),
+               L.sk_gemm_int8(*GEMM.values()), L.sk_experts_int8(*EXPERTS.values())):
+        assert st in (3, 5) and sk.last_error()
+
+
+def test_binding_refuses_other_tensors(sk):
+    def t(*shape, dtype=torch.int8):
+        return torch.zeros(*shape, dtype=dtype)
+
+    f = torch.float32
+    with pytest.raises(ValueError, match="logits"):
+        sk.route(t(2, 8, dtype=torch.float16), 2)
+    with pytest.raises(ValueError, match="CUDA"):
+        sk.route(t(2, 8, dtype=f), 2)
+    with pytest.raises(ValueError, match="z"):
+        sk.int8_quantize(t(2, 32, dtype=f))
+    with pytest.raises(ValueError, match="xq"):
+        sk.gemm_int8(t(2, 32, dtype=torch.uint8), t(2, dtype=f), t(4, 32), t(4, dtype=f))
+    with pytest.raises(ValueError, match="xq"):
+        sk.experts_int8(t(2, 32, dtype=f), t(2, dtype=f), t(4, 32, 32), t(4, 32, dtype=f), t(4, 32, 16),
+                        t(4, 32, dtype=f), t(2, 2, dtype=torch.int32), t(2, 2, dtype=f))
