@@ -152,8 +152,11 @@ sk_status sk_gemm_int8(const int8_t *xq, const float *x_scale, const int8_t *wq,
   sk::DeviceInfo info;
   int dev = 0;
   if ((st = sk::checked_device(&info, &dev)) != SK_OK) return st;
-  sk::Int8GemmArgs a{xq, wq, x_scale, w_scale, static_cast<uint16_t *>(y), m, n, k, splits};
-  return launch_status(sk::launch_gemm_int8(a, as_stream(stream), sk::pdl_on()), "gemm_int8");
+  sk::Int8GemmArgs a{xq, wq, x_scale, w_scale, static_cast<uint16_t *>(y), m, n, k,
+                     splits ? splits : sk::int8_splits(n, k, info.sm_count)};
+  CUtensorMap map;
+  if ((st = sk::make_int8_map(&map, wq, k, n, 1, 32, 1)) != SK_OK) return st;
+  return launch_status(sk::launch_gemm_int8(map, a, as_stream(stream), sk::pdl_on()), "gemm_int8");
 }
 
 static sk_status check_experts(int m, int top_k, int hidden, int inter) {
@@ -197,7 +200,12 @@ sk_status sk_experts_int8(const int8_t *xq, const float *x_scale, const int8_t *
                     reinterpret_cast<float *>(ws + w.act), reinterpret_cast<int8_t *>(ws + w.hq),
                     reinterpret_cast<float *>(ws + w.hs), reinterpret_cast<float *>(ws + w.o),
                     m, n_experts, top_k, hidden, inter};
-  return launch_status(sk::launch_experts_int8(a, as_stream(stream), sk::pdl_on()), "experts_int8");
+  CUtensorMap map13, map2;
+  if ((st = sk::make_int8_map(&map13, w13, hidden, inter, 2 * n_experts, 16, 2)) != SK_OK) return st;
+  if ((st = sk::make_int8_map(&map2, w2, inter, hidden, n_experts, 32, 1)) != SK_OK) return st;
+  return launch_status(sk::launch_experts_int8(map13, map2, a, info.sm_count, as_stream(stream),
+                                               sk::pdl_on()),
+                       "experts_int8");
 }
 
 }  // extern "C"
