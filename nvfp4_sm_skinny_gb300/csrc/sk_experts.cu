@@ -3,6 +3,7 @@
 // products (sk_experts_int8). include/sk.h has the formulas.
 #include <math_constants.h>
 
+#include <cstdlib>
 #include <type_traits>
 
 #include "sk.h"
@@ -206,10 +207,10 @@ __global__ void __launch_bounds__(256)
 //
 // Products at up to 16 tokens stream each weight once; 1 byte of weight meets
 // at most 16 tokens, far below what the tensor cores need to be busy, so HBM
-// is the bound and the rest has to stay out of its way. Each CTA owns items of
-// 32 weight rows and a K range. One producer thread copies them with TMA, a
-// stage of 32 rows x 512 codes (16 KiB) at a time, into a ring; eight consumer
-// warps each take one 64-code column block of every stage.
+// is the bound and the rest has to stay out of its way. One producer thread
+// copies weights with TMA, a stage of 16 KiB at a time, into a ring, and the
+// token rows' columns with them; eight consumer warps each take 32 rows and 64
+// columns of every stage.
 //
 // The tensor cores multiply int8 codes at FP16: a code widens to FP16 exactly
 // by placing code + 128 in the mantissa of 1024 and subtracting 1152 (one
@@ -222,24 +223,50 @@ __global__ void __launch_bounds__(256)
 // K order within a block is free as long as both operands agree: thread t of a
 // quad holds columns 16 t .. 16 t + 15 (one 16-byte load of a weight row, one of
 // a token row) and feeds four of them to each of four m16n8k16 products.
-constexpr int kTileRows = 32;
-constexpr int kStageK = 512;
-constexpr int kBoxK = 128;                                // one TMA box: 128-byte rows, swizzled
-constexpr int kBoxBytes = kTileRows * kBoxK;              // 4 KiB
-constexpr int kStageBytes = kTileRows * kStageK;          // 16 KiB
+constexpr int kBoxK = 128;                                // columns of a TMA box, swizzled over 128 bytes
+constexpr int kStageWBytes = 16 * 1024;                   // weights of a stage
 constexpr int kConsumers = 8;                             // warps
 constexpr int kCoreThreads = 32 * (kConsumers + 1);
 constexpr int kExactStages = 16;                          // stages between moves to integers
-constexpr int kRedPitch = kTileRows + 4;                  // ints per token of the sum buffer
-constexpr int kRedInts = SK_MAX_M * kRedPitch;
 constexpr uint64_t kCoreWaitNs = 2000000000ull;           // 2 s of wall time per wait
+
+// A stage's shape: 32 RG rows by 512 / RG columns; the warps form RG row groups
+// and 8 / RG column groups. kGather: the token rows come one by one (bulk
+// copies to rows of a fixed pitch); else they are a tile of the activations
+// ([m, k], TMA boxes of 8 or 16 rows).
+template <int RG, bool kGather>
+struct Shape {
+  static constexpr int kRows = 32 * RG;
+  static constexpr int kStageK = 512 / RG;
+  static constexpr int kBoxes = kStageK / kBoxK;
+  static constexpr int kBoxBytes = kRows * kBoxK;
+  static constexpr int kXPitch = kStageK + 64;           // kGather: bytes per token row of a stage
+  static constexpr int kRedPitch = kRows + (kGather ? 4 : 8);  // ints per token of the sum buffer
+  static constexpr int kRedInts = SK_MAX_M * kRedPitch;
+  __host__ __device__ static constexpr int x_rows(int m) { return m > 8 ? 16 : 8; }
+  __host__ __device__ static constexpr int stage_bytes(int m) {
+    return (kStageWBytes + x_rows(m) * (kGather ? kXPitch : kStageK) + 1023) / 1024 * 1024;
+  }
+};
 
 __device__ uint32_t g_core_status;  // OR of SK_DEVICE_WAIT_* bits
 
 struct Ring {
   uint32_t data, full, empty;  // shared addresses: stages, then their barriers
-  int stages;
+  int stages, stage_bytes, x_rows;
   volatile uint32_t *abort;
+};
+
+// A role's place in the ring.
+struct RingPos {
+  int st = 0;
+  uint32_t lap = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++st == stages) {
+      st = 0;
+      ++lap;
+    }
+  }
 };
 
 // A wait that runs out raises the abort flag, after which no wait of the CTA
@@ -257,27 +284,97 @@ __device__ __forceinline__ void ring_wait(const Ring &r, uint32_t bar, uint32_t 
   }
 }
 
-// Copies stage by stage the box rows at (row, batch) of the weight map for
-// columns [k0, k1) into the ring; `it` counts the CTA's stages.
-__device__ __forceinline__ void produce(const Ring &r, const CUtensorMap *map, int row, int batch,
-                                        int k0, int k1, int &it, uint64_t policy) {
-  for (int k = k0; k < k1; k += kStageK, ++it) {
-    const int st = it % r.stages, lap = it / r.stages;
-    if (lap) ring_wait(r, r.empty + 8 * st, (lap - 1) & 1, SK_DEVICE_WAIT_PRODUCER);
-    if (*r.abort) continue;
-    const int boxes = min(kStageK / kBoxK, (k1 - k + kBoxK - 1) / kBoxK);
-    mbar_arrive_expect_tx(r.full + 8 * st, boxes * kBoxBytes);
+// After an abort: waits (again with a limit) for the copies still in flight, of
+// the last of the `it` stages sent.
+__device__ __forceinline__ void drain(const Ring &r, int it) {
+  for (int i = max(0, it - r.stages); i < it; ++i)
+    mbar_wait_bounded(r.full + 8 * (i % r.stages), (i / r.stages) & 1, kCoreWaitNs / 100);
+}
+
+// One item's sources: the weight tile's coordinates; with kGather the token row
+// of each of the first `tokens` lanes.
+struct Source {
+  int row, batch, tokens;
+  const int8_t *x;
+};
+
+template <int RG, bool kGather>
+__device__ __forceinline__ void copy_weights(const Ring &r, const CUtensorMap *map, const Source &s,
+                                             int st, int k, int k1, uint64_t policy) {
+  using T = Shape<RG, kGather>;
+  const int boxes = min(T::kBoxes, (k1 - k + kBoxK - 1) / kBoxK);
+  const uint32_t bar = r.full + 8 * st;
+  mbar_arrive_expect_tx(bar, boxes * T::kBoxBytes + (kGather ? s.tokens * min(T::kStageK, k1 - k)
+                                                             : boxes * r.x_rows * kBoxK));
+  for (int b = 0; b < boxes; ++b)
+    tma_load_3d(r.data + st * r.stage_bytes + b * T::kBoxBytes, map, bar, k + b * kBoxK, s.row, s.batch,
+                policy);
+}
+
+template <int RG, bool kGather>
+__device__ __forceinline__ void copy_tokens(const Ring &r, const CUtensorMap *xmap, const Source &s,
+                                            int st, int k, int k1, uint64_t policy) {
+  using T = Shape<RG, kGather>;
+  const int lane = threadIdx.x & 31;
+  const uint32_t to = r.data + st * r.stage_bytes + kStageWBytes, bar = r.full + 8 * st;
+  if (kGather) {
+    if (lane < s.tokens)
+      asm volatile(
+          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+              to + lane * T::kXPitch),
+          "l"(__cvta_generic_to_global(s.x + k)), "r"(min(T::kStageK, k1 - k)), "r"(bar)
+          : "memory");
+  } else if (lane == 0) {
+    const int boxes = min(T::kBoxes, (k1 - k + kBoxK - 1) / kBoxK);
     for (int b = 0; b < boxes; ++b)
-      tma_load_3d(r.data + st * kStageBytes + b * kBoxBytes, map, r.full + 8 * st, k + b * kBoxK, row,
-                  batch, policy);
+      tma_load_3d(to + b * r.x_rows * kBoxK, xmap, bar, k + b * kBoxK, 0, 0, policy);
   }
 }
 
-// After an abort: waits (again with a limit) for the copies still in flight.
-__device__ __forceinline__ void drain(const Ring &r, int it) {
-  if (!*r.abort) return;
-  for (int i = max(0, it - r.stages); i < it; ++i)
-    mbar_wait_bounded(r.full + 8 * (i % r.stages), (i / r.stages) & 1, kCoreWaitNs / 100);
+// The producer warp: copies columns [k0, k1) of the items first, first + step,
+// ... below last, stage by stage. With `early` the token rows are not written
+// yet: the first ring of weights goes out before the wait for the kernel ahead,
+// its token rows after it.
+template <int RG, bool kGather, typename Items>
+__device__ __forceinline__ void produce(const Ring &r, const CUtensorMap *map, const CUtensorMap *xmap,
+                                        Items source, int first, int last, int step, int k0, int k1,
+                                        bool early) {
+  constexpr int kStageK = Shape<RG, kGather>::kStageK;
+  const int lane = threadIdx.x & 31;
+  const uint64_t policy = l2_policy_evict_first(), keep = l2_policy_evict_last();
+  int sent = 0;
+  if (early) {
+    for (int i = first; i < last && sent < r.stages; i += step) {
+      const Source s = source(i);
+      for (int k = k0; k < k1 && sent < r.stages; k += kStageK, ++sent)
+        if (lane == 0) copy_weights<RG, kGather>(r, map, s, sent, k, k1, policy);
+    }
+    __syncwarp();  // a stage's bytes are announced before any of its rows arrives
+    griddep_wait();
+    int n = 0;
+    for (int i = first; i < last && n < sent; i += step) {
+      const Source s = source(i);
+      for (int k = k0; k < k1 && n < sent; k += kStageK, ++n)
+        copy_tokens<RG, kGather>(r, xmap, s, n, k, k1, keep);
+    }
+  }
+  RingPos pos;
+  int it = 0;
+  for (int i = first; i < last; i += step) {
+    const Source s = source(i);
+    for (int k = k0; k < k1; k += kStageK, ++it, pos.next(r.stages)) {
+      if (it < sent) continue;
+      if (pos.lap) ring_wait(r, r.empty + 8 * pos.st, (pos.lap - 1) & 1, SK_DEVICE_WAIT_PRODUCER);
+      if (__any_sync(0xFFFFFFFFu, *r.abort)) {
+        drain(r, it);
+        return;
+      }
+      if (lane == 0) copy_weights<RG, kGather>(r, map, s, pos.st, k, k1, policy);
+      __syncwarp();
+      copy_tokens<RG, kGather>(r, xmap, s, pos.st, k, k1, keep);
+    }
+  }
+  if (__any_sync(0xFFFFFFFFu, *r.abort)) drain(r, it);
 }
 
 // Four int8 codes -> two FP16 pairs, exact.
@@ -300,30 +397,27 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 16 bytes of a token row, not through the read-only path: the kernel ahead
-// wrote them.
-__device__ __forceinline__ uint4 ldg128(const int8_t *p) {
-  uint4 v;
-  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
-// One consumer warp's part of an item: adds to red[token][row] its column
-// blocks' products of the 32 tile rows with NT * 8 tokens (red: a shared address). xp[nt]: this lane's
-// token row (token nt * 8 + lane / 4) at column 16 (lane % 4), or null.
-template <int NT>
-__device__ __forceinline__ void consume(const Ring &r, const int8_t *const (&xp)[NT], int k0, int k1,
-                                        int &it, uint32_t red) {
+// One consumer warp's part of an item: adds its column blocks' products of its
+// 32 tile rows with the first `tokens` (at most 8 NT) token rows of the stages to
+// red[token][row] (a shared address). Rows of a stage beyond `tokens` hold zeros
+// or leftovers, whose sums are not added.
+template <int RG, bool kGather, int NT>
+__device__ __forceinline__ void consume(const Ring &r, int tokens, int k0, int k1, RingPos &pos,
+                                        uint32_t red) {
+  using T = Shape<RG, kGather>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int cg = warp / RG, rg = warp % RG;  // column and row group
   // Tile row of the lane within eight: rows g = 2 i and 2 i + 1, which a load
   // phase reads together, are four apart, so their swizzles use both halves of
-  // the 128-byte row and no two lanes of the phase meet in a bank.
+  // the 128-byte row and no two lanes of the phase meet in a bank. Gathered
+  // token rows, at a pitch of an odd number of 64 bytes, need no reordering.
   const int pg = ((g & 1) << 2) | (g >> 1);
-  const uint32_t chunk = static_cast<uint32_t>((((warp & 1) << 2) | t) ^ pg) << 4;
-  const uint32_t at = (warp >> 1) * kBoxBytes + pg * kBoxK + chunk;
-  const int kw = warp * 64;
+  const uint32_t chunk = static_cast<uint32_t>((((cg & 1) << 2) | t) ^ pg) << 4;
+  const uint32_t at = r.data + (cg >> 1) * T::kBoxBytes + (rg * 32 + pg) * kBoxK + chunk;
+  const uint32_t xat = r.data + kStageWBytes +
+                       (kGather ? g * T::kXPitch + cg * 64 + t * 16
+                                : (cg >> 1) * r.x_rows * kBoxK + pg * kBoxK + chunk);
+  constexpr uint32_t kXStep = 8 * (kGather ? T::kXPitch : kBoxK);
   float acc[2][NT][4];
 #pragma unroll
   for (int i = 0; i < 2 * NT * 4; ++i) (&acc[0][0][0])[i] = 0.0f;
@@ -334,38 +428,33 @@ __device__ __forceinline__ void consume(const Ring &r, const int8_t *const (&xp)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int token = nt * 8 + 2 * t + (i & 1), row = rt * 16 + pg + (i >> 1) * 8;
-          asm volatile("red.shared.add.s32 [%0], %1;" ::"r"(red + 4u * (token * kRedPitch + row)),
-                       "r"(__float2int_rn(acc[rt][nt][i]))
-                       : "memory");
+          const int token = nt * 8 + (kGather ? 2 * t + (i & 1) : t + 4 * (i & 1));
+          const int row = rg * 32 + rt * 16 + pg + (i >> 1) * 8;
+          if (token < tokens)
+            asm volatile("red.shared.add.s32 [%0], %1;" ::"r"(red + 4u * (token * T::kRedPitch + row)),
+                         "r"(__float2int_rn(acc[rt][nt][i]))
+                         : "memory");
           acc[rt][nt][i] = 0.0f;
         }
   };
-  uint4 xn[NT];
-  auto load_x = [&](int k) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-      xn[nt] = xp[nt] && k + kw + 16 * t < k1 ? ldg128(xp[nt] + k + kw) : make_uint4(0, 0, 0, 0);
-  };
-  load_x(k0);
   int done = 0;
-  for (int k = k0; k < k1; k += kStageK, ++it) {
-    const int st = it % r.stages;
-    uint32_t b[NT][8];
+  for (int k = k0; k < k1; k += T::kStageK, pos.next(r.stages)) {
+    const uint32_t off = pos.st * r.stage_bytes;
+    ring_wait(r, r.full + 8 * pos.st, pos.lap & 1, SK_DEVICE_WAIT_MMA);
+    if (k + cg * 64 < k1) {
+      uint32_t b[NT][8];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      widen(xn[nt].x, b[nt][0], b[nt][1]);
-      widen(xn[nt].y, b[nt][2], b[nt][3]);
-      widen(xn[nt].z, b[nt][4], b[nt][5]);
-      widen(xn[nt].w, b[nt][6], b[nt][7]);
-    }
-    load_x(k + kStageK);
-    ring_wait(r, r.full + 8 * st, (it / r.stages) & 1, SK_DEVICE_WAIT_MMA);
-    if (k + kw < k1) {
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint4 x = lds128(xat + off + nt * kXStep);
+        widen(x.x, b[nt][0], b[nt][1]);
+        widen(x.y, b[nt][2], b[nt][3]);
+        widen(x.z, b[nt][4], b[nt][5]);
+        widen(x.w, b[nt][6], b[nt][7]);
+      }
 #pragma unroll
       for (int rt = 0; rt < 2; ++rt) {
-        const uint32_t base = r.data + st * kStageBytes + at + rt * 16 * kBoxK;
-        const uint4 w0 = lds128(base), w1 = lds128(base + 8 * kBoxK);
+        const uint4 w0 = lds128(at + off + rt * 16 * kBoxK);
+        const uint4 w1 = lds128(at + off + (rt * 16 + 8) * kBoxK);
         const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, hi[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -379,7 +468,7 @@ __device__ __forceinline__ void consume(const Ring &r, const int8_t *const (&xp)
       }
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(r.empty + 8 * st);
+    if (lane == 0) mbar_arrive(r.empty + 8 * pos.st);
     if (++done == kExactStages) {
       flush();
       done = 0;
@@ -397,10 +486,12 @@ __device__ __forceinline__ void consumer_sync() {
 struct CoreLayout {
   int red, bars, flag, extra, total;
 };
-__host__ __device__ inline CoreLayout core_layout(int stages, int extra) {
+template <int RG, bool kGather>
+__host__ __device__ inline CoreLayout core_layout(int m, int stages, int extra) {
+  using T = Shape<RG, kGather>;
   CoreLayout l;
-  l.red = stages * kStageBytes;
-  l.bars = l.red + 2 * kRedInts * 4;
+  l.red = stages * T::stage_bytes(m);
+  l.bars = l.red + 2 * T::kRedInts * 4;
   l.flag = l.bars + 2 * stages * 8;
   l.extra = l.flag + 16;
   l.total = l.extra + extra;
@@ -412,16 +503,20 @@ __device__ __forceinline__ uint8_t *core_smem(uint8_t *raw) {
 }
 
 // Set-up by all threads of a core kernel: barriers, abort flag, zeroed sums.
-__device__ __forceinline__ Ring core_setup(uint8_t *smem, const CoreLayout &l, int stages,
+template <int RG, bool kGather>
+__device__ __forceinline__ Ring core_setup(uint8_t *smem, const CoreLayout &l, int m, int stages,
                                            const CUtensorMap *map) {
+  using T = Shape<RG, kGather>;
   Ring r;
   r.data = smem_u32(smem);
   r.full = smem_u32(smem + l.bars);
   r.empty = r.full + 8 * stages;
   r.stages = stages;
+  r.stage_bytes = T::stage_bytes(m);
+  r.x_rows = T::x_rows(m);
   r.abort = reinterpret_cast<volatile uint32_t *>(smem + l.flag);
   int *red = reinterpret_cast<int *>(smem + l.red);
-  for (int i = threadIdx.x; i < 2 * kRedInts; i += kCoreThreads) red[i] = 0;
+  for (int i = threadIdx.x; i < 2 * T::kRedInts; i += kCoreThreads) red[i] = 0;
   if (threadIdx.x == 32 * kConsumers) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(r.full + 8 * s, 1);
@@ -436,57 +531,49 @@ __device__ __forceinline__ Ring core_setup(uint8_t *smem, const CoreLayout &l, i
 }
 
 // ----------------------------------------------------------------- int8 GEMM
-// Grid (tiles of 32 output features, S slices of K), cluster (1, S, 1): every
-// CTA holds its whole share in flight at once, two CTAs per SM, so that the
-// stream does not wait for scheduling. The S sums of a tile meet in shared
-// memory: rank r receives 32 / S rows of every rank and finishes them.
-template <int NT>
+// Grid (tiles of 32 RG output features, S slices of K), cluster (1, S, 1):
+// every CTA is resident from the start, two per SM, so that the stream does not
+// wait for scheduling. The S sums of a tile meet in shared memory: rank r
+// receives a slice of the rows from every rank and finishes them.
+template <int RG, int NT>
 __global__ void __launch_bounds__(kCoreThreads, 2)
-    gemm_int8_kernel(const __grid_constant__ CUtensorMap map, Int8GemmArgs a, int stages) {
+    gemm_int8_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap xmap,
+                     Int8GemmArgs a, int stages) {
+  using T = Shape<RG, false>;
   extern __shared__ uint8_t raw[];
   uint8_t *smem = core_smem(raw);
   const int S = a.splits;
-  const CoreLayout l = core_layout(stages, 0);
-  const Ring r = core_setup(smem, l, stages, &map);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int n0 = blockIdx.x * kTileRows, rank = blockIdx.y;
-  const int blocks = (a.k + kStageK - 1) / kStageK;
-  const int k0 = static_cast<int>(static_cast<long long>(blocks) * rank / S) * kStageK;
-  const int k1 = min(a.k, static_cast<int>(static_cast<long long>(blocks) * (rank + 1) / S) * kStageK);
+  const CoreLayout l = core_layout<RG, false>(a.m, stages, 0);
+  const Ring r = core_setup<RG, false>(smem, l, a.m, stages, &map);
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int n0 = blockIdx.x * T::kRows, rank = blockIdx.y;
+  const int blocks = (a.k + T::kStageK - 1) / T::kStageK;
+  const int k0 = static_cast<int>(static_cast<long long>(blocks) * rank / S) * T::kStageK;
+  const int k1 = min(a.k, static_cast<int>(static_cast<long long>(blocks) * (rank + 1) / S) * T::kStageK);
   int *red = reinterpret_cast<int *>(smem + l.red);
-  int *recv = red + kRedInts;  // the second sum buffer: [S ranks][16 tokens][32 / S rows]
+  int *recv = red + T::kRedInts;  // the second sum buffer: [S ranks][16 tokens][rows / S]
   griddep_launch_dependents();
   if (S > 1) cluster_arrive();
 
   if (warp == kConsumers) {
-    if (lane == 0) {
-      int it = 0;
-      produce(r, &map, n0, 0, k0, k1, it, l2_policy_evict_first());
-      drain(r, it);
-    }
+    produce<RG, false>(r, &map, &xmap, [&](int) { return Source{n0, 0, a.m, nullptr}; }, 0, 1, 1, k0, k1,
+                       true);
     __syncwarp();
-    griddep_wait();
   } else {
-    griddep_wait();
-    const int8_t *xp[NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int token = nt * 8 + (lane >> 2);
-      xp[nt] = token < a.m ? a.xq + static_cast<size_t>(token) * a.k + 16 * (lane & 3) : nullptr;
-    }
-    int it = 0;
-    consume<NT>(r, xp, k0, k1, it, smem_u32(red));
+    RingPos pos;
+    consume<RG, false, NT>(r, a.m, k0, k1, pos, smem_u32(red));
     consumer_sync();
+    griddep_wait();  // the scales, and the order of the stores to y
   }
-  const int rows = kTileRows / S;
+  const int rows = T::kRows / S;
   if (S > 1) {
     cluster_wait();  // every rank has started
     if (warp < kConsumers)
-      for (int i = tid; i < NT * 8 * kTileRows; i += 32 * kConsumers) {
-        const int row = i % kTileRows, token = i / kTileRows;
+      for (int i = tid; i < a.m * T::kRows; i += 32 * kConsumers) {
+        const int row = i % T::kRows, token = i / T::kRows;
         const uint32_t to = smem_u32(recv + (rank * SK_MAX_M + token) * rows + row % rows);
         asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dsmem_map(to, row / rows)),
-                     "r"(red[token * kRedPitch + row])
+                     "r"(red[token * T::kRedPitch + row])
                      : "memory");
       }
     cluster_arrive();
@@ -500,7 +587,7 @@ __global__ void __launch_bounds__(kCoreThreads, 2)
     if (S > 1)
       for (int q = 0; q < S; ++q) s += recv[(q * SK_MAX_M + token) * rows + j];
     else
-      s = red[token * kRedPitch + j];
+      s = red[token * T::kRedPitch + j];
     a.y[static_cast<size_t>(token) * a.n + n] =
         bf16_store_bits(__fmul_rn(__fmul_rn(__int2float_rn(s), a.x_scale[token]), a.w_scale[n]));
   }
@@ -581,8 +668,9 @@ __global__ void __launch_bounds__(kCoreThreads, 2)
     experts_kernel(const __grid_constant__ CUtensorMap map, ExpertsArgs a, int stages) {
   extern __shared__ uint8_t raw[];
   uint8_t *smem = core_smem(raw);
-  const CoreLayout l = core_layout(stages, sizeof(Roster));
-  const Ring r = core_setup(smem, l, stages, &map);
+  using T = Shape<1, true>;
+  const CoreLayout l = core_layout<1, true>(a.m, stages, sizeof(Roster));
+  const Ring r = core_setup<1, true>(smem, l, a.m, stages, &map);
   Roster &q = *reinterpret_cast<Roster *>(smem + l.extra);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // The ids may come from the kernel ahead. The kernels after this one start
@@ -592,45 +680,34 @@ __global__ void __launch_bounds__(kCoreThreads, 2)
   build_roster(q, a);
 
   const int K = kUp ? a.hidden : a.inter, N = kUp ? a.inter : a.hidden;
-  constexpr int kRows = kUp ? kTileRows / 2 : kTileRows;
+  constexpr int kRows = kUp ? T::kRows / 2 : T::kRows;
   const int tiles = (N + kRows - 1) / kRows, items = q.n_active * tiles;
-  int it = 0;
   if (warp == kConsumers) {
-    if (lane == 0) {
-      const uint64_t policy = l2_policy_evict_first();
-      for (int i = blockIdx.x; i < items; i += gridDim.x) {
-        const int e = q.active[i / tiles];
-        produce(r, &map, i % tiles * kRows, kUp ? 2 * e : e, 0, K, it, policy);
-      }
-      drain(r, it);
-    }
-    __syncwarp();
-    if (!kUp) griddep_wait();
+    produce<1, true>(r, &map, nullptr,
+            [&](int i) {
+              const int e = q.active[i / tiles], count = __popc(q.mask[e]);
+              const int row = q.rows[q.offset[e] + (lane < count ? lane : 0)];
+              return Source{i % tiles * kRows, kUp ? 2 * e : e, count,
+                            (kUp ? a.xq + static_cast<size_t>(row / a.top_k) * K
+                                 : a.hq + static_cast<size_t>(row) * K)};
+            },
+            blockIdx.x, items, gridDim.x, 0, K, !kUp);
     return;
   }
   if (!kUp) griddep_wait();
   int *red = reinterpret_cast<int *>(smem + l.red);
+  RingPos pos;
   for (int i = blockIdx.x; i < items; i += gridDim.x) {
     const int e = q.active[i / tiles], n0 = i % tiles * kRows;
     const uint16_t *rows = q.rows + q.offset[e];
     const int count = __popc(q.mask[e]);
-    auto token_row = [&](int c) -> const int8_t * {
-      if (c >= count) return nullptr;
-      const size_t row = kUp ? rows[c] / a.top_k : rows[c];
-      return (kUp ? a.xq : a.hq) + row * K + 16 * (lane & 3);
-    };
-    if (count > 8) {
-      const int8_t *const xp[2] = {token_row(lane >> 2), token_row(8 + (lane >> 2))};
-      consume<2>(r, xp, 0, K, it, smem_u32(red));
-    } else {
-      const int8_t *const xp[1] = {token_row(lane >> 2)};
-      consume<1>(r, xp, 0, K, it, smem_u32(red));
-    }
+    if (count > 8) consume<1, true, 2>(r, count, 0, K, pos, smem_u32(red));
+    else consume<1, true, 1>(r, count, 0, K, pos, smem_u32(red));
     consumer_sync();
     const bool store = !*r.abort;
     for (int j = tid; j < count * kRows; j += 32 * kConsumers) {
       const int c = j / kRows, n = n0 + j % kRows, row = rows[c];
-      int *sum = &red[c * kRedPitch + j % kRows];
+      int *sum = &red[c * T::kRedPitch + j % kRows];
       if (kUp) {
         if (store && n < N) {
           const size_t gate = static_cast<size_t>(e) * 2 * N + n;
@@ -648,7 +725,7 @@ __global__ void __launch_bounds__(kCoreThreads, 2)
     }
     // The next item adds to the other buffer; this one is zero again before the
     // item after it, whose adds come after the next item's barrier.
-    red = reinterpret_cast<int *>(smem + l.red) + (red == reinterpret_cast<int *>(smem + l.red) ? kRedInts : 0);
+    red = reinterpret_cast<int *>(smem + l.red) + (red == reinterpret_cast<int *>(smem + l.red) ? T::kRedInts : 0);
   }
 }
 
@@ -687,56 +764,79 @@ cudaError_t experts_setup(const DeviceInfo &info) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(info.max_smem_optin - fa.sharedSizeBytes));
   };
-  if ((e = all_smem(gemm_int8_kernel<1>))) return e;
-  if ((e = all_smem(gemm_int8_kernel<2>))) return e;
+  if ((e = all_smem(gemm_int8_kernel<1, 1>))) return e;
+  if ((e = all_smem(gemm_int8_kernel<1, 2>))) return e;
+  if ((e = all_smem(gemm_int8_kernel<4, 1>))) return e;
+  if ((e = all_smem(gemm_int8_kernel<4, 2>))) return e;
   if ((e = all_smem(experts_kernel<true>))) return e;
   return all_smem(experts_kernel<false>);
 }
 
 // Ring stages of a core kernel with two CTAs per SM.
-static int core_stages(int extra) {
+template <int RG, bool kGather>
+static int core_stages(int m, int extra) {
   int st = 1;
-  while (1024 + core_layout(st + 1, extra).total <= static_cast<int>(kTwoPerSmSmem)) ++st;
+  while (1024 + core_layout<RG, kGather>(m, st + 1, extra).total <= static_cast<int>(kTwoPerSmSmem)) ++st;
   return st;
 }
 
-// Slices of K: as many as leave every CTA resident (two per SM) with at least
-// one stage each.
-int int8_splits(int n, int k, int sm_count) {
-  const int tiles = (n + kTileRows - 1) / kTileRows, blocks = (k + kStageK - 1) / kStageK;
-  int s = 1;
-  while (s < 8 && 2 * s <= blocks && static_cast<long long>(tiles) * 2 * s <= 2 * sm_count) s *= 2;
-  return s;
+// Tiles of 128 rows where K can be cut into enough slices to fill the SMs, of
+// 32 rows otherwise: the tokens' codes pass L2 once per tile, at 16 tokens
+// 12.5 % of the weights' bytes with 128 rows and 50 % with 32. S is the largest
+// of 1, 2, 4, 8 that leaves every CTA resident (two per SM) with a stage at
+// least.
+Int8Plan plan_int8(int m, int n, int k, int splits, int sm_count) {
+  auto best = [&](int rows, int stage_k) {
+    const int tiles = (n + rows - 1) / rows, blocks = (k + stage_k - 1) / stage_k;
+    int s = 1;
+    while (s < 8 && 2 * s <= blocks && static_cast<long long>(tiles) * 2 * s <= 2 * sm_count) s *= 2;
+    return s;
+  };
+  const int tall = splits ? splits : best(128, 128);
+  Int8Plan p;
+  p.tall = m > 2 && static_cast<long long>((n + 127) / 128) * tall >= sm_count;
+  if (const char *v = std::getenv("SK_INT8_TALL")) p.tall = v[0] == '1';
+  p.splits = p.tall ? tall : splits ? splits : best(32, 512);
+  return p;
 }
 
-cudaError_t launch_gemm_int8(const CUtensorMap &map, const Int8GemmArgs &a, cudaStream_t stream, bool pdl) {
-  const int blocks = (a.k + kStageK - 1) / kStageK;
+template <int RG>
+static cudaError_t launch_gemm_int8_rows(const CUtensorMap &map, const CUtensorMap &xmap,
+                                         const Int8GemmArgs &a, cudaStream_t stream, bool pdl) {
+  using T = Shape<RG, false>;
+  const int blocks = (a.k + T::kStageK - 1) / T::kStageK;
   const int per = (blocks + a.splits - 1) / a.splits;
-  const int most = core_stages(0), stages = per < most ? per : most;
-  const size_t smem = 1024 + core_layout(stages, 0).total;
-  const dim3 grid((a.n + kTileRows - 1) / kTileRows, a.splits);
-  return launch(a.m > 8 ? gemm_int8_kernel<2> : gemm_int8_kernel<1>, grid, dim3(kCoreThreads), smem,
-                stream, pdl, a.splits, map, a, stages);
+  const int most = core_stages<RG, false>(a.m, 0), stages = per < most ? per : most;
+  const size_t smem = 1024 + core_layout<RG, false>(a.m, stages, 0).total;
+  const dim3 grid((a.n + T::kRows - 1) / T::kRows, a.splits);
+  return launch(a.m > 8 ? gemm_int8_kernel<RG, 2> : gemm_int8_kernel<RG, 1>, grid, dim3(kCoreThreads),
+                smem, stream, pdl, a.splits, map, xmap, a, stages);
+}
+
+cudaError_t launch_gemm_int8(const CUtensorMap &map, const CUtensorMap &xmap, const Int8GemmArgs &a,
+                             bool tall, cudaStream_t stream, bool pdl) {
+  return tall ? launch_gemm_int8_rows<4>(map, xmap, a, stream, pdl)
+              : launch_gemm_int8_rows<1>(map, xmap, a, stream, pdl);
 }
 
 cudaError_t launch_experts_int8(const CUtensorMap &map13, const CUtensorMap &map2, const ExpertsArgs &a,
                                 int sm_count, cudaStream_t stream, bool pdl) {
   const unsigned rows = static_cast<unsigned>(a.m * a.top_k);
-  const int stages = core_stages(sizeof(Roster));
-  const size_t smem = 1024 + core_layout(stages, sizeof(Roster)).total;
+  const int stages = core_stages<1, true>(a.m, sizeof(Roster));
+  const size_t smem = 1024 + core_layout<1, true>(a.m, stages, sizeof(Roster)).total;
   // no more CTAs than items if every choice names another expert
   const int active = a.n_experts < a.m * a.top_k ? a.n_experts : a.m * a.top_k;
   auto ctas = [&](int tiles) {
     const long long items = static_cast<long long>(active) * tiles;
     return dim3(static_cast<unsigned>(items < 2 * sm_count ? items : 2 * sm_count));
   };
-  cudaError_t e = launch(experts_kernel<true>, ctas((a.inter + kTileRows / 2 - 1) / (kTileRows / 2)),
+  cudaError_t e = launch(experts_kernel<true>, ctas((a.inter + 15) / 16),
                          dim3(kCoreThreads), smem, stream, pdl, 1, map13, a, stages);
   if (e != cudaSuccess) return e;
   e = launch(quantize_kernel<float>, dim3(rows), dim3(256), 0, stream, pdl, 1,
              static_cast<const float *>(a.act), a.hq, a.hs, a.inter, a.ids, a.n_experts);
   if (e != cudaSuccess) return e;
-  e = launch(experts_kernel<false>, ctas((a.hidden + kTileRows - 1) / kTileRows), dim3(kCoreThreads), smem,
+  e = launch(experts_kernel<false>, ctas((a.hidden + 31) / 32), dim3(kCoreThreads), smem,
              stream, pdl, 1, map2, a, stages);
   if (e != cudaSuccess) return e;
   return launch(experts_sum_kernel, dim3((a.hidden + 255) / 256, a.m), dim3(256), 0, stream, pdl, 1, a);

@@ -152,11 +152,13 @@ sk_status sk_gemm_int8(const int8_t *xq, const float *x_scale, const int8_t *wq,
   sk::DeviceInfo info;
   int dev = 0;
   if ((st = sk::checked_device(&info, &dev)) != SK_OK) return st;
-  sk::Int8GemmArgs a{xq, wq, x_scale, w_scale, static_cast<uint16_t *>(y), m, n, k,
-                     splits ? splits : sk::int8_splits(n, k, info.sm_count)};
-  CUtensorMap map;
-  if ((st = sk::make_int8_map(&map, wq, k, n, 1, 32, 1)) != SK_OK) return st;
-  return launch_status(sk::launch_gemm_int8(map, a, as_stream(stream), sk::pdl_on()), "gemm_int8");
+  const sk::Int8Plan plan = sk::plan_int8(m, n, k, splits, info.sm_count);
+  sk::Int8GemmArgs a{xq, wq, x_scale, w_scale, static_cast<uint16_t *>(y), m, n, k, plan.splits};
+  CUtensorMap map, xmap;
+  if ((st = sk::make_int8_map(&map, wq, k, n, 1, plan.tall ? 128 : 32, 1)) != SK_OK) return st;
+  if ((st = sk::make_int8_map(&xmap, xq, k, m, 1, m > 8 ? 16 : 8, 1)) != SK_OK) return st;
+  return launch_status(sk::launch_gemm_int8(map, xmap, a, plan.tall, as_stream(stream), sk::pdl_on()),
+                       "gemm_int8");
 }
 
 static sk_status check_experts(int m, int top_k, int hidden, int inter) {

@@ -228,9 +228,16 @@ struct Int8GemmArgs {
   uint16_t *y;
   int m, n, k, splits;
 };
-// map: weight codes {k, n, 1}, box {128, 32, 1}, 128-byte swizzle; a.splits >= 1.
-cudaError_t launch_gemm_int8(const CUtensorMap &map, const Int8GemmArgs &a, cudaStream_t stream, bool pdl);
-int int8_splits(int n, int k, int sm_count);
+// Tile height (tall: 128 output features per CTA, else 32) and slices of K.
+struct Int8Plan {
+  bool tall;
+  int splits;
+};
+Int8Plan plan_int8(int m, int n, int k, int splits, int sm_count);
+// map: weight codes {k, n, 1}, box {128, tile height, 1}; xmap: token codes
+// {k, m, 1}, box {128, 8 or 16 (m > 8), 1}; both swizzled over 128 bytes.
+cudaError_t launch_gemm_int8(const CUtensorMap &map, const CUtensorMap &xmap, const Int8GemmArgs &a,
+                             bool tall, cudaStream_t stream, bool pdl);
 
 // The routed experts (sk_experts_int8); act, hq, hs and o are parts of the
 // caller's workspace, one row per choice.
