@@ -209,16 +209,19 @@ __global__ void __launch_bounds__(256)
 // at most 16 tokens, far below what the tensor cores need to be busy, so HBM
 // is the bound and the rest has to stay out of its way. One producer thread
 // copies weights with TMA, a stage of 16 KiB at a time, into a ring, and the
-// token rows' columns with them; eight consumer warps each take 32 rows and 64
-// columns of every stage.
+// token rows' columns with them; eight consumer warps multiply.
 //
-// The tensor cores multiply int8 codes at FP16: a code widens to FP16 exactly
-// by placing code + 128 in the mantissa of 1024 and subtracting 1152 (one
-// exclusive-or, two byte permutes and two FP16x2 additions for four codes).
-// Products are integers below 2^15 and FP32 holds every partial sum exactly up
-// to 2^24, i.e. over 1024 columns of a warp: 16 stages, after which the
+// The tensor cores multiply int8 codes at FP16, exactly. A weight code w goes
+// in as the FP16 subnormal (w + 128) 2^-24, which costs no arithmetic: masked
+// bytes with the sign bit flipped (two three-input logic operations and a shift
+// for four codes). A token code x becomes the FP16 integer x: code + 128 in the
+// mantissa of 1024, less 1152. What is summed is (w + 128) x; the 128 sum x that
+// this adds is known from the token row alone and taken off at the end. Every
+// product is an integer below 2^15 (times 2^-24) and FP32 holds every partial
+// sum exactly up to 2^24, i.e. over 512 columns of a warp, after which the
 // accumulators move to 32-bit integers. The warps' and CTAs' sums are added as
-// integers, so neither the order nor the split count can change a result.
+// integers (modulo 2^32), so neither the order nor the split count can change a
+// result.
 //
 // K order within a block is free as long as both operands agree: thread t of a
 // quad holds columns 16 t .. 16 t + 15 (one 16-byte load of a weight row, one of
@@ -227,27 +230,37 @@ constexpr int kBoxK = 128;                                // columns of a TMA bo
 constexpr int kStageWBytes = 16 * 1024;                   // weights of a stage
 constexpr int kConsumers = 8;                             // warps
 constexpr int kCoreThreads = 32 * (kConsumers + 1);
-constexpr int kExactStages = 16;                          // stages between moves to integers
+constexpr int kExactStages = 8;                           // a warp's stages between moves to integers
 constexpr uint64_t kCoreWaitNs = 2000000000ull;           // 2 s of wall time per wait
 
-// A stage's shape: 32 RG rows by 512 / RG columns; the warps form RG row groups
-// and 8 / RG column groups. kGather: the token rows come one by one (bulk
-// copies to rows of a fixed pitch); else they are a tile of the activations
-// ([m, k], TMA boxes of 8 or 16 rows).
-template <int RG, bool kGather>
+// A stage's shape: kRows rows by 16 KiB / kRows columns. A warp takes 64 columns
+// and 16 kTiles rows of a stage, kWarps warps a whole stage; with kSets > 1 the
+// sets of warps take turns, so that one set's latency hides behind another's.
+// kGather: the token rows come one by one (bulk copies to rows of a fixed
+// pitch); else they are a tile of the activations ([m, k], TMA boxes of 8 or 16
+// rows).
+template <int kRows_, int kTiles_, bool kGather_>
 struct Shape {
-  static constexpr int kRows = 32 * RG;
-  static constexpr int kStageK = 512 / RG;
+  static constexpr bool kGather = kGather_;
+  static constexpr int kRows = kRows_, kTiles = kTiles_;
+  static constexpr int kStageK = kStageWBytes / kRows;
+  static constexpr int kRowGroups = kRows / (16 * kTiles);
+  static constexpr int kWarps = kStageK / 64 * kRowGroups;
+  static constexpr int kSets = kConsumers / kWarps;
   static constexpr int kBoxes = kStageK / kBoxK;
   static constexpr int kBoxBytes = kRows * kBoxK;
   static constexpr int kXPitch = kStageK + 64;           // kGather: bytes per token row of a stage
-  static constexpr int kRedPitch = kRows + (kGather ? 4 : 8);  // ints per token of the sum buffer
+  // ints per token of the sum buffer: the rows' sums, then the token's own
+  static constexpr int kRedPitch = kRows + (kGather ? 4 : 8);
   static constexpr int kRedInts = SK_MAX_M * kRedPitch;
   __host__ __device__ static constexpr int x_rows(int m) { return m > 8 ? 16 : 8; }
   __host__ __device__ static constexpr int stage_bytes(int m) {
     return (kStageWBytes + x_rows(m) * (kGather ? kXPitch : kStageK) + 1023) / 1024 * 1024;
   }
 };
+using TallShape = Shape<128, 4, false>;   // 128 rows x 128 columns, two sets of four warps
+using LowShape = Shape<32, 2, false>;     // 32 rows x 512 columns
+using ExpertShape = Shape<32, 2, true>;
 
 __device__ uint32_t g_core_status;  // OR of SK_DEVICE_WAIT_* bits
 
@@ -270,18 +283,20 @@ struct RingPos {
 };
 
 // A wait that runs out raises the abort flag, after which no wait of the CTA
-// waits: every role runs through its loops, nothing is stored.
-__device__ __forceinline__ void ring_wait(const Ring &r, uint32_t bar, uint32_t parity, uint32_t bit) {
-  if (mbar_try_wait(bar, parity)) return;
+// waits: every role runs through its loops, nothing is stored. False after an
+// abort.
+__device__ __forceinline__ bool ring_wait(const Ring &r, uint32_t bar, uint32_t parity, uint32_t bit) {
+  if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity)) {
-    if (*r.abort) return;
+    if (*r.abort) return false;
     if (globaltimer_ns() - t0 > kCoreWaitNs) {
       *r.abort = 1;
       atomicOr(&g_core_status, bit);
-      return;
+      return false;
     }
   }
+  return true;
 }
 
 // After an abort: waits (again with a limit) for the copies still in flight, of
@@ -298,64 +313,65 @@ struct Source {
   const int8_t *x;
 };
 
-template <int RG, bool kGather>
-__device__ __forceinline__ void copy_weights(const Ring &r, const CUtensorMap *map, const Source &s,
-                                             int st, int k, int k1, uint64_t policy) {
-  using T = Shape<RG, kGather>;
-  const int boxes = min(T::kBoxes, (k1 - k + kBoxK - 1) / kBoxK);
-  const uint32_t bar = r.full + 8 * st;
-  mbar_arrive_expect_tx(bar, boxes * T::kBoxBytes + (kGather ? s.tokens * min(T::kStageK, k1 - k)
-                                                             : boxes * r.x_rows * kBoxK));
-  for (int b = 0; b < boxes; ++b)
-    tma_load_3d(r.data + st * r.stage_bytes + b * T::kBoxBytes, map, bar, k + b * kBoxK, s.row, s.batch,
-                policy);
-}
-
-template <int RG, bool kGather>
-__device__ __forceinline__ void copy_tokens(const Ring &r, const CUtensorMap *xmap, const Source &s,
-                                            int st, int k, int k1, uint64_t policy) {
-  using T = Shape<RG, kGather>;
-  const int lane = threadIdx.x & 31;
-  const uint32_t to = r.data + st * r.stage_bytes + kStageWBytes, bar = r.full + 8 * st;
-  if (kGather) {
-    if (lane < s.tokens)
-      asm volatile(
-          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-              to + lane * T::kXPitch),
-          "l"(__cvta_generic_to_global(s.x + k)), "r"(min(T::kStageK, k1 - k)), "r"(bar)
-          : "memory");
-  } else if (lane == 0) {
-    const int boxes = min(T::kBoxes, (k1 - k + kBoxK - 1) / kBoxK);
-    for (int b = 0; b < boxes; ++b)
-      tma_load_3d(to + b * r.x_rows * kBoxK, xmap, bar, k + b * kBoxK, 0, 0, policy);
+// The copies of a stage, each by a lane of its own in one instruction: the
+// producer shares its scheduler with busy warps, and a loop over the copies by
+// one thread held the ring back (m1 [8192, 32768] in 32-row tiles: 60 us, the
+// copies alone 44 us). `tokens` tells whether the token rows are sent too, or
+// the weights alone, or (weights false) the token rows alone.
+template <typename T>
+__device__ __forceinline__ void copy_stage(const Ring &r, const CUtensorMap *map, const CUtensorMap *xmap,
+                                           const Source &s, int st, int k, int k1, bool weights,
+                                           bool tokens, uint64_t policy) {
+  const int lane = threadIdx.x & 31, left = k1 - k;
+  const uint32_t to = r.data + st * r.stage_bytes, bar = r.full + 8 * st;
+  if (weights) {
+    if (lane == 0) {
+      const int boxes = left >= T::kStageK ? T::kBoxes : (left + kBoxK - 1) / kBoxK;
+      mbar_arrive_expect_tx(bar, boxes * T::kBoxBytes + (T::kGather ? s.tokens * min(T::kStageK, left)
+                                                                    : boxes * r.x_rows * kBoxK));
+    }
+    __syncwarp();  // a stage's bytes are announced before any of them arrives
   }
+  // lanes 0 .. kBoxes - 1: weight boxes; the next kBoxes: token boxes
+  const int b = lane % T::kBoxes;
+  const bool w = lane < T::kBoxes;
+  const bool mine = w ? weights : !T::kGather && tokens && lane < 2 * T::kBoxes;
+  if (mine && b * kBoxK < left)
+    tma_load_3d(to + (w ? b * T::kBoxBytes : kStageWBytes + b * r.x_rows * kBoxK), w ? map : xmap, bar,
+                k + b * kBoxK, w ? s.row : 0, w ? s.batch : 0, policy);
+  if (T::kGather && tokens && lane < s.tokens)
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            to + kStageWBytes + lane * T::kXPitch),
+        "l"(__cvta_generic_to_global(s.x + k)), "r"(min(T::kStageK, left)), "r"(bar)
+        : "memory");
 }
 
 // The producer warp: copies columns [k0, k1) of the items first, first + step,
 // ... below last, stage by stage. With `early` the token rows are not written
 // yet: the first ring of weights goes out before the wait for the kernel ahead,
 // its token rows after it.
-template <int RG, bool kGather, typename Items>
+template <typename T, typename Items>
 __device__ __forceinline__ void produce(const Ring &r, const CUtensorMap *map, const CUtensorMap *xmap,
                                         Items source, int first, int last, int step, int k0, int k1,
                                         bool early) {
-  constexpr int kStageK = Shape<RG, kGather>::kStageK;
+  constexpr int kStageK = T::kStageK;
   const int lane = threadIdx.x & 31;
-  const uint64_t policy = l2_policy_evict_first(), keep = l2_policy_evict_last();
+  // each weight is read once, the token rows by every tile
+  const uint64_t policy = lane < T::kBoxes ? l2_policy_evict_first() : l2_policy_evict_last();
   int sent = 0;
   if (early) {
     for (int i = first; i < last && sent < r.stages; i += step) {
       const Source s = source(i);
       for (int k = k0; k < k1 && sent < r.stages; k += kStageK, ++sent)
-        if (lane == 0) copy_weights<RG, kGather>(r, map, s, sent, k, k1, policy);
+        copy_stage<T>(r, map, xmap, s, sent, k, k1, true, false, policy);
     }
-    __syncwarp();  // a stage's bytes are announced before any of its rows arrives
     griddep_wait();
     int n = 0;
     for (int i = first; i < last && n < sent; i += step) {
       const Source s = source(i);
       for (int k = k0; k < k1 && n < sent; k += kStageK, ++n)
-        copy_tokens<RG, kGather>(r, xmap, s, n, k, k1, keep);
+        copy_stage<T>(r, map, xmap, s, n, k, k1, false, true, policy);
     }
   }
   RingPos pos;
@@ -364,24 +380,40 @@ __device__ __forceinline__ void produce(const Ring &r, const CUtensorMap *map, c
     const Source s = source(i);
     for (int k = k0; k < k1; k += kStageK, ++it, pos.next(r.stages)) {
       if (it < sent) continue;
-      if (pos.lap) ring_wait(r, r.empty + 8 * pos.st, (pos.lap - 1) & 1, SK_DEVICE_WAIT_PRODUCER);
-      if (__any_sync(0xFFFFFFFFu, *r.abort)) {
+      const bool go = !pos.lap || ring_wait(r, r.empty + 8 * pos.st, (pos.lap - 1) & 1,
+                                            SK_DEVICE_WAIT_PRODUCER);
+      if (!__all_sync(0xFFFFFFFFu, go)) {
         drain(r, it);
         return;
       }
-      if (lane == 0) copy_weights<RG, kGather>(r, map, s, pos.st, k, k1, policy);
-      __syncwarp();
-      copy_tokens<RG, kGather>(r, xmap, s, pos.st, k, k1, keep);
+      copy_stage<T>(r, map, xmap, s, pos.st, k, k1, true, true, policy);
     }
   }
   if (__any_sync(0xFFFFFFFFu, *r.abort)) drain(r, it);
 }
 
-// Four int8 codes -> two FP16 pairs, exact.
-__device__ __forceinline__ void widen(uint32_t w, uint32_t &lo, uint32_t &hi) {
+// The constants of widen_weight in registers: a three-input logic operation
+// takes one immediate only.
+struct WidenConst {
+  uint32_t mask, flip;
+  __device__ __forceinline__ WidenConst() {
+    asm volatile("mov.u32 %0, 0x00FF00FF;" : "=r"(mask));
+    asm volatile("mov.u32 %0, 0x00800080;" : "=r"(flip));
+  }
+};
+
+// Four codes of a weight -> two FP16 pairs (bytes 0 and 2, 1 and 3) of
+// (code + 128) 2^-24.
+__device__ __forceinline__ void widen_weight(const WidenConst &c, uint32_t w, uint32_t &lo, uint32_t &hi) {
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(lo) : "r"(w), "r"(c.mask), "r"(c.flip));  // (w & mask) ^ flip
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(hi) : "r"(w >> 8), "r"(c.mask), "r"(c.flip));
+}
+
+// Four codes of a token -> two FP16 pairs of the codes, in the same order.
+__device__ __forceinline__ void widen_token(uint32_t w, uint32_t &lo, uint32_t &hi) {
   const uint32_t u = w ^ 0x80808080u;
   const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
-  uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+  uint32_t a = __byte_perm(u, 0x64646464u, 0x4240), b = __byte_perm(u, 0x64646464u, 0x4341);
   __half2 x = __hsub2(*reinterpret_cast<__half2 *>(&a), off);
   __half2 y = __hsub2(*reinterpret_cast<__half2 *>(&b), off);
   lo = *reinterpret_cast<uint32_t *>(&x);
@@ -390,82 +422,96 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t &lo, uint32_t &hi) {
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// One consumer warp's part of an item: adds its column blocks' products of its
-// 32 tile rows with the first `tokens` (at most 8 NT) token rows of the stages to
-// red[token][row] (a shared address). Rows of a stage beyond `tokens` hold zeros
-// or leftovers, whose sums are not added.
-template <int RG, bool kGather, int NT>
-__device__ __forceinline__ void consume(const Ring &r, int tokens, int k0, int k1, RingPos &pos,
+__device__ __forceinline__ void red_shared(uint32_t addr, int v) {
+  asm volatile("red.shared.add.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// One consumer warp's part of an item: adds its products with the first `tokens`
+// (at most 8 NT) token rows of the stages to red[token][row] (a shared address),
+// and the token rows' own sums to red[token][kRows]. Rows of a stage beyond
+// `tokens` hold zeros or leftovers, whose sums are not added. seq counts the
+// CTA's stages, for the sets' turns.
+template <typename T, int NT>
+__device__ __forceinline__ void consume(const Ring &r, int tokens, int k0, int k1, int &seq, RingPos &pos,
                                         uint32_t red) {
-  using T = Shape<RG, kGather>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int cg = warp / RG, rg = warp % RG;  // column and row group
+  const int set = warp / T::kWarps, w = warp % T::kWarps;
+  const int cg = w / T::kRowGroups, rg = w % T::kRowGroups;  // column and row group
   // Tile row of the lane within eight: rows g = 2 i and 2 i + 1, which a load
   // phase reads together, are four apart, so their swizzles use both halves of
   // the 128-byte row and no two lanes of the phase meet in a bank. Gathered
   // token rows, at a pitch of an odd number of 64 bytes, need no reordering.
   const int pg = ((g & 1) << 2) | (g >> 1);
   const uint32_t chunk = static_cast<uint32_t>((((cg & 1) << 2) | t) ^ pg) << 4;
-  const uint32_t at = r.data + (cg >> 1) * T::kBoxBytes + (rg * 32 + pg) * kBoxK + chunk;
+  const uint32_t at = r.data + (cg >> 1) * T::kBoxBytes + (rg * 16 * T::kTiles + pg) * kBoxK + chunk;
   const uint32_t xat = r.data + kStageWBytes +
-                       (kGather ? g * T::kXPitch + cg * 64 + t * 16
-                                : (cg >> 1) * r.x_rows * kBoxK + pg * kBoxK + chunk);
-  constexpr uint32_t kXStep = 8 * (kGather ? T::kXPitch : kBoxK);
-  float acc[2][NT][4];
+                       (T::kGather ? g * T::kXPitch + cg * 64 + t * 16
+                                   : (cg >> 1) * r.x_rows * kBoxK + pg * kBoxK + chunk);
+  constexpr uint32_t kXStep = 8 * (T::kGather ? T::kXPitch : kBoxK);
+  const WidenConst wc;
+  const int ones = rg == 0 ? 0x01010101 : 0;  // one row group sums the token's codes
+  float acc[T::kTiles][NT][4];
+  int xsum[NT];
 #pragma unroll
-  for (int i = 0; i < 2 * NT * 4; ++i) (&acc[0][0][0])[i] = 0.0f;
+  for (int i = 0; i < T::kTiles * NT * 4; ++i) (&acc[0][0][0])[i] = 0.0f;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) xsum[nt] = 0;
   auto flush = [&] {
 #pragma unroll
-    for (int rt = 0; rt < 2; ++rt)
+    for (int rt = 0; rt < T::kTiles; ++rt)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int token = nt * 8 + (kGather ? 2 * t + (i & 1) : t + 4 * (i & 1));
-          const int row = rg * 32 + rt * 16 + pg + (i >> 1) * 8;
+          const int token = nt * 8 + (T::kGather ? 2 * t + (i & 1) : t + 4 * (i & 1));
+          const int row = (rg * T::kTiles + rt) * 16 + pg + (i >> 1) * 8;
           if (token < tokens)
-            asm volatile("red.shared.add.s32 [%0], %1;" ::"r"(red + 4u * (token * T::kRedPitch + row)),
-                         "r"(__float2int_rn(acc[rt][nt][i]))
-                         : "memory");
+            red_shared(red + 4u * (token * T::kRedPitch + row), __float2int_rn(acc[rt][nt][i] * 0x1p24f));
           acc[rt][nt][i] = 0.0f;
         }
   };
   int done = 0;
-  for (int k = k0; k < k1; k += T::kStageK, pos.next(r.stages)) {
+  for (int k = k0; k < k1; k += T::kStageK, pos.next(r.stages), ++seq) {
+    if (T::kSets > 1 && seq % T::kSets != set) continue;
     const uint32_t off = pos.st * r.stage_bytes;
     ring_wait(r, r.full + 8 * pos.st, pos.lap & 1, SK_DEVICE_WAIT_MMA);
     if (k + cg * 64 < k1) {
+      uint4 x[NT], wt[T::kTiles][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) x[nt] = lds128(xat + off + nt * kXStep);
+#pragma unroll
+      for (int rt = 0; rt < T::kTiles; ++rt) {
+        wt[rt][0] = lds128(at + off + rt * 16 * kBoxK);
+        wt[rt][1] = lds128(at + off + (rt * 16 + 8) * kBoxK);
+      }
       uint32_t b[NT][8];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const uint4 x = lds128(xat + off + nt * kXStep);
-        widen(x.x, b[nt][0], b[nt][1]);
-        widen(x.y, b[nt][2], b[nt][3]);
-        widen(x.z, b[nt][4], b[nt][5]);
-        widen(x.w, b[nt][6], b[nt][7]);
-      }
-#pragma unroll
-      for (int rt = 0; rt < 2; ++rt) {
-        const uint4 w0 = lds128(at + off + rt * 16 * kBoxK);
-        const uint4 w1 = lds128(at + off + (rt * 16 + 8) * kBoxK);
-        const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, hi[4] = {w1.x, w1.y, w1.z, w1.w};
+        const uint32_t xw[4] = {x[nt].x, x[nt].y, x[nt].z, x[nt].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+          widen_token(xw[i], b[nt][2 * i], b[nt][2 * i + 1]);
+          xsum[nt] = __dp4a(static_cast<int>(xw[i]), ones, xsum[nt]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int rt = 0; rt < T::kTiles; ++rt) {
+          const uint4 &w0 = wt[rt][0], &w1 = wt[rt][1];
           uint32_t a0, a1, a2, a3;
-          widen(lo[i], a0, a2);
-          widen(hi[i], a1, a3);
+          widen_weight(wc, i == 0 ? w0.x : i == 1 ? w0.y : i == 2 ? w0.z : w0.w, a0, a2);
+          widen_weight(wc, i == 0 ? w1.x : i == 1 ? w1.y : i == 2 ? w1.z : w1.w, a1, a3);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
             mma_f16(acc[rt][nt], a0, a1, a2, a3, b[nt][2 * i], b[nt][2 * i + 1]);
         }
-      }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(r.empty + 8 * pos.st);
@@ -475,6 +521,20 @@ __device__ __forceinline__ void consume(const Ring &r, int tokens, int k0, int k
     }
   }
   if (done) flush();
+  if (rg == 0)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int token = nt * 8 + (T::kGather ? g : pg);
+      if (token < tokens) red_shared(red + 4u * (token * T::kRedPitch + T::kRows), xsum[nt]);
+    }
+}
+
+// The sum of products of a token with a tile row: the correction of the weights'
+// offset by 128 (modulo 2^32).
+template <typename T>
+__device__ __forceinline__ int red_sum(const int *red, int token, int row) {
+  const uint32_t s = red[token * T::kRedPitch + row], x = red[token * T::kRedPitch + T::kRows];
+  return static_cast<int>(s - 128u * x);
 }
 
 __device__ __forceinline__ void consumer_sync() {
@@ -486,9 +546,8 @@ __device__ __forceinline__ void consumer_sync() {
 struct CoreLayout {
   int red, bars, flag, extra, total;
 };
-template <int RG, bool kGather>
+template <typename T>
 __host__ __device__ inline CoreLayout core_layout(int m, int stages, int extra) {
-  using T = Shape<RG, kGather>;
   CoreLayout l;
   l.red = stages * T::stage_bytes(m);
   l.bars = l.red + 2 * T::kRedInts * 4;
@@ -503,10 +562,9 @@ __device__ __forceinline__ uint8_t *core_smem(uint8_t *raw) {
 }
 
 // Set-up by all threads of a core kernel: barriers, abort flag, zeroed sums.
-template <int RG, bool kGather>
+template <typename T>
 __device__ __forceinline__ Ring core_setup(uint8_t *smem, const CoreLayout &l, int m, int stages,
                                            const CUtensorMap *map) {
-  using T = Shape<RG, kGather>;
   Ring r;
   r.data = smem_u32(smem);
   r.full = smem_u32(smem + l.bars);
@@ -520,7 +578,7 @@ __device__ __forceinline__ Ring core_setup(uint8_t *smem, const CoreLayout &l, i
   if (threadIdx.x == 32 * kConsumers) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(r.full + 8 * s, 1);
-      mbar_init(r.empty + 8 * s, kConsumers);
+      mbar_init(r.empty + 8 * s, T::kWarps);
     }
     *r.abort = 0;
     fence_barrier_init();
@@ -531,20 +589,19 @@ __device__ __forceinline__ Ring core_setup(uint8_t *smem, const CoreLayout &l, i
 }
 
 // ----------------------------------------------------------------- int8 GEMM
-// Grid (tiles of 32 RG output features, S slices of K), cluster (1, S, 1):
+// Grid (tiles of kRows output features, S slices of K), cluster (1, S, 1):
 // every CTA is resident from the start, two per SM, so that the stream does not
 // wait for scheduling. The S sums of a tile meet in shared memory: rank r
 // receives a slice of the rows from every rank and finishes them.
-template <int RG, int NT>
+template <typename T, int NT>
 __global__ void __launch_bounds__(kCoreThreads, 2)
     gemm_int8_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap xmap,
                      Int8GemmArgs a, int stages) {
-  using T = Shape<RG, false>;
   extern __shared__ uint8_t raw[];
   uint8_t *smem = core_smem(raw);
   const int S = a.splits;
-  const CoreLayout l = core_layout<RG, false>(a.m, stages, 0);
-  const Ring r = core_setup<RG, false>(smem, l, a.m, stages, &map);
+  const CoreLayout l = core_layout<T>(a.m, stages, 0);
+  const Ring r = core_setup<T>(smem, l, a.m, stages, &map);
   const int tid = threadIdx.x, warp = tid >> 5;
   const int n0 = blockIdx.x * T::kRows, rank = blockIdx.y;
   const int blocks = (a.k + T::kStageK - 1) / T::kStageK;
@@ -556,12 +613,13 @@ __global__ void __launch_bounds__(kCoreThreads, 2)
   if (S > 1) cluster_arrive();
 
   if (warp == kConsumers) {
-    produce<RG, false>(r, &map, &xmap, [&](int) { return Source{n0, 0, a.m, nullptr}; }, 0, 1, 1, k0, k1,
+    produce<T>(r, &map, &xmap, [&](int) { return Source{n0, 0, a.m, nullptr}; }, 0, 1, 1, k0, k1,
                        true);
     __syncwarp();
   } else {
     RingPos pos;
-    consume<RG, false, NT>(r, a.m, k0, k1, pos, smem_u32(red));
+    int seq = 0;
+    consume<T, NT>(r, a.m, k0, k1, seq, pos, smem_u32(red));
     consumer_sync();
     griddep_wait();  // the scales, and the order of the stores to y
   }
@@ -573,7 +631,7 @@ __global__ void __launch_bounds__(kCoreThreads, 2)
         const int row = i % T::kRows, token = i / T::kRows;
         const uint32_t to = smem_u32(recv + (rank * SK_MAX_M + token) * rows + row % rows);
         asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dsmem_map(to, row / rows)),
-                     "r"(red[token * T::kRedPitch + row])
+                     "r"(red_sum<T>(red, token, row))
                      : "memory");
       }
     cluster_arrive();
@@ -587,7 +645,7 @@ __global__ void __launch_bounds__(kCoreThreads, 2)
     if (S > 1)
       for (int q = 0; q < S; ++q) s += recv[(q * SK_MAX_M + token) * rows + j];
     else
-      s = red[token * T::kRedPitch + j];
+      s = red_sum<T>(red, token, j);
     a.y[static_cast<size_t>(token) * a.n + n] =
         bf16_store_bits(__fmul_rn(__fmul_rn(__int2float_rn(s), a.x_scale[token]), a.w_scale[n]));
   }
@@ -668,9 +726,9 @@ __global__ void __launch_bounds__(kCoreThreads, 2)
     experts_kernel(const __grid_constant__ CUtensorMap map, ExpertsArgs a, int stages) {
   extern __shared__ uint8_t raw[];
   uint8_t *smem = core_smem(raw);
-  using T = Shape<1, true>;
-  const CoreLayout l = core_layout<1, true>(a.m, stages, sizeof(Roster));
-  const Ring r = core_setup<1, true>(smem, l, a.m, stages, &map);
+  using T = ExpertShape;
+  const CoreLayout l = core_layout<T>(a.m, stages, sizeof(Roster));
+  const Ring r = core_setup<T>(smem, l, a.m, stages, &map);
   Roster &q = *reinterpret_cast<Roster *>(smem + l.extra);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // The ids may come from the kernel ahead. The kernels after this one start
@@ -683,7 +741,7 @@ __global__ void __launch_bounds__(kCoreThreads, 2)
   constexpr int kRows = kUp ? T::kRows / 2 : T::kRows;
   const int tiles = (N + kRows - 1) / kRows, items = q.n_active * tiles;
   if (warp == kConsumers) {
-    produce<1, true>(r, &map, nullptr,
+    produce<T>(r, &map, nullptr,
             [&](int i) {
               const int e = q.active[i / tiles], count = __popc(q.mask[e]);
               const int row = q.rows[q.offset[e] + (lane < count ? lane : 0)];
@@ -697,32 +755,33 @@ __global__ void __launch_bounds__(kCoreThreads, 2)
   if (!kUp) griddep_wait();
   int *red = reinterpret_cast<int *>(smem + l.red);
   RingPos pos;
+  int seq = 0;
   for (int i = blockIdx.x; i < items; i += gridDim.x) {
     const int e = q.active[i / tiles], n0 = i % tiles * kRows;
     const uint16_t *rows = q.rows + q.offset[e];
     const int count = __popc(q.mask[e]);
-    if (count > 8) consume<1, true, 2>(r, count, 0, K, pos, smem_u32(red));
-    else consume<1, true, 1>(r, count, 0, K, pos, smem_u32(red));
+    if (count > 8) consume<T, 2>(r, count, 0, K, seq, pos, smem_u32(red));
+    else consume<T, 1>(r, count, 0, K, seq, pos, smem_u32(red));
     consumer_sync();
     const bool store = !*r.abort;
     for (int j = tid; j < count * kRows; j += 32 * kConsumers) {
-      const int c = j / kRows, n = n0 + j % kRows, row = rows[c];
-      int *sum = &red[c * T::kRedPitch + j % kRows];
+      const int c = j / kRows, at = j % kRows, n = n0 + at, row = rows[c];
+      if (!store || n >= N) continue;
+      const float s0 = __int2float_rn(red_sum<T>(red, c, at));
       if (kUp) {
-        if (store && n < N) {
-          const size_t gate = static_cast<size_t>(e) * 2 * N + n;
-          const float xs = a.x_scale[row / a.top_k];
-          const float g = __fmul_rn(__fmul_rn(__int2float_rn(sum[0]), xs), a.s13[gate]);
-          const float u = __fmul_rn(__fmul_rn(__int2float_rn(sum[kRows]), xs), a.s13[gate + N]);
-          a.act[static_cast<size_t>(row) * N + n] = g / (1.0f + expf(-g)) * u;
-        }
-        sum[kRows] = 0;
-      } else if (store && n < N) {
+        const size_t gate = static_cast<size_t>(e) * 2 * N + n;
+        const float xs = a.x_scale[row / a.top_k];
+        const float g = __fmul_rn(__fmul_rn(s0, xs), a.s13[gate]);
+        const float u = __fmul_rn(__fmul_rn(__int2float_rn(red_sum<T>(red, c, kRows + at)), xs),
+                                  a.s13[gate + N]);
+        a.act[static_cast<size_t>(row) * N + n] = g / (1.0f + expf(-g)) * u;
+      } else {
         a.o[static_cast<size_t>(row) * N + n] =
-            __fmul_rn(__fmul_rn(__int2float_rn(sum[0]), a.hs[row]), a.s2[static_cast<size_t>(e) * N + n]);
+            __fmul_rn(__fmul_rn(s0, a.hs[row]), a.s2[static_cast<size_t>(e) * N + n]);
       }
-      sum[0] = 0;
     }
+    consumer_sync();
+    for (int j = tid; j < count * T::kRedPitch; j += 32 * kConsumers) red[j] = 0;
     // The next item adds to the other buffer; this one is zero again before the
     // item after it, whose adds come after the next item's barrier.
     red = reinterpret_cast<int *>(smem + l.red) + (red == reinterpret_cast<int *>(smem + l.red) ? T::kRedInts : 0);
@@ -764,19 +823,23 @@ cudaError_t experts_setup(const DeviceInfo &info) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(info.max_smem_optin - fa.sharedSizeBytes));
   };
-  if ((e = all_smem(gemm_int8_kernel<1, 1>))) return e;
-  if ((e = all_smem(gemm_int8_kernel<1, 2>))) return e;
-  if ((e = all_smem(gemm_int8_kernel<4, 1>))) return e;
-  if ((e = all_smem(gemm_int8_kernel<4, 2>))) return e;
+  if ((e = all_smem(gemm_int8_kernel<LowShape, 1>))) return e;
+  if ((e = all_smem(gemm_int8_kernel<LowShape, 2>))) return e;
+  if ((e = all_smem(gemm_int8_kernel<TallShape, 1>))) return e;
+  if ((e = all_smem(gemm_int8_kernel<TallShape, 2>))) return e;
   if ((e = all_smem(experts_kernel<true>))) return e;
   return all_smem(experts_kernel<false>);
 }
 
-// Ring stages of a core kernel with two CTAs per SM.
-template <int RG, bool kGather>
-static int core_stages(int m, int extra) {
-  int st = 1;
-  while (1024 + core_layout<RG, kGather>(m, st + 1, extra).total <= static_cast<int>(kTwoPerSmSmem)) ++st;
+// Ring stages of a core kernel with two CTAs per SM, for `need` stages of work.
+// A multiple of the sets: a slot then belongs to one set, which waits for each
+// of its laps in turn (a wait for a lap before the one ahead has landed would
+// fall through, as it goes by the lap's parity).
+template <typename T>
+static int core_stages(int m, int extra, long long need) {
+  int st = T::kSets;
+  while (st < need && 1024 + core_layout<T>(m, st + T::kSets, extra).total <= static_cast<int>(kTwoPerSmSmem))
+    st += T::kSets;
   return st;
 }
 
@@ -800,30 +863,29 @@ Int8Plan plan_int8(int m, int n, int k, int splits, int sm_count) {
   return p;
 }
 
-template <int RG>
+template <typename T>
 static cudaError_t launch_gemm_int8_rows(const CUtensorMap &map, const CUtensorMap &xmap,
                                          const Int8GemmArgs &a, cudaStream_t stream, bool pdl) {
-  using T = Shape<RG, false>;
   const int blocks = (a.k + T::kStageK - 1) / T::kStageK;
   const int per = (blocks + a.splits - 1) / a.splits;
-  const int most = core_stages<RG, false>(a.m, 0), stages = per < most ? per : most;
-  const size_t smem = 1024 + core_layout<RG, false>(a.m, stages, 0).total;
+  const int stages = core_stages<T>(a.m, 0, per);
+  const size_t smem = 1024 + core_layout<T>(a.m, stages, 0).total;
   const dim3 grid((a.n + T::kRows - 1) / T::kRows, a.splits);
-  return launch(a.m > 8 ? gemm_int8_kernel<RG, 2> : gemm_int8_kernel<RG, 1>, grid, dim3(kCoreThreads),
+  return launch(a.m > 8 ? gemm_int8_kernel<T, 2> : gemm_int8_kernel<T, 1>, grid, dim3(kCoreThreads),
                 smem, stream, pdl, a.splits, map, xmap, a, stages);
 }
 
 cudaError_t launch_gemm_int8(const CUtensorMap &map, const CUtensorMap &xmap, const Int8GemmArgs &a,
                              bool tall, cudaStream_t stream, bool pdl) {
-  return tall ? launch_gemm_int8_rows<4>(map, xmap, a, stream, pdl)
-              : launch_gemm_int8_rows<1>(map, xmap, a, stream, pdl);
+  return tall ? launch_gemm_int8_rows<TallShape>(map, xmap, a, stream, pdl)
+              : launch_gemm_int8_rows<LowShape>(map, xmap, a, stream, pdl);
 }
 
 cudaError_t launch_experts_int8(const CUtensorMap &map13, const CUtensorMap &map2, const ExpertsArgs &a,
                                 int sm_count, cudaStream_t stream, bool pdl) {
   const unsigned rows = static_cast<unsigned>(a.m * a.top_k);
-  const int stages = core_stages<1, true>(a.m, sizeof(Roster));
-  const size_t smem = 1024 + core_layout<1, true>(a.m, stages, sizeof(Roster)).total;
+  const int stages = core_stages<ExpertShape>(a.m, sizeof(Roster), 64);
+  const size_t smem = 1024 + core_layout<ExpertShape>(a.m, stages, sizeof(Roster)).total;
   // no more CTAs than items if every choice names another expert
   const int active = a.n_experts < a.m * a.top_k ? a.n_experts : a.m * a.top_k;
   auto ctas = [&](int tiles) {
