@@ -3,7 +3,6 @@
 // products (sk_experts_int8). include/sk.h has the formulas.
 #include <math_constants.h>
 
-#include <cstdlib>
 #include <type_traits>
 
 #include "sk.h"
@@ -207,9 +206,16 @@ __global__ void __launch_bounds__(256)
 //
 // Products at up to 16 tokens stream each weight once; 1 byte of weight meets
 // at most 16 tokens, far below what the tensor cores need to be busy, so HBM
-// is the bound and the rest has to stay out of its way. One producer thread
-// copies weights with TMA, a stage of 16 KiB at a time, into a ring, and the
-// token rows' columns with them; eight consumer warps multiply.
+// is the bound and the rest has to stay out of its way. A CTA owns 32 weight
+// rows; its eight warps take blocks of 64 columns in turn.
+//
+// Each thread streams for itself: 16-byte asynchronous copies bring the pieces
+// that this thread multiplies into a queue of its own in shared memory, kDepth
+// blocks ahead, where no other thread reads or writes. So nothing but the
+// thread's own copies is ever waited for. (A shared ring filled by TMA was
+// slower: its boxes of 128-byte rows passed the copy engine at about four
+// cycles a row, 60 GB/s for an SM with two CTAs, and a producer, its barriers
+// and the slowest of the warps held back the refill.)
 //
 // The tensor cores multiply int8 codes at FP16, exactly. A weight code w goes
 // in as the FP16 subnormal (w + 128) 2^-24, which costs no arithmetic: masked
@@ -221,175 +227,47 @@ __global__ void __launch_bounds__(256)
 // sum exactly up to 2^24, i.e. over 512 columns of a warp, after which the
 // accumulators move to 32-bit integers. The warps' and CTAs' sums are added as
 // integers (modulo 2^32), so neither the order nor the split count can change a
-// result.
+// result. (The integer tensor-core product of the same size issues at an eighth
+// of the FP16 one's rate on this GPU.)
 //
 // K order within a block is free as long as both operands agree: thread t of a
-// quad holds columns 16 t .. 16 t + 15 (one 16-byte load of a weight row, one of
+// quad holds columns 16 t .. 16 t + 15 (one 16-byte piece of a weight row, one of
 // a token row) and feeds four of them to each of four m16n8k16 products.
-constexpr int kBoxK = 128;                                // columns of a TMA box, swizzled over 128 bytes
-constexpr int kStageWBytes = 16 * 1024;                   // weights of a stage
-constexpr int kConsumers = 8;                             // warps
-constexpr int kCoreThreads = 32 * (kConsumers + 1);
-constexpr int kExactStages = 8;                           // a warp's stages between moves to integers
-constexpr uint64_t kCoreWaitNs = 2000000000ull;           // 2 s of wall time per wait
-
-// A stage's shape: kRows rows by 16 KiB / kRows columns. A warp takes 64 columns
-// and 16 kTiles rows of a stage, kWarps warps a whole stage; with kSets > 1 the
-// sets of warps take turns, so that one set's latency hides behind another's.
-// kGather: the token rows come one by one (bulk copies to rows of a fixed
-// pitch); else they are a tile of the activations ([m, k], TMA boxes of 8 or 16
-// rows).
-template <int kRows_, int kTiles_, bool kGather_>
-struct Shape {
-  static constexpr bool kGather = kGather_;
-  static constexpr int kRows = kRows_, kTiles = kTiles_;
-  static constexpr int kStageK = kStageWBytes / kRows;
-  static constexpr int kRowGroups = kRows / (16 * kTiles);
-  static constexpr int kWarps = kStageK / 64 * kRowGroups;
-  static constexpr int kSets = kConsumers / kWarps;
-  static constexpr int kBoxes = kStageK / kBoxK;
-  static constexpr int kBoxBytes = kRows * kBoxK;
-  static constexpr int kXPitch = kStageK + 64;           // kGather: bytes per token row of a stage
-  // ints per token of the sum buffer: the rows' sums, then the token's own
-  static constexpr int kRedPitch = kRows + (kGather ? 4 : 8);
-  static constexpr int kRedInts = SK_MAX_M * kRedPitch;
-  __host__ __device__ static constexpr int x_rows(int m) { return m > 8 ? 16 : 8; }
-  __host__ __device__ static constexpr int stage_bytes(int m) {
-    return (kStageWBytes + x_rows(m) * (kGather ? kXPitch : kStageK) + 1023) / 1024 * 1024;
-  }
-};
-using TallShape = Shape<128, 4, false>;   // 128 rows x 128 columns, two sets of four warps
-using LowShape = Shape<32, 2, false>;     // 32 rows x 512 columns
-using ExpertShape = Shape<32, 2, true>;
+constexpr int kRows = 32;                        // weight rows of a CTA
+constexpr int kBlockCols = 64;                   // columns of a warp's block
+constexpr int kWarps = 8;
+constexpr int kCoreThreads = 32 * kWarps;
+constexpr int kExactBlocks = 8;                  // a warp's blocks between moves to integers
+constexpr int kRedPitch = kRows + 4;             // ints per token of the sum buffer: rows, then the token's own sum
+constexpr int kRedInts = SK_MAX_M * kRedPitch;
+constexpr uint64_t kCoreWaitNs = 2000000000ull;  // 2 s of wall time per wait
 
 __device__ uint32_t g_core_status;  // OR of SK_DEVICE_WAIT_* bits
 
-struct Ring {
-  uint32_t data, full, empty;  // shared addresses: stages, then their barriers
-  int stages, stage_bytes, x_rows;
-  volatile uint32_t *abort;
+// Blocks in flight per thread, and pieces of a block: four of the weight, one
+// for each eight tokens. About 100 KiB of queue per CTA, two CTAs per SM.
+template <int NT>
+struct Queue {
+  static constexpr int kPieces = 4 + NT;
+  static constexpr int kDepth = NT == 1 ? 5 : 4;
+  static constexpr int kBytes = kWarps * kDepth * kPieces * 512;
 };
 
-// A role's place in the ring.
-struct RingPos {
-  int st = 0;
-  uint32_t lap = 0;
-  __device__ __forceinline__ void next(int stages) {
-    if (++st == stages) {
-      st = 0;
-      ++lap;
-    }
-  }
-};
-
-// A wait that runs out raises the abort flag, after which no wait of the CTA
-// waits: every role runs through its loops, nothing is stored. False after an
-// abort.
-__device__ __forceinline__ bool ring_wait(const Ring &r, uint32_t bar, uint32_t parity, uint32_t bit) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (*r.abort) return false;
-    if (globaltimer_ns() - t0 > kCoreWaitNs) {
-      *r.abort = 1;
-      atomicOr(&g_core_status, bit);
-      return false;
-    }
-  }
-  return true;
+// 16 bytes global -> shared, or zeros.
+__device__ __forceinline__ void copy16(uint32_t to, const int8_t *from, bool real) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
+               "r"(real ? 16 : 0)
+               : "memory");
 }
-
-// After an abort: waits (again with a limit) for the copies still in flight, of
-// the last of the `it` stages sent.
-__device__ __forceinline__ void drain(const Ring &r, int it) {
-  for (int i = max(0, it - r.stages); i < it; ++i)
-    mbar_wait_bounded(r.full + 8 * (i % r.stages), (i / r.stages) & 1, kCoreWaitNs / 100);
+__device__ __forceinline__ void copy16_once(uint32_t to, const int8_t *from, bool real, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::128B [%0], [%1], 16, %2, %3;" ::"r"(to),
+               "l"(from), "r"(real ? 16 : 0), "l"(policy)
+               : "memory");
 }
-
-// One item's sources: the weight tile's coordinates; with kGather the token row
-// of each of the first `tokens` lanes.
-struct Source {
-  int row, batch, tokens;
-  const int8_t *x;
-};
-
-// The copies of a stage, each by a lane of its own in one instruction: the
-// producer shares its scheduler with busy warps, and a loop over the copies by
-// one thread held the ring back (m1 [8192, 32768] in 32-row tiles: 60 us, the
-// copies alone 44 us). `tokens` tells whether the token rows are sent too, or
-// the weights alone, or (weights false) the token rows alone.
-template <typename T>
-__device__ __forceinline__ void copy_stage(const Ring &r, const CUtensorMap *map, const CUtensorMap *xmap,
-                                           const Source &s, int st, int k, int k1, bool weights,
-                                           bool tokens, uint64_t policy) {
-  const int lane = threadIdx.x & 31, left = k1 - k;
-  const uint32_t to = r.data + st * r.stage_bytes, bar = r.full + 8 * st;
-  if (weights) {
-    if (lane == 0) {
-      const int boxes = left >= T::kStageK ? T::kBoxes : (left + kBoxK - 1) / kBoxK;
-      mbar_arrive_expect_tx(bar, boxes * T::kBoxBytes + (T::kGather ? s.tokens * min(T::kStageK, left)
-                                                                    : boxes * r.x_rows * kBoxK));
-    }
-    __syncwarp();  // a stage's bytes are announced before any of them arrives
-  }
-  // lanes 0 .. kBoxes - 1: weight boxes; the next kBoxes: token boxes
-  const int b = lane % T::kBoxes;
-  const bool w = lane < T::kBoxes;
-  const bool mine = w ? weights : !T::kGather && tokens && lane < 2 * T::kBoxes;
-  if (mine && b * kBoxK < left)
-    tma_load_3d(to + (w ? b * T::kBoxBytes : kStageWBytes + b * r.x_rows * kBoxK), w ? map : xmap, bar,
-                k + b * kBoxK, w ? s.row : 0, w ? s.batch : 0, policy);
-  if (T::kGather && tokens && lane < s.tokens)
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            to + kStageWBytes + lane * T::kXPitch),
-        "l"(__cvta_generic_to_global(s.x + k)), "r"(min(T::kStageK, left)), "r"(bar)
-        : "memory");
-}
-
-// The producer warp: copies columns [k0, k1) of the items first, first + step,
-// ... below last, stage by stage. With `early` the token rows are not written
-// yet: the first ring of weights goes out before the wait for the kernel ahead,
-// its token rows after it.
-template <typename T, typename Items>
-__device__ __forceinline__ void produce(const Ring &r, const CUtensorMap *map, const CUtensorMap *xmap,
-                                        Items source, int first, int last, int step, int k0, int k1,
-                                        bool early) {
-  constexpr int kStageK = T::kStageK;
-  const int lane = threadIdx.x & 31;
-  // each weight is read once, the token rows by every tile
-  const uint64_t policy = lane < T::kBoxes ? l2_policy_evict_first() : l2_policy_evict_last();
-  int sent = 0;
-  if (early) {
-    for (int i = first; i < last && sent < r.stages; i += step) {
-      const Source s = source(i);
-      for (int k = k0; k < k1 && sent < r.stages; k += kStageK, ++sent)
-        copy_stage<T>(r, map, xmap, s, sent, k, k1, true, false, policy);
-    }
-    griddep_wait();
-    int n = 0;
-    for (int i = first; i < last && n < sent; i += step) {
-      const Source s = source(i);
-      for (int k = k0; k < k1 && n < sent; k += kStageK, ++n)
-        copy_stage<T>(r, map, xmap, s, n, k, k1, false, true, policy);
-    }
-  }
-  RingPos pos;
-  int it = 0;
-  for (int i = first; i < last; i += step) {
-    const Source s = source(i);
-    for (int k = k0; k < k1; k += kStageK, ++it, pos.next(r.stages)) {
-      if (it < sent) continue;
-      const bool go = !pos.lap || ring_wait(r, r.empty + 8 * pos.st, (pos.lap - 1) & 1,
-                                            SK_DEVICE_WAIT_PRODUCER);
-      if (!__all_sync(0xFFFFFFFFu, go)) {
-        drain(r, it);
-        return;
-      }
-      copy_stage<T>(r, map, xmap, s, pos.st, k, k1, true, true, policy);
-    }
-  }
-  if (__any_sync(0xFFFFFFFFu, *r.abort)) drain(r, it);
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // The constants of widen_weight in registers: a three-input logic operation
@@ -432,223 +310,227 @@ __device__ __forceinline__ void red_shared(uint32_t addr, int v) {
   asm volatile("red.shared.add.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// One consumer warp's part of an item: adds its products with the first `tokens`
-// (at most 8 NT) token rows of the stages to red[token][row] (a shared address),
-// and the token rows' own sums to red[token][kRows]. Rows of a stage beyond
-// `tokens` hold zeros or leftovers, whose sums are not added. seq counts the
-// CTA's stages, for the sets' turns.
-template <typename T, int NT>
-__device__ __forceinline__ void consume(const Ring &r, int tokens, int k0, int k1, int &seq, RingPos &pos,
-                                        uint32_t red) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int set = warp / T::kWarps, w = warp % T::kWarps;
-  const int cg = w / T::kRowGroups, rg = w % T::kRowGroups;  // column and row group
-  // Tile row of the lane within eight: rows g = 2 i and 2 i + 1, which a load
-  // phase reads together, are four apart, so their swizzles use both halves of
-  // the 128-byte row and no two lanes of the phase meet in a bank. Gathered
-  // token rows, at a pitch of an odd number of 64 bytes, need no reordering.
-  const int pg = ((g & 1) << 2) | (g >> 1);
-  const uint32_t chunk = static_cast<uint32_t>((((cg & 1) << 2) | t) ^ pg) << 4;
-  const uint32_t at = r.data + (cg >> 1) * T::kBoxBytes + (rg * 16 * T::kTiles + pg) * kBoxK + chunk;
-  const uint32_t xat = r.data + kStageWBytes +
-                       (T::kGather ? g * T::kXPitch + cg * 64 + t * 16
-                                   : (cg >> 1) * r.x_rows * kBoxK + pg * kBoxK + chunk);
-  constexpr uint32_t kXStep = 8 * (T::kGather ? T::kXPitch : kBoxK);
-  const WidenConst wc;
-  const int ones = rg == 0 ? 0x01010101 : 0;  // one row group sums the token's codes
-  float acc[T::kTiles][NT][4];
-  int xsum[NT];
+// A warp's sums of one item: its products with the first 8 NT token rows.
+template <int NT>
+struct Sums {
+  float acc[2][NT][4];
+  int xsum[NT];  // this thread's columns of token nt * 8 + lane / 4
+  int blocks;    // since the last move to integers
+
+  __device__ __forceinline__ Sums() : blocks(0) {
 #pragma unroll
-  for (int i = 0; i < T::kTiles * NT * 4; ++i) (&acc[0][0][0])[i] = 0.0f;
+    for (int i = 0; i < 2 * NT * 4; ++i) (&acc[0][0][0])[i] = 0.0f;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) xsum[nt] = 0;
-  auto flush = [&] {
+    for (int nt = 0; nt < NT; ++nt) xsum[nt] = 0;
+  }
+
+  // Adds a block's products; x[nt], w[tile][row half]: this thread's pieces.
+  __device__ __forceinline__ void add(const WidenConst &wc, const uint4 (&x)[NT], const uint4 (&w)[2][2]) {
+    uint32_t b[NT][8];
 #pragma unroll
-    for (int rt = 0; rt < T::kTiles; ++rt)
+    for (int nt = 0; nt < NT; ++nt) {
+      const uint32_t xw[4] = {x[nt].x, x[nt].y, x[nt].z, x[nt].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        widen_token(xw[i], b[nt][2 * i], b[nt][2 * i + 1]);
+        xsum[nt] = __dp4a(static_cast<int>(xw[i]), 0x01010101, xsum[nt]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) {
+        const uint4 &w0 = w[rt][0], &w1 = w[rt][1];
+        uint32_t a0, a1, a2, a3;
+        widen_weight(wc, i == 0 ? w0.x : i == 1 ? w0.y : i == 2 ? w0.z : w0.w, a0, a2);
+        widen_weight(wc, i == 0 ? w1.x : i == 1 ? w1.y : i == 2 ? w1.z : w1.w, a1, a3);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma_f16(acc[rt][nt], a0, a1, a2, a3, b[nt][2 * i], b[nt][2 * i + 1]);
+      }
+  }
+
+  // Moves the products' sums of the first `tokens` tokens to red[token][row]
+  // (a shared address).
+  __device__ __forceinline__ void move(uint32_t red, int tokens) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    blocks = 0;
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int token = nt * 8 + (T::kGather ? 2 * t + (i & 1) : t + 4 * (i & 1));
-          const int row = (rg * T::kTiles + rt) * 16 + pg + (i >> 1) * 8;
+          const int token = nt * 8 + 2 * t + (i & 1), row = rt * 16 + g + (i >> 1) * 8;
           if (token < tokens)
-            red_shared(red + 4u * (token * T::kRedPitch + row), __float2int_rn(acc[rt][nt][i] * 0x1p24f));
+            red_shared(red + 4u * (token * kRedPitch + row), __float2int_rn(acc[rt][nt][i] * 0x1p24f));
           acc[rt][nt][i] = 0.0f;
         }
-  };
-  int done = 0;
-  for (int k = k0; k < k1; k += T::kStageK, pos.next(r.stages), ++seq) {
-    if (T::kSets > 1 && seq % T::kSets != set) continue;
-    const uint32_t off = pos.st * r.stage_bytes;
-    ring_wait(r, r.full + 8 * pos.st, pos.lap & 1, SK_DEVICE_WAIT_MMA);
-    if (k + cg * 64 < k1) {
-      uint4 x[NT], wt[T::kTiles][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) x[nt] = lds128(xat + off + nt * kXStep);
-#pragma unroll
-      for (int rt = 0; rt < T::kTiles; ++rt) {
-        wt[rt][0] = lds128(at + off + rt * 16 * kBoxK);
-        wt[rt][1] = lds128(at + off + (rt * 16 + 8) * kBoxK);
-      }
-      uint32_t b[NT][8];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const uint32_t xw[4] = {x[nt].x, x[nt].y, x[nt].z, x[nt].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          widen_token(xw[i], b[nt][2 * i], b[nt][2 * i + 1]);
-          xsum[nt] = __dp4a(static_cast<int>(xw[i]), ones, xsum[nt]);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int rt = 0; rt < T::kTiles; ++rt) {
-          const uint4 &w0 = wt[rt][0], &w1 = wt[rt][1];
-          uint32_t a0, a1, a2, a3;
-          widen_weight(wc, i == 0 ? w0.x : i == 1 ? w0.y : i == 2 ? w0.z : w0.w, a0, a2);
-          widen_weight(wc, i == 0 ? w1.x : i == 1 ? w1.y : i == 2 ? w1.z : w1.w, a1, a3);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma_f16(acc[rt][nt], a0, a1, a2, a3, b[nt][2 * i], b[nt][2 * i + 1]);
-        }
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(r.empty + 8 * pos.st);
-    if (++done == kExactStages) {
-      flush();
-      done = 0;
-    }
   }
-  if (done) flush();
-  if (rg == 0)
+
+  // The same for the last time, and the tokens' own sums to red[token][kRows].
+  __device__ __forceinline__ void finish(uint32_t red, int tokens) {
+    const int g = (threadIdx.x & 31) >> 2;
+    if (blocks) move(red, tokens);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int token = nt * 8 + (T::kGather ? g : pg);
-      if (token < tokens) red_shared(red + 4u * (token * T::kRedPitch + T::kRows), xsum[nt]);
-    }
-}
+    for (int nt = 0; nt < NT; ++nt)
+      if (nt * 8 + g < tokens) red_shared(red + 4u * ((nt * 8 + g) * kRedPitch + kRows), xsum[nt]);
+  }
+};
 
 // The sum of products of a token with a tile row: the correction of the weights'
 // offset by 128 (modulo 2^32).
-template <typename T>
 __device__ __forceinline__ int red_sum(const int *red, int token, int row) {
-  const uint32_t s = red[token * T::kRedPitch + row], x = red[token * T::kRedPitch + T::kRows];
+  const uint32_t s = red[token * kRedPitch + row], x = red[token * kRedPitch + kRows];
   return static_cast<int>(s - 128u * x);
 }
 
-__device__ __forceinline__ void consumer_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory");
-}
-
-// Shared memory of a core kernel, from its 1024-aligned base: the ring, two
-// sum buffers, the barriers and the abort flag, then `extra` bytes.
-struct CoreLayout {
-  int red, bars, flag, extra, total;
+// ----------------------------------------------------------------- int8 GEMM
+// Grid (tiles of 32 output features, S slices of K), cluster (1, S, 1): every
+// CTA is resident from the start, two per SM, so that the stream does not wait
+// for scheduling. The S sums of a tile meet in shared memory: rank r receives
+// rows [32 r / S, ...) of every other rank (st.async, counted by its exchange
+// barrier) and finishes them.
+template <int NT>
+struct GemmShared {
+  uint8_t queue[Queue<NT>::kBytes];
+  int red[kRedInts];
+  int recv[SK_MAX_M * kRows];  // [S ranks][16 tokens][32 / S rows]
+  uint64_t exchange;
+  int abort;
 };
-template <typename T>
-__host__ __device__ inline CoreLayout core_layout(int m, int stages, int extra) {
-  CoreLayout l;
-  l.red = stages * T::stage_bytes(m);
-  l.bars = l.red + 2 * T::kRedInts * 4;
-  l.flag = l.bars + 2 * stages * 8;
-  l.extra = l.flag + 16;
-  l.total = l.extra + extra;
-  return l;
-}
 
-__device__ __forceinline__ uint8_t *core_smem(uint8_t *raw) {
-  return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
-}
+template <int NT>
+__global__ void __launch_bounds__(kCoreThreads, 2) gemm_int8_kernel(Int8GemmArgs a) {
+  using Q = Queue<NT>;
+  extern __shared__ __align__(16) uint8_t raw[];
+  GemmShared<NT> &sh = *reinterpret_cast<GemmShared<NT> *>(raw);
+  const int S = a.splits, rows = kRows / S, rank = blockIdx.y;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int n0 = blockIdx.x * kRows;
+  griddep_launch_dependents();
 
-// Set-up by all threads of a core kernel: barriers, abort flag, zeroed sums.
-template <typename T>
-__device__ __forceinline__ Ring core_setup(uint8_t *smem, const CoreLayout &l, int m, int stages,
-                                           const CUtensorMap *map) {
-  Ring r;
-  r.data = smem_u32(smem);
-  r.full = smem_u32(smem + l.bars);
-  r.empty = r.full + 8 * stages;
-  r.stages = stages;
-  r.stage_bytes = T::stage_bytes(m);
-  r.x_rows = T::x_rows(m);
-  r.abort = reinterpret_cast<volatile uint32_t *>(smem + l.flag);
-  int *red = reinterpret_cast<int *>(smem + l.red);
-  for (int i = threadIdx.x; i < 2 * T::kRedInts; i += kCoreThreads) red[i] = 0;
-  if (threadIdx.x == 32 * kConsumers) {
-    for (int s = 0; s < stages; ++s) {
-      mbar_init(r.full + 8 * s, 1);
-      mbar_init(r.empty + 8 * s, T::kWarps);
-    }
-    *r.abort = 0;
+  // This warp's blocks: every eighth of the slice [k0, k1).
+  const int slices = (a.k + kWarps * kBlockCols - 1) / (kWarps * kBlockCols);
+  const int k0 = static_cast<int>(static_cast<long long>(slices) * rank / S) * kWarps * kBlockCols;
+  const int k1 = min(a.k, static_cast<int>(static_cast<long long>(slices) * (rank + 1) / S) * kWarps * kBlockCols);
+  const int col = k0 + warp * kBlockCols + 16 * t;  // this thread's first column
+  const int blocks = max(0, (k1 - k0 - warp * kBlockCols + kWarps * kBlockCols - 1) / (kWarps * kBlockCols));
+  const uint32_t queue = smem_u32(sh.queue) + warp * (Q::kDepth * Q::kPieces * 512) + lane * 16;
+  const uint64_t policy = l2_policy_evict_first();
+  const int8_t *wp[2][2], *xp[NT];
+#pragma unroll
+  for (int h = 0; h < 4; ++h)  // rows past n repeat the last one; their sums are not stored
+    wp[h >> 1][h & 1] = a.wq + static_cast<size_t>(min(n0 + h * 8 + g, a.n - 1)) * a.k + col;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+    xp[nt] = a.xq + static_cast<size_t>(min(nt * 8 + g, a.m - 1)) * a.k + col;
+  auto copy_weights = [&](int i, int slot) {
+    const bool real = i < blocks && col + i * kWarps * kBlockCols < k1;
+    const int off = real ? i * kWarps * kBlockCols : 0;
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+      copy16_once(queue + (slot * Q::kPieces + h) * 512, wp[h >> 1][h & 1] + off, real, policy);
+  };
+  auto copy_tokens = [&](int i, int slot) {
+    const bool real = i < blocks && col + i * kWarps * kBlockCols < k1;
+    const int off = real ? i * kWarps * kBlockCols : 0;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      copy16(queue + (slot * Q::kPieces + 4 + nt) * 512, xp[nt] + off, real && nt * 8 + g < a.m);
+  };
+#pragma unroll
+  for (int i = 0; i < Q::kDepth; ++i) copy_weights(i, i);  // ahead of the kernel before this one
+
+  for (int i = tid; i < kRedInts; i += kCoreThreads) sh.red[i] = 0;
+  if (S > 1 && tid == 0) {
+    mbar_init(smem_u32(&sh.exchange), 1);
+    mbar_arrive_expect_tx(smem_u32(&sh.exchange), (S - 1) * a.m * rows * 4);
+    sh.abort = 0;
     fence_barrier_init();
-    tma_prefetch_map(map);
   }
   __syncthreads();
-  return r;
-}
-
-// ----------------------------------------------------------------- int8 GEMM
-// Grid (tiles of kRows output features, S slices of K), cluster (1, S, 1):
-// every CTA is resident from the start, two per SM, so that the stream does not
-// wait for scheduling. The S sums of a tile meet in shared memory: rank r
-// receives a slice of the rows from every rank and finishes them.
-template <typename T, int NT>
-__global__ void __launch_bounds__(kCoreThreads, 2)
-    gemm_int8_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap xmap,
-                     Int8GemmArgs a, int stages) {
-  extern __shared__ uint8_t raw[];
-  uint8_t *smem = core_smem(raw);
-  const int S = a.splits;
-  const CoreLayout l = core_layout<T>(a.m, stages, 0);
-  const Ring r = core_setup<T>(smem, l, a.m, stages, &map);
-  const int tid = threadIdx.x, warp = tid >> 5;
-  const int n0 = blockIdx.x * T::kRows, rank = blockIdx.y;
-  const int blocks = (a.k + T::kStageK - 1) / T::kStageK;
-  const int k0 = static_cast<int>(static_cast<long long>(blocks) * rank / S) * T::kStageK;
-  const int k1 = min(a.k, static_cast<int>(static_cast<long long>(blocks) * (rank + 1) / S) * T::kStageK);
-  int *red = reinterpret_cast<int *>(smem + l.red);
-  int *recv = red + T::kRedInts;  // the second sum buffer: [S ranks][16 tokens][rows / S]
-  griddep_launch_dependents();
   if (S > 1) cluster_arrive();
-
-  if (warp == kConsumers) {
-    produce<T>(r, &map, &xmap, [&](int) { return Source{n0, 0, a.m, nullptr}; }, 0, 1, 1, k0, k1,
-                       true);
-    __syncwarp();
-  } else {
-    RingPos pos;
-    int seq = 0;
-    consume<T, NT>(r, a.m, k0, k1, seq, pos, smem_u32(red));
-    consumer_sync();
-    griddep_wait();  // the scales, and the order of the stores to y
+  griddep_wait();
+#pragma unroll
+  for (int i = 0; i < Q::kDepth; ++i) {
+    copy_tokens(i, i);
+    copy_commit();
   }
-  const int rows = T::kRows / S;
+  // The scales of the outputs that this thread finishes: one output feature
+  // (rows divides the threads), kKeep tokens; fetched before the stream ends.
+  constexpr int kKeep = NT * 8 * kRows / kCoreThreads;
+  const int n = n0 + rank * rows + tid % rows;
+  const float w_scale = n < a.n ? a.w_scale[n] : 0.0f;
+  float x_scale[kKeep];
+#pragma unroll
+  for (int q = 0; q < kKeep; ++q) {
+    const int token = (tid + q * kCoreThreads) / rows;
+    x_scale[q] = token < a.m ? a.x_scale[token] : 0.0f;
+  }
+
+  const uint32_t red = smem_u32(sh.red);
+  const WidenConst wc;
+  Sums<NT> sums;
+  int slot = 0;
+  for (int i = 0; i < blocks; ++i) {
+    copy_wait<Q::kDepth - 1>();
+    const uint32_t at = queue + slot * (Q::kPieces * 512);
+    uint4 w[2][2], x[NT];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) w[h >> 1][h & 1] = lds128(at + h * 512);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) x[nt] = lds128(at + (4 + nt) * 512);
+    if (i + Q::kDepth < blocks) {
+      copy_weights(i + Q::kDepth, slot);
+      copy_tokens(i + Q::kDepth, slot);
+    }
+    copy_commit();
+    slot = slot + 1 == Q::kDepth ? 0 : slot + 1;
+    sums.add(wc, x, w);
+    if (++sums.blocks == kExactBlocks) sums.move(red, a.m);
+  }
+  sums.finish(red, a.m);
+  copy_wait<0>();
+  __syncthreads();
+
   if (S > 1) {
     cluster_wait();  // every rank has started
-    if (warp < kConsumers)
-      for (int i = tid; i < a.m * T::kRows; i += 32 * kConsumers) {
-        const int row = i % T::kRows, token = i / T::kRows;
-        const uint32_t to = smem_u32(recv + (rank * SK_MAX_M + token) * rows + row % rows);
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dsmem_map(to, row / rows)),
-                     "r"(red_sum<T>(red, token, row))
-                     : "memory");
+    for (int i = tid; i < a.m * kRows / 4; i += kCoreThreads) {
+      const int row = i * 4 % kRows, token = i * 4 / kRows, to = row / rows;
+      int v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = red_sum(sh.red, token, row + j);
+      int *at = sh.recv + (rank * SK_MAX_M + token) * rows + row % rows;
+      if (to == rank) {
+        *reinterpret_cast<int4 *>(at) = make_int4(v[0], v[1], v[2], v[3]);
+      } else {
+        st_async_v4_f32(dsmem_map(smem_u32(at), to), __int_as_float(v[0]), __int_as_float(v[1]),
+                        __int_as_float(v[2]), __int_as_float(v[3]), dsmem_map(smem_u32(&sh.exchange), to));
       }
-    cluster_arrive();
-    cluster_wait();
+    }
+    __syncthreads();  // the rank's own part
+    if (!mbar_wait_bounded(smem_u32(&sh.exchange), 0, kCoreWaitNs)) {
+      sh.abort = 1;
+      atomicOr(&g_core_status, SK_DEVICE_WAIT_EPILOGUE);
+    }
+    cluster_arrive();  // this rank has what it waits for, and sends no more
   }
-  if (warp == kConsumers || *r.abort) return;
-  for (int i = tid; i < a.m * rows; i += 32 * kConsumers) {
-    const int token = i / rows, j = i % rows, n = n0 + rank * rows + j;
-    if (n >= a.n) continue;
-    int s = 0;
-    if (S > 1)
-      for (int q = 0; q < S; ++q) s += recv[(q * SK_MAX_M + token) * rows + j];
-    else
-      s = red_sum<T>(red, token, j);
-    a.y[static_cast<size_t>(token) * a.n + n] =
-        bf16_store_bits(__fmul_rn(__fmul_rn(__int2float_rn(s), a.x_scale[token]), a.w_scale[n]));
+  if (S == 1 || !*reinterpret_cast<volatile int *>(&sh.abort)) {
+#pragma unroll
+    for (int q = 0; q < kKeep; ++q) {
+      const int i = tid + q * kCoreThreads, token = i / rows;
+      if (i >= a.m * rows || n >= a.n) break;
+      int s = 0;
+      if (S > 1)
+        for (int p = 0; p < S; ++p) s += sh.recv[(p * SK_MAX_M + token) * rows + tid % rows];
+      else
+        s = red_sum(sh.red, token, tid % rows);
+      a.y[static_cast<size_t>(token) * a.n + n] =
+          bf16_store_bits(__fmul_rn(__fmul_rn(__int2float_rn(s), x_scale[q]), w_scale));
+    }
   }
+  if (S > 1) cluster_wait();  // shared memory stays until every rank is done with it
 }
 
 // ------------------------------------------------------------------- experts
@@ -683,7 +565,7 @@ __device__ __forceinline__ void build_roster(Roster &q, const ExpertsArgs &a) {
   const int choices = a.m * a.top_k;
   for (int e = threadIdx.x; e < a.n_experts; e += kCoreThreads) q.mask[e] = 0;
   __syncthreads();
-  const int c = threadIdx.x;  // at most 256 choices, 288 threads
+  const int c = threadIdx.x;  // at most 256 choices, as many threads
   const bool mine = c < choices && choice_row(a, c) == c;
   const int e = mine ? load_id(a.ids + c) : 0, token = c / a.top_k;
   if (mine) atomicOr(&q.mask[e], 1u << token);
@@ -717,75 +599,151 @@ __device__ __forceinline__ void build_roster(Roster &q, const ExpertsArgs &a) {
 
 // Gate and up (kUp), or down: persistent CTAs, two per SM, that take items
 // (active expert, tile) in turn, expert-major, so that at any time the grid
-// streams neighbouring tiles. An up item is 16 gate rows and their 16 up rows
-// (one box of two batches of the [2 n_experts, inter, hidden] view), a down item
-// 32 rows of the output. The token rows come from the caller (up) or from the
-// codes of the activations (down).
-template <bool kUp>
-__global__ void __launch_bounds__(kCoreThreads, 2)
-    experts_kernel(const __grid_constant__ CUtensorMap map, ExpertsArgs a, int stages) {
-  extern __shared__ uint8_t raw[];
-  uint8_t *smem = core_smem(raw);
-  using T = ExpertShape;
-  const CoreLayout l = core_layout<T>(a.m, stages, sizeof(Roster));
-  const Ring r = core_setup<T>(smem, l, a.m, stages, &map);
-  Roster &q = *reinterpret_cast<Roster *>(smem + l.extra);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+// streams neighbouring tiles. An up item is 16 gate rows and their 16 up rows, a
+// down item 32 rows of the output. The token rows come from the caller (up) or
+// from the codes of the activations (down). The queues run on over the items'
+// ends: while one item is finished the next one's weights arrive.
+template <int NT>
+struct ExpertShared {
+  uint8_t queue[Queue<NT>::kBytes];
+  int red[2][kRedInts];
+  Roster roster;
+};
+
+template <bool kUp, int NT>
+__global__ void __launch_bounds__(kCoreThreads, 2) experts_kernel(ExpertsArgs a) {
+  using Q = Queue<NT>;
+  extern __shared__ __align__(16) uint8_t raw[];
+  ExpertShared<NT> &sh = *reinterpret_cast<ExpertShared<NT> *>(raw);
+  const Roster &q = sh.roster;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  for (int i = tid; i < 2 * kRedInts; i += kCoreThreads) (&sh.red[0][0])[i] = 0;
   // The ids may come from the kernel ahead. The kernels after this one start
   // only now, so they may read the ids at once, and start on their weights.
   if (kUp) griddep_wait();
   griddep_launch_dependents();
-  build_roster(q, a);
+  build_roster(sh.roster, a);
 
   const int K = kUp ? a.hidden : a.inter, N = kUp ? a.inter : a.hidden;
-  constexpr int kRows = kUp ? T::kRows / 2 : T::kRows;
-  const int tiles = (N + kRows - 1) / kRows, items = q.n_active * tiles;
-  if (warp == kConsumers) {
-    produce<T>(r, &map, nullptr,
-            [&](int i) {
-              const int e = q.active[i / tiles], count = __popc(q.mask[e]);
-              const int row = q.rows[q.offset[e] + (lane < count ? lane : 0)];
-              return Source{i % tiles * kRows, kUp ? 2 * e : e, count,
-                            (kUp ? a.xq + static_cast<size_t>(row / a.top_k) * K
-                                 : a.hq + static_cast<size_t>(row) * K)};
-            },
-            blockIdx.x, items, gridDim.x, 0, K, !kUp);
-    return;
+  constexpr int kTile = kUp ? kRows / 2 : kRows;
+  const int tiles = (N + kTile - 1) / kTile, items = q.n_active * tiles;
+  const int col = warp * kBlockCols + 16 * t;  // this thread's first column
+  const int blocks = max(0, (K - warp * kBlockCols + kWarps * kBlockCols - 1) / (kWarps * kBlockCols));
+  const uint32_t queue = smem_u32(sh.queue) + warp * (Q::kDepth * Q::kPieces * 512) + lane * 16;
+  const uint64_t policy = l2_policy_evict_first();
+
+  // What is copied next: block fb of item fi, from these rows.
+  int fi = blockIdx.x, fb = 0, count = 0;
+  const int8_t *wp[2][2], *xp[NT];
+  auto open = [&] {
+    if (fi >= items) return;
+    const int e = q.active[fi / tiles], n0 = fi % tiles * kTile;
+    count = __popc(q.mask[e]);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {  // rows past N repeat the last one; their sums are not stored
+      const size_t row = kUp ? (static_cast<size_t>(e) * 2 + (h >> 1)) * N + min(n0 + (h & 1) * 8 + g, N - 1)
+                             : static_cast<size_t>(e) * N + min(n0 + h * 8 + g, N - 1);
+      wp[h >> 1][h & 1] = (kUp ? a.w13 : a.w2) + row * K + col;
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = q.rows[q.offset[e] + min(nt * 8 + g, count - 1)];
+      xp[nt] = kUp ? a.xq + static_cast<size_t>(row / a.top_k) * K + col : a.hq + static_cast<size_t>(row) * K + col;
+    }
+  };
+  auto copy_weights = [&](int slot) {
+    const bool real = col + fb * kWarps * kBlockCols < K;
+    const int off = real ? fb * kWarps * kBlockCols : 0;
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+      copy16_once(queue + (slot * Q::kPieces + h) * 512, wp[h >> 1][h & 1] + off, real, policy);
+  };
+  auto copy_tokens = [&](int slot) {
+    const bool real = col + fb * kWarps * kBlockCols < K;
+    const int off = real ? fb * kWarps * kBlockCols : 0;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      if (nt * 8 + g < count) copy16(queue + (slot * Q::kPieces + 4 + nt) * 512, xp[nt] + off, real);
+  };
+  auto next = [&] {
+    if (++fb == blocks) {
+      fb = 0;
+      fi += gridDim.x;
+      open();
+    }
+  };
+
+  open();
+  if (!kUp && blocks) {  // the weights go ahead of the kernel before this one
+    for (int d = 0; d < Q::kDepth && fi < items; ++d, next()) copy_weights(d);
+    fi = blockIdx.x;
+    fb = 0;
+    open();
   }
   if (!kUp) griddep_wait();
-  int *red = reinterpret_cast<int *>(smem + l.red);
-  RingPos pos;
-  int seq = 0;
-  for (int i = blockIdx.x; i < items; i += gridDim.x) {
-    const int e = q.active[i / tiles], n0 = i % tiles * kRows;
+  if (blocks)
+    for (int d = 0; d < Q::kDepth; ++d) {
+      if (fi < items) {
+        if (kUp) copy_weights(d);
+        copy_tokens(d);
+        next();
+      }
+      copy_commit();
+    }
+
+  const WidenConst wc;
+  int slot = 0, side = 0;
+  for (int i = blockIdx.x; i < items; i += gridDim.x, side ^= 1) {
+    const int e = q.active[i / tiles], n0 = i % tiles * kTile;
     const uint16_t *rows = q.rows + q.offset[e];
-    const int count = __popc(q.mask[e]);
-    if (count > 8) consume<T, 2>(r, count, 0, K, seq, pos, smem_u32(red));
-    else consume<T, 1>(r, count, 0, K, seq, pos, smem_u32(red));
-    consumer_sync();
-    const bool store = !*r.abort;
-    for (int j = tid; j < count * kRows; j += 32 * kConsumers) {
-      const int c = j / kRows, at = j % kRows, n = n0 + at, row = rows[c];
-      if (!store || n >= N) continue;
-      const float s0 = __int2float_rn(red_sum<T>(red, c, at));
+    const int tokens = __popc(q.mask[e]);
+    int *red = sh.red[side];
+    auto stream = [&](auto sums) {
+      constexpr int kT = sizeof(sums.xsum) / sizeof(int);
+      for (int b = 0; b < blocks; ++b) {
+        copy_wait<Q::kDepth - 1>();
+        const uint32_t at = queue + slot * (Q::kPieces * 512);
+        uint4 w[2][2], x[kT];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) w[h >> 1][h & 1] = lds128(at + h * 512);
+#pragma unroll
+        for (int nt = 0; nt < kT; ++nt) x[nt] = lds128(at + (4 + nt) * 512);
+        if (fi < items) {
+          copy_weights(slot);
+          copy_tokens(slot);
+          next();
+        }
+        copy_commit();
+        slot = slot + 1 == Q::kDepth ? 0 : slot + 1;
+        sums.add(wc, x, w);
+        if (++sums.blocks == kExactBlocks) sums.move(smem_u32(red), tokens);
+      }
+      sums.finish(smem_u32(red), tokens);
+    };
+    if (NT == 2 && tokens > 8) stream(Sums<NT>());
+    else stream(Sums<1>());
+    __syncthreads();
+    for (int j = tid; j < tokens * kTile; j += kCoreThreads) {
+      const int c = j / kTile, at = j % kTile, n = n0 + at, row = rows[c];
+      if (n >= N) continue;
+      const float s0 = __int2float_rn(red_sum(red, c, at));
       if (kUp) {
         const size_t gate = static_cast<size_t>(e) * 2 * N + n;
         const float xs = a.x_scale[row / a.top_k];
-        const float g = __fmul_rn(__fmul_rn(s0, xs), a.s13[gate]);
-        const float u = __fmul_rn(__fmul_rn(__int2float_rn(red_sum<T>(red, c, kRows + at)), xs),
-                                  a.s13[gate + N]);
-        a.act[static_cast<size_t>(row) * N + n] = g / (1.0f + expf(-g)) * u;
+        const float v = __fmul_rn(__fmul_rn(s0, xs), a.s13[gate]);
+        const float u = __fmul_rn(__fmul_rn(__int2float_rn(red_sum(red, c, kTile + at)), xs), a.s13[gate + N]);
+        a.act[static_cast<size_t>(row) * N + n] = v / (1.0f + expf(-v)) * u;
       } else {
         a.o[static_cast<size_t>(row) * N + n] =
             __fmul_rn(__fmul_rn(s0, a.hs[row]), a.s2[static_cast<size_t>(e) * N + n]);
       }
     }
-    consumer_sync();
-    for (int j = tid; j < count * T::kRedPitch; j += 32 * kConsumers) red[j] = 0;
-    // The next item adds to the other buffer; this one is zero again before the
-    // item after it, whose adds come after the next item's barrier.
-    red = reinterpret_cast<int *>(smem + l.red) + (red == reinterpret_cast<int *>(smem + l.red) ? T::kRedInts : 0);
+    // The next item adds to the other buffer. This one is cleared once all have
+    // read it, before the barrier of the next item, i.e. before it is used again.
+    __syncthreads();
+    for (int j = tid; j < tokens * kRedPitch; j += kCoreThreads) red[j] = 0;
   }
+  copy_wait<0>();
 }
 
 // Weighted sum of a token's choices, in their order.
@@ -815,91 +773,52 @@ cudaError_t launch_int8_quantize(const uint16_t *z, int8_t *q, float *scale, int
                 static_cast<const int32_t *>(nullptr), 0);
 }
 
-cudaError_t experts_setup(const DeviceInfo &info) {
-  cudaFuncAttributes fa;
+cudaError_t experts_setup() {
   cudaError_t e;
-  auto all_smem = [&](auto *kernel) {
-    if ((e = cudaFuncGetAttributes(&fa, kernel))) return e;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(info.max_smem_optin - fa.sharedSizeBytes));
+  auto smem = [&](auto *kernel, size_t bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
   };
-  if ((e = all_smem(gemm_int8_kernel<LowShape, 1>))) return e;
-  if ((e = all_smem(gemm_int8_kernel<LowShape, 2>))) return e;
-  if ((e = all_smem(gemm_int8_kernel<TallShape, 1>))) return e;
-  if ((e = all_smem(gemm_int8_kernel<TallShape, 2>))) return e;
-  if ((e = all_smem(experts_kernel<true>))) return e;
-  return all_smem(experts_kernel<false>);
+  if ((e = smem(gemm_int8_kernel<1>, sizeof(GemmShared<1>)))) return e;
+  if ((e = smem(gemm_int8_kernel<2>, sizeof(GemmShared<2>)))) return e;
+  if ((e = smem(experts_kernel<true, 1>, sizeof(ExpertShared<1>)))) return e;
+  if ((e = smem(experts_kernel<true, 2>, sizeof(ExpertShared<2>)))) return e;
+  if ((e = smem(experts_kernel<false, 1>, sizeof(ExpertShared<1>)))) return e;
+  return smem(experts_kernel<false, 2>, sizeof(ExpertShared<2>));
 }
 
-// Ring stages of a core kernel with two CTAs per SM, for `need` stages of work.
-// A multiple of the sets: a slot then belongs to one set, which waits for each
-// of its laps in turn (a wait for a lap before the one ahead has landed would
-// fall through, as it goes by the lap's parity).
-template <typename T>
-static int core_stages(int m, int extra, long long need) {
-  int st = T::kSets;
-  while (st < need && 1024 + core_layout<T>(m, st + T::kSets, extra).total <= static_cast<int>(kTwoPerSmSmem))
-    st += T::kSets;
-  return st;
+// Slices of K: as many as leave every CTA resident (two per SM) with a block
+// for each of its warps.
+int int8_splits(int n, int k, int sm_count) {
+  const int tiles = (n + kRows - 1) / kRows, slices = (k + kWarps * kBlockCols - 1) / (kWarps * kBlockCols);
+  int s = 1;
+  while (s < 8 && 2 * s <= slices && static_cast<long long>(tiles) * 2 * s <= 2 * sm_count) s *= 2;
+  return s;
 }
 
-// Tiles of 128 rows where K can be cut into enough slices to fill the SMs, of
-// 32 rows otherwise: the tokens' codes pass L2 once per tile, at 16 tokens
-// 12.5 % of the weights' bytes with 128 rows and 50 % with 32. S is the largest
-// of 1, 2, 4, 8 that leaves every CTA resident (two per SM) with a stage at
-// least.
-Int8Plan plan_int8(int m, int n, int k, int splits, int sm_count) {
-  auto best = [&](int rows, int stage_k) {
-    const int tiles = (n + rows - 1) / rows, blocks = (k + stage_k - 1) / stage_k;
-    int s = 1;
-    while (s < 8 && 2 * s <= blocks && static_cast<long long>(tiles) * 2 * s <= 2 * sm_count) s *= 2;
-    return s;
-  };
-  const int tall = splits ? splits : best(128, 128);
-  Int8Plan p;
-  p.tall = m > 2 && static_cast<long long>((n + 127) / 128) * tall >= sm_count;
-  if (const char *v = std::getenv("SK_INT8_TALL")) p.tall = v[0] == '1';
-  p.splits = p.tall ? tall : splits ? splits : best(32, 512);
-  return p;
+cudaError_t launch_gemm_int8(const Int8GemmArgs &a, cudaStream_t stream, bool pdl) {
+  const dim3 grid((a.n + kRows - 1) / kRows, a.splits);
+  return launch(a.m > 8 ? gemm_int8_kernel<2> : gemm_int8_kernel<1>, grid, dim3(kCoreThreads),
+                a.m > 8 ? sizeof(GemmShared<2>) : sizeof(GemmShared<1>), stream, pdl, a.splits, a);
 }
 
-template <typename T>
-static cudaError_t launch_gemm_int8_rows(const CUtensorMap &map, const CUtensorMap &xmap,
-                                         const Int8GemmArgs &a, cudaStream_t stream, bool pdl) {
-  const int blocks = (a.k + T::kStageK - 1) / T::kStageK;
-  const int per = (blocks + a.splits - 1) / a.splits;
-  const int stages = core_stages<T>(a.m, 0, per);
-  const size_t smem = 1024 + core_layout<T>(a.m, stages, 0).total;
-  const dim3 grid((a.n + T::kRows - 1) / T::kRows, a.splits);
-  return launch(a.m > 8 ? gemm_int8_kernel<T, 2> : gemm_int8_kernel<T, 1>, grid, dim3(kCoreThreads),
-                smem, stream, pdl, a.splits, map, xmap, a, stages);
-}
-
-cudaError_t launch_gemm_int8(const CUtensorMap &map, const CUtensorMap &xmap, const Int8GemmArgs &a,
-                             bool tall, cudaStream_t stream, bool pdl) {
-  return tall ? launch_gemm_int8_rows<TallShape>(map, xmap, a, stream, pdl)
-              : launch_gemm_int8_rows<LowShape>(map, xmap, a, stream, pdl);
-}
-
-cudaError_t launch_experts_int8(const CUtensorMap &map13, const CUtensorMap &map2, const ExpertsArgs &a,
-                                int sm_count, cudaStream_t stream, bool pdl) {
+cudaError_t launch_experts_int8(const ExpertsArgs &a, int sm_count, cudaStream_t stream, bool pdl) {
   const unsigned rows = static_cast<unsigned>(a.m * a.top_k);
-  const int stages = core_stages<ExpertShape>(a.m, sizeof(Roster), 64);
-  const size_t smem = 1024 + core_layout<ExpertShape>(a.m, stages, sizeof(Roster)).total;
+  const bool many = a.m > 8;
+  const size_t smem = many ? sizeof(ExpertShared<2>) : sizeof(ExpertShared<1>);
   // no more CTAs than items if every choice names another expert
   const int active = a.n_experts < a.m * a.top_k ? a.n_experts : a.m * a.top_k;
   auto ctas = [&](int tiles) {
     const long long items = static_cast<long long>(active) * tiles;
     return dim3(static_cast<unsigned>(items < 2 * sm_count ? items : 2 * sm_count));
   };
-  cudaError_t e = launch(experts_kernel<true>, ctas((a.inter + 15) / 16),
-                         dim3(kCoreThreads), smem, stream, pdl, 1, map13, a, stages);
+  cudaError_t e = launch(many ? experts_kernel<true, 2> : experts_kernel<true, 1>,
+                         ctas((a.inter + kRows / 2 - 1) / (kRows / 2)), dim3(kCoreThreads), smem, stream, pdl, 1, a);
   if (e != cudaSuccess) return e;
   e = launch(quantize_kernel<float>, dim3(rows), dim3(256), 0, stream, pdl, 1,
              static_cast<const float *>(a.act), a.hq, a.hs, a.inter, a.ids, a.n_experts);
   if (e != cudaSuccess) return e;
-  e = launch(experts_kernel<false>, ctas((a.hidden + 31) / 32), dim3(kCoreThreads), smem,
-             stream, pdl, 1, map2, a, stages);
+  e = launch(many ? experts_kernel<false, 2> : experts_kernel<false, 1>, ctas((a.hidden + kRows - 1) / kRows),
+             dim3(kCoreThreads), smem, stream, pdl, 1, a);
   if (e != cudaSuccess) return e;
   return launch(experts_sum_kernel, dim3((a.hidden + 255) / 256, a.m), dim3(256), 0, stream, pdl, 1, a);
 }

@@ -152,13 +152,9 @@ sk_status sk_gemm_int8(const int8_t *xq, const float *x_scale, const int8_t *wq,
   sk::DeviceInfo info;
   int dev = 0;
   if ((st = sk::checked_device(&info, &dev)) != SK_OK) return st;
-  const sk::Int8Plan plan = sk::plan_int8(m, n, k, splits, info.sm_count);
-  sk::Int8GemmArgs a{xq, wq, x_scale, w_scale, static_cast<uint16_t *>(y), m, n, k, plan.splits};
-  CUtensorMap map, xmap;
-  if ((st = sk::make_int8_map(&map, wq, k, n, 1, plan.tall ? 128 : 32, 1)) != SK_OK) return st;
-  if ((st = sk::make_int8_map(&xmap, xq, k, m, 1, m > 8 ? 16 : 8, 1)) != SK_OK) return st;
-  return launch_status(sk::launch_gemm_int8(map, xmap, a, plan.tall, as_stream(stream), sk::pdl_on()),
-                       "gemm_int8");
+  sk::Int8GemmArgs a{xq, wq, x_scale, w_scale, static_cast<uint16_t *>(y), m, n, k,
+                     splits ? splits : sk::int8_splits(n, k, info.sm_count)};
+  return launch_status(sk::launch_gemm_int8(a, as_stream(stream), sk::pdl_on()), "gemm_int8");
 }
 
 static sk_status check_experts(int m, int top_k, int hidden, int inter) {
@@ -202,11 +198,7 @@ sk_status sk_experts_int8(const int8_t *xq, const float *x_scale, const int8_t *
                     reinterpret_cast<float *>(ws + w.act), reinterpret_cast<int8_t *>(ws + w.hq),
                     reinterpret_cast<float *>(ws + w.hs), reinterpret_cast<float *>(ws + w.o),
                     m, n_experts, top_k, hidden, inter};
-  CUtensorMap map13, map2;
-  if ((st = sk::make_int8_map(&map13, w13, hidden, inter, 2 * n_experts, 16, 2)) != SK_OK) return st;
-  if ((st = sk::make_int8_map(&map2, w2, inter, hidden, n_experts, 32, 1)) != SK_OK) return st;
-  return launch_status(sk::launch_experts_int8(map13, map2, a, info.sm_count, as_stream(stream),
-                                               sk::pdl_on()),
+  return launch_status(sk::launch_experts_int8(a, info.sm_count, as_stream(stream), sk::pdl_on()),
                        "experts_int8");
 }
 

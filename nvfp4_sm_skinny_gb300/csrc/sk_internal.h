@@ -228,16 +228,8 @@ struct Int8GemmArgs {
   uint16_t *y;
   int m, n, k, splits;
 };
-// Tile height (tall: 128 output features per CTA, else 32) and slices of K.
-struct Int8Plan {
-  bool tall;
-  int splits;
-};
-Int8Plan plan_int8(int m, int n, int k, int splits, int sm_count);
-// map: weight codes {k, n, 1}, box {128, tile height, 1}; xmap: token codes
-// {k, m, 1}, box {128, 8 or 16 (m > 8), 1}; both swizzled over 128 bytes.
-cudaError_t launch_gemm_int8(const CUtensorMap &map, const CUtensorMap &xmap, const Int8GemmArgs &a,
-                             bool tall, cudaStream_t stream, bool pdl);
+cudaError_t launch_gemm_int8(const Int8GemmArgs &a, cudaStream_t stream, bool pdl);
+int int8_splits(int n, int k, int sm_count);  // the automatic slices of K
 
 // The routed experts (sk_experts_int8); act, hq, hs and o are parts of the
 // caller's workspace, one row per choice.
@@ -257,21 +249,12 @@ struct ExpertsArgs {
   float *o;    // [m top_k, hidden]
   int m, n_experts, top_k, hidden, inter;
 };
-// map13: {hidden, inter, 2 n_experts}, box {128, 16, 2}; map2: {inter, hidden,
-// n_experts}, box {128, 32, 1}; both swizzled over 128 bytes.
-cudaError_t launch_experts_int8(const CUtensorMap &map13, const CUtensorMap &map2, const ExpertsArgs &a,
-                                int sm_count, cudaStream_t stream, bool pdl);
+cudaError_t launch_experts_int8(const ExpertsArgs &a, int sm_count, cudaStream_t stream, bool pdl);
 
 // One-time attributes of these kernels on the current device, and their part
 // of the device status word.
-cudaError_t experts_setup(const DeviceInfo &info);
+cudaError_t experts_setup();
 cudaError_t read_core_status(uint32_t *out, bool clear);
-
-// Tensor map of int8 weights [batches, rows, k] with boxes of 128 columns,
-// box_rows rows and box_batches batches, swizzled over 128 bytes. Columns past k
-// and rows past `rows` read as zero.
-sk_status make_int8_map(CUtensorMap *map, const void *base, int k, int rows, int batches, int box_rows,
-                        int box_batches);
 
 // The current device, checked to be compute capability 10.3, set up.
 sk_status checked_device(DeviceInfo *info, int *device);

@@ -1150,7 +1150,7 @@ cudaError_t device_setup(int device, DeviceInfo *info) {
       if ((e = cudaFuncSetAttribute(gemm_nvfp4w_kernel,
                                     cudaFuncAttributeNonPortableClusterSizeAllowed, 1)))
         return e;
-      if ((e = experts_setup(d))) return e;
+      if ((e = experts_setup())) return e;
     }
     g_info[device] = d;
     g_ready[device] = true;
