@@ -401,22 +401,23 @@ def gemm_nvfp4w(x, wq, wsf, w_scale, out=None, splits: int = 0, stream=None):
 SCORES = {"softmax": 0, "sigmoid": 1}
 
 
-def _launch_on(stream, *tensors):
+def _launch_on(stream, dev: int, *tensors):
     """The raw stream handle of a call on ``stream`` (the current one if None);
-    refuses tensors that are not on its device, where the kernels would run."""
-    dev = tensors[0].device
-    for t in tensors[1:]:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {t.device} and {dev}: needs all of them on one device")
-    if stream is None:
-        if dev.index != torch.cuda.current_device():
-            raise ValueError(f"tensors on {dev}: needs that device to be the current one "
-                             f"(cuda:{torch.cuda.current_device()})")
-        return torch.cuda.current_stream().cuda_stream
-    if stream.device != dev or dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {dev}, a stream of {stream.device}: needs both on the current "
-                         f"device (cuda:{torch.cuda.current_device()})")
-    return stream.cuda_stream
+    refuses tensors that are not on device ``dev``, the current one, where the
+    kernels run."""
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {t.device} and cuda:{dev}: needs all of them on one device")
+    if dev != torch._C._cuda_getDevice() or (stream is not None and stream.device.index != dev):
+        raise ValueError(f"tensors on cuda:{dev}: needs that device to be the current one "
+                         f"(cuda:{torch.cuda.current_device()}) and the stream's")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _want(t, dtype, shape, name):
+    """_need, with the common case checked first."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _need(t, dtype, shape, name)
 
 
 def _new(shape, dtype, device, stream):
@@ -435,22 +436,20 @@ def route(logits, top_k: int, bias=None, n_groups: int = 1, topk_groups: int = 1
     index; ``bias`` (FP32 [n_experts]) is added to the scores for the choice
     only; ids are -1 where nothing is left to choose (sk_route)."""
     m, n = logits.shape
-    if logits.dtype != torch.bfloat16:
-        _need(logits, torch.float32, (m, n), "logits")
-    else:
-        _need(logits, torch.bfloat16, (m, n), "logits")
+    bf16 = logits.dtype is torch.bfloat16
+    _want(logits, torch.bfloat16 if bf16 else torch.float32, (m, n), "logits")
     if score not in SCORES:
         raise ValueError(f"score: {score!r}, needs one of {sorted(SCORES)}")
     if bias is not None:
-        _need(bias, torch.float32, (n,), "bias")
+        _want(bias, torch.float32, (n,), "bias")
     if ids is None:
         ids = _new((m, top_k), torch.int32, logits.device, stream)
     if weights is None:
         weights = _new((m, top_k), torch.float32, logits.device, stream)
-    _need(ids, torch.int32, (m, top_k), "ids")
-    _need(weights, torch.float32, (m, top_k), "weights")
-    s = _launch_on(stream, logits, bias, ids, weights)
-    _check(lib().sk_route(logits.data_ptr(), 1 if logits.dtype == torch.float32 else 0,
+    _want(ids, torch.int32, (m, top_k), "ids")
+    _want(weights, torch.float32, (m, top_k), "weights")
+    s = _launch_on(stream, logits.get_device(), bias, ids, weights)
+    _check(lib().sk_route(logits.data_ptr(), 0 if bf16 else 1,
                           None if bias is None else bias.data_ptr(), ids.data_ptr(),
                           weights.data_ptr(), m, n, n_groups, topk_groups, top_k, SCORES[score],
                           1 if renormalize else 0, scale, s))
@@ -461,14 +460,14 @@ def int8_quantize(z, q=None, scale=None, stream=None):
     """(q int8 [m, n], scale FP32 [m]): int8 codes of BF16 z [m, n], one scale
     per row (amax / 127): m token rows, or the output features of a weight."""
     m, n = z.shape
-    _need(z, torch.bfloat16, (m, n), "z")
+    _want(z, torch.bfloat16, (m, n), "z")
     if q is None:
         q = _new((m, n), torch.int8, z.device, stream)
     if scale is None:
         scale = _new((m,), torch.float32, z.device, stream)
-    _need(q, torch.int8, (m, n), "q")
-    _need(scale, torch.float32, (m,), "scale")
-    s = _launch_on(stream, z, q, scale)
+    _want(q, torch.int8, (m, n), "q")
+    _want(scale, torch.float32, (m,), "scale")
+    s = _launch_on(stream, z.get_device(), q, scale)
     _check(lib().sk_int8_quantize(z.data_ptr(), q.data_ptr(), scale.data_ptr(), m, n, s))
     return q, scale
 
@@ -484,14 +483,14 @@ def gemm_int8(xq, x_scale, wq, w_scale, out=None, splits: int = 0, stream=None):
     codes, an exact integer sum, FP32 scales per token and output feature."""
     m, k = xq.shape
     n = wq.shape[0]
-    _need(xq, torch.int8, (m, k), "xq")
-    _need(x_scale, torch.float32, (m,), "x_scale")
-    _need(wq, torch.int8, (n, k), "wq")
-    _need(w_scale, torch.float32, (n,), "w_scale")
+    _want(xq, torch.int8, (m, k), "xq")
+    _want(x_scale, torch.float32, (m,), "x_scale")
+    _want(wq, torch.int8, (n, k), "wq")
+    _want(w_scale, torch.float32, (n,), "w_scale")
     if out is None:
         out = _new((m, n), torch.bfloat16, xq.device, stream)
-    _need(out, torch.bfloat16, (m, n), "out")
-    s = _launch_on(stream, xq, x_scale, wq, w_scale, out)
+    _want(out, torch.bfloat16, (m, n), "out")
+    s = _launch_on(stream, xq.get_device(), x_scale, wq, w_scale, out)
     _check(lib().sk_gemm_int8(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(),
                               out.data_ptr(), m, n, k, splits, s))
     return out
@@ -512,22 +511,22 @@ def experts_int8(xq, x_scale, w13, s13, w2, s2, ids, weights, out=None, workspac
     m, hidden = xq.shape
     n_experts, _, inter = w2.shape
     top_k = ids.shape[1]
-    _need(xq, torch.int8, (m, hidden), "xq")
-    _need(x_scale, torch.float32, (m,), "x_scale")
-    _need(w13, torch.int8, (n_experts, 2 * inter, hidden), "w13")
-    _need(s13, torch.float32, (n_experts, 2 * inter), "s13")
-    _need(w2, torch.int8, (n_experts, hidden, inter), "w2")
-    _need(s2, torch.float32, (n_experts, hidden), "s2")
-    _need(ids, torch.int32, (m, top_k), "ids")
-    _need(weights, torch.float32, (m, top_k), "weights")
+    _want(xq, torch.int8, (m, hidden), "xq")
+    _want(x_scale, torch.float32, (m,), "x_scale")
+    _want(w13, torch.int8, (n_experts, 2 * inter, hidden), "w13")
+    _want(s13, torch.float32, (n_experts, 2 * inter), "s13")
+    _want(w2, torch.int8, (n_experts, hidden, inter), "w2")
+    _want(s2, torch.float32, (n_experts, hidden), "s2")
+    _want(ids, torch.int32, (m, top_k), "ids")
+    _want(weights, torch.float32, (m, top_k), "weights")
     if out is None:
         out = _new((m, hidden), torch.bfloat16, xq.device, stream)
-    _need(out, torch.bfloat16, (m, hidden), "out")
+    _want(out, torch.bfloat16, (m, hidden), "out")
     if workspace is None:
         workspace = _new((experts_int8_workspace(m, top_k, hidden, inter),), torch.uint8, xq.device,
                          stream)
-    _need(workspace, torch.uint8, (workspace.numel(),), "workspace")
-    s = _launch_on(stream, xq, x_scale, w13, s13, w2, s2, ids, weights, out, workspace)
+    _want(workspace, torch.uint8, (workspace.numel(),), "workspace")
+    s = _launch_on(stream, xq.get_device(), x_scale, w13, s13, w2, s2, ids, weights, out, workspace)
     _check(lib().sk_experts_int8(
         xq.data_ptr(), x_scale.data_ptr(), w13.data_ptr(), s13.data_ptr(), w2.data_ptr(),
         s2.data_ptr(), ids.data_ptr(), weights.data_ptr(), out.data_ptr(), workspace.data_ptr(),

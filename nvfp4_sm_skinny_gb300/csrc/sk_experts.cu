@@ -38,11 +38,21 @@ cudaError_t launch(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, 
 }
 
 // ------------------------------------------------------------------ routing
+// One warp per token row, kVals logits per lane (expert 32 j + lane in value j).
+// What a row costs is the chain of selections, each two warp reductions, not
+// its bytes; so the values are compared as order-preserving 32-bit integers, for
+// which a reduction is one instruction.
+//
+// Without a bias the order is that of the logits, exactly. With one it is that
+// of p + bias, computed in FP32 here, and two values nearer than the rounding
+// errors of either decide nothing: such a row (about one in a thousand of random
+// ones) is done again in FP64.
 constexpr int kRouteWarps = 4;  // token rows per CTA
 
 __device__ __forceinline__ float route_logit(const RouteArgs &a, size_t at) {
-  if (a.fp32) return static_cast<const float *>(a.logits)[at];
-  return bf16_bits_to_f32(static_cast<const uint16_t *>(a.logits)[at]);
+  const float x = a.fp32 ? static_cast<const float *>(a.logits)[at]
+                         : bf16_bits_to_f32(static_cast<const uint16_t *>(a.logits)[at]);
+  return isnan(x) ? -CUDART_INF_F : x + 0.0f;  // -0 becomes 0
 }
 
 // Largest value of the warp's lanes and, among equals, the lowest index; lanes
@@ -59,22 +69,15 @@ __device__ __forceinline__ void warp_best(double &v, int &at) {
   }
 }
 
-// One warp per token row, all selection values in FP64 in shared memory.
-__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(RouteArgs a) {
-  extern __shared__ double route_smem[];
-  griddep_launch_dependents();
-  griddep_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.x * kRouteWarps + warp;
-  if (row >= a.m) return;
+// A row in FP64, its selection values in v[n_experts] (shared memory).
+__device__ __noinline__ void route_row_f64(const RouteArgs &a, int row, double *v) {
+  const int lane = threadIdx.x & 31;
   const int E = a.n_experts;
-  double *v = route_smem + warp * E;
   const size_t base = static_cast<size_t>(row) * E;
 
   double top = -CUDART_INF;
   for (int e = lane; e < E; e += 32) {
-    double x = static_cast<double>(route_logit(a, base + e)) + 0.0;
-    if (isnan(x)) x = -CUDART_INF;
+    const double x = static_cast<double>(route_logit(a, base + e));
     v[e] = x;
     top = fmax(top, x);
   }
@@ -150,6 +153,175 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(RouteArgs a) {
   }
 }
 
+
+// FP32 -> integer with the same order; 0 stands for "cannot be chosen" (-inf and
+// NaN, and nothing else).
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  if (!(v > -CUDART_INF_F)) return 0u;
+  return b ^ (static_cast<int>(b) < 0 ? 0xFFFFFFFFu : 0x80000000u);
+}
+
+template <int kVals>
+__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(RouteArgs a) {
+  extern __shared__ double route_smem[];
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.x * kRouteWarps + warp;
+  if (row >= a.m) return;
+  const int E = a.n_experts;
+  const size_t base = static_cast<size_t>(row) * E;
+  double *scratch = route_smem + warp * E;
+
+  float x[kVals];
+#pragma unroll
+  for (int j = 0; j < kVals; ++j) x[j] = j * 32 + lane < E ? route_logit(a, base + j * 32 + lane) : -CUDART_INF_F;
+  float top = 0.0f, unit = 1.0f;  // softmax: the largest logit, 1 / sum
+  if (!a.sigmoid) {
+    top = x[0];
+#pragma unroll
+    for (int j = 1; j < kVals; ++j) top = fmaxf(top, x[j]);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kVals; ++j)
+      if (x[j] > -CUDART_INF_F) sum += __expf(x[j] == top ? 0.0f : x[j] - top);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+    unit = 1.0f / sum;
+  }
+  auto score = [&](float v) {
+    return a.sigmoid ? 1.0f / (1.0f + __expf(-v)) : __expf(v == top ? 0.0f : v - top) * unit;
+  };
+  uint32_t key[kVals];
+#pragma unroll
+  for (int j = 0; j < kVals; ++j) {
+    const int e = j * 32 + lane;
+    float v = x[j];
+    if (a.bias && v > -CUDART_INF_F) v = score(v) + a.bias[e];
+    key[j] = order_key(v);
+    if (a.n_groups > 1 && e < E) reinterpret_cast<uint32_t *>(scratch)[e] = key[j];
+  }
+  auto value = [](uint32_t k) {  // of a key
+    return k == 0u ? -CUDART_INF_F : __uint_as_float(k ^ (k & 0x80000000u ? 0x80000000u : 0xFFFFFFFFu));
+  };
+
+  bool near = false;  // FP32 cannot tell
+  if (a.n_groups > 1) {
+    // `lanes` lanes per group look for its two best; they start apart so that
+    // groups of a multiple of 32 experts do not meet in one bank.
+    __syncwarp();
+    const int per = E / a.n_groups;
+    int lanes = 1;
+    while (2 * lanes * a.n_groups <= 32) lanes *= 2;
+    const int grp = lane / lanes, sub = lane % lanes;
+    uint32_t b0 = 0u, b1 = 0u;
+    if (grp < a.n_groups) {
+      const uint32_t *k = reinterpret_cast<const uint32_t *>(scratch) + grp * per;
+      const int turns = (per + lanes - 1) / lanes;
+      for (int i = 0, s = grp % turns; i < turns; ++i) {
+        const int at = s * lanes + sub;
+        const uint32_t v = at < per ? k[at] : 0u;
+        b1 = max(b1, min(b0, v));
+        b0 = max(b0, v);
+        s = s + 1 == turns ? 0 : s + 1;
+      }
+    }
+    for (int d = 1; d < lanes; d <<= 1) {
+      const uint32_t o0 = __shfl_xor_sync(kAll, b0, d), o1 = __shfl_xor_sync(kAll, b1, d);
+      b1 = max(max(b1, o1), min(b0, o0));
+      b0 = max(b0, o0);
+    }
+    float gv = value(b0);
+    if (a.bias && b1) gv += value(b1);
+    // (of NaN, from infinities of both signs, nothing is made: those are never both chosen)
+    const uint32_t gk = grp < a.n_groups ? order_key(gv) : 0u;
+    int rank = 0;
+    for (int o = 0; o < a.n_groups; ++o) {
+      const uint32_t ok = __shfl_sync(kAll, gk, o * lanes);
+      rank += ok > gk || (ok == gk && o < grp);
+    }
+    const bool lead = sub == 0 && grp < a.n_groups;
+    const bool kept = lead && gk && rank < a.topk_groups;
+    if (a.bias && a.topk_groups < a.n_groups) {
+      const uint32_t last = __ballot_sync(kAll, lead && rank == a.topk_groups - 1);
+      const uint32_t first = __ballot_sync(kAll, lead && rank == a.topk_groups);
+      const uint32_t k0 = __shfl_sync(kAll, gk, __ffs(last) - 1), k1 = __shfl_sync(kAll, gk, __ffs(first) - 1);
+      const float v0 = value(k0), v1 = value(k1);
+      near = k1 && !(v0 - v1 > 2e-6f * (2.0f + fabsf(v0) + fabsf(v1)));
+    }
+    const uint32_t leads = __ballot_sync(kAll, kept);  // bit g * lanes
+    const uint32_t magic = per == 1 ? 0u : 0xFFFFFFFFu / per + 1;
+#pragma unroll
+    for (int j = 0; j < kVals; ++j) {
+      const uint32_t e = j * 32 + lane, g = per == 1 ? e : __umulhi(e, magic);  // e / per
+      if (e < static_cast<uint32_t>(E) && !((leads >> (g * lanes)) & 1u)) key[j] = 0u;
+    }
+  }
+
+  // The choices, and with a bias the one after them: lane c holds choice c.
+  int id = -1, found = 0;
+  uint32_t mine = 0u;
+  const int want = a.top_k + (a.bias ? 1 : 0);
+  uint32_t best = 0u;
+  int at = 0;
+  auto look = [&] {
+    best = 0u;
+#pragma unroll
+    for (int j = 0; j < kVals; ++j)
+      if (key[j] > best) {
+        best = key[j];
+        at = j * 32 + lane;
+      }
+  };
+  look();
+  for (; found < want; ++found) {
+    const uint32_t k = __reduce_max_sync(kAll, best);
+    if (!k) break;
+    const uint32_t e = __reduce_min_sync(kAll, best == k ? static_cast<uint32_t>(at) : kAll);
+    if (lane == found) {
+      id = static_cast<int>(e);
+      mine = k;
+    }
+    if ((e & 31u) == static_cast<uint32_t>(lane)) {
+#pragma unroll
+      for (int j = 0; j < kVals; ++j)
+        if (j == static_cast<int>(e >> 5)) key[j] = 0u;
+      look();
+    }
+  }
+  const float chosen = id >= 0 ? route_logit(a, base + id) : 0.0f;
+  float w = id >= 0 ? score(chosen) : 0.0f;
+  if (a.bias) {
+    const float b = id >= 0 ? a.bias[id] : 0.0f, v = value(mine);
+    const float v1 = __shfl_down_sync(kAll, v, 1), w1 = __shfl_down_sync(kAll, w, 1);
+    const float c1 = __shfl_down_sync(kAll, chosen, 1), b1 = __shfl_down_sync(kAll, b, 1);
+    // the errors of both: the exponential's, growing with its argument, the
+    // sum's and the quotient's on p; one rounding on p + bias
+    const float grow = 2e-6f + 3e-7f * (a.sigmoid ? fabsf(chosen) + fabsf(c1) : 2.0f * top - chosen - c1);
+    const float tol = grow * (w + w1) + 1.2e-7f * (fabsf(v) + fabsf(v1));
+    const bool same = c1 == chosen && b1 == b;  // equal in any precision
+    near = near || (lane + 1 < found && !same && !(v - v1 > tol));
+    if (__any_sync(kAll, near)) {
+      __syncwarp();
+      route_row_f64(a, row, scratch);
+      return;
+    }
+  }
+  if (lane >= a.top_k) w = 0.0f;
+  float total = w;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(kAll, total, d);
+  if (a.renormalize) w = total > 0.0f ? w / total : 0.0f;
+  if (lane < a.top_k) {
+    a.ids[static_cast<size_t>(row) * a.top_k + lane] = id;
+    a.weights[static_cast<size_t>(row) * a.top_k + lane] = w * a.scale;
+  }
+}
+
 // ------------------------------------------------------------- quantization
 // Row maximum of |z| over the CTA; NaN when the row holds an Inf or NaN (the
 // bits of |z| order as integers, Inf and NaN above every finite value).
@@ -164,42 +336,106 @@ __device__ __forceinline__ float cta_row_max(uint32_t bits) {
   return bits >= 0x7F800000u ? CUDART_NAN_F : __uint_as_float(bits);
 }
 
-// Code of v in a row of maximum amax (not 0, not NaN): round to nearest even of
-// 127 v / amax. f (2^-8 for amax >= 1, else 1) keeps 127 v finite.
-__device__ __forceinline__ int int8_code(float v, float amax, float f) {
-  return __float2int_rn(__fdiv_rn(__fmul_rn(__fmul_rn(v, f), 127.0f), __fmul_rn(amax, f)));
-}
+// A row's codes: round to nearest even of 127 v / amax, as of the exact quotient.
+// The product with 127 / amax, within 3e-5 of it, settles all but the neighbours
+// of half an integer (of BF16 inputs: but the halves themselves, the others are
+// 1/512 away or more); those take an IEEE division, for which f (2^-8 for
+// amax >= 1, else 1) keeps 127 v finite.
+struct RowCodes {
+  float amax, inv, f;
+  bool plain;  // neither zero nor NaN
+  __device__ __forceinline__ explicit RowCodes(float row_max) {
+    amax = row_max;
+    inv = __fdiv_rn(127.0f, amax);
+    f = amax >= 1.0f ? 0x1p-8f : 1.0f;
+    plain = amax > 0.0f;
+  }
+  __device__ __forceinline__ int operator()(float v) const {
+    const float t = v * inv, r = rintf(t);
+    if (fabsf(t - r) <= 0.499f) return static_cast<int>(r);
+    return __float2int_rn(__fdiv_rn(__fmul_rn(__fmul_rn(v, f), 127.0f), __fmul_rn(amax, f)));
+  }
+};
 
-template <typename T>  // uint16_t (BF16 bits) or float
-__device__ __forceinline__ float as_f32(T v) {
-  if constexpr (std::is_same<T, float>::value) return v;
-  else return bf16_bits_to_f32(v);
-}
-
-// One CTA per row, two passes over it. A caller's codes (ids null) may be the
-// weight of a call that reads it ahead of its dependency wait, so dependents
-// start only once they are written. The codes of the experts' activations are
-// read after the wait.
+// 16 bytes of a row as values: 8 BF16 or 4 FP32.
 template <typename T>
+struct Chunk {
+  static constexpr int kVals = 16 / sizeof(T);
+  uint4 raw;
+  __device__ __forceinline__ uint32_t bits(int i) const {  // FP32 bits of value i
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    if constexpr (sizeof(T) == 4) return w[i];
+    else return i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16;
+  }
+  __device__ __forceinline__ uint32_t max_bits(uint32_t m) const {
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) m = max(m, bits(i) & 0x7FFFFFFFu);
+    return m;
+  }
+  __device__ __forceinline__ void store(int8_t *q, const RowCodes &code) const {
+    uint32_t w[2] = {0u, 0u};
+    if (code.plain) {
+#pragma unroll
+      for (int i = 0; i < kVals; ++i)
+        w[i >> 2] |= (static_cast<uint32_t>(code(__uint_as_float(bits(i)))) & 0xFFu) << (8 * (i & 3));
+    }
+    if constexpr (kVals == 8) *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t *>(q) = w[0];
+  }
+};
+
+// One CTA per row. kKeep > 0: the row stays in registers, kKeep 16-byte chunks
+// per thread, and is read once; 0: any length, read twice. A caller's codes (ids
+// null) may be the weight of a call that reads it ahead of its dependency wait,
+// so dependents start only once they are written; the codes of the experts'
+// activations are read after the wait.
+template <typename T, int kKeep>
 __global__ void __launch_bounds__(256)
     quantize_kernel(const T *z, int8_t *q, float *scale, int n, const int32_t *ids, int n_experts) {
+  constexpr int kVals = Chunk<T>::kVals;
   if (ids) griddep_launch_dependents();
   griddep_wait();
   const size_t row = blockIdx.x;
   if (ids && static_cast<unsigned>(ids[row]) >= static_cast<unsigned>(n_experts)) return;
+  const uint4 *from = reinterpret_cast<const uint4 *>(z + row * n);
+  int8_t *to = q + row * n;
+  const int chunks = n / kVals;
   uint32_t bits = 0;
-  for (int j = threadIdx.x; j < n; j += blockDim.x)
-    bits = max(bits, __float_as_uint(as_f32(z[row * n + j])) & 0x7FFFFFFFu);
-  const float amax = cta_row_max(bits);
-  const float f = amax >= 1.0f ? 0x1p-8f : 1.0f;
-  const bool plain = amax > 0.0f;  // neither zero nor NaN
-  for (int j = threadIdx.x; j < n; j += blockDim.x)
-    q[row * n + j] = static_cast<int8_t>(plain ? int8_code(as_f32(z[row * n + j]), amax, f) : 0);
-  if (threadIdx.x == 0) scale[row] = __fdiv_rn(amax, 127.0f);
+  if constexpr (kKeep > 0) {
+    Chunk<T> c[kKeep];
+#pragma unroll
+    for (int j = 0; j < kKeep; ++j) {
+      const int at = threadIdx.x + j * 256;
+      c[j].raw = at < chunks ? from[at] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < kKeep; ++j) bits = c[j].max_bits(bits);
+    const RowCodes code(cta_row_max(bits));
+#pragma unroll
+    for (int j = 0; j < kKeep; ++j) {
+      const int at = threadIdx.x + j * 256;
+      if (at < chunks) c[j].store(to + at * kVals, code);
+    }
+    if (threadIdx.x == 0) scale[row] = __fdiv_rn(code.amax, 127.0f);
+  } else {
+    for (int at = threadIdx.x; at < chunks; at += 256) bits = Chunk<T>{from[at]}.max_bits(bits);
+    const RowCodes code(cta_row_max(bits));
+    for (int at = threadIdx.x; at < chunks; at += 256) Chunk<T>{from[at]}.store(to + at * kVals, code);
+    if (threadIdx.x == 0) scale[row] = __fdiv_rn(code.amax, 127.0f);
+  }
   if (ids) return;
   __threadfence();
   __syncthreads();
   griddep_launch_dependents();
+}
+
+template <typename T>
+static cudaError_t launch_quantize(const T *z, int8_t *q, float *scale, int rows, int n, const int32_t *ids,
+                            int n_experts, cudaStream_t stream, bool pdl) {
+  const int per = (n / Chunk<T>::kVals + 255) / 256;
+  auto *kernel = per <= 1 ? quantize_kernel<T, 1> : per <= 2 ? quantize_kernel<T, 2>
+               : per <= 4 ? quantize_kernel<T, 4> : per <= 8 ? quantize_kernel<T, 8> : quantize_kernel<T, 0>;
+  return launch(kernel, dim3(rows), dim3(256), 0, stream, pdl, 1, z, q, scale, n, ids, n_experts);
 }
 
 // ------------------------------------------------------- the int8 product core
@@ -763,14 +999,16 @@ __global__ void __launch_bounds__(256) experts_sum_kernel(ExpertsArgs a) {
 }  // namespace
 
 cudaError_t launch_route(const RouteArgs &a, cudaStream_t stream, bool pdl) {
-  return launch(route_kernel, dim3((a.m + kRouteWarps - 1) / kRouteWarps), dim3(32 * kRouteWarps),
+  const int per = (a.n_experts + 31) / 32;
+  auto *kernel = per <= 1 ? route_kernel<1> : per <= 2 ? route_kernel<2> : per <= 4 ? route_kernel<4>
+               : per <= 8 ? route_kernel<8> : per <= 16 ? route_kernel<16> : route_kernel<32>;
+  return launch(kernel, dim3((a.m + kRouteWarps - 1) / kRouteWarps), dim3(32 * kRouteWarps),
                 static_cast<size_t>(kRouteWarps) * a.n_experts * sizeof(double), stream, pdl, 1, a);
 }
 
 cudaError_t launch_int8_quantize(const uint16_t *z, int8_t *q, float *scale, int m, int n,
                                  cudaStream_t stream, bool pdl) {
-  return launch(quantize_kernel<uint16_t>, dim3(m), dim3(256), 0, stream, pdl, 1, z, q, scale, n,
-                static_cast<const int32_t *>(nullptr), 0);
+  return launch_quantize(z, q, scale, m, n, static_cast<const int32_t *>(nullptr), 0, stream, pdl);
 }
 
 cudaError_t experts_setup() {
@@ -814,8 +1052,8 @@ cudaError_t launch_experts_int8(const ExpertsArgs &a, int sm_count, cudaStream_t
   cudaError_t e = launch(many ? experts_kernel<true, 2> : experts_kernel<true, 1>,
                          ctas((a.inter + kRows / 2 - 1) / (kRows / 2)), dim3(kCoreThreads), smem, stream, pdl, 1, a);
   if (e != cudaSuccess) return e;
-  e = launch(quantize_kernel<float>, dim3(rows), dim3(256), 0, stream, pdl, 1,
-             static_cast<const float *>(a.act), a.hq, a.hs, a.inter, a.ids, a.n_experts);
+  e = launch_quantize(static_cast<const float *>(a.act), a.hq, a.hs, static_cast<int>(rows), a.inter, a.ids,
+                      a.n_experts, stream, pdl);
   if (e != cudaSuccess) return e;
   e = launch(many ? experts_kernel<false, 2> : experts_kernel<false, 1>, ctas((a.hidden + kRows - 1) / kRows),
              dim3(kCoreThreads), smem, stream, pdl, 1, a);
