@@ -350,10 +350,16 @@ struct RowCodes {
     f = amax >= 1.0f ? 0x1p-8f : 1.0f;
     plain = amax > 0.0f;
   }
-  __device__ __forceinline__ int operator()(float v) const {
-    const float t = v * inv, r = rintf(t);
-    if (fabsf(t - r) <= 0.499f) return static_cast<int>(r);
-    return __float2int_rn(__fdiv_rn(__fmul_rn(__fmul_rn(v, f), 127.0f), __fmul_rn(amax, f)));
+  // The code in the low byte. Adding 1.5 2^23 rounds to an integer and leaves it,
+  // in two's complement, in the low bits; `off`: how far from the quotient it is.
+  __device__ __forceinline__ uint32_t quick(float v, float &off) const {
+    const float t = __fmul_rn(v, inv), b = __fadd_rn(t, 12582912.0f);
+    off = fabsf(__fsub_rn(t, __fsub_rn(b, 12582912.0f)));
+    return __float_as_uint(b);
+  }
+  __device__ __forceinline__ uint32_t slow(float v) const {
+    return static_cast<uint32_t>(
+        __float2int_rn(__fdiv_rn(__fmul_rn(__fmul_rn(v, f), 127.0f), __fmul_rn(amax, f))));
   }
 };
 
@@ -362,23 +368,43 @@ template <typename T>
 struct Chunk {
   static constexpr int kVals = 16 / sizeof(T);
   uint4 raw;
-  __device__ __forceinline__ uint32_t bits(int i) const {  // FP32 bits of value i
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    if constexpr (sizeof(T) == 4) return w[i];
-    else return i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16;
+  __device__ __forceinline__ uint32_t word(int i) const {
+    return i == 0 ? raw.x : i == 1 ? raw.y : i == 2 ? raw.z : raw.w;
   }
+  __device__ __forceinline__ float value(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(word(i));
+    else return __uint_as_float(i & 1 ? word(i >> 1) & 0xFFFF0000u : word(i >> 1) << 16);
+  }
+  // The largest magnitude's bits: of BF16, in either half.
   __device__ __forceinline__ uint32_t max_bits(uint32_t m) const {
 #pragma unroll
-    for (int i = 0; i < kVals; ++i) m = max(m, bits(i) & 0x7FFFFFFFu);
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) m = max(m, word(i) & 0x7FFFFFFFu);
+      else m = __vmaxu2(m, word(i) & 0x7FFF7FFFu);
+    }
     return m;
   }
+  static __device__ __forceinline__ uint32_t fp32_bits(uint32_t m) {  // of max_bits' result
+    if constexpr (sizeof(T) == 4) return m;
+    else return max(m << 16, m & 0xFFFF0000u);
+  }
   __device__ __forceinline__ void store(int8_t *q, const RowCodes &code) const {
-    uint32_t w[2] = {0u, 0u};
-    if (code.plain) {
+    uint32_t c[kVals];
+    float far = 0.0f, off;
 #pragma unroll
-      for (int i = 0; i < kVals; ++i)
-        w[i >> 2] |= (static_cast<uint32_t>(code(__uint_as_float(bits(i)))) & 0xFFu) << (8 * (i & 3));
+    for (int i = 0; i < kVals; ++i) {
+      c[i] = code.quick(value(i), off);
+      far = off <= 0.499f ? far : 1.0f;  // (1 for NaN too)
     }
+    if (far > 0.0f) {
+#pragma unroll
+      for (int i = 0; i < kVals; ++i) c[i] = code.plain ? code.slow(value(i)) : 0u;
+    }
+    uint32_t w[kVals / 4];
+#pragma unroll
+    for (int i = 0; i < kVals / 4; ++i)
+      w[i] = __byte_perm(__byte_perm(c[4 * i], c[4 * i + 1], 0x0040), __byte_perm(c[4 * i + 2], c[4 * i + 3], 0x0040),
+                         0x5410);
     if constexpr (kVals == 8) *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint32_t *>(q) = w[0];
   }
@@ -410,7 +436,7 @@ __global__ void __launch_bounds__(256)
     }
 #pragma unroll
     for (int j = 0; j < kKeep; ++j) bits = c[j].max_bits(bits);
-    const RowCodes code(cta_row_max(bits));
+    const RowCodes code(cta_row_max(Chunk<T>::fp32_bits(bits)));
 #pragma unroll
     for (int j = 0; j < kKeep; ++j) {
       const int at = threadIdx.x + j * 256;
@@ -419,7 +445,7 @@ __global__ void __launch_bounds__(256)
     if (threadIdx.x == 0) scale[row] = __fdiv_rn(code.amax, 127.0f);
   } else {
     for (int at = threadIdx.x; at < chunks; at += 256) bits = Chunk<T>{from[at]}.max_bits(bits);
-    const RowCodes code(cta_row_max(bits));
+    const RowCodes code(cta_row_max(Chunk<T>::fp32_bits(bits)));
     for (int at = threadIdx.x; at < chunks; at += 256) Chunk<T>{from[at]}.store(to + at * kVals, code);
     if (threadIdx.x == 0) scale[row] = __fdiv_rn(code.amax, 127.0f);
   }
@@ -778,6 +804,7 @@ struct Roster {
   uint16_t offset[SK_MAX_EXPERTS];             // its first entry of `rows`
   uint16_t rows[SK_MAX_M * SK_MAX_TOP_K];
   uint16_t active[SK_MAX_M * SK_MAX_TOP_K];
+  int ids[SK_MAX_M * SK_MAX_TOP_K];
   int n_active;
 };
 
@@ -787,23 +814,23 @@ __device__ __forceinline__ int load_id(const int32_t *p) {
   return v;
 }
 
-// The workspace row of choice `c` (token * top_k + j): that of the token's
+// The workspace row of choice c of ids (shared memory): that of the token's
 // first choice of the same expert, or -1 where the choice is masked.
-__device__ __forceinline__ int choice_row(const ExpertsArgs &a, int c) {
-  const int e = load_id(a.ids + c);
-  if (static_cast<unsigned>(e) >= static_cast<unsigned>(a.n_experts)) return -1;
-  int f = c / a.top_k * a.top_k;
-  while (load_id(a.ids + f) != e) ++f;
+__device__ __forceinline__ int choice_row(const int *ids, int c, int top_k, int n_experts) {
+  const int e = ids[c];
+  if (static_cast<unsigned>(e) >= static_cast<unsigned>(n_experts)) return -1;
+  int f = c / top_k * top_k;
+  while (ids[f] != e) ++f;
   return f;
 }
 
 __device__ __forceinline__ void build_roster(Roster &q, const ExpertsArgs &a) {
-  const int choices = a.m * a.top_k;
+  const int choices = a.m * a.top_k, c = threadIdx.x;  // at most 256 choices, as many threads
+  if (c < choices) q.ids[c] = load_id(a.ids + c);
   for (int e = threadIdx.x; e < a.n_experts; e += kCoreThreads) q.mask[e] = 0;
   __syncthreads();
-  const int c = threadIdx.x;  // at most 256 choices, as many threads
-  const bool mine = c < choices && choice_row(a, c) == c;
-  const int e = mine ? load_id(a.ids + c) : 0, token = c / a.top_k;
+  const bool mine = c < choices && choice_row(q.ids, c, a.top_k, a.n_experts) == c;
+  const int e = mine ? q.ids[c] : 0, token = c / a.top_k;
   if (mine) atomicOr(&q.mask[e], 1u << token);
   __syncthreads();
   if (threadIdx.x < 32) {
@@ -982,18 +1009,37 @@ __global__ void __launch_bounds__(kCoreThreads, 2) experts_kernel(ExpertsArgs a)
   copy_wait<0>();
 }
 
-// Weighted sum of a token's choices, in their order.
-__global__ void __launch_bounds__(256) experts_sum_kernel(ExpertsArgs a) {
+// Weighted sum of a token's choices, in their order; four columns per thread.
+constexpr int kSumThreads = 64;
+__global__ void __launch_bounds__(kSumThreads) experts_sum_kernel(ExpertsArgs a) {
+  __shared__ int ids[SK_MAX_TOP_K];
+  __shared__ float weights[SK_MAX_TOP_K];
   griddep_launch_dependents();
   griddep_wait();
-  const int n = blockIdx.x * 256 + threadIdx.x, i = blockIdx.y;
-  if (n >= a.hidden) return;
-  float s = 0.0f;
-  for (int j = 0; j < a.top_k; ++j) {
-    const int row = choice_row(a, i * a.top_k + j);
-    if (row >= 0) s = fmaf(a.weights[i * a.top_k + j], a.o[static_cast<size_t>(row) * a.hidden + n], s);
+  const int i = blockIdx.y, n = 4 * (blockIdx.x * kSumThreads + threadIdx.x);
+  if (static_cast<int>(threadIdx.x) < a.top_k) {
+    ids[threadIdx.x] = a.ids[i * a.top_k + threadIdx.x];
+    weights[threadIdx.x] = a.weights[i * a.top_k + threadIdx.x];
   }
-  a.y[static_cast<size_t>(i) * a.hidden + n] = bf16_store_bits(s);
+  __syncthreads();
+  if (n >= a.hidden) return;
+  float4 o[SK_MAX_TOP_K], s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int j = 0; j < SK_MAX_TOP_K; ++j) {
+    const int f = j < a.top_k ? choice_row(ids, j, SK_MAX_TOP_K, a.n_experts) : -1;
+    if (f >= 0) o[j] = *reinterpret_cast<const float4 *>(a.o + static_cast<size_t>(i * a.top_k + f) * a.hidden + n);
+  }
+#pragma unroll
+  for (int j = 0; j < SK_MAX_TOP_K; ++j) {
+    if (j >= a.top_k || static_cast<unsigned>(ids[j]) >= static_cast<unsigned>(a.n_experts)) continue;
+    s.x = fmaf(weights[j], o[j].x, s.x);
+    s.y = fmaf(weights[j], o[j].y, s.y);
+    s.z = fmaf(weights[j], o[j].z, s.z);
+    s.w = fmaf(weights[j], o[j].w, s.w);
+  }
+  const uint32_t lo = bf16_store_bits(s.x) | static_cast<uint32_t>(bf16_store_bits(s.y)) << 16;
+  const uint32_t hi = bf16_store_bits(s.z) | static_cast<uint32_t>(bf16_store_bits(s.w)) << 16;
+  *reinterpret_cast<uint2 *>(a.y + static_cast<size_t>(i) * a.hidden + n) = make_uint2(lo, hi);
 }
 
 }  // namespace
@@ -1058,7 +1104,8 @@ cudaError_t launch_experts_int8(const ExpertsArgs &a, int sm_count, cudaStream_t
   e = launch(many ? experts_kernel<false, 2> : experts_kernel<false, 1>, ctas((a.hidden + kRows - 1) / kRows),
              dim3(kCoreThreads), smem, stream, pdl, 1, a);
   if (e != cudaSuccess) return e;
-  return launch(experts_sum_kernel, dim3((a.hidden + 255) / 256, a.m), dim3(256), 0, stream, pdl, 1, a);
+  return launch(experts_sum_kernel, dim3((a.hidden / 4 + kSumThreads - 1) / kSumThreads, a.m), dim3(kSumThreads), 0,
+                stream, pdl, 1, a);
 }
 
 cudaError_t read_core_status(uint32_t *out, bool clear) {
