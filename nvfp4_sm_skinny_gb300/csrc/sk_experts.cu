@@ -323,24 +323,27 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(RouteArgs a) {
 }
 
 // ------------------------------------------------------------- quantization
-// Row maximum of |z| over the CTA; NaN when the row holds an Inf or NaN (the
-// bits of |z| order as integers, Inf and NaN above every finite value).
-__device__ __forceinline__ float cta_row_max(uint32_t bits) {
-  __shared__ uint32_t part[32];
+// Largest of a row's values, W warps to a row, as FP32 bits of a magnitude; NaN
+// when the row holds an Inf or NaN (the bits of |z| order as integers, Inf and NaN
+// above every finite value).
+template <int W>
+__device__ __forceinline__ float row_max(uint32_t bits) {
   bits = __reduce_max_sync(0xFFFFFFFFu, bits);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = bits;
-  __syncthreads();
-  const int warps = blockDim.x >> 5;
-  bits = (threadIdx.x & 31) < warps ? part[threadIdx.x & 31] : 0u;
-  bits = __reduce_max_sync(0xFFFFFFFFu, bits);
+  if constexpr (W > 1) {
+    __shared__ uint32_t part[W];
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = bits;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < W; ++w) bits = max(bits, part[w]);
+  }
   return bits >= 0x7F800000u ? CUDART_NAN_F : __uint_as_float(bits);
 }
 
 // A row's codes: round to nearest even of 127 v / amax, as of the exact quotient.
-// The product with 127 / amax, within 3e-5 of it, settles all but the neighbours
-// of half an integer (of BF16 inputs: but the halves themselves, the others are
-// 1/512 away or more); those take an IEEE division, for which f (2^-8 for
-// amax >= 1, else 1) keeps 127 v finite.
+// The product with 127 / amax, within 127 2^-23 = 1.5e-5 of it, settles all but
+// the neighbours of half an integer (of BF16 inputs: but the halves themselves,
+// the others are 1/512 away or more); those take an IEEE division, for which f
+// (2^-8 for amax >= 1, else 1) keeps 127 v finite.
 struct RowCodes {
   float amax, inv, f;
   bool plain;  // neither zero nor NaN
@@ -394,7 +397,7 @@ struct Chunk {
 #pragma unroll
     for (int i = 0; i < kVals; ++i) {
       c[i] = code.quick(value(i), off);
-      far = off <= 0.499f ? far : 1.0f;  // (1 for NaN too)
+      far = off <= 0.4999f ? far : 1.0f;  // (1 for NaN too)
     }
     if (far > 0.0f) {
 #pragma unroll
@@ -410,44 +413,54 @@ struct Chunk {
   }
 };
 
-// One CTA per row. kKeep > 0: the row stays in registers, kKeep 16-byte chunks
-// per thread, and is read once; 0: any length, read twice. A caller's codes (ids
-// null) may be the weight of a call that reads it ahead of its dependency wait,
-// so dependents start only once they are written; the codes of the experts'
-// activations are read after the wait.
-template <typename T, int kKeep>
-__global__ void __launch_bounds__(256)
-    quantize_kernel(const T *z, int8_t *q, float *scale, int n, const int32_t *ids, int n_experts) {
-  constexpr int kVals = Chunk<T>::kVals;
+// CTAs of four warps, W of them (1 or 4) to a row. kKeep > 0: rows of at most
+// kKeep 16-byte chunks per thread, kept in registers, so that a row is read once;
+// 0: rows of any length, read twice. The row's maximum is all that its codes wait
+// for, so what counts is rows in flight: ten CTAs per SM where registers allow
+// ([8192, 8192]: 38 us, 5.2 TB/s; with 256 threads per row 42 us; with CTAs that
+// stay and load the next row ahead 48 us), and one warp to a short row (starting
+// a CTA takes 1.3 ns). A caller's codes (ids null) may be the weight of a call that
+// reads it ahead of its dependency wait, so dependents start only once they are
+// written; the codes of the experts' activations are read after the wait.
+constexpr int kQuantThreads = 128;
+template <typename T, int kKeep, int W>
+__global__ void __launch_bounds__(kQuantThreads, 10)
+    quantize_kernel(const T *z, int8_t *q, float *scale, int rows, int n, const int32_t *ids, int n_experts) {
+  constexpr int kVals = Chunk<T>::kVals, kThreads = 32 * W;
   if (ids) griddep_launch_dependents();
   griddep_wait();
-  const size_t row = blockIdx.x;
-  if (ids && static_cast<unsigned>(ids[row]) >= static_cast<unsigned>(n_experts)) return;
-  const uint4 *from = reinterpret_cast<const uint4 *>(z + row * n);
-  int8_t *to = q + row * n;
-  const int chunks = n / kVals;
-  uint32_t bits = 0;
-  if constexpr (kKeep > 0) {
-    Chunk<T> c[kKeep];
+  const int row = blockIdx.x * (kQuantThreads / kThreads) + threadIdx.x / kThreads;
+  const int tid = threadIdx.x % kThreads, chunks = n / kVals;
+  // (all the warps of a row, and with W = 4 all of the CTA, agree)
+  const bool done = row >= rows || (ids && static_cast<unsigned>(ids[row]) >= static_cast<unsigned>(n_experts));
+  if (!done) {
+    const uint4 *from = reinterpret_cast<const uint4 *>(z + static_cast<size_t>(row) * n);
+    int8_t *to = q + static_cast<size_t>(row) * n;
+    uint32_t bits = 0;
+    float amax;
+    if constexpr (kKeep > 0) {
+      Chunk<T> c[kKeep];
 #pragma unroll
-    for (int j = 0; j < kKeep; ++j) {
-      const int at = threadIdx.x + j * 256;
-      c[j].raw = at < chunks ? from[at] : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < kKeep; ++j) {
+        const int at = tid + j * kThreads;
+        c[j].raw = at < chunks ? from[at] : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < kKeep; ++j) bits = c[j].max_bits(bits);
+      amax = row_max<W>(Chunk<T>::fp32_bits(bits));
+      const RowCodes code(amax);
+#pragma unroll
+      for (int j = 0; j < kKeep; ++j) {
+        const int at = tid + j * kThreads;
+        if (at < chunks) c[j].store(to + at * kVals, code);
+      }
+    } else {
+      for (int at = tid; at < chunks; at += kThreads) bits = Chunk<T>{from[at]}.max_bits(bits);
+      amax = row_max<W>(Chunk<T>::fp32_bits(bits));
+      const RowCodes code(amax);
+      for (int at = tid; at < chunks; at += kThreads) Chunk<T>{from[at]}.store(to + at * kVals, code);
     }
-#pragma unroll
-    for (int j = 0; j < kKeep; ++j) bits = c[j].max_bits(bits);
-    const RowCodes code(cta_row_max(Chunk<T>::fp32_bits(bits)));
-#pragma unroll
-    for (int j = 0; j < kKeep; ++j) {
-      const int at = threadIdx.x + j * 256;
-      if (at < chunks) c[j].store(to + at * kVals, code);
-    }
-    if (threadIdx.x == 0) scale[row] = __fdiv_rn(code.amax, 127.0f);
-  } else {
-    for (int at = threadIdx.x; at < chunks; at += 256) bits = Chunk<T>{from[at]}.max_bits(bits);
-    const RowCodes code(cta_row_max(Chunk<T>::fp32_bits(bits)));
-    for (int at = threadIdx.x; at < chunks; at += 256) Chunk<T>{from[at]}.store(to + at * kVals, code);
-    if (threadIdx.x == 0) scale[row] = __fdiv_rn(code.amax, 127.0f);
+    if (tid == 0) scale[row] = __fdiv_rn(amax, 127.0f);
   }
   if (ids) return;
   __threadfence();
@@ -456,12 +469,16 @@ __global__ void __launch_bounds__(256)
 }
 
 template <typename T>
-static cudaError_t launch_quantize(const T *z, int8_t *q, float *scale, int rows, int n, const int32_t *ids,
+cudaError_t launch_quantize(const T *z, int8_t *q, float *scale, int rows, int n, const int32_t *ids,
                             int n_experts, cudaStream_t stream, bool pdl) {
-  const int per = (n / Chunk<T>::kVals + 255) / 256;
-  auto *kernel = per <= 1 ? quantize_kernel<T, 1> : per <= 2 ? quantize_kernel<T, 2>
-               : per <= 4 ? quantize_kernel<T, 4> : per <= 8 ? quantize_kernel<T, 8> : quantize_kernel<T, 0>;
-  return launch(kernel, dim3(rows), dim3(256), 0, stream, pdl, 1, z, q, scale, n, ids, n_experts);
+  const int chunks = n / Chunk<T>::kVals, lane = (chunks + 31) / 32, thread = (chunks + 127) / 128;
+  auto *kernel = lane <= 1 ? quantize_kernel<T, 1, 1> : lane <= 2 ? quantize_kernel<T, 2, 1>
+               : lane <= 4 ? quantize_kernel<T, 4, 1> : thread <= 2 ? quantize_kernel<T, 2, 4>
+               : thread <= 4 ? quantize_kernel<T, 4, 4> : thread <= 8 ? quantize_kernel<T, 8, 4>
+               : quantize_kernel<T, 0, 4>;
+  const int per_cta = lane <= 4 ? 4 : 1;
+  return launch(kernel, dim3((rows + per_cta - 1) / per_cta), dim3(kQuantThreads), 0, stream, pdl, 1, z, q, scale,
+                rows, n, ids, n_experts);
 }
 
 // ------------------------------------------------------- the int8 product core
