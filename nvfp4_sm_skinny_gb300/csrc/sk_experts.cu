@@ -972,12 +972,28 @@ __global__ void __launch_bounds__(kCoreThreads, 2) experts_kernel(ExpertsArgs a)
     }
 
   const WidenConst wc;
-  int slot = 0, side = 0;
-  for (int i = blockIdx.x; i < items; i += gridDim.x, side ^= 1) {
-    const int e = q.active[i / tiles], n0 = i % tiles * kTile;
+  int slot = 0, side = 0, turn = 0;
+  for (int i = blockIdx.x; i < items; i += gridDim.x, side ^= 1, ++turn) {
+    const int e = q.active[i / tiles], n = i % tiles * kTile + lane % kTile;
     const uint16_t *rows = q.rows + q.offset[e];
     const int tokens = __popc(q.mask[e]);
     int *red = sh.red[side];
+    // A warp finishes whole tokens, kTile outputs each, and the warps take turns
+    // over the items; what it needs besides the sums is fetched ahead of them.
+    const int first = (warp + turn) % kWarps;
+    const bool store = lane < kTile && n < N;
+    float scale0 = 0.0f, scale1 = 0.0f, row_scale[NT];
+    if (store) {
+      const size_t at = static_cast<size_t>(e) * (kUp ? 2 * N : N) + n;
+      scale0 = (kUp ? a.s13 : a.s2)[at];
+      if (kUp) scale1 = a.s13[at + N];
+    }
+#pragma unroll
+    for (int k = 0; k < NT; ++k)
+      if (first + k * kWarps < tokens) {
+        const int row = rows[first + k * kWarps];
+        row_scale[k] = kUp ? a.x_scale[row / a.top_k] : a.hs[row];
+      }
     auto stream = [&](auto sums) {
       constexpr int kT = sizeof(sums.xsum) / sizeof(int);
       for (int b = 0; b < blocks; ++b) {
@@ -1003,25 +1019,26 @@ __global__ void __launch_bounds__(kCoreThreads, 2) experts_kernel(ExpertsArgs a)
     if (NT == 2 && tokens > 8) stream(Sums<NT>());
     else stream(Sums<1>());
     __syncthreads();
-    for (int j = tid; j < tokens * kTile; j += kCoreThreads) {
-      const int c = j / kTile, at = j % kTile, n = n0 + at, row = rows[c];
-      if (n >= N) continue;
-      const float s0 = __int2float_rn(red_sum(red, c, at));
-      if (kUp) {
-        const size_t gate = static_cast<size_t>(e) * 2 * N + n;
-        const float xs = a.x_scale[row / a.top_k];
-        const float v = __fmul_rn(__fmul_rn(s0, xs), a.s13[gate]);
-        const float u = __fmul_rn(__fmul_rn(__int2float_rn(red_sum(red, c, kTile + at)), xs), a.s13[gate + N]);
-        a.act[static_cast<size_t>(row) * N + n] = v / (1.0f + expf(-v)) * u;
-      } else {
-        a.o[static_cast<size_t>(row) * N + n] =
-            __fmul_rn(__fmul_rn(s0, a.hs[row]), a.s2[static_cast<size_t>(e) * N + n]);
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+      const int c = first + k * kWarps;
+      if (c >= tokens) break;
+      const size_t at = static_cast<size_t>(rows[c]) * N + n;
+      if (store) {
+        const float s0 = __fmul_rn(__fmul_rn(__int2float_rn(red_sum(red, c, lane)), row_scale[k]), scale0);
+        if (kUp) {
+          const float up =
+              __fmul_rn(__fmul_rn(__int2float_rn(red_sum(red, c, kTile + lane)), row_scale[k]), scale1);
+          a.act[at] = s0 / (1.0f + expf(-s0)) * up;
+        } else {
+          a.o[at] = s0;
+        }
       }
+      // The token's sums are zero again before this warp passes the barrier of the
+      // next item, after which this buffer's turn comes again.
+      __syncwarp();
+      for (int j = lane; j <= kRows; j += 32) red[c * kRedPitch + j] = 0;
     }
-    // The next item adds to the other buffer. This one is cleared once all have
-    // read it, before the barrier of the next item, i.e. before it is used again.
-    __syncthreads();
-    for (int j = tid; j < tokens * kRedPitch; j += kCoreThreads) red[j] = 0;
   }
   copy_wait<0>();
 }
