@@ -37,6 +37,13 @@ cudaError_t launch(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, 
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// A load that stays in its place.
+__device__ __forceinline__ int load_id(const int32_t *p) {
+  int v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
 // ------------------------------------------------------------------ routing
 // One warp per token row, kVals logits per lane (expert 32 j + lane in value j).
 // What a row costs is the chain of selections, each two warp reductions, not
@@ -428,11 +435,12 @@ __global__ void __launch_bounds__(kQuantThreads, 10)
     quantize_kernel(const T *z, int8_t *q, float *scale, int rows, int n, const int32_t *ids, int n_experts) {
   constexpr int kVals = Chunk<T>::kVals, kThreads = 32 * W;
   if (ids) griddep_launch_dependents();
-  griddep_wait();
   const int row = blockIdx.x * (kQuantThreads / kThreads) + threadIdx.x / kThreads;
   const int tid = threadIdx.x % kThreads, chunks = n / kVals;
-  // (all the warps of a row, and with W = 4 all of the CTA, agree)
-  const bool done = row >= rows || (ids && static_cast<unsigned>(ids[row]) >= static_cast<unsigned>(n_experts));
+  // (all the warps of a row, and with W = 4 all of the CTA, agree; the kernel
+  // ahead started after the one that wrote the ids was done)
+  const bool done = row >= rows || (ids && static_cast<unsigned>(load_id(ids + row)) >= static_cast<unsigned>(n_experts));
+  griddep_wait();
   if (!done) {
     const uint4 *from = reinterpret_cast<const uint4 *>(z + static_cast<size_t>(row) * n);
     int8_t *to = q + static_cast<size_t>(row) * n;
@@ -817,63 +825,82 @@ __global__ void __launch_bounds__(kCoreThreads, 2) gemm_int8_kernel(Int8GemmArgs
 // order, and for each the workspace rows (token * top_k + first choice) of its
 // tokens in ascending order.
 struct Roster {
-  uint32_t mask[SK_MAX_EXPERTS];               // tokens of an expert
+  uint16_t mask[SK_MAX_EXPERTS];               // tokens of an expert
   uint16_t offset[SK_MAX_EXPERTS];             // its first entry of `rows`
-  uint16_t rows[SK_MAX_M * SK_MAX_TOP_K];
   uint16_t active[SK_MAX_M * SK_MAX_TOP_K];
-  int ids[SK_MAX_M * SK_MAX_TOP_K];
+  int16_t ids[SK_MAX_M * SK_MAX_TOP_K];        // -1: masked
+  uint8_t rows[SK_MAX_M * SK_MAX_TOP_K];
+  uint8_t some[SK_MAX_EXPERTS / 32], count[SK_MAX_EXPERTS / 32];  // per 32 experts: active ones, their tokens
   int n_active;
 };
 
-__device__ __forceinline__ int load_id(const int32_t *p) {
-  int v;
-  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
-}
-
-// The workspace row of choice c of ids (shared memory): that of the token's
-// first choice of the same expert, or -1 where the choice is masked.
-__device__ __forceinline__ int choice_row(const int *ids, int c, int top_k, int n_experts) {
+// The workspace row of choice c of ids (shared memory, -1 where masked): that of
+// the token's first choice of the same expert, or -1.
+template <typename Id>
+__device__ __forceinline__ int choice_row(const Id *ids, int c, int top_k) {
   const int e = ids[c];
-  if (static_cast<unsigned>(e) >= static_cast<unsigned>(n_experts)) return -1;
+  if (e < 0) return -1;
   int f = c / top_k * top_k;
   while (ids[f] != e) ++f;
   return f;
 }
 
+__device__ __forceinline__ void clear_roster(Roster &q, int n_experts) {
+  uint32_t *mask = reinterpret_cast<uint32_t *>(q.mask);
+  for (int e = threadIdx.x; e < (n_experts + 31) / 32 * 16; e += kCoreThreads) mask[e] = 0;
+}
+
+// By all threads, after clear_roster.
 __device__ __forceinline__ void build_roster(Roster &q, const ExpertsArgs &a) {
   const int choices = a.m * a.top_k, c = threadIdx.x;  // at most 256 choices, as many threads
-  if (c < choices) q.ids[c] = load_id(a.ids + c);
-  for (int e = threadIdx.x; e < a.n_experts; e += kCoreThreads) q.mask[e] = 0;
-  __syncthreads();
-  const bool mine = c < choices && choice_row(q.ids, c, a.top_k, a.n_experts) == c;
-  const int e = mine ? q.ids[c] : 0, token = c / a.top_k;
-  if (mine) atomicOr(&q.mask[e], 1u << token);
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    int n = 0, rows = 0;
-    for (int e0 = 0; e0 < a.n_experts; e0 += 32) {
-      const int x = e0 + threadIdx.x;
-      const int count = x < a.n_experts ? __popc(q.mask[x]) : 0;
-      const uint32_t some = __ballot_sync(0xFFFFFFFFu, count);
-      if (!some) continue;
-      int sum = count;  // inclusive prefix
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
-        if (static_cast<int>(threadIdx.x) >= d) sum += o;
-      }
-      if (count) {
-        q.active[n + __popc(some & ((1u << threadIdx.x) - 1))] = static_cast<uint16_t>(x);
-        q.offset[x] = static_cast<uint16_t>(rows + sum - count);
-      }
-      n += __popc(some);
-      rows += __shfl_sync(0xFFFFFFFFu, sum, 31);
-    }
-    if (threadIdx.x == 0) q.n_active = n;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (c < choices) {
+    const int e = load_id(a.ids + c);
+    q.ids[c] = static_cast<int16_t>(static_cast<unsigned>(e) < static_cast<unsigned>(a.n_experts) ? e : -1);
   }
   __syncthreads();
-  if (mine) q.rows[q.offset[e] + __popc(q.mask[e] & ((1u << token) - 1))] = static_cast<uint16_t>(c);
+  const bool mine = c < choices && choice_row(q.ids, c, a.top_k) == c;
+  const int e = mine ? q.ids[c] : 0, token = c / a.top_k;
+  if (mine) atomicOr(reinterpret_cast<uint32_t *>(q.mask) + e / 2, 1u << (token + 16 * (e & 1)));
+  __syncthreads();
+  // Prefix sums over the experts: within groups of 32, a warp each ...
+  const int groups = (a.n_experts + 31) / 32;
+  for (int g = warp; g < groups; g += kWarps) {
+    const int tokens = __popc(static_cast<uint32_t>(q.mask[g * 32 + lane]));
+    int sum = tokens;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+      if (lane >= d) sum += o;
+    }
+    q.offset[g * 32 + lane] = static_cast<uint16_t>(sum - tokens);
+    const uint32_t some = __ballot_sync(0xFFFFFFFFu, tokens);
+    if (lane == 31) {
+      q.some[g] = static_cast<uint8_t>(__popc(some));
+      q.count[g] = static_cast<uint8_t>(min(sum, 255));  // 256 only if nothing comes after
+    }
+  }
+  __syncthreads();
+  // ... then over the groups, by every warp for itself.
+  int n = lane < groups ? q.some[lane] : 0, tokens = lane < groups ? q.count[lane] : 0;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int on = __shfl_up_sync(0xFFFFFFFFu, n, d), ot = __shfl_up_sync(0xFFFFFFFFu, tokens, d);
+    if (lane >= d) {
+      n += on;
+      tokens += ot;
+    }
+  }
+  if (threadIdx.x == 31) q.n_active = n;
+  for (int g = warp; g < groups; g += kWarps) {
+    const int n0 = g ? __shfl_sync(0xFFFFFFFFu, n, g - 1) : 0, t0 = g ? __shfl_sync(0xFFFFFFFFu, tokens, g - 1) : 0;
+    const int x = g * 32 + lane;
+    const uint32_t some = __ballot_sync(0xFFFFFFFFu, q.mask[x]);
+    q.offset[x] = static_cast<uint16_t>(q.offset[x] + t0);
+    if (q.mask[x]) q.active[n0 + __popc(some & ((1u << lane) - 1))] = static_cast<uint16_t>(x);
+  }
+  __syncthreads();
+  if (mine) q.rows[q.offset[e] + __popc(static_cast<uint32_t>(q.mask[e]) & ((1u << token) - 1))] = static_cast<uint8_t>(c);
   __syncthreads();
 }
 
@@ -898,6 +925,7 @@ __global__ void __launch_bounds__(kCoreThreads, 2) experts_kernel(ExpertsArgs a)
   const Roster &q = sh.roster;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   for (int i = tid; i < 2 * kRedInts; i += kCoreThreads) (&sh.red[0][0])[i] = 0;
+  clear_roster(sh.roster, a.n_experts);
   // The ids may come from the kernel ahead. The kernels after this one start
   // only now, so they may read the ids at once, and start on their weights.
   if (kUp) griddep_wait();
@@ -918,7 +946,7 @@ __global__ void __launch_bounds__(kCoreThreads, 2) experts_kernel(ExpertsArgs a)
   auto open = [&] {
     if (fi >= items) return;
     const int e = q.active[fi / tiles], n0 = fi % tiles * kTile;
-    count = __popc(q.mask[e]);
+    count = __popc(static_cast<uint32_t>(q.mask[e]));
 #pragma unroll
     for (int h = 0; h < 4; ++h) {  // rows past N repeat the last one; their sums are not stored
       const size_t row = kUp ? (static_cast<size_t>(e) * 2 + (h >> 1)) * N + min(n0 + (h & 1) * 8 + g, N - 1)
@@ -975,8 +1003,8 @@ __global__ void __launch_bounds__(kCoreThreads, 2) experts_kernel(ExpertsArgs a)
   int slot = 0, side = 0, turn = 0;
   for (int i = blockIdx.x; i < items; i += gridDim.x, side ^= 1, ++turn) {
     const int e = q.active[i / tiles], n = i % tiles * kTile + lane % kTile;
-    const uint16_t *rows = q.rows + q.offset[e];
-    const int tokens = __popc(q.mask[e]);
+    const uint8_t *rows = q.rows + q.offset[e];
+    const int tokens = __popc(static_cast<uint32_t>(q.mask[e]));
     int *red = sh.red[side];
     // A warp finishes whole tokens, kTile outputs each, and the warps take turns
     // over the items; what it needs besides the sums is fetched ahead of them.
@@ -1049,23 +1077,26 @@ __global__ void __launch_bounds__(kSumThreads) experts_sum_kernel(ExpertsArgs a)
   __shared__ int ids[SK_MAX_TOP_K];
   __shared__ float weights[SK_MAX_TOP_K];
   griddep_launch_dependents();
-  griddep_wait();
   const int i = blockIdx.y, n = 4 * (blockIdx.x * kSumThreads + threadIdx.x);
+  // (the products' kernels, which this one waits for, started after what wrote
+  // the ids and the weights)
   if (static_cast<int>(threadIdx.x) < a.top_k) {
-    ids[threadIdx.x] = a.ids[i * a.top_k + threadIdx.x];
-    weights[threadIdx.x] = a.weights[i * a.top_k + threadIdx.x];
+    const int e = load_id(a.ids + i * a.top_k + threadIdx.x);
+    ids[threadIdx.x] = static_cast<unsigned>(e) < static_cast<unsigned>(a.n_experts) ? e : -1;
+    weights[threadIdx.x] = __int_as_float(load_id(reinterpret_cast<const int32_t *>(a.weights) + i * a.top_k + threadIdx.x));
   }
   __syncthreads();
+  griddep_wait();
   if (n >= a.hidden) return;
   float4 o[SK_MAX_TOP_K], s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
   for (int j = 0; j < SK_MAX_TOP_K; ++j) {
-    const int f = j < a.top_k ? choice_row(ids, j, SK_MAX_TOP_K, a.n_experts) : -1;
+    const int f = j < a.top_k ? choice_row(ids, j, SK_MAX_TOP_K) : -1;
     if (f >= 0) o[j] = *reinterpret_cast<const float4 *>(a.o + static_cast<size_t>(i * a.top_k + f) * a.hidden + n);
   }
 #pragma unroll
   for (int j = 0; j < SK_MAX_TOP_K; ++j) {
-    if (j >= a.top_k || static_cast<unsigned>(ids[j]) >= static_cast<unsigned>(a.n_experts)) continue;
+    if (j >= a.top_k || ids[j] < 0) continue;
     s.x = fmaf(weights[j], o[j].x, s.x);
     s.y = fmaf(weights[j], o[j].y, s.y);
     s.z = fmaf(weights[j], o[j].z, s.z);
