@@ -53,7 +53,8 @@ __device__ __forceinline__ int load_id(const int32_t *p) {
 // Without a bias the order is that of the logits, exactly. With one it is that
 // of p + bias, computed in FP32 here, and two values nearer than the rounding
 // errors of either decide nothing: such a row (about one in a thousand of random
-// ones) is done again in FP64.
+// ones) is done again in pairs of FP32, and one that these cannot settle either in
+// FP64, whose exponential alone takes microseconds on this GPU.
 constexpr int kRouteWarps = 4;  // token rows per CTA
 
 __device__ __forceinline__ float route_logit(const RouteArgs &a, size_t at) {
@@ -161,6 +162,194 @@ __device__ __noinline__ void route_row_f64(const RouteArgs &a, int row, double *
 }
 
 
+// A value as the sum of two FP32, hi the nearest to it: about 45 significant bits,
+// by the error-free sums and products of Dekker and Knuth.
+struct Pair {
+  float hi, lo;
+};
+
+__device__ __forceinline__ Pair quick_sum(float a, float b) {  // |a| >= |b|
+  const float s = __fadd_rn(a, b);
+  return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ __forceinline__ Pair exact_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  const Pair s = exact_sum(a.hi, b.hi), t = exact_sum(a.lo, b.lo);
+  const Pair r = quick_sum(s.hi, __fadd_rn(s.lo, t.hi));
+  return quick_sum(r.hi, __fadd_rn(r.lo, t.lo));
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  const float p = __fmul_rn(a.hi, b.hi);
+  const float e = __fmaf_rn(a.hi, b.hi, -p);
+  return quick_sum(p, __fadd_rn(e, __fmaf_rn(a.hi, b.lo, __fmul_rn(a.lo, b.hi))));
+}
+__device__ __forceinline__ Pair operator/(Pair a, Pair b) {
+  const float q = __fdiv_rn(a.hi, b.hi);
+  const float r = __fadd_rn(__fmaf_rn(-q, b.hi, a.hi), __fmaf_rn(-q, b.lo, a.lo));
+  return quick_sum(q, __fdiv_rn(r, b.hi));
+}
+__device__ __forceinline__ bool above(Pair a, Pair b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
+
+// exp(x) for -80 <= x <= 80: x = k ln 2 + r, and exp(r) - 1 from that of r / 8 by
+// its series and three squarings, 1 + y -> (1 + y)^2.
+__device__ __forceinline__ Pair pair_exp(Pair x) {
+  constexpr float kLn2Hi = 0x1.62ep-1f;                  // 12 bits, so that k times it is exact
+  constexpr float kLn2Mid = 0x1.0bfbe8p-15f;             // the next 24
+  constexpr float kLn2Lo = 0x1.cf79acp-40f;              // and the rest
+  const float k = rintf(__fmul_rn(x.hi, 1.44269504f));
+  const float a = __fmaf_rn(-k, kLn2Hi, x.hi);           // exact
+  const float m = __fmul_rn(-k, kLn2Mid), e = __fmaf_rn(-k, kLn2Mid, -m);
+  const Pair s = exact_sum(a, m);
+  const Pair r = quick_sum(s.hi, __fadd_rn(s.lo, __fadd_rn(__fmaf_rn(-k, kLn2Lo, e), x.lo)));
+  const Pair z = {r.hi * 0.125f, r.lo * 0.125f};
+  // z^4 / 24 + ... + z^8 / 40320, below 2e-7 with |z| <= 0.0434
+  const float h = z.hi, t = __fmul_rn(__fmul_rn(__fmul_rn(h, h), __fmul_rn(h, h)),
+                                      1.0f / 24 + h * (1.0f / 120 + h * (1.0f / 720 + h * (1.0f / 5040 + h * (1.0f / 40320)))));
+  const Pair z2 = z * z, z3 = z2 * z;
+  Pair y = z + Pair{0.5f * z2.hi, 0.5f * z2.lo} + z3 * Pair{0x1.555556p-3f, -0x1.555556p-28f} + Pair{t, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 3; ++i) y = Pair{2.0f * y.hi, 2.0f * y.lo} + y * y;
+  const Pair v = Pair{1.0f, 0.0f} + y;
+  const float scale = __int_as_float((static_cast<int>(k) + 127) << 23);
+  return {v.hi * scale, v.lo * scale};
+}
+
+// route_row_f64 in pairs: false where these cannot tell two values apart. The
+// selection values are in hi[n_experts], lo[n_experts] (shared memory).
+__device__ __noinline__ bool route_row_pairs(const RouteArgs &a, int row, float *hi, float *lo) {
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
+  const int lane = threadIdx.x & 31, E = a.n_experts;
+  const size_t base = static_cast<size_t>(row) * E;
+  float top = -CUDART_INF_F;
+  if (!a.sigmoid) {
+    for (int e = lane; e < E; e += 32) top = fmaxf(top, route_logit(a, base + e));
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
+  }
+  // exp(x - top) or exp(-x); tiny ones to FP32 only, within the tolerance below
+  auto power = [&](float x) -> Pair {
+    Pair d = a.sigmoid ? Pair{-x, 0.0f} : x == top ? Pair{0.0f, 0.0f} : exact_sum(x, -top);
+    if (!(fabsf(d.hi) <= 80.0f)) return {d.hi > 0.0f ? CUDART_INF_F : __expf(d.hi), 0.0f};
+    return pair_exp(d);
+  };
+  Pair sum = {0.0f, 0.0f};
+  if (!a.sigmoid) {
+    for (int e = lane; e < E; e += 32) {
+      const float x = route_logit(a, base + e);
+      if (x > -CUDART_INF_F) sum = sum + power(x);
+    }
+    for (int d = 16; d; d >>= 1)
+      sum = sum + Pair{__shfl_xor_sync(kAll, sum.hi, d), __shfl_xor_sync(kAll, sum.lo, d)};
+  }
+  auto score = [&](float x) -> Pair {
+    const Pair p = power(x);
+    if (!a.sigmoid) return p / sum;
+    if (p.hi == CUDART_INF_F) return {__expf(x), 0.0f};
+    return Pair{1.0f, 0.0f} / (Pair{1.0f, 0.0f} + p);
+  };
+  const Pair none = {-CUDART_INF_F, 0.0f};
+  for (int e = lane; e < E; e += 32) {
+    const float x = route_logit(a, base + e), b = a.bias[e];
+    Pair v = none;
+    if (x > -CUDART_INF_F && b > -CUDART_INF_F)
+      v = b < CUDART_INF_F ? score(x) + Pair{b, 0.0f} : Pair{CUDART_INF_F, 0.0f};
+    hi[e] = v.hi;
+    lo[e] = v.lo;
+  }
+  __syncwarp();
+  // Whether a, not below b, may be b all the same. Scores are within 2^-38 of
+  // their size (1e-34 for tiny ones), values and sums of two another 2^-44.
+  auto close = [](Pair a, Pair b, float scores, float sizes) {
+    return !(__fadd_rn(a.hi - b.hi, a.lo - b.lo) > scores * 0x1p-37f + sizes * 0x1p-43f + 1e-34f);
+  };
+
+  const int per = E / a.n_groups;
+  uint32_t keep = a.n_groups > 1 ? 0u : 1u;
+  if (a.n_groups > 1) {
+    Pair gv = none;
+    float size = 0.0f;
+    if (lane < a.n_groups) {
+      Pair b0 = none, b1 = none;
+      for (int j = 0; j < per; ++j) {
+        const Pair x = {hi[lane * per + j], lo[lane * per + j]};
+        if (above(x, b0)) {
+          b1 = b0;
+          b0 = x;
+        } else if (above(x, b1)) {
+          b1 = x;
+        }
+      }
+      const bool two = b1.hi > -CUDART_INF_F;
+      gv = !two ? b0 : fmaxf(b0.hi, b1.hi) < CUDART_INF_F ? b0 + b1 : Pair{CUDART_INF_F, 0.0f};
+      size = fabsf(b0.hi) + (two ? fabsf(b1.hi) : 0.0f);
+    }
+    int rank = 0;
+    for (int o = 0; o < a.n_groups; ++o) {
+      const Pair v = {__shfl_sync(kAll, gv.hi, o), __shfl_sync(kAll, gv.lo, o)};
+      rank += above(v, gv) || (!above(gv, v) && o < lane);
+    }
+    const bool lead = lane < a.n_groups;
+    keep = __ballot_sync(kAll, lead && rank < a.topk_groups && gv.hi > -CUDART_INF_F);
+    if (a.topk_groups < a.n_groups) {
+      const int last = __ffs(__ballot_sync(kAll, lead && rank == a.topk_groups - 1)) - 1;
+      const int next = __ffs(__ballot_sync(kAll, lead && rank == a.topk_groups)) - 1;
+      const Pair v0 = {__shfl_sync(kAll, gv.hi, last), __shfl_sync(kAll, gv.lo, last)};
+      const Pair v1 = {__shfl_sync(kAll, gv.hi, next), __shfl_sync(kAll, gv.lo, next)};
+      const float sizes = __shfl_sync(kAll, size, last) + __shfl_sync(kAll, size, next);
+      if (v1.hi > -CUDART_INF_F && close(v0, v1, 4.0f, sizes)) return false;
+    }
+  }
+
+  int id = -1, found = 0;
+  Pair mine = none;
+  for (; found < a.top_k + 1; ++found) {
+    Pair b = none;
+    int at = INT_MAX;
+    for (int e = lane; e < E; e += 32)
+      if ((keep >> (a.n_groups > 1 ? e / per : 0)) & 1u) {
+        const Pair x = {hi[e], lo[e]};
+        if (above(x, b)) {
+          b = x;
+          at = e;
+        }
+      }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+      const Pair o = {__shfl_xor_sync(kAll, b.hi, d), __shfl_xor_sync(kAll, b.lo, d)};
+      const int oat = __shfl_xor_sync(kAll, at, d);
+      if (above(o, b) || (!above(b, o) && oat < at)) {
+        b = o;
+        at = oat;
+      }
+    }
+    if (at == INT_MAX) break;
+    if (lane == 0) hi[at] = -CUDART_INF_F;
+    __syncwarp();
+    if (lane == found) {
+      id = at;
+      mine = b;
+    }
+  }
+  const float x = id >= 0 ? route_logit(a, base + id) : 0.0f, b = id >= 0 ? a.bias[id] : 0.0f;
+  const Pair v1 = {__shfl_down_sync(kAll, mine.hi, 1), __shfl_down_sync(kAll, mine.lo, 1)};
+  const float x1 = __shfl_down_sync(kAll, x, 1), b1 = __shfl_down_sync(kAll, b, 1);
+  const Pair p = id >= 0 ? score(x) : Pair{0.0f, 0.0f};
+  const float p1 = __shfl_down_sync(kAll, p.hi, 1);
+  if (__any_sync(kAll, lane + 1 < found && !(x1 == x && b1 == b) &&
+                           close(mine, v1, p.hi + p1, fabsf(mine.hi) + fabsf(v1.hi))))
+    return false;
+  float w = lane < a.top_k ? p.hi : 0.0f, total = w;
+  for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(kAll, total, d);
+  if (a.renormalize) w = total > 0.0f ? w / total : 0.0f;
+  if (lane < a.top_k) {
+    a.ids[static_cast<size_t>(row) * a.top_k + lane] = id;
+    a.weights[static_cast<size_t>(row) * a.top_k + lane] = w * a.scale;
+  }
+  return true;
+}
+
 // FP32 -> integer with the same order; 0 stands for "cannot be chosen" (-inf and
 // NaN, and nothing else).
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -242,8 +431,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(RouteArgs a) {
       b1 = max(max(b1, o1), min(b0, o0));
       b0 = max(b0, o0);
     }
-    float gv = value(b0);
-    if (a.bias && b1) gv += value(b1);
+    float gv = value(b0), size = fabsf(gv);
+    if (a.bias && b1) {
+      gv += value(b1);
+      size += fabsf(value(b1));
+    }
     // (of NaN, from infinities of both signs, nothing is made: those are never both chosen)
     const uint32_t gk = grp < a.n_groups ? order_key(gv) : 0u;
     int rank = 0;
@@ -258,7 +450,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(RouteArgs a) {
       const uint32_t first = __ballot_sync(kAll, lead && rank == a.topk_groups);
       const uint32_t k0 = __shfl_sync(kAll, gk, __ffs(last) - 1), k1 = __shfl_sync(kAll, gk, __ffs(first) - 1);
       const float v0 = value(k0), v1 = value(k1);
-      near = k1 && !(v0 - v1 > 2e-6f * (2.0f + fabsf(v0) + fabsf(v1)));
+      // Four scores are in it. With u = 2^-24, a sigmoid's is within 4 u (the
+      // exponential's error counts p (1 - p) times), a softmax's within 60 u; a
+      // sum of two and their biases another 2 u of the sizes.
+      const float sizes = __shfl_sync(kAll, size, __ffs(last) - 1) + __shfl_sync(kAll, size, __ffs(first) - 1);
+      near = k1 && !(v0 - v1 > (a.sigmoid ? 1.2e-6f : 1.5e-5f) + 1.5e-7f * sizes);
     }
     const uint32_t leads = __ballot_sync(kAll, kept);  // bit g * lanes
     const uint32_t magic = per == 1 ? 0u : 0xFFFFFFFFu / per + 1;
@@ -306,15 +502,23 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(RouteArgs a) {
     const float b = id >= 0 ? a.bias[id] : 0.0f, v = value(mine);
     const float v1 = __shfl_down_sync(kAll, v, 1), w1 = __shfl_down_sync(kAll, w, 1);
     const float c1 = __shfl_down_sync(kAll, chosen, 1), b1 = __shfl_down_sync(kAll, b, 1);
-    // the errors of both: the exponential's, growing with its argument, the
-    // sum's and the quotient's on p; one rounding on p + bias
-    const float grow = 2e-6f + 3e-7f * (a.sigmoid ? fabsf(chosen) + fabsf(c1) : 2.0f * top - chosen - c1);
-    const float tol = grow * (w + w1) + 1.2e-7f * (fabsf(v) + fabsf(v1));
+    // Rounding errors in units of 2^-24: of p, the exponential's 4 + 2.4 times its
+    // argument (in a sigmoid (1 - p) times that, and two more), and 45 of softmax's
+    // sum; one of p + bias.
+    auto error = [&](float p, float x, float v) {
+      const float grow = a.sigmoid ? 2.0f + (1.0f - p) * (4.0f + 2.4f * fabsf(x)) : 50.0f + 2.4f * (top - x);
+      return p * grow + fabsf(v);
+    };
+    const float tol = 7.5e-8f * (error(w, chosen, v) + error(w1, c1, v1));
     const bool same = c1 == chosen && b1 == b;  // equal in any precision
     near = near || (lane + 1 < found && !same && !(v - v1 > tol));
     if (__any_sync(kAll, near)) {
       __syncwarp();
-      route_row_f64(a, row, scratch);
+      float *parts = reinterpret_cast<float *>(scratch);
+      if (!route_row_pairs(a, row, parts, parts + E)) {
+        __syncwarp();
+        route_row_f64(a, row, scratch);
+      }
       return;
     }
   }

@@ -132,6 +132,19 @@ def test_route_order_of_values_that_fp32_cannot_tell_apart(sk, score, groups, to
     check_route(sk, gpu(a, F32), k, gpu(b, F32), n_groups=groups, topk_groups=topk_groups, score=score)
 
 
+@pytest.mark.parametrize("base", [0.01, 1.7, -1.7, 6.0, -6.0, 12.0, 16.0, 20.0, 36.0, -40.0, -90.0])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,topk_groups", [(1, 1), (8, 4)])
+def test_route_order_of_neighbouring_logits(sk, base, score, groups, topk_groups):
+    # scores from 1e-7 apart to equal in 64 bits, by the slope of the score there
+    rng = np.random.default_rng(17)
+    steps = rng.integers(0, 40, (24, 64)).astype(np.int32)
+    a = (np.float32(base).view(np.int32) + steps).astype(np.int32).view(np.float32)
+    a[:, 0] = 1.0                                # a largest one for softmax, elsewhere
+    for bias in (np.zeros(64), np.full(64, -0.25), np.where(np.arange(64) % 2, 0.125, -3.0)):
+        check_route(sk, gpu(a, F32), 8, gpu(bias, F32), n_groups=groups, topk_groups=topk_groups, score=score)
+
+
 def test_route_many_rows(sk):
     g = torch.Generator(device=DEV).manual_seed(3)
     logits = torch.randn(5000, 64, generator=g, device=DEV)
