@@ -217,6 +217,27 @@ __device__ __forceinline__ Pair pair_exp(Pair x) {
   return {v.hi * scale, v.lo * scale};
 }
 
+// exp(x - top) of a softmax or exp(-x) of a sigmoid; tiny ones to FP32 only,
+// within the tolerance of `close`.
+__device__ __forceinline__ Pair pair_power(bool sigmoid, float x, float top) {
+  const Pair d = sigmoid ? Pair{-x, 0.0f} : x == top ? Pair{0.0f, 0.0f} : exact_sum(x, -top);
+  if (!(fabsf(d.hi) <= 80.0f)) return {d.hi > 0.0f ? CUDART_INF_F : __expf(d.hi), 0.0f};
+  return pair_exp(d);
+}
+__device__ __forceinline__ Pair pair_sigmoid(float x) {
+  const Pair p = pair_power(true, x, 0.0f);
+  if (p.hi == CUDART_INF_F) return {__expf(x), 0.0f};
+  return Pair{1.0f, 0.0f} / (Pair{1.0f, 0.0f} + p);
+}
+__device__ __forceinline__ Pair pair_biased(Pair p, float b) {  // b > -inf
+  return b < CUDART_INF_F ? p + Pair{b, 0.0f} : Pair{CUDART_INF_F, 0.0f};
+}
+// Whether a, not below b, may be b all the same. Scores are within 2^-38 of their
+// size (1e-34 for tiny ones), values and sums of two another 2^-44.
+__device__ __forceinline__ bool close(Pair a, Pair b, float scores, float sizes) {
+  return !(__fadd_rn(a.hi - b.hi, a.lo - b.lo) > scores * 0x1p-37f + sizes * 0x1p-43f + 1e-34f);
+}
+
 // route_row_f64 in pairs: false where these cannot tell two values apart. The
 // selection values are in hi[n_experts], lo[n_experts] (shared memory).
 __device__ __noinline__ bool route_row_pairs(const RouteArgs &a, int row, float *hi, float *lo) {
@@ -228,43 +249,25 @@ __device__ __noinline__ bool route_row_pairs(const RouteArgs &a, int row, float 
     for (int e = lane; e < E; e += 32) top = fmaxf(top, route_logit(a, base + e));
     for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
   }
-  // exp(x - top) or exp(-x); tiny ones to FP32 only, within the tolerance below
-  auto power = [&](float x) -> Pair {
-    Pair d = a.sigmoid ? Pair{-x, 0.0f} : x == top ? Pair{0.0f, 0.0f} : exact_sum(x, -top);
-    if (!(fabsf(d.hi) <= 80.0f)) return {d.hi > 0.0f ? CUDART_INF_F : __expf(d.hi), 0.0f};
-    return pair_exp(d);
-  };
   Pair sum = {0.0f, 0.0f};
   if (!a.sigmoid) {
     for (int e = lane; e < E; e += 32) {
       const float x = route_logit(a, base + e);
-      if (x > -CUDART_INF_F) sum = sum + power(x);
+      if (x > -CUDART_INF_F) sum = sum + pair_power(false, x, top);
     }
     for (int d = 16; d; d >>= 1)
       sum = sum + Pair{__shfl_xor_sync(kAll, sum.hi, d), __shfl_xor_sync(kAll, sum.lo, d)};
   }
-  auto score = [&](float x) -> Pair {
-    const Pair p = power(x);
-    if (!a.sigmoid) return p / sum;
-    if (p.hi == CUDART_INF_F) return {__expf(x), 0.0f};
-    return Pair{1.0f, 0.0f} / (Pair{1.0f, 0.0f} + p);
-  };
+  auto score = [&](float x) { return a.sigmoid ? pair_sigmoid(x) : pair_power(false, x, top) / sum; };
   const Pair none = {-CUDART_INF_F, 0.0f};
   for (int e = lane; e < E; e += 32) {
     const float x = route_logit(a, base + e), b = a.bias[e];
     Pair v = none;
-    if (x > -CUDART_INF_F && b > -CUDART_INF_F)
-      v = b < CUDART_INF_F ? score(x) + Pair{b, 0.0f} : Pair{CUDART_INF_F, 0.0f};
+    if (x > -CUDART_INF_F && b > -CUDART_INF_F) v = pair_biased(score(x), b);
     hi[e] = v.hi;
     lo[e] = v.lo;
   }
   __syncwarp();
-  // Whether a, not below b, may be b all the same. Scores are within 2^-38 of
-  // their size (1e-34 for tiny ones), values and sums of two another 2^-44.
-  auto close = [](Pair a, Pair b, float scores, float sizes) {
-    return !(__fadd_rn(a.hi - b.hi, a.lo - b.lo) > scores * 0x1p-37f + sizes * 0x1p-43f + 1e-34f);
-  };
-
   const int per = E / a.n_groups;
   uint32_t keep = a.n_groups > 1 ? 0u : 1u;
   if (a.n_groups > 1) {
@@ -302,9 +305,11 @@ __device__ __noinline__ bool route_row_pairs(const RouteArgs &a, int row, float 
     }
   }
 
+  // The choices and those after them, down to one that is clearly apart.
   int id = -1, found = 0;
-  Pair mine = none;
-  for (; found < a.top_k + 1; ++found) {
+  Pair mine = none, before = none;
+  bool apart = false;
+  while (found < 32 && !apart) {
     Pair b = none;
     int at = INT_MAX;
     for (int e = lane; e < E; e += 32)
@@ -331,15 +336,21 @@ __device__ __noinline__ bool route_row_pairs(const RouteArgs &a, int row, float 
       id = at;
       mine = b;
     }
+    apart = found >= a.top_k && !close(before, b, 2.0f, fabsf(before.hi) + fabsf(b.hi));
+    before = b;
+    ++found;
   }
+  if (found == 32 && !apart) return false;
+  const int count = apart ? found - 1 : found;  // all of them but the one apart
   const float x = id >= 0 ? route_logit(a, base + id) : 0.0f, b = id >= 0 ? a.bias[id] : 0.0f;
   const Pair v1 = {__shfl_down_sync(kAll, mine.hi, 1), __shfl_down_sync(kAll, mine.lo, 1)};
   const float x1 = __shfl_down_sync(kAll, x, 1), b1 = __shfl_down_sync(kAll, b, 1);
   const Pair p = id >= 0 ? score(x) : Pair{0.0f, 0.0f};
   const float p1 = __shfl_down_sync(kAll, p.hi, 1);
-  if (__any_sync(kAll, lane + 1 < found && !(x1 == x && b1 == b) &&
+  if (__any_sync(kAll, lane + 1 < count && !(x1 == x && b1 == b) &&
                            close(mine, v1, p.hi + p1, fabsf(mine.hi) + fabsf(v1.hi))))
     return false;
+  if (lane >= a.top_k) id = -1;
   float w = lane < a.top_k ? p.hi : 0.0f, total = w;
   for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(kAll, total, d);
   if (a.renormalize) w = total > 0.0f ? w / total : 0.0f;
@@ -358,8 +369,27 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return b ^ (static_cast<int>(b) < 0 ? 0xFFFFFFFFu : 0x80000000u);
 }
 
+// The two largest of a lane's keys, and how many of them are still to be taken
+// (0: none is left, or the next one has to be looked for).
+struct Best {
+  uint32_t key, next;
+  int at, next_at;
+  __device__ __forceinline__ Best() : key(0u), next(0u), at(0), next_at(0) {}
+  __device__ __forceinline__ void offer(uint32_t k, int e) {  // in ascending order of e
+    if (k > key) {
+      next = key;
+      next_at = at;
+      key = k;
+      at = e;
+    } else if (k > next) {
+      next = k;
+      next_at = e;
+    }
+  }
+};
+
 template <int kVals>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(RouteArgs a) {
+__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_constant__ RouteArgs a) {
   extern __shared__ double route_smem[];
   constexpr uint32_t kAll = 0xFFFFFFFFu;
   griddep_launch_dependents();
@@ -371,14 +401,20 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(RouteArgs a) {
   const size_t base = static_cast<size_t>(row) * E;
   double *scratch = route_smem + warp * E;
 
-  float x[kVals];
+  float x[kVals];  // NaN where the logit is: no comparison below takes one
+  if (a.fp32) {
+    const float *p = static_cast<const float *>(a.logits) + base + lane;
 #pragma unroll
-  for (int j = 0; j < kVals; ++j) x[j] = j * 32 + lane < E ? route_logit(a, base + j * 32 + lane) : -CUDART_INF_F;
-  float top = 0.0f, unit = 1.0f;  // softmax: the largest logit, 1 / sum
+    for (int j = 0; j < kVals; ++j) x[j] = j * 32 + lane < E ? p[j * 32] : -CUDART_INF_F;
+  } else {
+    const uint16_t *p = static_cast<const uint16_t *>(a.logits) + base + lane;
+#pragma unroll
+    for (int j = 0; j < kVals; ++j) x[j] = j * 32 + lane < E ? bf16_bits_to_f32(p[j * 32]) : -CUDART_INF_F;
+  }
+  float top = -CUDART_INF_F, unit = 1.0f;  // softmax: the largest logit, 1 / sum
   if (!a.sigmoid) {
-    top = x[0];
 #pragma unroll
-    for (int j = 1; j < kVals; ++j) top = fmaxf(top, x[j]);
+    for (int j = 0; j < kVals; ++j) top = fmaxf(top, x[j]);
 #pragma unroll
     for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
     float sum = 0.0f;
@@ -390,16 +426,14 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(RouteArgs a) {
     unit = 1.0f / sum;
   }
   auto score = [&](float v) {
-    return a.sigmoid ? 1.0f / (1.0f + __expf(-v)) : __expf(v == top ? 0.0f : v - top) * unit;
+    return a.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-v)) : __expf(v == top ? 0.0f : v - top) * unit;
   };
   uint32_t key[kVals];
 #pragma unroll
   for (int j = 0; j < kVals; ++j) {
-    const int e = j * 32 + lane;
     float v = x[j];
-    if (a.bias && v > -CUDART_INF_F) v = score(v) + a.bias[e];
+    if (a.bias && j * 32 + lane < E) v = v > -CUDART_INF_F ? score(v) + a.bias[j * 32 + lane] : v;
     key[j] = order_key(v);
-    if (a.n_groups > 1 && e < E) reinterpret_cast<uint32_t *>(scratch)[e] = key[j];
   }
   auto value = [](uint32_t k) {  // of a key
     return k == 0u ? -CUDART_INF_F : __uint_as_float(k ^ (k & 0x80000000u ? 0x80000000u : 0xFFFFFFFFu));
@@ -407,94 +441,144 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(RouteArgs a) {
 
   bool near = false;  // FP32 cannot tell
   if (a.n_groups > 1) {
-    // `lanes` lanes per group look for its two best; they start apart so that
-    // groups of a multiple of 32 experts do not meet in one bank.
-    __syncwarp();
+    // The two best of each group, that of group `lane` in b0, b1.
     const int per = E / a.n_groups;
-    int lanes = 1;
-    while (2 * lanes * a.n_groups <= 32) lanes *= 2;
-    const int grp = lane / lanes, sub = lane % lanes;
     uint32_t b0 = 0u, b1 = 0u;
-    if (grp < a.n_groups) {
-      const uint32_t *k = reinterpret_cast<const uint32_t *>(scratch) + grp * per;
-      const int turns = (per + lanes - 1) / lanes;
-      for (int i = 0, s = grp % turns; i < turns; ++i) {
-        const int at = s * lanes + sub;
-        const uint32_t v = at < per ? k[at] : 0u;
-        b1 = max(b1, min(b0, v));
-        b0 = max(b0, v);
-        s = s + 1 == turns ? 0 : s + 1;
+    if (per % 32 == 0) {
+      // whole values of all lanes: group g is values j with 32 j in [g per, ...)
+      uint32_t l0 = 0u, l1 = 0u;
+      int left = per, grp = 0;
+#pragma unroll
+      for (int j = 0; j < kVals; ++j) {
+        if (j * 32 >= E) break;
+        l1 = max(l1, min(l0, key[j]));
+        l0 = max(l0, key[j]);
+        left -= 32;
+        if (left == 0) {
+          const uint32_t m0 = __reduce_max_sync(kAll, l0);
+          uint32_t m1 = 0u;
+          if (a.bias) {
+            const int who = __ffs(__ballot_sync(kAll, l0 == m0)) - 1;
+            m1 = __reduce_max_sync(kAll, lane == who ? l1 : l0);
+          }
+          if (lane == grp) {
+            b0 = m0;
+            b1 = m1;
+          }
+          l0 = l1 = 0u;
+          left = per;
+          ++grp;
+        }
       }
-    }
-    for (int d = 1; d < lanes; d <<= 1) {
-      const uint32_t o0 = __shfl_xor_sync(kAll, b0, d), o1 = __shfl_xor_sync(kAll, b1, d);
-      b1 = max(max(b1, o1), min(b0, o0));
-      b0 = max(b0, o0);
+    } else {
+      // `lanes` lanes per group read them from shared memory, starting apart so
+      // that groups do not meet in one bank
+      uint32_t *keys = reinterpret_cast<uint32_t *>(scratch);
+#pragma unroll
+      for (int j = 0; j < kVals; ++j)
+        if (j * 32 + lane < E) keys[j * 32 + lane] = key[j];
+      __syncwarp();
+      int lanes = 1;
+      while (2 * lanes * a.n_groups <= 32) lanes *= 2;
+      const int grp = lane / lanes, sub = lane % lanes;
+      if (grp < a.n_groups) {
+        const uint32_t *k = keys + grp * per;
+        const int turns = (per + lanes - 1) / lanes;
+        for (int i = 0, s = grp % turns; i < turns; ++i) {
+          const int at = s * lanes + sub;
+          const uint32_t v = at < per ? k[at] : 0u;
+          b1 = max(b1, min(b0, v));
+          b0 = max(b0, v);
+          s = s + 1 == turns ? 0 : s + 1;
+        }
+      }
+      for (int d = 1; d < lanes; d <<= 1) {
+        const uint32_t o0 = __shfl_xor_sync(kAll, b0, d), o1 = __shfl_xor_sync(kAll, b1, d);
+        b1 = max(max(b1, o1), min(b0, o0));
+        b0 = max(b0, o0);
+      }
+      b0 = __shfl_sync(kAll, b0, lane * lanes);
+      b1 = __shfl_sync(kAll, b1, lane * lanes);
     }
     float gv = value(b0), size = fabsf(gv);
     if (a.bias && b1) {
       gv += value(b1);
       size += fabsf(value(b1));
     }
-    // (of NaN, from infinities of both signs, nothing is made: those are never both chosen)
-    const uint32_t gk = grp < a.n_groups ? order_key(gv) : 0u;
+    // (infinities of opposite signs never meet: -inf is no value)
+    const uint32_t gk = lane < a.n_groups ? order_key(gv) : 0u;
     int rank = 0;
     for (int o = 0; o < a.n_groups; ++o) {
-      const uint32_t ok = __shfl_sync(kAll, gk, o * lanes);
-      rank += ok > gk || (ok == gk && o < grp);
+      const uint32_t ok = __shfl_sync(kAll, gk, o);
+      rank += ok > gk || (ok == gk && o < lane);
     }
-    const bool lead = sub == 0 && grp < a.n_groups;
-    const bool kept = lead && gk && rank < a.topk_groups;
+    const bool lead = lane < a.n_groups;
+    const uint32_t kept = __ballot_sync(kAll, lead && gk && rank < a.topk_groups);
     if (a.bias && a.topk_groups < a.n_groups) {
-      const uint32_t last = __ballot_sync(kAll, lead && rank == a.topk_groups - 1);
-      const uint32_t first = __ballot_sync(kAll, lead && rank == a.topk_groups);
-      const uint32_t k0 = __shfl_sync(kAll, gk, __ffs(last) - 1), k1 = __shfl_sync(kAll, gk, __ffs(first) - 1);
-      const float v0 = value(k0), v1 = value(k1);
-      // Four scores are in it. With u = 2^-24, a sigmoid's is within 4 u (the
+      const int last = __ffs(__ballot_sync(kAll, lead && rank == a.topk_groups - 1)) - 1;
+      const int first = __ffs(__ballot_sync(kAll, lead && rank == a.topk_groups)) - 1;
+      const uint32_t k1 = __shfl_sync(kAll, gk, first);
+      const float v0 = value(__shfl_sync(kAll, gk, last)), v1 = value(k1);
+      // Four scores are in it. With u = 2^-24, a sigmoid's is within 5 u (the
       // exponential's error counts p (1 - p) times), a softmax's within 60 u; a
       // sum of two and their biases another 2 u of the sizes.
-      const float sizes = __shfl_sync(kAll, size, __ffs(last) - 1) + __shfl_sync(kAll, size, __ffs(first) - 1);
-      near = k1 && !(v0 - v1 > (a.sigmoid ? 1.2e-6f : 1.5e-5f) + 1.5e-7f * sizes);
+      const float sizes = __shfl_sync(kAll, size, last) + __shfl_sync(kAll, size, first);
+      near = k1 && !(v0 - v1 > (a.sigmoid ? 1.3e-6f : 1.5e-5f) + 1.5e-7f * sizes);
     }
-    const uint32_t leads = __ballot_sync(kAll, kept);  // bit g * lanes
     const uint32_t magic = per == 1 ? 0u : 0xFFFFFFFFu / per + 1;
+    int at = lane;  // expert of value j, by groups of whole values: 32 j
 #pragma unroll
     for (int j = 0; j < kVals; ++j) {
-      const uint32_t e = j * 32 + lane, g = per == 1 ? e : __umulhi(e, magic);  // e / per
-      if (e < static_cast<uint32_t>(E) && !((leads >> (g * lanes)) & 1u)) key[j] = 0u;
+      const uint32_t g = per == 1 ? at : __umulhi(static_cast<uint32_t>(at), magic);  // at / per
+      if (at < E && !((kept >> g) & 1u)) key[j] = 0u;
+      at += 32;
     }
   }
 
-  // The choices, and with a bias the one after them: lane c holds choice c.
+  // The choices: lane c holds choice c. With a bias also those after them, down to
+  // one that is clearly apart (by the largest tolerance that there is).
   int id = -1, found = 0;
   uint32_t mine = 0u;
-  const int want = a.top_k + (a.bias ? 1 : 0);
-  uint32_t best = 0u;
-  int at = 0;
-  auto look = [&] {
-    best = 0u;
+  const int want = a.bias ? 32 : a.top_k;
+  float before = 0.0f;
+  bool apart = false;
+  Best best;
 #pragma unroll
-    for (int j = 0; j < kVals; ++j)
-      if (key[j] > best) {
-        best = key[j];
-        at = j * 32 + lane;
-      }
-  };
-  look();
-  for (; found < want; ++found) {
-    const uint32_t k = __reduce_max_sync(kAll, best);
+  for (int j = 0; j < kVals; ++j) best.offer(key[j], j * 32 + lane);
+  bool whole = true;  // best.next is this lane's second
+  while (found < want && !apart) {
+    const uint32_t k = __reduce_max_sync(kAll, best.key);
     if (!k) break;
-    const uint32_t e = __reduce_min_sync(kAll, best == k ? static_cast<uint32_t>(at) : kAll);
+    const uint32_t who = __ballot_sync(kAll, best.key == k);
+    int e = __shfl_sync(kAll, best.at, __ffs(who) - 1);
+    if (who & (who - 1)) e = static_cast<int>(__reduce_min_sync(kAll, best.key == k ? static_cast<uint32_t>(best.at) : kAll));
     if (lane == found) {
-      id = static_cast<int>(e);
+      id = e;
       mine = k;
     }
-    if ((e & 31u) == static_cast<uint32_t>(lane)) {
+    if (best.key == k && best.at == e) {
+      if (whole) {
+        best.key = best.next;
+        best.at = best.next_at;
+        whole = false;
+      } else {  // look for the two best below this one
+        Best b;
 #pragma unroll
-      for (int j = 0; j < kVals; ++j)
-        if (j == static_cast<int>(e >> 5)) key[j] = 0u;
-      look();
+        for (int j = 0; j < kVals; ++j) {
+          const int o = j * 32 + lane;
+          b.offer(key[j] < k || (key[j] == k && o > e) ? key[j] : 0u, o);
+        }
+        best = b;
+        whole = true;
+      }
     }
+    if (a.bias) {
+      const float v = value(k);
+      apart = found >= a.top_k &&
+              before - v > 7.5e-8f * ((a.sigmoid ? 16.0f : 102.0f) + fabsf(before) + fabsf(v));
+      before = v;
+    }
+    ++found;
   }
   const float chosen = id >= 0 ? route_logit(a, base + id) : 0.0f;
   float w = id >= 0 ? score(chosen) : 0.0f;
@@ -503,16 +587,42 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(RouteArgs a) {
     const float v1 = __shfl_down_sync(kAll, v, 1), w1 = __shfl_down_sync(kAll, w, 1);
     const float c1 = __shfl_down_sync(kAll, chosen, 1), b1 = __shfl_down_sync(kAll, b, 1);
     // Rounding errors in units of 2^-24: of p, the exponential's 4 + 2.4 times its
-    // argument (in a sigmoid (1 - p) times that, and two more), and 45 of softmax's
-    // sum; one of p + bias.
+    // argument (in a sigmoid (1 - p) times that, and three more), and 45 of
+    // softmax's sum; one of p + bias.
     auto error = [&](float p, float x, float v) {
-      const float grow = a.sigmoid ? 2.0f + (1.0f - p) * (4.0f + 2.4f * fabsf(x)) : 50.0f + 2.4f * (top - x);
+      const float grow = a.sigmoid ? 3.0f + (1.0f - p) * (4.0f + 2.4f * fabsf(x)) : 50.0f + 2.4f * (top - x);
       return p * grow + fabsf(v);
     };
     const float tol = 7.5e-8f * (error(w, chosen, v) + error(w1, c1, v1));
     const bool same = c1 == chosen && b1 == b;  // equal in any precision
-    near = near || (lane + 1 < found && !same && !(v - v1 > tol));
-    if (__any_sync(kAll, near)) {
+    const int count = apart ? found - 1 : found;  // all of them but the one apart
+    near = near || (found == 32 && !apart);
+    bool again = near || __any_sync(kAll, lane + 1 < count && !same && !(v - v1 > tol));
+    if (again && !near && a.sigmoid) {
+      // Nobody else can be among them: their values decide in pairs, a lane each.
+      Pair p = {-CUDART_INF_F, 0.0f};
+      if (lane < count) p = pair_biased(pair_sigmoid(chosen), b);
+      int rank = 0;
+      bool doubt = false;
+      for (int o = 0; o < count; ++o) {
+        const Pair q = {__shfl_sync(kAll, p.hi, o), __shfl_sync(kAll, p.lo, o)};
+        const float qc = __shfl_sync(kAll, chosen, o), qb = __shfl_sync(kAll, b, o), qw = __shfl_sync(kAll, w, o);
+        const int qid = __shfl_sync(kAll, id, o);
+        const bool equal = qc == chosen && qb == b;
+        rank += equal ? qid < id : above(q, p);
+        doubt = doubt || (!equal && close(above(q, p) ? q : p, above(q, p) ? p : q, w + qw, fabsf(p.hi) + fabsf(q.hi)));
+      }
+      if (!__any_sync(kAll, doubt && lane < count)) {
+        again = false;
+        int from = lane;
+        for (int o = 0; o < count; ++o)
+          if (__shfl_sync(kAll, rank, o) == lane) from = o;
+        id = __shfl_sync(kAll, id, from);
+        w = __shfl_sync(kAll, w, from);
+      }
+    }
+    if (lane >= a.top_k) id = -1;
+    if (again) {
       __syncwarp();
       float *parts = reinterpret_cast<float *>(scratch);
       if (!route_row_pairs(a, row, parts, parts + E)) {

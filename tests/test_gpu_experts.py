@@ -145,6 +145,26 @@ def test_route_order_of_neighbouring_logits(sk, base, score, groups, topk_groups
         check_route(sk, gpu(a, F32), 8, gpu(bias, F32), n_groups=groups, topk_groups=topk_groups, score=score)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_ties_at_the_last_choice(sk, score):
+    # the last choice ties with the next ones, and the one after those is above
+    # them by less than FP32 can tell
+    n, k = 64, 4
+    a = np.linspace(-3, -1, n).astype(np.float32)[None].repeat(6, 0)
+    a[:, 40:44] = 1.5
+    a[:, 50] = np.nextafter(np.float32(1.5), np.float32(2))   # the largest, by its index not
+    a[1, 3:7] = 1.5
+    a[2, 10] = np.nextafter(np.float32(1.5), np.float32(1))
+    a[3] = 1.5
+    a[3, 63] = np.nextafter(np.float32(1.5), np.float32(2))
+    a[4, :] = np.nextafter(np.float32(1.5), np.float32(1))
+    a[4, 20:60:2] = 1.5
+    a[5, ::3] = 1.5
+    for bias in (np.zeros(n), np.full(n, 100.0), np.full(n, -1e-3)):
+        check_route(sk, gpu(a, F32), k, gpu(bias, F32), score=score)
+        check_route(sk, gpu(a, F32), k, gpu(bias, F32), score=score, n_groups=4, topk_groups=2)
+
+
 def test_route_many_rows(sk):
     g = torch.Generator(device=DEV).manual_seed(3)
     logits = torch.randn(5000, 64, generator=g, device=DEV)
