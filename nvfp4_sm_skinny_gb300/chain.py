@@ -7,12 +7,20 @@ One layer, at M token rows (HIDDEN H = 8192, POOLED P = 4096):
     a, a_sf, z = nvfp4(rmsnorm(u @ W_p^T)) pooler     [4096, 8192]   (sk_gemm_rmsnorm_nvfp4)
     h_{l+1} = z @ W_u^T                   unpooler    [8192, 4096]   (sk_gemm_bf16)
 
-The routed experts between the pooler and the unpooler are outside this
-path, so the unpooler reads the expert input z in their place (the order of
+The routed experts stand between the pooler and the unpooler (the order of
 the pages: o_proj -> attention boundary -> pooler -> experts -> unpooler ->
-next boundary). This module only allocates buffers and calls the binding;
-every step runs in libsk's kernels. ``capture()`` records one pass into a
-CUDA graph (the calls allocate nothing and are capturable).
+next boundary). The pages leave them to another package, and by default so does
+the chain: the unpooler reads the expert input z in their place. With
+``experts`` = E > 0 each layer runs E routed experts in int8 on z:
+
+    logits  = z @ W_r^T                   router       [E, 4096]      (sk_gemm_bf16)
+    ids, g  = top_k of sigmoid(logits) + bias                         (sk_route)
+    zq, zs  = int8 codes of z's rows                                  (sk_int8_quantize)
+    e       = sum_j g_j W2(silu(W1 z) * W3 z)  [E, 2 I, 4096], [E, 4096, I] (sk_experts_int8)
+
+and the unpooler reads e. This module only allocates buffers and calls the
+binding; every step runs in libsk's kernels. ``capture()`` records one pass into
+a CUDA graph (the calls allocate nothing and are capturable).
 """
 from __future__ import annotations
 
@@ -49,8 +57,10 @@ class DecodeChain:
 
     def __init__(self, layers: int = 48, m: int = 16, device="cuda", eps: float = synth.EPS,
                  gain_center: float = synth.GAIN_CENTER, splits: int = 0,
-                 prefetch_next: bool = True):
+                 prefetch_next: bool = True, experts: int = 0, top_k: int = 8,
+                 inter: int = 1024):
         self.L, self.m, self.device = layers, m, torch.device(device)
+        self.experts, self.top_k, self.inter = experts, top_k, inter
         # each GEMM starts the next GEMM's first weight stages towards L2
         self.prefetch_next = prefetch_next
         self.eps, self.gc, self.splits = eps, gain_center, splits
@@ -78,12 +88,39 @@ class DecodeChain:
         self.ws_p = torch.zeros(layers, sk.gemm_rmsnorm_nvfp4_workspace(m, P), dtype=torch.uint8,
                                 device=dev)
 
+        if experts:
+            self._add_experts(bf)
+
+    def _add_experts(self, bf) -> None:
+        L, m, E, I, dev = self.L, self.m, self.experts, self.inter, self.device
+        self.w_r, self.bias, self.w13, self.s13, self.w2, self.s2 = ([] for _ in range(6))
+        for l in range(L):
+            self.w_r.append(synth.chain_weight(l, 7, (E, P), device=dev))
+            self.bias.append(synth.chain_weight(l, 8, (E,), std=0.05, device=dev).float())
+            for rows, k, role, codes, scales in ((2 * I, P, 9, self.w13, self.s13),
+                                                 (P, I, 10, self.w2, self.s2)):
+                w = synth.chain_weight(l, role, (E * rows, k), device=dev)
+                q, s = sk.int8_quantize(w)
+                codes.append(q.view(E, rows, k))
+                scales.append(s.view(E, rows))
+        self.logits = torch.zeros(L, m, E, **bf)
+        self.ids = torch.zeros(L, m, self.top_k, dtype=torch.int32, device=dev)
+        self.gates = torch.zeros(L, m, self.top_k, dtype=torch.float32, device=dev)
+        self.zq = torch.zeros(L, m, P, dtype=torch.int8, device=dev)
+        self.zs = torch.zeros(L, m, dtype=torch.float32, device=dev)
+        self.e = torch.zeros(L, m, P, **bf)                    # routed experts' outputs
+        self.ws_e = torch.zeros(sk.experts_int8_workspace(m, self.top_k, P, I), dtype=torch.uint8,
+                                device=dev)
+
     def twin(self) -> "DecodeChain":
         """A chain on the same weights and global scales with its own
         activation buffers and workspaces, so that two steps can be in flight
         (one copying its inputs in or results out while the other runs)."""
         t = copy.copy(self)
-        for name in ("h", "s", "u", "z", "a", "a_sf", "ws_o", "ws_p"):
+        names = ("h", "s", "u", "z", "a", "a_sf", "ws_o", "ws_p")
+        if self.experts:
+            names += ("logits", "ids", "gates", "zq", "zs", "e", "ws_e")
+        for name in names:
             setattr(t, name, torch.zeros_like(getattr(self, name)))
         return t
 
@@ -104,15 +141,25 @@ class DecodeChain:
                                   self.gs[l], a=self.a[l], a_sf=self.a_sf[l], z_out=self.z[l],
                                   workspace=self.ws_p[l], splits=self.splits, stream=stream)
         else:
-            sk.gemm_bf16(self.z[l], self.w_u[l], out=self.h[l + 1], splits=self.splits,
-                         stream=stream)
+            x = self.e[l] if self.experts else self.z[l]
+            sk.gemm_bf16(x, self.w_u[l], out=self.h[l + 1], splits=self.splits, stream=stream)
+
+    def routed(self, l: int, stream=None) -> None:
+        """The routed experts of layer l: z[l] to e[l] (a chain with experts)."""
+        sk.gemm_bf16(self.z[l], self.w_r[l], out=self.logits[l], stream=stream)
+        sk.route(self.logits[l], self.top_k, bias=self.bias[l], score="sigmoid", ids=self.ids[l],
+                 weights=self.gates[l], stream=stream)
+        sk.int8_quantize(self.z[l], q=self.zq[l], scale=self.zs[l], stream=stream)
+        sk.experts_int8(self.zq[l], self.zs[l], self.w13[l], self.s13[l], self.w2[l], self.s2[l],
+                        self.ids[l], self.gates[l], out=self.e[l], workspace=self.ws_e,
+                        stream=stream)
 
     def next_weight(self, l: int, op: int):
         """The weight of the GEMM after layer l's call `op` (None after the last)."""
         if op == 0:
             return self.w_p[l]
         if op == 1:
-            return self.w_u[l]
+            return self.w_r[l] if self.experts else self.w_u[l]
         return self.w_o[l + 1] if l + 1 < self.L else None
 
     def layer(self, l: int, stream=None) -> None:
@@ -120,6 +167,8 @@ class DecodeChain:
             if self.prefetch_next:
                 sk.gemm_prefetch_next(self.next_weight(l, op))
             self.layer_op(l, op, stream)
+            if op == 1 and self.experts:
+                self.routed(l, stream)
 
     def forward(self, stream=None) -> None:
         for l in range(self.L):
@@ -165,5 +214,5 @@ class DecodeChain:
         torch.cuda.synchronize(self.device)
         return g
 
-    launches_per_layer = 5
+    launches_per_layer = 5          # without experts, which add 7
     gemm_launches_per_layer = 3

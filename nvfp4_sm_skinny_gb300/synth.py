@@ -100,7 +100,8 @@ def chain_weight(layer: int, role: int, shape, std: float = 0.02, mean: float = 
     """Per-layer weight of the 48-layer decode chain, drawn on ``device``.
     Roles: 0 o_proj [8192, 8192], 1 pooler [4096, 8192], 2 unpooler
     [8192, 4096], 3 post-norm weight, 4 pre-norm weight, 5 beta, 6 pooler norm
-    weight."""
+    weight; with routed experts 7 router, 8 router bias, 9 gate and up rows, 10
+    down rows (BF16, quantized to int8 by the chain)."""
     seed = 10000 + 16 * layer + role
     return normal_bf16(shape, std, seed, mean=mean, device=device)
 
