@@ -444,10 +444,12 @@ def route(logits, top_k: int, bias=None, n_groups: int = 1, topk_groups: int = 1
         _want(bias, torch.float32, (n,), "bias")
     if ids is None:
         ids = _new((m, top_k), torch.int32, logits.device, stream)
+    else:
+        _want(ids, torch.int32, (m, top_k), "ids")
     if weights is None:
         weights = _new((m, top_k), torch.float32, logits.device, stream)
-    _want(ids, torch.int32, (m, top_k), "ids")
-    _want(weights, torch.float32, (m, top_k), "weights")
+    else:
+        _want(weights, torch.float32, (m, top_k), "weights")
     s = _launch_on(stream, logits.get_device(), bias, ids, weights)
     _check(lib().sk_route(logits.data_ptr(), 0 if bf16 else 1,
                           None if bias is None else bias.data_ptr(), ids.data_ptr(),
@@ -463,10 +465,12 @@ def int8_quantize(z, q=None, scale=None, stream=None):
     _want(z, torch.bfloat16, (m, n), "z")
     if q is None:
         q = _new((m, n), torch.int8, z.device, stream)
+    else:
+        _want(q, torch.int8, (m, n), "q")
     if scale is None:
         scale = _new((m,), torch.float32, z.device, stream)
-    _want(q, torch.int8, (m, n), "q")
-    _want(scale, torch.float32, (m,), "scale")
+    else:
+        _want(scale, torch.float32, (m,), "scale")
     s = _launch_on(stream, z.get_device(), q, scale)
     _check(lib().sk_int8_quantize(z.data_ptr(), q.data_ptr(), scale.data_ptr(), m, n, s))
     return q, scale
@@ -489,7 +493,8 @@ def gemm_int8(xq, x_scale, wq, w_scale, out=None, splits: int = 0, stream=None):
     _want(w_scale, torch.float32, (n,), "w_scale")
     if out is None:
         out = _new((m, n), torch.bfloat16, xq.device, stream)
-    _want(out, torch.bfloat16, (m, n), "out")
+    else:
+        _want(out, torch.bfloat16, (m, n), "out")
     s = _launch_on(stream, xq.get_device(), x_scale, wq, w_scale, out)
     _check(lib().sk_gemm_int8(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(),
                               out.data_ptr(), m, n, k, splits, s))
@@ -521,11 +526,13 @@ def experts_int8(xq, x_scale, w13, s13, w2, s2, ids, weights, out=None, workspac
     _want(weights, torch.float32, (m, top_k), "weights")
     if out is None:
         out = _new((m, hidden), torch.bfloat16, xq.device, stream)
-    _want(out, torch.bfloat16, (m, hidden), "out")
+    else:
+        _want(out, torch.bfloat16, (m, hidden), "out")
     if workspace is None:
         workspace = _new((experts_int8_workspace(m, top_k, hidden, inter),), torch.uint8, xq.device,
                          stream)
-    _want(workspace, torch.uint8, (workspace.numel(),), "workspace")
+    else:
+        _want(workspace, torch.uint8, (workspace.numel(),), "workspace")
     s = _launch_on(stream, xq.get_device(), x_scale, w13, s13, w2, s2, ids, weights, out, workspace)
     _check(lib().sk_experts_int8(
         xq.data_ptr(), x_scale.data_ptr(), w13.data_ptr(), s13.data_ptr(), w2.data_ptr(),
