@@ -63,6 +63,34 @@ __device__ __forceinline__ float route_logit(const RouteArgs &a, size_t at) {
   return isnan(x) ? -CUDART_INF_F : x + 0.0f;  // -0 becomes 0
 }
 
+// The last step of a row: lane c holds choice c (id -1: none), its logit x and its
+// score p. Renormalized weights are ratios of scores, which FP32 would lose where
+// all of them are tiny (the likely experts masked by the bias, far negative logits):
+// those of a softmax, and of sigmoids so small that they are exp(x), are ratios of
+// exp(x - the largest chosen x). `top`: the logit that scores refer to (0: sigmoid);
+// a score is 0 where FP64's is.
+__device__ __forceinline__ void route_store(const RouteArgs &a, int row, int id, float x, float p, float top) {
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
+  const int lane = threadIdx.x & 31;
+  const bool mine = lane < a.top_k && id >= 0;
+  float w = mine ? p : 0.0f;
+  if (a.renormalize) {
+    float most = mine ? x : -CUDART_INF_F;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, d));
+    if (!a.sigmoid || most < -60.0f)
+      w = !mine || (most != top && most - top < -745.0f) ? 0.0f : __expf(x == most ? 0.0f : x - most);
+    float total = w;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(kAll, total, d);
+    w = total > 0.0f ? w / total : 0.0f;
+  }
+  if (lane < a.top_k) {
+    a.ids[static_cast<size_t>(row) * a.top_k + lane] = id;
+    a.weights[static_cast<size_t>(row) * a.top_k + lane] = w * a.scale;
+  }
+}
+
 // Largest value of the warp's lanes and, among equals, the lowest index; lanes
 // without a candidate give -inf and index INT_MAX.
 __device__ __forceinline__ void warp_best(double &v, int &at) {
@@ -350,14 +378,7 @@ __device__ __noinline__ bool route_row_pairs(const RouteArgs &a, int row, float 
   if (__any_sync(kAll, lane + 1 < count && !(x1 == x && b1 == b) &&
                            close(mine, v1, p.hi + p1, fabsf(mine.hi) + fabsf(v1.hi))))
     return false;
-  if (lane >= a.top_k) id = -1;
-  float w = lane < a.top_k ? p.hi : 0.0f, total = w;
-  for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(kAll, total, d);
-  if (a.renormalize) w = total > 0.0f ? w / total : 0.0f;
-  if (lane < a.top_k) {
-    a.ids[static_cast<size_t>(row) * a.top_k + lane] = id;
-    a.weights[static_cast<size_t>(row) * a.top_k + lane] = w * a.scale;
-  }
+  route_store(a, row, id, x, p.hi, a.sigmoid ? 0.0f : top);
   return true;
 }
 
@@ -395,8 +416,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.x * kRouteWarps + warp;
-  if (row >= a.m) return;
+  const unsigned row = blockIdx.x * kRouteWarps + warp;
+  if (row >= static_cast<unsigned>(a.m)) return;
   const int E = a.n_experts;
   const size_t base = static_cast<size_t>(row) * E;
   double *scratch = route_smem + warp * E;
@@ -580,7 +601,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
     }
     ++found;
   }
-  const float chosen = id >= 0 ? route_logit(a, base + id) : 0.0f;
+  float chosen = id >= 0 ? route_logit(a, base + id) : 0.0f;
   float w = id >= 0 ? score(chosen) : 0.0f;
   if (a.bias) {
     const float b = id >= 0 ? a.bias[id] : 0.0f, v = value(mine);
@@ -619,9 +640,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
           if (__shfl_sync(kAll, rank, o) == lane) from = o;
         id = __shfl_sync(kAll, id, from);
         w = __shfl_sync(kAll, w, from);
+        chosen = __shfl_sync(kAll, chosen, from);
       }
     }
-    if (lane >= a.top_k) id = -1;
     if (again) {
       __syncwarp();
       float *parts = reinterpret_cast<float *>(scratch);
@@ -632,15 +653,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
       return;
     }
   }
-  if (lane >= a.top_k) w = 0.0f;
-  float total = w;
-#pragma unroll
-  for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(kAll, total, d);
-  if (a.renormalize) w = total > 0.0f ? w / total : 0.0f;
-  if (lane < a.top_k) {
-    a.ids[static_cast<size_t>(row) * a.top_k + lane] = id;
-    a.weights[static_cast<size_t>(row) * a.top_k + lane] = w * a.scale;
-  }
+  route_store(a, row, id, chosen, w, a.sigmoid ? 0.0f : top);
 }
 
 // ------------------------------------------------------------- quantization
@@ -749,11 +762,11 @@ __global__ void __launch_bounds__(kQuantThreads, 10)
     quantize_kernel(const T *z, int8_t *q, float *scale, int rows, int n, const int32_t *ids, int n_experts) {
   constexpr int kVals = Chunk<T>::kVals, kThreads = 32 * W;
   if (ids) griddep_launch_dependents();
-  const int row = blockIdx.x * (kQuantThreads / kThreads) + threadIdx.x / kThreads;
+  const unsigned row = blockIdx.x * (kQuantThreads / kThreads) + threadIdx.x / kThreads;
   const int tid = threadIdx.x % kThreads, chunks = n / kVals;
   // (all the warps of a row, and with W = 4 all of the CTA, agree; the kernel
   // ahead started after the one that wrote the ids was done)
-  const bool done = row >= rows || (ids && static_cast<unsigned>(load_id(ids + row)) >= static_cast<unsigned>(n_experts));
+  const bool done = row >= static_cast<unsigned>(rows) || (ids && static_cast<unsigned>(load_id(ids + row)) >= static_cast<unsigned>(n_experts));
   griddep_wait();
   if (!done) {
     const uint4 *from = reinterpret_cast<const uint4 *>(z + static_cast<size_t>(row) * n);
@@ -799,7 +812,7 @@ cudaError_t launch_quantize(const T *z, int8_t *q, float *scale, int rows, int n
                : thread <= 4 ? quantize_kernel<T, 4, 4> : thread <= 8 ? quantize_kernel<T, 8, 4>
                : quantize_kernel<T, 0, 4>;
   const int per_cta = lane <= 4 ? 4 : 1;
-  return launch(kernel, dim3((rows + per_cta - 1) / per_cta), dim3(kQuantThreads), 0, stream, pdl, 1, z, q, scale,
+  return launch(kernel, dim3((static_cast<unsigned>(rows) + per_cta - 1) / per_cta), dim3(kQuantThreads), 0, stream, pdl, 1, z, q, scale,
                 rows, n, ids, n_experts);
 }
 
@@ -1025,12 +1038,13 @@ __global__ void __launch_bounds__(kCoreThreads, 2) gemm_int8_kernel(Int8GemmArgs
   const uint32_t queue = smem_u32(sh.queue) + warp * (Q::kDepth * Q::kPieces * 512) + lane * 16;
   const uint64_t policy = l2_policy_evict_first();
   const int8_t *wp[2][2], *xp[NT];
+  const int from = col < k1 ? col : 0;  // a thread without columns copies zeros, but names an address all the same
 #pragma unroll
   for (int h = 0; h < 4; ++h)  // rows past n repeat the last one; their sums are not stored
-    wp[h >> 1][h & 1] = a.wq + static_cast<size_t>(min(n0 + h * 8 + g, a.n - 1)) * a.k + col;
+    wp[h >> 1][h & 1] = a.wq + static_cast<size_t>(min(n0 + h * 8 + g, a.n - 1)) * a.k + from;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
-    xp[nt] = a.xq + static_cast<size_t>(min(nt * 8 + g, a.m - 1)) * a.k + col;
+    xp[nt] = a.xq + static_cast<size_t>(min(nt * 8 + g, a.m - 1)) * a.k + from;
   auto copy_weights = [&](int i, int slot) {
     const bool real = i < blocks && col + i * kWarps * kBlockCols < k1;
     const int off = real ? i * kWarps * kBlockCols : 0;
@@ -1267,6 +1281,7 @@ __global__ void __launch_bounds__(kCoreThreads, 2) experts_kernel(ExpertsArgs a)
   const uint64_t policy = l2_policy_evict_first();
 
   // What is copied next: block fb of item fi, from these rows.
+  const int from = col < K ? col : 0;  // a thread without columns copies zeros, but names an address all the same
   int fi = blockIdx.x, fb = 0, count = 0;
   const int8_t *wp[2][2], *xp[NT];
   auto open = [&] {
@@ -1277,12 +1292,12 @@ __global__ void __launch_bounds__(kCoreThreads, 2) experts_kernel(ExpertsArgs a)
     for (int h = 0; h < 4; ++h) {  // rows past N repeat the last one; their sums are not stored
       const size_t row = kUp ? (static_cast<size_t>(e) * 2 + (h >> 1)) * N + min(n0 + (h & 1) * 8 + g, N - 1)
                              : static_cast<size_t>(e) * N + min(n0 + h * 8 + g, N - 1);
-      wp[h >> 1][h & 1] = (kUp ? a.w13 : a.w2) + row * K + col;
+      wp[h >> 1][h & 1] = (kUp ? a.w13 : a.w2) + row * K + from;
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int row = q.rows[q.offset[e] + min(nt * 8 + g, count - 1)];
-      xp[nt] = kUp ? a.xq + static_cast<size_t>(row / a.top_k) * K + col : a.hq + static_cast<size_t>(row) * K + col;
+      xp[nt] = kUp ? a.xq + static_cast<size_t>(row / a.top_k) * K + from : a.hq + static_cast<size_t>(row) * K + from;
     }
   };
   auto copy_weights = [&](int slot) {
@@ -1442,7 +1457,7 @@ cudaError_t launch_route(const RouteArgs &a, cudaStream_t stream, bool pdl) {
   const int per = (a.n_experts + 31) / 32;
   auto *kernel = per <= 1 ? route_kernel<1> : per <= 2 ? route_kernel<2> : per <= 4 ? route_kernel<4>
                : per <= 8 ? route_kernel<8> : per <= 16 ? route_kernel<16> : route_kernel<32>;
-  return launch(kernel, dim3((a.m + kRouteWarps - 1) / kRouteWarps), dim3(32 * kRouteWarps),
+  return launch(kernel, dim3((static_cast<unsigned>(a.m) + kRouteWarps - 1) / kRouteWarps), dim3(32 * kRouteWarps),
                 static_cast<size_t>(kRouteWarps) * a.n_experts * sizeof(double), stream, pdl, 1, a);
 }
 

@@ -145,6 +145,35 @@ def test_route_order_of_neighbouring_logits(sk, base, score, groups, topk_groups
         check_route(sk, gpu(a, F32), 8, gpu(bias, F32), n_groups=groups, topk_groups=topk_groups, score=score)
 
 
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("groups,topk_groups", [(1, 1), (4, 2)])
+def test_route_weights_of_tiny_scores(sk, with_bias, groups, topk_groups):
+    # renormalized weights are ratios, however small the scores are: below FP32's
+    # smallest values they still add up to one
+    rng = np.random.default_rng(19)
+    a = rng.normal(size=(12, 32)).astype(np.float32)
+    a -= np.array([0, 30, 59, 61, 85, 88, 90, 100, 104, 200, 500, 650], np.float32)[:, None]
+    bias = gpu(rng.normal(0, 0.05, 32), F32) if with_bias else None
+    # ratios of exp(x - the largest chosen): exponents of at most 8
+    kw = dict(n_groups=groups, topk_groups=topk_groups, score="sigmoid")
+    ids, w = sk.route(gpu(a, F32), 4, bias=bias, **kw)
+    rids, rw = ox.route(a, 4, bias=None if bias is None else host(bias), **kw)
+    assert np.array_equal(host(ids), rids)
+    assert np.all(np.abs(host(w) - rw) <= rw * (2 * np.minimum(np.abs(a).max(1, keepdims=True), 60 + 8) + 96) * ox.U)
+    # softmax with its likeliest experts masked by the bias
+    a = rng.normal(size=(8, 32)).astype(np.float32)
+    a[:, 5], a[:, 20] = np.array([0, 10, 60, 90, 120, 300, 650, 1e30]), 90.0
+    b = np.zeros(32)
+    b[[5, 20]] = -np.inf
+    kw["score"] = "softmax"
+    ids, w = sk.route(gpu(a, F32), 4, bias=gpu(b, F32), **kw)
+    rids, rw = ox.route(a, 4, bias=b.astype(np.float32), **kw)
+    # where scores are nothing in 64 bits either, the order is the index's, the weights 0
+    assert np.array_equal(host(ids), rids)
+    assert np.all(np.abs(host(w) - rw) <= rw * (2 * 8 + 96) * ox.U)
+    assert not host(w)[-1].any() and np.all(np.abs(host(w)[:-1].sum(1) - 1) < 1e-6)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route_ties_at_the_last_choice(sk, score):
     # the last choice ties with the next ones, and the one after those is above
