@@ -408,9 +408,10 @@ def _launch_on(stream, dev: int, *tensors):
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"tensors on {t.device} and cuda:{dev}: needs all of them on one device")
-    if dev != torch._C._cuda_getDevice() or (stream is not None and stream.device.index != dev):
+    current = torch._C._cuda_getDevice()
+    if dev != current or (stream is not None and stream.device.index != dev):
         raise ValueError(f"tensors on cuda:{dev}: needs that device to be the current one "
-                         f"(cuda:{torch.cuda.current_device()}) and the stream's")
+                         f"(cuda:{current}) and the stream's")
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 

@@ -541,8 +541,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
       const uint32_t k1 = __shfl_sync(kAll, gk, first);
       const float v0 = value(__shfl_sync(kAll, gk, last)), v1 = value(k1);
       // Four scores are in it. With u = 2^-24, a sigmoid's is within 5 u (the
-      // exponential's error counts p (1 - p) times), a softmax's within 60 u; a
-      // sum of two and their biases another 2 u of the sizes.
+      // exponential's error counts p (1 - p) times), all softmax's together within
+      // 75 u; a sum of two and their biases another 2 u of the sizes.
       const float sizes = __shfl_sync(kAll, size, last) + __shfl_sync(kAll, size, first);
       near = k1 && !(v0 - v1 > (a.sigmoid ? 1.3e-6f : 1.5e-5f) + 1.5e-7f * sizes);
     }
@@ -608,10 +608,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
     const float v1 = __shfl_down_sync(kAll, v, 1), w1 = __shfl_down_sync(kAll, w, 1);
     const float c1 = __shfl_down_sync(kAll, chosen, 1), b1 = __shfl_down_sync(kAll, b, 1);
     // Rounding errors in units of 2^-24: of p, the exponential's 4 + 2.4 times its
-    // argument (in a sigmoid (1 - p) times that, and three more), and 45 of
-    // softmax's sum; one of p + bias.
+    // argument (in a sigmoid (1 - p) times that, and three more), and 64 of
+    // softmax's sum (37 of adding, and its terms' own, whose arguments average at
+    // most ln 1024); one of p + bias.
     auto error = [&](float p, float x, float v) {
-      const float grow = a.sigmoid ? 3.0f + (1.0f - p) * (4.0f + 2.4f * fabsf(x)) : 50.0f + 2.4f * (top - x);
+      const float grow = a.sigmoid ? 3.0f + (1.0f - p) * (4.0f + 2.4f * fabsf(x)) : 70.0f + 2.4f * (top - x);
       return p * grow + fabsf(v);
     };
     const float tol = 7.5e-8f * (error(w, chosen, v) + error(w1, c1, v1));

@@ -119,3 +119,29 @@ def test_binding_refuses_other_tensors(sk):
     with pytest.raises(ValueError, match="xq"):
         sk.experts_int8(t(2, 32, dtype=f), t(2, dtype=f), t(4, 32, 32), t(4, 32, dtype=f), t(4, 32, 16),
                         t(4, 32, dtype=f), t(2, 2, dtype=torch.int32), t(2, 2, dtype=f))
+
+
+def test_binding_refuses_other_devices(sk, monkeypatch):
+    class Tensor:
+        def __init__(self, dev):
+            self.dev, self.device = dev, f"cuda:{dev}"
+
+        def get_device(self):
+            return self.dev
+
+    class Stream:
+        cuda_stream = 5
+
+        def __init__(self, dev):
+            self.device = torch.device("cuda", dev)
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 7, raising=False)
+    assert sk._launch_on(None, 0, Tensor(0), None) == 7
+    assert sk._launch_on(Stream(0), 0, Tensor(0)) == 5
+    with pytest.raises(ValueError, match="one device"):
+        sk._launch_on(None, 0, Tensor(0), Tensor(1))
+    with pytest.raises(ValueError, match="current"):
+        sk._launch_on(None, 1, Tensor(1))
+    with pytest.raises(ValueError, match="current"):
+        sk._launch_on(Stream(1), 0, Tensor(0))

@@ -378,7 +378,8 @@ def check_experts(sk, c):
 @pytest.mark.parametrize("m,experts,k,hidden,inter", [
     (1, 1, 1, 16, 16), (1, 8, 2, 64, 32), (2, 16, 4, 528, 272), (16, 8, 2, 256, 128),
     (16, 4, 4, 1040, 80), (7, 60, 4, 1040, 528), (5, 40, 16, 128, 48), (16, 32, 8, 512, 1040),
-    (3, 1024, 8, 32, 16), (9, 3, 1, 2064, 560),
+    (3, 1024, 8, 32, 16), (9, 3, 1, 2064, 560), (16, 24, 16, 64, 48), (16, 1024, 16, 32, 16),
+    (2, 2, 1, 131056, 16), (1, 2, 2, 16, 131056),
 ])
 def test_experts(sk, m, experts, k, hidden, inter):
     k = min(k, experts)
@@ -541,3 +542,36 @@ def test_offsets_beyond_31_bits(sk):
     ref, bound = ox.experts_int8(host(xq), host(xs), one(w13), one(s13), one(w2), one(s2),
                                  np.zeros((m, 1), np.int32), host(gw))
     assert np.all(np.abs(host(y) - ref) <= bound)
+
+
+def test_large_offsets_of_routing_and_quantization(sk):
+    g = torch.Generator(device=DEV).manual_seed(9)
+    m, n = 16400, 131056
+    z = torch.zeros(m, n, dtype=BF16, device=DEV)
+    z[-3:] = torch.randn(3, n, generator=g, device=DEV).to(BF16)
+    assert z.numel() > 2 ** 31
+    q, scale = sk.int8_quantize(z)
+    rq, rs = ox.int8_quantize(host(z[-3:]))
+    assert np.array_equal(host(q[-3:]), rq) and not host(scale[:-3]).any()
+    del z, q
+    m, n = 2 ** 21 + 5, 1024
+    a = torch.zeros(m, n, dtype=BF16, device=DEV)
+    a[-4:] = torch.randn(4, n, generator=g, device=DEV).to(BF16)
+    assert a.numel() > 2 ** 31
+    ids, w = sk.route(a, 3)
+    rids, rw = ox.route(host(a[-4:]), 3)
+    assert np.array_equal(host(ids[-4:]), rids)
+    assert torch.equal(ids[:-4], torch.arange(3, dtype=I32, device=DEV).expand(m - 4, 3))
+
+
+def test_gemm_offsets_beyond_31_bits(sk):
+    g = torch.Generator(device=DEV).manual_seed(10)
+    m, n, k = 3, 16400, 131056
+    wq = torch.zeros(n, k, dtype=I8, device=DEV)
+    wq[-40:] = torch.randint(-128, 128, (40, k), generator=g, device=DEV, dtype=I8)
+    xq = torch.randint(-128, 128, (m, k), generator=g, device=DEV, dtype=I8)
+    assert wq.numel() > 2 ** 31
+    xs, ws = torch.full((m,), 0.01, device=DEV), torch.full((n,), 0.01, device=DEV)
+    y = host(sk.gemm_int8(xq, xs, wq, ws))
+    ref = ox.gemm_int8(host(xq), host(xs), host(wq[-40:]), host(ws[-40:]))
+    assert np.all(np.abs(y[:, -40:] - ref) <= ox.gemm_int8_bound(ref)) and not y[:, :-40].any()
