@@ -75,14 +75,15 @@ __device__ __forceinline__ void route_store(const RouteArgs &a, int row, int id,
   const bool mine = lane < a.top_k && id >= 0;
   float w = mine ? p : 0.0f;
   if (a.renormalize) {
-    float most = mine ? x : -CUDART_INF_F;
+    if (!a.sigmoid || !__any_sync(kAll, mine && x >= -60.0f)) {
+      float most = mine ? x : -CUDART_INF_F;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, d));
-    if (!a.sigmoid || most < -60.0f)
+      for (int d = SK_MAX_TOP_K / 2; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, d));
       w = !mine || (most != top && most - top < -745.0f) ? 0.0f : __expf(x == most ? 0.0f : x - most);
-    float total = w;
+    }
+    float total = w;  // of the first lanes, which hold the choices
 #pragma unroll
-    for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(kAll, total, d);
+    for (int d = SK_MAX_TOP_K / 2; d; d >>= 1) total += __shfl_xor_sync(kAll, total, d);
     w = total > 0.0f ? w / total : 0.0f;
   }
   if (lane < a.top_k) {
@@ -527,32 +528,51 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
       size += fabsf(value(b1));
     }
     // (infinities of opposite signs never meet: -inf is no value)
-    const uint32_t gk = lane < a.n_groups ? order_key(gv) : 0u;
-    int rank = 0;
-    for (int o = 0; o < a.n_groups; ++o) {
-      const uint32_t ok = __shfl_sync(kAll, gk, o);
-      rank += ok > gk || (ok == gk && o < lane);
-    }
-    const bool lead = lane < a.n_groups;
-    const uint32_t kept = __ballot_sync(kAll, lead && gk && rank < a.topk_groups);
-    if (a.bias && a.topk_groups < a.n_groups) {
-      const int last = __ffs(__ballot_sync(kAll, lead && rank == a.topk_groups - 1)) - 1;
-      const int first = __ffs(__ballot_sync(kAll, lead && rank == a.topk_groups)) - 1;
-      const uint32_t k1 = __shfl_sync(kAll, gk, first);
-      const float v0 = value(__shfl_sync(kAll, gk, last)), v1 = value(k1);
-      // Four scores are in it. With u = 2^-24, a sigmoid's is within 5 u (the
-      // exponential's error counts p (1 - p) times), all softmax's together within
-      // 75 u; a sum of two and their biases another 2 u of the sizes.
-      const float sizes = __shfl_sync(kAll, size, last) + __shfl_sync(kAll, size, first);
-      near = k1 && !(v0 - v1 > (a.sigmoid ? 1.3e-6f : 1.5e-5f) + 1.5e-7f * sizes);
-    }
-    const uint32_t magic = per == 1 ? 0u : 0xFFFFFFFFu / per + 1;
-    int at = lane;  // expert of value j, by groups of whole values: 32 j
+    // The best groups one by one, and with a bias the first of the others.
+    uint32_t gk = lane < a.n_groups ? order_key(gv) : 0u, kept = 0u;
+    float last = 0.0f, last_size = 0.0f;
+    for (int o = 0; o < a.topk_groups; ++o) {
+      const uint32_t k = __reduce_max_sync(kAll, gk);
+      if (!k) break;
+      const int who = __ffs(__ballot_sync(kAll, gk == k)) - 1;
+      kept |= 1u << who;
+      if (lane == who) gk = 0u;
+      if (o == a.topk_groups - 1 && a.bias) {
+        last = value(k);
+        last_size = __shfl_sync(kAll, size, who);
+        const uint32_t next = __reduce_max_sync(kAll, gk);
+        if (next) {
+          // Four scores are in it. With u = 2^-24, a sigmoid's is within 5 u (the
+          // exponential's error counts p (1 - p) times), all softmax's together
+          // within 75 u; a sum of two and their biases another 2 u of the sizes,
+          // of which the largest of the others' stands for all.
+          float sizes = gk ? size : 0.0f;
 #pragma unroll
-    for (int j = 0; j < kVals; ++j) {
-      const uint32_t g = per == 1 ? at : __umulhi(static_cast<uint32_t>(at), magic);  // at / per
-      if (at < E && !((kept >> g) & 1u)) key[j] = 0u;
-      at += 32;
+          for (int d = 16; d; d >>= 1) sizes = fmaxf(sizes, __shfl_xor_sync(kAll, sizes, d));
+          near = !(last - value(next) > (a.sigmoid ? 1.3e-6f : 1.5e-5f) + 1.5e-7f * (sizes + last_size));
+        }
+      }
+    }
+    if (per % 32 == 0) {
+      int left = per, g = 0;
+#pragma unroll
+      for (int j = 0; j < kVals; ++j) {
+        if (!((kept >> g) & 1u)) key[j] = 0u;
+        left -= 32;
+        if (left == 0) {
+          left = per;
+          ++g;
+        }
+      }
+    } else {
+      const uint32_t magic = per == 1 ? 0u : 0xFFFFFFFFu / per + 1;
+      int at = lane;  // expert of value j
+#pragma unroll
+      for (int j = 0; j < kVals; ++j) {
+        const uint32_t g = per == 1 ? at : __umulhi(static_cast<uint32_t>(at), magic);  // at / per
+        if (at < E && !((kept >> g) & 1u)) key[j] = 0u;
+        at += 32;
+      }
     }
   }
 
