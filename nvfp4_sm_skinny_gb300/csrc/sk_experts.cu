@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
   if (row >= static_cast<unsigned>(a.m)) return;
   const int E = a.n_experts;
   const size_t base = static_cast<size_t>(row) * E;
-  double *scratch = route_smem + warp * E;
+  double *scratch = route_smem + warp * max(E, 16);
 
   float x[kVals];  // NaN where the logit is: no comparison below takes one
   if (a.fp32) {
@@ -578,8 +578,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
 
   // The choices: lane c holds choice c. With a bias also those after them, down to
   // one that is clearly apart (by the largest tolerance that there is).
-  int id = -1, found = 0;
-  uint32_t mine = 0u;
+  int *list = reinterpret_cast<int *>(scratch), found = 0;
   const int want = a.bias ? 32 : a.top_k;
   float before = 0.0f;
   bool apart = false;
@@ -587,31 +586,30 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
 #pragma unroll
   for (int j = 0; j < kVals; ++j) best.offer(key[j], j * 32 + lane);
   bool whole = true;  // best.next is this lane's second
+  __syncwarp();
   while (found < want && !apart) {
     const uint32_t k = __reduce_max_sync(kAll, best.key);
     if (!k) break;
-    const uint32_t who = __ballot_sync(kAll, best.key == k);
-    int e = __shfl_sync(kAll, best.at, __ffs(who) - 1);
-    if (who & (who - 1)) e = static_cast<int>(__reduce_min_sync(kAll, best.key == k ? static_cast<uint32_t>(best.at) : kAll));
-    if (lane == found) {
-      id = e;
-      mine = k;
+    bool win = best.key == k;
+    const uint32_t who = __ballot_sync(kAll, win);
+    if (who & (who - 1)) {
+      const uint32_t e = __reduce_min_sync(kAll, win ? static_cast<uint32_t>(best.at) : kAll);
+      win = win && best.at == static_cast<int>(e);
     }
-    if (best.key == k && best.at == e) {
-      if (whole) {
-        best.key = best.next;
-        best.at = best.next_at;
-        whole = false;
-      } else {  // look for the two best below this one
-        Best b;
+    if (win) list[found] = best.at;
+    if (win && !whole) {  // look for the two best below this one
+      const int e = best.at;
+      best = Best();
 #pragma unroll
-        for (int j = 0; j < kVals; ++j) {
-          const int o = j * 32 + lane;
-          b.offer(key[j] < k || (key[j] == k && o > e) ? key[j] : 0u, o);
-        }
-        best = b;
-        whole = true;
+      for (int j = 0; j < kVals; ++j) {
+        const int o = j * 32 + lane;
+        best.offer(key[j] < k || (key[j] == k && o > e) ? key[j] : 0u, o);
       }
+      whole = true;
+    } else {
+      best.key = win ? best.next : best.key;
+      best.at = win ? best.next_at : best.at;
+      whole = whole && !win;
     }
     if (a.bias) {
       const float v = value(k);
@@ -621,10 +619,12 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
     }
     ++found;
   }
+  __syncwarp();
+  int id = lane < found ? list[lane] : -1;
   float chosen = id >= 0 ? route_logit(a, base + id) : 0.0f;
   float w = id >= 0 ? score(chosen) : 0.0f;
   if (a.bias) {
-    const float b = id >= 0 ? a.bias[id] : 0.0f, v = value(mine);
+    const float b = id >= 0 ? a.bias[id] : 0.0f, v = w + b;
     const float v1 = __shfl_down_sync(kAll, v, 1), w1 = __shfl_down_sync(kAll, w, 1);
     const float c1 = __shfl_down_sync(kAll, chosen, 1), b1 = __shfl_down_sync(kAll, b, 1);
     // Rounding errors in units of 2^-24: of p, the exponential's 4 + 2.4 times its
@@ -1479,7 +1479,7 @@ cudaError_t launch_route(const RouteArgs &a, cudaStream_t stream, bool pdl) {
   auto *kernel = per <= 1 ? route_kernel<1> : per <= 2 ? route_kernel<2> : per <= 4 ? route_kernel<4>
                : per <= 8 ? route_kernel<8> : per <= 16 ? route_kernel<16> : route_kernel<32>;
   return launch(kernel, dim3((static_cast<unsigned>(a.m) + kRouteWarps - 1) / kRouteWarps), dim3(32 * kRouteWarps),
-                static_cast<size_t>(kRouteWarps) * a.n_experts * sizeof(double), stream, pdl, 1, a);
+                sizeof(double) * kRouteWarps * (a.n_experts > 16 ? a.n_experts : 16), stream, pdl, 1, a);
 }
 
 cudaError_t launch_int8_quantize(const uint16_t *z, int8_t *q, float *scale, int m, int n,
