@@ -702,18 +702,25 @@ __device__ __forceinline__ float row_max(uint32_t bits) {
 struct RowCodes {
   float amax, inv, f;
   bool plain;  // neither zero nor NaN
+  bool quick;  // 127 / amax is finite
   __device__ __forceinline__ explicit RowCodes(float row_max) {
     amax = row_max;
     inv = __fdiv_rn(127.0f, amax);
     f = amax >= 1.0f ? 0x1p-8f : 1.0f;
     plain = amax > 0.0f;
+    quick = inv < CUDART_INF_F;
   }
-  // The code in the low byte. Adding 1.5 2^23 rounds to an integer and leaves it,
-  // in two's complement, in the low bits; `off`: how far from the quotient it is.
-  __device__ __forceinline__ uint32_t quick(float v, float &off) const {
-    const float t = __fmul_rn(v, inv), b = __fadd_rn(t, 12582912.0f);
-    off = fabsf(__fsub_rn(t, __fsub_rn(b, 12582912.0f)));
-    return __float_as_uint(b);
+  // The codes of two values in their low bytes. Adding 1.5 2^23 rounds to an
+  // integer and leaves it, in two's complement, in the low bits; `far` grows to the
+  // largest distance from the quotient.
+  __device__ __forceinline__ void two(float2 v, uint32_t &c0, uint32_t &c1, float &far) const {
+    const float2 t = __fmul2_rn(v, make_float2(inv, inv));
+    const float2 b = __fadd2_rn(t, make_float2(12582912.0f, 12582912.0f));
+    const float2 r = __fadd2_rn(b, make_float2(-12582912.0f, -12582912.0f));
+    const float2 d = __ffma2_rn(r, make_float2(-1.0f, -1.0f), t);
+    far = fmaxf(fmaxf(far, fabsf(d.x)), fabsf(d.y));
+    c0 = __float_as_uint(b.x);
+    c1 = __float_as_uint(b.y);
   }
   __device__ __forceinline__ uint32_t slow(float v) const {
     return static_cast<uint32_t>(
@@ -748,13 +755,10 @@ struct Chunk {
   }
   __device__ __forceinline__ void store(int8_t *q, const RowCodes &code) const {
     uint32_t c[kVals];
-    float far = 0.0f, off;
+    float far = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kVals; ++i) {
-      c[i] = code.quick(value(i), off);
-      far = off <= 0.4999f ? far : 1.0f;  // (1 for NaN too)
-    }
-    if (far > 0.0f) {
+    for (int i = 0; i < kVals; i += 2) code.two(make_float2(value(i), value(i + 1)), c[i], c[i + 1], far);
+    if (!code.quick || far > 0.4999f) {
 #pragma unroll
       for (int i = 0; i < kVals; ++i) c[i] = code.plain ? code.slow(value(i)) : 0u;
     }
