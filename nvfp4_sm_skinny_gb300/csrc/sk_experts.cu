@@ -391,22 +391,17 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return b ^ (static_cast<int>(b) < 0 ? 0xFFFFFFFFu : 0x80000000u);
 }
 
-// The two largest of a lane's keys, and how many of them are still to be taken
-// (0: none is left, or the next one has to be looked for).
+// The two largest of a lane's keys and their experts (key 0: none).
 struct Best {
   uint32_t key, next;
   int at, next_at;
   __device__ __forceinline__ Best() : key(0u), next(0u), at(0), next_at(0) {}
   __device__ __forceinline__ void offer(uint32_t k, int e) {  // in ascending order of e
-    if (k > key) {
-      next = key;
-      next_at = at;
-      key = k;
-      at = e;
-    } else if (k > next) {
-      next = k;
-      next_at = e;
-    }
+    const bool first = k > key, second = k > next;
+    next_at = first ? at : second ? e : next_at;
+    next = max(next, min(key, k));
+    at = first ? e : at;
+    key = max(key, k);
   }
 };
 
