@@ -1017,6 +1017,47 @@ struct Sums {
   }
 };
 
+// The same for one or two tokens (C), without the tensor cores: four-way integer
+// products of the codes as they are, half the instructions of widening them. Every
+// lane needs the pieces of all token rows, which the lanes 4 c + t brought.
+template <int C>
+struct Dots {
+  static constexpr int kTokens = C;
+  int acc[4][C];
+
+  __device__ __forceinline__ Dots() {
+#pragma unroll
+    for (int i = 0; i < 4 * C; ++i) (&acc[0][0])[i] = 0;
+  }
+  __device__ __forceinline__ void add(const uint4 (&x)[C], const uint4 (&w)[2][2]) {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const uint4 &v = w[h >> 1][h & 1];
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        int s = acc[h][c];
+        s = __dp4a(static_cast<int>(v.x), static_cast<int>(x[c].x), s);
+        s = __dp4a(static_cast<int>(v.y), static_cast<int>(x[c].y), s);
+        s = __dp4a(static_cast<int>(v.z), static_cast<int>(x[c].z), s);
+        acc[h][c] = __dp4a(static_cast<int>(v.w), static_cast<int>(x[c].w), s);
+      }
+    }
+  }
+  // To red[token][row]; the tokens' own sums stay 0, as nothing is to be taken off.
+  __device__ __forceinline__ void finish(uint32_t red) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        int s = acc[h][c];
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
+        if (t == 0) red_shared(red + 4u * (c * kRedPitch + h * 8 + g), s);
+      }
+  }
+};
+
 // The sum of products of a token with a tile row: the correction of the weights'
 // offset by 128 (modulo 2^32).
 __device__ __forceinline__ int red_sum(const int *red, int token, int row) {
@@ -1405,7 +1446,32 @@ __global__ void __launch_bounds__(kCoreThreads, 2) experts_kernel(ExpertsArgs a)
       }
       sums.finish(smem_u32(red), tokens);
     };
-    if (NT == 2 && tokens > 8) stream(Sums<NT>());
+    auto stream_few = [&](auto dots) {
+      constexpr int C = decltype(dots)::kTokens;
+      for (int b = 0; b < blocks; ++b) {
+        copy_wait<Q::kDepth - 1>();
+        __syncwarp();
+        const uint32_t at = queue + slot * (Q::kPieces * 512);
+        uint4 w[2][2], x[C];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) w[h >> 1][h & 1] = lds128(at + h * 512);
+#pragma unroll
+        for (int c = 0; c < C; ++c) x[c] = lds128(at + 4 * 512 + (4 * c + t - lane) * 16);
+        __syncwarp();
+        if (fi < items) {
+          copy_weights(slot);
+          copy_tokens(slot);
+          next();
+        }
+        copy_commit();
+        slot = slot + 1 == Q::kDepth ? 0 : slot + 1;
+        dots.add(x, w);
+      }
+      dots.finish(smem_u32(red));
+    };
+    if (tokens == 1) stream_few(Dots<1>());
+    else if (tokens == 2) stream_few(Dots<2>());
+    else if (NT == 2 && tokens > 8) stream(Sums<NT>());
     else stream(Sums<1>());
     __syncthreads();
 #pragma unroll
