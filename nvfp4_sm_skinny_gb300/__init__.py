@@ -15,6 +15,7 @@ or ``python nvfp4_sm_skinny_gb300/build.py``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -506,6 +507,9 @@ def experts_int8_workspace(m: int, top_k: int, hidden: int, inter: int) -> int:
     return int(lib().sk_experts_int8_workspace(m, top_k, hidden, inter))
 
 
+_experts_workspace = functools.lru_cache(maxsize=256)(experts_int8_workspace)
+
+
 def experts_int8(xq, x_scale, w13, s13, w2, s2, ids, weights, out=None, workspace=None,
                  stream=None):
     """(out BF16 [m, hidden], workspace): the routed experts of each token,
@@ -530,8 +534,7 @@ def experts_int8(xq, x_scale, w13, s13, w2, s2, ids, weights, out=None, workspac
     else:
         _want(out, torch.bfloat16, (m, hidden), "out")
     if workspace is None:
-        workspace = _new((experts_int8_workspace(m, top_k, hidden, inter),), torch.uint8, xq.device,
-                         stream)
+        workspace = _new((_experts_workspace(m, top_k, hidden, inter),), torch.uint8, xq.device, stream)
     else:
         _want(workspace, torch.uint8, (workspace.numel(),), "workspace")
     s = _launch_on(stream, xq.get_device(), x_scale, w13, s13, w2, s2, ids, weights, out, workspace)
