@@ -289,6 +289,7 @@ __device__ __noinline__ bool route_row_pairs(const RouteArgs &a, int row, float 
   }
   auto score = [&](float x) { return a.sigmoid ? pair_sigmoid(x) : pair_power(false, x, top) / sum; };
   const Pair none = {-CUDART_INF_F, 0.0f};
+#pragma unroll 2
   for (int e = lane; e < E; e += 32) {
     const float x = route_logit(a, base + e), b = a.bias[e];
     Pair v = none;
@@ -304,7 +305,9 @@ __device__ __noinline__ bool route_row_pairs(const RouteArgs &a, int row, float 
     float size = 0.0f;
     if (lane < a.n_groups) {
       Pair b0 = none, b1 = none;
-      for (int j = 0; j < per; ++j) {
+      int j = lane % per;  // apart, so that groups do not meet in one bank
+#pragma unroll 4
+      for (int i = 0; i < per; ++i, j = j + 1 == per ? 0 : j + 1) {
         const Pair x = {hi[lane * per + j], lo[lane * per + j]};
         if (above(x, b0)) {
           b1 = b0;
@@ -334,6 +337,11 @@ __device__ __noinline__ bool route_row_pairs(const RouteArgs &a, int row, float 
     }
   }
 
+  if (a.n_groups > 1)
+    for (int e = lane; e < E; e += 32)
+      if (!((keep >> (e / per)) & 1u)) hi[e] = -CUDART_INF_F;
+  __syncwarp();
+
   // The choices and those after them, down to one that is clearly apart.
   int id = -1, found = 0;
   Pair mine = none, before = none;
@@ -341,14 +349,14 @@ __device__ __noinline__ bool route_row_pairs(const RouteArgs &a, int row, float 
   while (found < 32 && !apart) {
     Pair b = none;
     int at = INT_MAX;
-    for (int e = lane; e < E; e += 32)
-      if ((keep >> (a.n_groups > 1 ? e / per : 0)) & 1u) {
-        const Pair x = {hi[e], lo[e]};
-        if (above(x, b)) {
-          b = x;
-          at = e;
-        }
+#pragma unroll 4
+    for (int e = lane; e < E; e += 32) {
+      const Pair x = {hi[e], lo[e]};
+      if (above(x, b)) {
+        b = x;
+        at = e;
       }
+    }
 #pragma unroll
     for (int d = 16; d; d >>= 1) {
       const Pair o = {__shfl_xor_sync(kAll, b.hi, d), __shfl_xor_sync(kAll, b.lo, d)};
