@@ -388,8 +388,8 @@ sk_status sk_int8_quantize(const void *z, int8_t *q, float *scale, int m, int n,
  * with the sum exact in 32-bit integers (any codes, -128 included); the two
  * FP32 products follow in that order, then one rounding to BF16.
  *   xq int8 [m, k], x_scale FP32 [m], wq int8 [n, k], w_scale FP32 [n],
- *   y BF16 [m, n];  1 <= m <= 16, n >= 1, k % 16 == 0, 16 <= k <= 131056
- *   (a sum of k products of magnitude up to 2^14 fits 31 bits);
+ *   y BF16 [m, n];  1 <= m <= 16, 1 <= n <= 2^30, k % 16 == 0,
+ *   16 <= k <= 131056 (a sum of k products of magnitude up to 2^14 fits 31 bits);
  *   xq, wq, y 16-byte aligned, the scales 4-byte aligned.
  *   splits  0 (automatic), 1, 2, 4 or 8 slices of K. Results do not depend on
  *           it: integer sums have no order.

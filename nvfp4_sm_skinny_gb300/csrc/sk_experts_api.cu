@@ -11,6 +11,7 @@
 
 namespace {
 
+constexpr int kMaxInt8N = 1 << 30;    // row indices of whole tiles stay below 2^31
 constexpr int kMaxInt8K = 131056;  // the largest multiple of 16 with k * 2^14 < 2^31
 
 sk_status fail(sk_status st, const char *fmt, ...) {
@@ -60,7 +61,8 @@ sk_status check_rows(int m) {
 sk_status check_gemm(int m, int n, int k, int splits) {
   sk_status st;
   if ((st = check_rows(m)) != SK_OK) return st;
-  if (n < 1) return fail(SK_ERR_INVALID_ARG, "n=%d: needs n >= 1 output features", n);
+  if (n < 1 || n > kMaxInt8N)
+    return fail(SK_ERR_INVALID_ARG, "n=%d: needs 1 <= n <= %d output features", n, kMaxInt8N);
   if ((st = check_width("k", k)) != SK_OK) return st;
   if (splits != 0 && splits != 1 && splits != 2 && splits != 4 && splits != 8)
     return fail(SK_ERR_UNSUPPORTED, "unsupported split count %d (0, 1, 2, 4 or 8)", splits);

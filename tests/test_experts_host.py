@@ -52,7 +52,8 @@ GEMM = dict(xq=P, x_scale=P, wq=P, w_scale=P, y=P, m=1, n=128, k=256, splits=0, 
 
 
 @pytest.mark.parametrize("change,status,word", [
-    (dict(m=0), 1, "m=0"), (dict(m=17), 1, "m=17"), (dict(n=0), 1, "n=0"), (dict(k=0), 1, "k=0"),
+    (dict(m=0), 1, "m=0"), (dict(m=17), 1, "m=17"), (dict(n=0), 1, "n=0"),
+    (dict(n=2 ** 30 + 1), 1, "n=1073741825"), (dict(n=2 ** 31 - 1), 1, "n=2147483647"), (dict(k=0), 1, "k=0"),
     (dict(k=24), 1, "k=24"), (dict(k=131072), 1, "k=131072"), (dict(splits=3), 2, "split"),
     (dict(splits=16), 2, "split"), (dict(xq=None), 1, "xq"), (dict(wq=P + 8), 1, "wq"),
     (dict(y=P + 2), 1, "y "), (dict(x_scale=P + 2), 1, "x_scale"), (dict(w_scale=None), 1, "w_scale"),
