@@ -316,9 +316,11 @@ __device__ __noinline__ bool route_row_pairs(const RouteArgs &a, int row, float 
           b1 = x;
         }
       }
+      // half of the sum, as the whole may be beyond FP32
       const bool two = b1.hi > -CUDART_INF_F;
-      gv = !two ? b0 : fmaxf(b0.hi, b1.hi) < CUDART_INF_F ? b0 + b1 : Pair{CUDART_INF_F, 0.0f};
-      size = fabsf(b0.hi) + (two ? fabsf(b1.hi) : 0.0f);
+      const Pair h0 = {0.5f * b0.hi, 0.5f * b0.lo}, h1 = {0.5f * b1.hi, 0.5f * b1.lo};
+      gv = !two ? h0 : fmaxf(b0.hi, b1.hi) < CUDART_INF_F ? h0 + h1 : Pair{CUDART_INF_F, 0.0f};
+      size = fabsf(h0.hi) + (two ? fabsf(h1.hi) : 0.0f);
     }
     int rank = 0;
     for (int o = 0; o < a.n_groups; ++o) {
@@ -333,7 +335,7 @@ __device__ __noinline__ bool route_row_pairs(const RouteArgs &a, int row, float 
       const Pair v0 = {__shfl_sync(kAll, gv.hi, last), __shfl_sync(kAll, gv.lo, last)};
       const Pair v1 = {__shfl_sync(kAll, gv.hi, next), __shfl_sync(kAll, gv.lo, next)};
       const float sizes = __shfl_sync(kAll, size, last) + __shfl_sync(kAll, size, next);
-      if (v1.hi > -CUDART_INF_F && close(v0, v1, 4.0f, sizes)) return false;
+      if (v1.hi > -CUDART_INF_F && close(v0, v1, 2.0f, sizes)) return false;  // halves of four scores
     }
   }
 
@@ -525,10 +527,12 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
       b0 = __shfl_sync(kAll, b0, lane * lanes);
       b1 = __shfl_sync(kAll, b1, lane * lanes);
     }
-    float gv = value(b0), size = fabsf(gv);
+    // With a bias half of the sum, as the whole may be beyond FP32 (two biases of its
+    // lowest value, as a mask).
+    float gv = a.bias ? 0.5f * value(b0) : value(b0), size = fabsf(gv);
     if (a.bias && b1) {
-      gv += value(b1);
-      size += fabsf(value(b1));
+      gv += 0.5f * value(b1);
+      size += 0.5f * fabsf(value(b1));
     }
     // (infinities of opposite signs never meet: -inf is no value)
     // The best groups one by one, and with a bias the first of the others.
@@ -545,14 +549,14 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
         last_size = __shfl_sync(kAll, size, who);
         const uint32_t next = __reduce_max_sync(kAll, gk);
         if (next) {
-          // Four scores are in it. With u = 2^-24, a sigmoid's is within 5 u (the
-          // exponential's error counts p (1 - p) times), all softmax's together
-          // within 75 u; a sum of two and their biases another 2 u of the sizes,
-          // of which the largest of the others' stands for all.
+          // Halves of four scores are in it. With u = 2^-24, a sigmoid's is within
+          // 5 u (the exponential's error counts p (1 - p) times), all softmax's
+          // together within 75 u; a sum of two and their biases another 2 u of the
+          // sizes, of which the largest of the others' stands for all.
           float sizes = gk ? size : 0.0f;
 #pragma unroll
           for (int d = 16; d; d >>= 1) sizes = fmaxf(sizes, __shfl_xor_sync(kAll, sizes, d));
-          near = !(last - value(next) > (a.sigmoid ? 1.3e-6f : 1.5e-5f) + 1.5e-7f * (sizes + last_size));
+          near = !(last - value(next) > (a.sigmoid ? 0.65e-6f : 0.75e-5f) + 1.5e-7f * (sizes + last_size));
         }
       }
     }

@@ -201,6 +201,25 @@ def test_route_many_rows(sk):
     check_route(sk, logits, 6, bias, n_groups=8, topk_groups=4, score="sigmoid", scale=2.0)
 
 
+LOW, HIGH = (float(v) for v in (np.finfo(np.float32).min, np.finfo(np.float32).max))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_groups_of_the_largest_biases(sk, score):
+    # sums of two biases beyond FP32: the type's lowest value is a mask that still
+    # leaves its experts to be chosen where nothing else is left
+    bias = np.array([0, 0] + 6 * [LOW])
+    ids, _ = check_route(sk, gpu(np.zeros((1, 8)), F32), 4, gpu(bias, F32), n_groups=4, topk_groups=2, score=score)
+    assert host(ids).tolist() == [[0, 1, 2, 3]]
+    rng = np.random.default_rng(29)
+    for _ in range(60):
+        a = rng.normal(size=(12, 32))
+        values = [0.0, 0.25, LOW, LOW / 2, HIGH, HIGH / 2, -np.inf, np.inf, np.nan]
+        bias = rng.choice(values, 32, p=[0.2, 0.1, 0.3, 0.1, 0.08, 0.08, 0.06, 0.04, 0.04])
+        for topk_groups, k in ((1, 3), (3, 12), (7, 16)):
+            check_route(sk, gpu(a, F32), k, gpu(bias, F32), n_groups=8, topk_groups=topk_groups, score=score)
+
+
 # ----------------------------------------------------------- quantization ----
 def check_quantize(sk, z):
     q, scale = sk.int8_quantize(z)
