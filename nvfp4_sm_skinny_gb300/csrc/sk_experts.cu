@@ -535,30 +535,24 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
       size += 0.5f * fabsf(value(b1));
     }
     // (infinities of opposite signs never meet: -inf is no value)
-    // The best groups one by one, and with a bias the first of the others.
     uint32_t gk = lane < a.n_groups ? order_key(gv) : 0u, kept = 0u;
-    float last = 0.0f, last_size = 0.0f;
-    for (int o = 0; o < a.topk_groups; ++o) {
+    for (int o = 0; o < a.topk_groups; ++o) {  // the best groups one by one
       const uint32_t k = __reduce_max_sync(kAll, gk);
       if (!k) break;
       const int who = __ffs(__ballot_sync(kAll, gk == k)) - 1;
       kept |= 1u << who;
       if (lane == who) gk = 0u;
-      if (o == a.topk_groups - 1 && a.bias) {
-        last = value(k);
-        last_size = __shfl_sync(kAll, size, who);
-        const uint32_t next = __reduce_max_sync(kAll, gk);
-        if (next) {
-          // Halves of four scores are in it. With u = 2^-24, a sigmoid's is within
-          // 5 u (the exponential's error counts p (1 - p) times), all softmax's
-          // together within 75 u; a sum of two and their biases another 2 u of the
-          // sizes, of which the largest of the others' stands for all.
-          float sizes = gk ? size : 0.0f;
-#pragma unroll
-          for (int d = 16; d; d >>= 1) sizes = fmaxf(sizes, __shfl_xor_sync(kAll, sizes, d));
-          near = !(last - value(next) > (a.sigmoid ? 0.65e-6f : 0.75e-5f) + 1.5e-7f * (sizes + last_size));
-        }
-      }
+    }
+    if (a.bias && a.topk_groups < a.n_groups) {
+      // The least that a kept group may be against the most that another may. With
+      // u = 2^-24, a group's half sum is within 2 u of its size, whatever it cancels
+      // to (3.2 u here, for the rounding of the bounds themselves). Its scores count
+      // apart: halves of four meet, each sigmoid's within 5 u (the exponential's
+      // error counts p (1 - p) times), all softmax's together within 75 u.
+      const float slack = size < CUDART_INF_F ? 1.9e-7f * size : 0.0f;  // +inf is exact
+      const uint32_t low = __reduce_min_sync(kAll, (kept >> lane) & 1u ? order_key(gv - slack) : kAll);
+      const uint32_t high = __reduce_max_sync(kAll, gk ? order_key(gv + slack) : 0u);
+      near = high && !(value(low) - value(high) > (a.sigmoid ? 0.65e-6f : 0.75e-5f));
     }
     if (per % 32 == 0) {
       int left = per, g = 0;

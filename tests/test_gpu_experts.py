@@ -220,6 +220,31 @@ def test_route_groups_of_the_largest_biases(sk, score):
             check_route(sk, gpu(a, F32), k, gpu(bias, F32), n_groups=8, topk_groups=topk_groups, score=score)
 
 
+def test_route_groups_of_cancelling_biases(sk):
+    # a group whose two best biases nearly cancel is known far worse than its sum's
+    # size says, wherever it ranks
+    h = float.fromhex
+    bias = np.array([h("0x1.ffe006p+9"), h("-0x1.ffep+9"), -3000, -3000, 0, h("0x1.98f1d4p-13"), -3000, -3000,
+                     0, h("0x1.83f91ep-13"), -3000, -3000, -1, -1, -1, -1])
+    kw = dict(n_groups=4, topk_groups=2, score="sigmoid")
+    ids, _ = check_route(sk, gpu(np.zeros((1, 16)), F32), 2, gpu(bias, F32), **kw)
+    assert host(ids).tolist() == [[5, 9]]
+
+
+@pytest.mark.parametrize("score,spread", [("softmax", 1e-6), ("sigmoid", 1e-7)])
+@pytest.mark.parametrize("pin", [30.0, 1e3, 1e5])
+def test_route_groups_pinned_and_dropped(sk, score, spread, pin):
+    # two groups have one expert pinned, one dropped as far and two further; the groups
+    # are as far apart as an FP32 step of the pin
+    rng = np.random.default_rng(31)
+    a = rng.normal(0, spread * pin, (3000, 32))
+    bias = np.zeros((8, 4))
+    bias[:, 2:] = -3 * pin
+    bias[[1, 4], :2] = pin, -pin
+    for topk_groups in (2, 5):
+        check_route(sk, gpu(a, F32), 4, gpu(bias.reshape(-1), F32), n_groups=8, topk_groups=topk_groups, score=score)
+
+
 # ----------------------------------------------------------- quantization ----
 def check_quantize(sk, z):
     q, scale = sk.int8_quantize(z)
