@@ -341,7 +341,7 @@ __device__ __noinline__ bool route_row_pairs(const RouteArgs &a, int row, float 
 
   if (a.n_groups > 1)
     for (int e = lane; e < E; e += 32)
-      if (!((keep >> (e / per)) & 1u)) hi[e] = -CUDART_INF_F;
+      if (!((keep >> (e / per)) & 1u)) hi[e] = -CUDART_INF_F, lo[e] = 0.0f;  // as `none`: never above it
   __syncwarp();
 
   // The choices and those after them, down to one that is clearly apart.
@@ -369,7 +369,7 @@ __device__ __noinline__ bool route_row_pairs(const RouteArgs &a, int row, float 
       }
     }
     if (at == INT_MAX) break;
-    if (lane == 0) hi[at] = -CUDART_INF_F;
+    if (lane == 0) hi[at] = -CUDART_INF_F, lo[at] = 0.0f;
     __syncwarp();
     if (lane == found) {
       id = at;

@@ -245,6 +245,21 @@ def test_route_groups_pinned_and_dropped(sk, score, spread, pin):
         check_route(sk, gpu(a, F32), 4, gpu(bias.reshape(-1), F32), n_groups=8, topk_groups=topk_groups, score=score)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,topk_groups,k", [(1, 1, 6), (1, 1, 16), (8, 2, 8), (8, 2, 5)])
+def test_route_doubtful_rows_that_run_out_of_experts(sk, score, groups, topk_groups, k):
+    # scores that FP32 cannot tell apart, and no more experts than choices, or fewer
+    rng = np.random.default_rng(41)
+    steps = rng.integers(0, 4, (200, 32)).astype(np.int32)
+    a = (np.float32(1.7).view(np.int32) + steps).astype(np.int32).view(np.float32)
+    bias = np.full(32, 0.125)
+    if groups == 1:
+        bias[6:] = -np.inf
+    check_route(sk, gpu(a, F32), k, gpu(bias, F32), n_groups=groups, topk_groups=topk_groups, score=score)
+    a[::2, 3::2] = -np.inf
+    check_route(sk, gpu(a, F32), k, gpu(bias, F32), n_groups=groups, topk_groups=topk_groups, score=score)
+
+
 # ----------------------------------------------------------- quantization ----
 def check_quantize(sk, z):
     q, scale = sk.int8_quantize(z)
