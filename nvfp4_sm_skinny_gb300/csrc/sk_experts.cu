@@ -544,15 +544,15 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
       if (lane == who) gk = 0u;
     }
     if (a.bias && a.topk_groups < a.n_groups) {
-      // The least that a kept group may be against the most that another may. With
+      // The least that each kept group may be against the most that another may. With
       // u = 2^-24, a group's half sum is within 2 u of its size, whatever it cancels
-      // to (3.2 u here, for the rounding of the bounds themselves). Its scores count
-      // apart: halves of four meet, each sigmoid's within 5 u (the exponential's
-      // error counts p (1 - p) times), all softmax's together within 75 u.
-      const float slack = size < CUDART_INF_F ? 1.9e-7f * size : 0.0f;  // +inf is exact
-      const uint32_t low = __reduce_min_sync(kAll, (kept >> lane) & 1u ? order_key(gv - slack) : kAll);
-      const uint32_t high = __reduce_max_sync(kAll, gk ? order_key(gv + slack) : 0u);
-      near = high && !(value(low) - value(high) > (a.sigmoid ? 0.65e-6f : 0.75e-5f));
+      // to, and the bound's own rounding takes another. Its scores count apart: halves
+      // of four meet, each sigmoid's within 4 u (3 p, and the exponential's error
+      // p (1 - p) times), all softmax's together within 75 u.
+      const float slack = size < CUDART_INF_F ? 1.8e-7f * size : 0.0f;  // +inf is exact
+      const uint32_t most = __reduce_max_sync(kAll, gk ? order_key(gv + slack) : 0u);
+      const bool clear = gv - slack - value(most) > (a.sigmoid ? 0.55e-6f : 0.75e-5f);
+      near = most && __any_sync(kAll, ((kept >> lane) & 1u) && !clear);
     }
     if (per % 32 == 0) {
       int left = per, g = 0;
