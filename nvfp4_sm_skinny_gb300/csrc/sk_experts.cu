@@ -327,16 +327,18 @@ __device__ __noinline__ bool route_row_pairs(const RouteArgs &a, int row, float 
       const Pair v = {__shfl_sync(kAll, gv.hi, o), __shfl_sync(kAll, gv.lo, o)};
       rank += above(v, gv) || (!above(gv, v) && o < lane);
     }
-    const bool lead = lane < a.n_groups;
-    keep = __ballot_sync(kAll, lead && rank < a.topk_groups && gv.hi > -CUDART_INF_F);
-    if (a.topk_groups < a.n_groups) {
-      const int last = __ffs(__ballot_sync(kAll, lead && rank == a.topk_groups - 1)) - 1;
-      const int next = __ffs(__ballot_sync(kAll, lead && rank == a.topk_groups)) - 1;
-      const Pair v0 = {__shfl_sync(kAll, gv.hi, last), __shfl_sync(kAll, gv.lo, last)};
-      const Pair v1 = {__shfl_sync(kAll, gv.hi, next), __shfl_sync(kAll, gv.lo, next)};
-      const float sizes = __shfl_sync(kAll, size, last) + __shfl_sync(kAll, size, next);
-      if (v1.hi > -CUDART_INF_F && close(v0, v1, 2.0f, sizes)) return false;  // halves of four scores
+    keep = __ballot_sync(kAll, lane < a.n_groups && rank < a.topk_groups && gv.hi > -CUDART_INF_F);
+    // Each kept group against each of the others, with the sizes of both: what a sum
+    // has cancelled to does not tell how well it is known.
+    const bool in = (keep >> lane) & 1u;
+    bool doubt = false;
+    for (int o = 0; o < a.n_groups; ++o) {
+      const Pair v = {__shfl_sync(kAll, gv.hi, o), __shfl_sync(kAll, gv.lo, o)};
+      const float other = __shfl_sync(kAll, size, o);
+      if (in && !((keep >> o) & 1u) && v.hi > -CUDART_INF_F)
+        doubt = doubt || close(gv, v, 2.0f, size + other);  // halves of four scores
     }
+    if (__any_sync(kAll, doubt)) return false;
   }
 
   if (a.n_groups > 1)

@@ -260,6 +260,20 @@ def test_route_doubtful_rows_that_run_out_of_experts(sk, score, groups, topk_gro
     check_route(sk, gpu(a, F32), k, gpu(bias, F32), n_groups=groups, topk_groups=topk_groups, score=score)
 
 
+@pytest.mark.parametrize("score,base", [("sigmoid", 8.0), ("softmax", 0.01)])
+@pytest.mark.parametrize("topk_groups", [2, 4, 7])
+def test_route_groups_that_pairs_cannot_tell_apart(sk, score, base, topk_groups):
+    # groups some 1e-10 apart, which pairs of FP32 tell, and among them one whose
+    # biases cancel, which these know to some 1e-9 only
+    rng = np.random.default_rng(37)
+    a = np.repeat(rng.normal(size=(2000, 1)), 16, 1).astype(np.float32)
+    steps = rng.integers(0, 40, (2000, 8)).astype(np.int32)
+    a[:, ::2] = (np.float32(base).view(np.int32) + steps).astype(np.int32).view(np.float32)
+    bias = np.zeros(16)
+    bias[6:8] = 2.0 ** 22, -2.0 ** 22
+    check_route(sk, gpu(a, F32), 2 * topk_groups - 1, gpu(bias, F32), n_groups=8, topk_groups=topk_groups, score=score)
+
+
 # ----------------------------------------------------------- quantization ----
 def check_quantize(sk, z):
     q, scale = sk.int8_quantize(z)
