@@ -65,21 +65,24 @@ __device__ __forceinline__ float route_logit(const RouteArgs &a, size_t at) {
 
 // The last step of a row: lane c holds choice c (id -1: none), its logit x and its
 // score p. Renormalized weights are ratios of scores, which FP32 would lose where
-// all of them are tiny (the likely experts masked by the bias, far negative logits):
-// those of a softmax, and of sigmoids so small that they are exp(x), are ratios of
-// exp(x - the largest chosen x). `top`: the logit that scores refer to (0: sigmoid);
-// a score is 0 where FP64's is.
+// some of them are tiny (the likely experts masked by the bias, far negative logits):
+// those of a softmax are ratios of exp(x - the largest chosen x), those of sigmoids
+// where one is that small, of exp(x - ref) / (1 + exp(x)), ref the largest chosen x
+// or 0 if that is positive. `top`: the logit that scores refer to (0: sigmoid); a
+// score is 0 where FP64's is.
 __device__ __forceinline__ void route_store(const RouteArgs &a, int row, int id, float x, float p, float top) {
   constexpr uint32_t kAll = 0xFFFFFFFFu;
   const int lane = threadIdx.x & 31;
   const bool mine = lane < a.top_k && id >= 0;
   float w = mine ? p : 0.0f;
   if (a.renormalize) {
-    if (!a.sigmoid || !__any_sync(kAll, mine && x >= -60.0f)) {
+    if (!a.sigmoid || __any_sync(kAll, mine && x < -60.0f)) {
       float most = mine ? x : -CUDART_INF_F;
 #pragma unroll
       for (int d = SK_MAX_TOP_K / 2; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, d));
-      w = !mine || (most != top && most - top < -745.0f) ? 0.0f : __expf(x == most ? 0.0f : x - most);
+      const bool nothing = !mine || (most != top && most - top < -745.0f);
+      if (!a.sigmoid) w = nothing ? 0.0f : __expf(x == most ? 0.0f : x - most);
+      else if (!(x > 0.0f)) w = nothing ? 0.0f : __expf(x - fminf(most, 0.0f)) / (1.0f + __expf(x));
     }
     float total = w;  // of the first lanes, which hold the choices
 #pragma unroll

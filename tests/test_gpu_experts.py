@@ -274,6 +274,16 @@ def test_route_groups_that_pairs_cannot_tell_apart(sk, score, base, topk_groups)
     check_route(sk, gpu(a, F32), 2 * topk_groups - 1, gpu(bias, F32), n_groups=8, topk_groups=topk_groups, score=score)
 
 
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_route_weights_of_sigmoids_far_apart(sk, with_bias):
+    # ratios of scores of which some are beyond FP32 and others are not
+    a = np.array([[-30, -95, -100, -88], [-50, -100, -110, -120], [-59, -61, -87.5, -88.5], [-60, -60.001, -140, -90],
+                  [3, -70, -80, -60], [100, -61, 0, -59], [-0.5, -87, -61, -100], [-61, -62, -150, -95]])
+    bias = gpu(np.array([0.5, 0.25, 0.125, 0]), F32) if with_bias else None
+    for k in (2, 4):
+        check_route(sk, gpu(a, F32), k, bias, score="sigmoid")
+
+
 # ----------------------------------------------------------- quantization ----
 def check_quantize(sk, z):
     q, scale = sk.int8_quantize(z)
