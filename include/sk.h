@@ -356,7 +356,8 @@ sk_status sk_gemm_rmsnorm_nvfp4_static(const void *x, const void *w, const void 
  * Where fewer than top_k experts may be chosen, the remaining ids are -1 and
  * their weights 0: a row of -inf logits routes to nobody.
  * The order is that of values computed in FP64 (p + bias, sums of two); the
- * weights are FP32.
+ * weights are FP32, renormalized ones ratios however small the scores are, but
+ * a score that is 0 in FP64 (a sigmoid below a = -709.78) weighs nothing.
  *   logits      BF16 or FP32 [m, n_experts] (logits_type SK_TYPE_*), aligned to
  *               its element size
  *   bias        FP32 [n_experts] or NULL

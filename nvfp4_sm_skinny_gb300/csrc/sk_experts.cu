@@ -68,8 +68,8 @@ __device__ __forceinline__ float route_logit(const RouteArgs &a, size_t at) {
 // some of them are tiny (the likely experts masked by the bias, far negative logits):
 // those of a softmax are ratios of exp(x - the largest chosen x), those of sigmoids
 // where one is that small, of exp(x - ref) / (1 + exp(x)), ref the largest chosen x
-// or 0 if that is positive. `top`: the logit that scores refer to (0: sigmoid); a
-// score is 0 where FP64's is.
+// or 0 if that is positive. `top`: the logit that scores refer to (softmax). A score
+// weighs nothing where it is 0 in FP64, where exp(-x) is infinite or exp(x - top) 0.
 __device__ __forceinline__ void route_store(const RouteArgs &a, int row, int id, float x, float p, float top) {
   constexpr uint32_t kAll = 0xFFFFFFFFu;
   const int lane = threadIdx.x & 31;
@@ -80,7 +80,7 @@ __device__ __forceinline__ void route_store(const RouteArgs &a, int row, int id,
       float most = mine ? x : -CUDART_INF_F;
 #pragma unroll
       for (int d = SK_MAX_TOP_K / 2; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, d));
-      const bool nothing = !mine || (most != top && most - top < -745.0f);
+      const bool nothing = !mine || (a.sigmoid ? x < -709.78266f : x != top && x - top < -745.13f);
       if (!a.sigmoid) w = nothing ? 0.0f : __expf(x == most ? 0.0f : x - most);
       else if (!(x > 0.0f)) w = nothing ? 0.0f : __expf(x - fminf(most, 0.0f)) / (1.0f + __expf(x));
     }

@@ -284,6 +284,19 @@ def test_route_weights_of_sigmoids_far_apart(sk, with_bias):
         check_route(sk, gpu(a, F32), k, bias, score="sigmoid")
 
 
+@pytest.mark.parametrize("doubt", [False, True])
+def test_route_weights_of_scores_that_are_nothing_in_64_bits(sk, doubt):
+    # sigmoids below -709.78 and softmaxes 746 below the largest logit are 0 in FP64:
+    # they weigh nothing, whether the row's order took FP64 or not
+    bias = np.zeros(8) if doubt else np.arange(8, 0, -1) / 8
+    a = np.array([[-705, -712, -720, -800, -720, -712, -706, -900], [-710, -715, -720, -730, -740, -744, -746, -800],
+                  [-3, -650, -705, -711, -800, -900, -1000, -709]])
+    check_route(sk, gpu(a, F32), 6, gpu(bias, F32), score="sigmoid")
+    bias[0] = -np.inf
+    a = np.array([[0, -735, -747, -748, -760, -800, -900, -1000]])
+    check_route(sk, gpu(a, F32), 6, gpu(bias, F32), score="softmax")
+
+
 # ----------------------------------------------------------- quantization ----
 def check_quantize(sk, z):
     q, scale = sk.int8_quantize(z)
