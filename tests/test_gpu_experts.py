@@ -398,6 +398,37 @@ def test_gemm_sums_are_exact(sk, k, splits):
     assert y.shape == (9, 35)
 
 
+def cancelling(rng, rows, half):
+    """Weight codes [rows, 2 half] whose halves are alike: extremes or random."""
+    first = np.stack([(np.full(half, 127), np.full(half, -128), rng.integers(-128, 128, half))[r % 3] for r in range(rows)])
+    return np.concatenate([first, first], 1).astype(np.int8)
+
+
+@pytest.mark.parametrize("m", [1, 2, 8, 16])
+@pytest.mark.parametrize("k", [1024, 8208, 16384, 33024, 131056])
+@pytest.mark.parametrize("splits", [1, 8])
+def test_gemm_sums_that_cancel_are_exact(sk, m, k, splits):
+    # the first half of K adds up to as much as sums can hold, the second takes it off
+    # again; a token code and a weight code one step off leave an integer of at most
+    # 128 + 128, which BF16 holds
+    rng = np.random.default_rng(k + m)
+    half, n = k // 2, 42
+    xq = np.full((m, k), 127, np.int8)
+    xq[1::2] = -127
+    xq[:, half:] *= -1
+    wq = cancelling(rng, n, half)
+    for x in xq[2:]:
+        c = rng.integers(k)
+        x[c] -= np.sign(x[c])
+    for w in wq[1::2]:
+        c = rng.integers(k)
+        w[c] += 1 if w[c] < 0 else -1
+    ref = xq.astype(np.int64) @ wq.astype(np.int64).T
+    assert np.abs(ref).max() <= 256 and ref.any()
+    y = sk.gemm_int8(gpu(xq, I8), gpu(np.ones(m), F32), gpu(wq, I8), gpu(np.ones(n), F32), splits=splits)
+    assert np.array_equal(host(y), ref)
+
+
 def test_gemm_scales(sk):
     rng = np.random.default_rng(2)
     xq, wq = codes(rng, 6, 128), codes(rng, 48, 128)
@@ -524,6 +555,45 @@ def test_experts_extreme_activations(sk):
     c = make_experts(rng, 5, 4, 2, 64, 64)
     c["xs"][:] = [1e-30, 10.0, 0.3, 1.0, 3.0]       # gates far into silu's tails
     check_experts(sk, c)
+
+
+def small_sums(rng, w, places):
+    """Makes the sums of `cancelling` rows small integers, by changes at places where the
+    other operand is 1."""
+    w[:, places] = 100
+    w[:, places + w.shape[1] // 2] = 100
+    w[:, places] += rng.integers(-5, 6, (len(w), len(places))).astype(np.int8)
+
+
+@pytest.mark.parametrize("m", [1, 2, 8, 16])
+@pytest.mark.parametrize("k", [1040, 16384, 131056])
+def test_experts_sums_that_cancel_are_exact(sk, m, k):
+    # as above, in gate and up (over hidden) and in down (over inter): sums of a few
+    # units, of which one would be far outside the bound
+    rng = np.random.default_rng(k + m)
+    half = k // 2
+    places = rng.choice(half, 3, replace=False)
+    sign = np.where(np.arange(m) % 2, -1, 1)
+    row = np.full(k, 127)
+    row[places] = 1
+    row[half:] = -row[:half]
+    c = make_experts(rng, m, 2, 2, k, 16)
+    c["xq"] = (sign[:, None] * row).astype(np.int8)
+    c["xs"][:], c["s13"][:] = 0.25, 1.0
+    for w in c["w13"]:
+        w[:] = cancelling(rng, 32, half)
+        small_sums(rng, w, places)
+    check_experts(sk, c)
+    c = make_experts(rng, m, 2, 2, 16, k)
+    c["xq"][:], c["xq"][:, 0], c["xq"][:, 1] = 0, 127, 127 * sign
+    c["xs"][:], c["s13"][:] = 1 / 127, 1 / 127
+    c["w13"][:] = 0
+    c["w13"][:, :k, 0], c["w13"][:, k:, 1] = 127, row  # gates of 1, ups of the row / 127
+    for w in c["w2"]:
+        w[:] = cancelling(rng, 16, half)
+        small_sums(rng, w, places)
+    y = check_experts(sk, c)
+    assert host(y).any()
 
 
 # ------------------------------------------------- calls as a program makes ----
