@@ -701,10 +701,11 @@ __device__ __forceinline__ float row_max(uint32_t bits) {
 }
 
 // A row's codes: round to nearest even of 127 v / amax, as of the exact quotient.
-// The product with 127 / amax, within 127 2^-23 = 1.5e-5 of it, settles all but
-// the neighbours of half an integer (of BF16 inputs: but the halves themselves,
-// the others are 1/512 away or more); those take an IEEE division, for which f
-// (2^-8 for amax >= 1, else 1) keeps 127 v finite.
+// The product with 127 / amax, within 127 2^-23 = 1.51e-5 of it, settles all that are
+// further than 1e-4 from half an integer. The others take an IEEE division, whose
+// rounding crosses no half, nor lands on one from a quotient of BF16 inputs: the
+// nearest is 127 (255 / 256) / 253, 1/64768 = 1.54e-5 away. For it f (2^-8 for
+// amax >= 1, else 1) keeps 127 v finite.
 struct RowCodes {
   float amax, inv, f;
   bool plain;  // neither zero nor NaN

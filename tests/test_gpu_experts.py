@@ -342,6 +342,20 @@ def test_quantize_special_rows(sk):
     assert not host(q)[[0, 1, 2, 9, 11]].any()
 
 
+@pytest.mark.parametrize("exponent", [-120, -8, 0, 110])
+def test_quantize_every_quotient(sk, exponent):
+    # every significand of the row's largest value against every one of a value, with
+    # codes from 127 to below 1: the nearest to half an integer, but not one, is
+    # 127 (255 / 256) / 253 = 1/2 + 1/64768
+    amax = np.arange(128, 256.0)[:, None]
+    z = (np.arange(128, 256.0)[:, None] * 2.0 ** -np.arange(9)).reshape(1, -1)
+    z = np.where(z <= amax, z, 0.0) * (-1) ** np.arange(z.size)
+    z = np.concatenate([amax, z, np.zeros((128, 15))], 1) * 2.0 ** exponent
+    t = gpu(z, torch.float64).to(BF16)
+    assert np.array_equal(host(t), z) and z.shape[1] == 1168
+    check_quantize(sk, t)
+
+
 # ------------------------------------------------------------------- gemm ----
 def codes(rng, *shape):
     return rng.integers(-128, 128, shape).astype(np.int8)
