@@ -146,3 +146,27 @@ def test_binding_refuses_other_devices(sk, monkeypatch):
         sk._launch_on(None, 1, Tensor(1))
     with pytest.raises(ValueError, match="current"):
         sk._launch_on(Stream(1), 0, Tensor(0))
+
+
+@pytest.mark.parametrize("change,message", [
+    (dict(z=None), "sk_int8_quantize: z is a null pointer"), (dict(z=P + 8), "sk_int8_quantize: z (0x100008) is not 16-byte"),
+    (dict(q=None), "sk_int8_quantize: q is a null pointer"), (dict(q=P + 4), "sk_int8_quantize: q (0x100004) is not 16-byte"),
+    (dict(scale=None), "sk_int8_quantize: scale is a null"), (dict(scale=P + 2), "sk_int8_quantize: scale (0x100002) is not 4-byte"),
+])
+def test_quantize_refusals_name_the_argument(sk, change, message):
+    a = {**dict(z=P, q=P, scale=P, m=1, n=64, stream=None), **change}
+    assert sk.lib().sk_int8_quantize(*a.values()) == 1
+    assert sk.last_error().startswith(message)
+
+
+def test_binding_refusals_name_the_argument(sk):
+    def t(*shape, dtype=torch.int8):
+        return torch.zeros(*shape, dtype=dtype)
+
+    f = torch.float32
+    with pytest.raises(ValueError, match="^z: dtype"):
+        sk.int8_quantize(t(2, 32, dtype=f))
+    with pytest.raises(ValueError, match="^xq: dtype"):
+        sk.gemm_int8(t(2, 32, dtype=torch.uint8), t(2, dtype=f), t(4, 32), t(4, dtype=f))
+    with pytest.raises(ValueError, match="^logits: dtype"):
+        sk.route(t(2, 8, dtype=torch.float16), 2)
