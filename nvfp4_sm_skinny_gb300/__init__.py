@@ -422,6 +422,20 @@ def _want(t, dtype, shape, name):
         _need(t, dtype, shape, name)
 
 
+def _misfit(**sizes) -> str | None:
+    """Names the first size that the library's 32-bit arguments cannot hold."""
+    for name, v in sizes.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            return f"{name}={v}: needs a size of at most {2 ** 31 - 1}"
+    return None
+
+
+def _fits(**sizes) -> None:
+    why = _misfit(**sizes)
+    if why:
+        raise ValueError(why)
+
+
 def _new(shape, dtype, device, stream):
     """An output of a call on ``stream``, from that stream's memory."""
     if stream is None:
@@ -438,6 +452,8 @@ def route(logits, top_k: int, bias=None, n_groups: int = 1, topk_groups: int = 1
     index; ``bias`` (FP32 [n_experts]) is added to the scores for the choice
     only; ids are -1 where nothing is left to choose (sk_route)."""
     m, n = logits.shape
+    if (m | n | top_k | n_groups | topk_groups) >> 31:  # any negative, or beyond 31 bits
+        _fits(m=m, n_experts=n, top_k=top_k, n_groups=n_groups, topk_groups=topk_groups)
     bf16 = logits.dtype is torch.bfloat16
     _want(logits, torch.bfloat16 if bf16 else torch.float32, (m, n), "logits")
     if score not in SCORES:
@@ -464,6 +480,8 @@ def int8_quantize(z, q=None, scale=None, stream=None):
     """(q int8 [m, n], scale FP32 [m]): int8 codes of BF16 z [m, n], one scale
     per row (amax / 127): m token rows, or the output features of a weight."""
     m, n = z.shape
+    if (m | n) >> 31:
+        _fits(m=m, n=n)
     _want(z, torch.bfloat16, (m, n), "z")
     if q is None:
         q = _new((m, n), torch.int8, z.device, stream)
@@ -480,6 +498,9 @@ def int8_quantize(z, q=None, scale=None, stream=None):
 
 def gemm_int8_supported(m: int, n: int, k: int, splits: int = 0) -> str | None:
     """None if the int8 GEMM has a launch for the shape, else why."""
+    why = _misfit(m=m, n=n, k=k, splits=splits)
+    if why:
+        return why
     st = lib().sk_gemm_int8_supported(m, n, k, splits)
     return None if st == SK_OK else last_error()
 
@@ -489,6 +510,8 @@ def gemm_int8(xq, x_scale, wq, w_scale, out=None, splits: int = 0, stream=None):
     codes, an exact integer sum, FP32 scales per token and output feature."""
     m, k = xq.shape
     n = wq.shape[0]
+    if (m | n | k | splits) >> 31:
+        _fits(m=m, n=n, k=k, splits=splits)
     _want(xq, torch.int8, (m, k), "xq")
     _want(x_scale, torch.float32, (m,), "x_scale")
     _want(wq, torch.int8, (n, k), "wq")
@@ -504,6 +527,8 @@ def gemm_int8(xq, x_scale, wq, w_scale, out=None, splits: int = 0, stream=None):
 
 
 def experts_int8_workspace(m: int, top_k: int, hidden: int, inter: int) -> int:
+    if _misfit(m=m, top_k=top_k, hidden=hidden, inter=inter):
+        return 0
     return int(lib().sk_experts_int8_workspace(m, top_k, hidden, inter))
 
 
@@ -521,6 +546,8 @@ def experts_int8(xq, x_scale, w13, s13, w2, s2, ids, weights, out=None, workspac
     m, hidden = xq.shape
     n_experts, _, inter = w2.shape
     top_k = ids.shape[1]
+    if (m | n_experts | top_k | hidden | inter) >> 31:
+        _fits(m=m, n_experts=n_experts, top_k=top_k, hidden=hidden, inter=inter)
     _want(xq, torch.int8, (m, hidden), "xq")
     _want(x_scale, torch.float32, (m,), "x_scale")
     _want(w13, torch.int8, (n_experts, 2 * inter, hidden), "w13")

@@ -170,3 +170,49 @@ def test_binding_refusals_name_the_argument(sk):
         sk.gemm_int8(t(2, 32, dtype=torch.uint8), t(2, dtype=f), t(4, 32), t(4, dtype=f))
     with pytest.raises(ValueError, match="^logits: dtype"):
         sk.route(t(2, 8, dtype=torch.float16), 2)
+
+
+def test_binding_refuses_sizes_beyond_32_bits(sk, monkeypatch):
+    # the C arguments are 32-bit: 2^32 + 4 rows would run as 4
+    class Tensor:
+        is_cuda, device = True, "cuda:0"
+
+        def __init__(self, dtype, *shape):
+            self.dtype, self.shape = dtype, torch.Size(shape)
+
+        def is_contiguous(self):
+            return True
+
+        def get_device(self):
+            return 0
+
+        def data_ptr(self):
+            return P
+
+        def numel(self):
+            return self.shape.numel()
+
+    class Lib:
+        def __getattr__(self, name):
+            raise AssertionError(f"{name} is called")
+
+    monkeypatch.setattr(sk, "lib", Lib)
+    monkeypatch.setattr(sk, "_launch_on", lambda *args: 0)
+    bf, f, i8, i32, many = torch.bfloat16, torch.float32, torch.int8, torch.int32, 2 ** 32
+    for change in (dict(), dict(n_groups=many + 1), dict(n_groups=1 - many), dict(topk_groups=many + 1)):
+        m = 2 if change else many + 4
+        with pytest.raises(ValueError, match=f"^{next(iter(change), 'm')}=-?429496"):
+            sk.route(Tensor(bf, m, 8), 2, ids=Tensor(i32, m, 2), weights=Tensor(f, m, 2), **change)
+    with pytest.raises(ValueError, match="^m=4294967297"):
+        sk.int8_quantize(Tensor(bf, many + 1, 16), q=Tensor(i8, many + 1, 16), scale=Tensor(f, many + 1))
+    for m, n, k, splits in ((1, many + 5, 16, 0), (many + 1, 8, 16, 0), (1, 8, many + 16, 0), (1, 8, 16, many)):
+        with pytest.raises(ValueError, match="=429496"):
+            sk.gemm_int8(Tensor(i8, m, k), Tensor(f, m), Tensor(i8, n, k), Tensor(f, n), out=Tensor(bf, m, n), splits=splits)
+        assert "=429496" in sk.gemm_int8_supported(m, n, k, splits)
+    for m, e, k, hidden, inter in ((1, 1, many + 2, 16, 16), (1, 1, 2, many + 16, 16), (1, 1, 2, 16, many + 16),
+                                   (1, many + 1, 2, 16, 16), (many + 1, 1, 2, 16, 16)):
+        assert max(m, k, hidden, inter) < many or sk.experts_int8_workspace(m, k, hidden, inter) == 0
+        with pytest.raises(ValueError, match="=429496"):
+            sk.experts_int8(Tensor(i8, m, hidden), Tensor(f, m), Tensor(i8, e, 2 * inter, hidden), Tensor(f, e, 2 * inter),
+                            Tensor(i8, e, hidden, inter), Tensor(f, e, hidden), Tensor(i32, m, k), Tensor(f, m, k),
+                            out=Tensor(bf, m, hidden), workspace=Tensor(torch.uint8, 4096))
