@@ -182,7 +182,7 @@ class DecodeChain:
             hint(self.next_weight(l, 0))
             sk.gemm_bf16(self.h[l], self.w_o[l], out=self.ws_o[l][: self.m * H * 2].view(
                 torch.bfloat16).view(self.m, H), splits=self.splits, stream=stream)
-            hint(self.next_weight(l, 1))
+            hint(self.w_u[l])  # next here, routed experts or not
             sk.gemm_bf16(self.u[l], self.w_p[l], out=self.ws_p[l][: self.m * P * 2].view(
                 torch.bfloat16).view(self.m, P), splits=self.splits, stream=stream)
             hint(self.next_weight(l, 2))

@@ -216,3 +216,23 @@ def test_binding_refuses_sizes_beyond_32_bits(sk, monkeypatch):
             sk.experts_int8(Tensor(i8, m, hidden), Tensor(f, m), Tensor(i8, e, 2 * inter, hidden), Tensor(f, e, 2 * inter),
                             Tensor(i8, e, hidden, inter), Tensor(f, e, hidden), Tensor(i32, m, k), Tensor(f, m, k),
                             out=Tensor(bf, m, hidden), workspace=Tensor(torch.uint8, 4096))
+
+
+@pytest.mark.parametrize("experts", [0, 4])
+def test_chain_hints_name_the_next_gemm(sk, monkeypatch, experts):
+    from nvfp4_sm_skinny_gb300 import chain
+
+    c = chain.DecodeChain.__new__(chain.DecodeChain)
+    c.L, c.m, c.experts, c.prefetch_next, c.splits, c.eps, c.gc = 2, 1, experts, True, 0, 0.0, 0.0
+    for name in ("w_o", "w_p", "w_u", "w_r"):
+        setattr(c, name, [f"{name}{l}" for l in range(c.L)])
+    for name, n in (("ws_o", chain.H), ("ws_p", chain.P)):
+        setattr(c, name, torch.zeros(c.L, 2 * n, dtype=torch.uint8))
+    c.h, c.u, c.z = ([None] * (c.L + 1) for _ in range(3))
+    calls = []
+    monkeypatch.setattr(sk, "gemm_prefetch_next", lambda w: calls.append(("hint", w)))
+    monkeypatch.setattr(sk, "gemm_bf16", lambda x, w, **kw: calls.append(("gemm", w)))
+    c.gemms_only()
+    order = [f"{name}{l}" for l in range(c.L) for name in ("w_o", "w_p", "w_u")]
+    assert calls == [call for w, ahead in zip(order, order[1:] + [None]) for call in (("hint", ahead), ("gemm", w))]
+    assert c.next_weight(0, 1) == ("w_r0" if experts else "w_u0")  # with routed experts the router's GEMM follows
