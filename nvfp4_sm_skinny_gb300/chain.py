@@ -11,16 +11,18 @@ The routed experts stand between the pooler and the unpooler (the order of
 the pages: o_proj -> attention boundary -> pooler -> experts -> unpooler ->
 next boundary). The pages leave them to another package, and by default so does
 the chain: the unpooler reads the expert input z in their place. With
-``experts`` = E > 0 each layer runs E routed experts in int8 on z:
+``experts`` = E > 0 (a multiple of 16, the router being a GEMM) each layer runs E
+routed experts in int8 on z:
 
     logits  = z @ W_r^T                   router       [E, 4096]      (sk_gemm_bf16)
     ids, g  = top_k of sigmoid(logits) + bias                         (sk_route)
     zq, zs  = int8 codes of z's rows                                  (sk_int8_quantize)
     e       = sum_j g_j W2(silu(W1 z) * W3 z)  [E, 2 I, 4096], [E, 4096, I] (sk_experts_int8)
 
-and the unpooler reads e. This module only allocates buffers and calls the
-binding; every step runs in libsk's kernels. ``capture()`` records one pass into
-a CUDA graph (the calls allocate nothing and are capturable).
+and the unpooler reads e; the NVFP4 codes a and a_sf have no reader then. This
+module only allocates buffers and calls the binding; every step runs in libsk's
+kernels. ``capture()`` records one pass into a CUDA graph (the calls allocate
+nothing and are capturable).
 """
 from __future__ import annotations
 
