@@ -373,7 +373,7 @@ def run(state):
         return _plain_resize(s["new_lens"], s["cache"], table, lens, refs, s["ps"])
     if op == "fork":
         if own:
-            return sk.kv_fork(s["parents"], table, lens, refs, s["ps"])[0], table, lens, refs
+            return sk.kv_fork(s["parents"], table, lens, refs, s["ps"]), table, lens, refs
         return _plain_fork(s["parents"], table, lens, refs, s["ps"])
     if own:
         page_map, _ = sk.kv_compact(s["cache"], table, lens, refs, s["ps"])
