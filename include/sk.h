@@ -439,6 +439,150 @@ sk_status sk_experts_int8(const int8_t *xq, const float *x_scale, const int8_t *
                           const float *weights, void *y, void *workspace, size_t workspace_bytes,
                           int m, int n_experts, int top_k, int hidden, int inter, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The key/value cache before the o_proj, held in 4 bits. No counterpart on the
+ * pages, which start at the attention's output. Values have the pooler page's
+ * NVFP4 form (cutedsl/moe/pooler_gather, module docstring): a value is
+ * e2m1(code) * e4m3(scale) / global scale, one scale per 16 columns of a token's
+ * head, made as sk_nvfp4_quantize makes them.
+ *
+ * The cache of one layer is uint8 [pages, kv_heads, block]. A block, of
+ * sk_kv_block_bytes = page_size * head_dim * 9 / 8 bytes, holds a KV head's part of
+ * a page of page_size tokens:
+ *     K codes  [page_size, head_dim / 2]   column 2c in the low nibble
+ *     V codes  [page_size, head_dim / 2]
+ *     K scales [page_size, head_dim / 16]  float8_e4m3fn bytes
+ *     V scales [head_dim / 16, page_size]
+ * The caches of all layers are uint8 [layers, pages, kv_heads, block].
+ *   table int32 [rows, width]  token p of row r lies in page table[r, p / page_size],
+ *                              at place p % page_size; entries behind a row's last
+ *                              page are not read
+ *   lens  int32 [rows]         the tokens of a row
+ *   refs  int32 [pages]        how many rows hold a page; 0: it is free
+ * A page number outside [0, pages) names no page: nothing is written there, and
+ * attention leaves its tokens out. page_size is 16, 32 or 64, head_dim 64 or 128,
+ * width * page_size at most 2^30.
+ *
+ * One step of a program that decodes t tokens of every row: sk_kv_resize to the
+ * new lengths, once; then, for each layer, sk_kv_append and sk_attn_nvfp4.
+ * ------------------------------------------------------------------------ */
+
+#define SK_MAX_CACHE_ROWS 4096 /* rows of a table whose pages are managed */
+#define SK_MAX_SMS 160         /* SMs that sk_attn_nvfp4 uses, at most */
+
+/* Bytes of a KV head's part of a page; 0 for sizes that the calls reject. */
+size_t sk_kv_block_bytes(int page_size, int head_dim);
+
+/*
+ * sk_kv_append -- quantizes the last t tokens of each of b rows into the cache of
+ * a layer: token j of row i goes to position lens[i] - t + j. A token whose
+ * position is negative or has no page is left out (a padded batch: put the tokens
+ * last). All other bytes of the cache keep their values.
+ *   k, v   BF16 [b, t, kv_heads, head_dim]; k_stride, v_stride: values from a token
+ *          to the next (multiples of 8, at least kv_heads * head_dim), so that both
+ *          may be parts of the rows of one product
+ *   k_global_scale, v_global_scale  FP32 [1] on the device
+ *   cache  the layer's, written;  table int32 [b, width], lens int32 [b]
+ *   b t <= 2^24, kv_heads <= 1024; k, v and cache 16-byte, the rest 4-byte aligned.
+ * No two tokens of a call may have the same place: pages that rows share are
+ * parted by sk_kv_resize before anything is appended to them.
+ */
+sk_status sk_kv_append(const void *k, const void *v, const float *k_global_scale,
+                       const float *v_global_scale, uint8_t *cache, const int32_t *table,
+                       const int32_t *lens, int b, int t, int kv_heads, int head_dim, int page_size,
+                       int pages, int width, int64_t k_stride, int64_t v_stride, void *stream);
+
+/* Size in bytes of the workspace sk_attn_nvfp4 needs (whatever the lengths);
+   0 for sizes that the call rejects. */
+size_t sk_attn_nvfp4_workspace(int b, int t, int q_heads, int kv_heads, int head_dim);
+
+/*
+ * sk_attn_nvfp4 -- attention of the last t tokens of each of b rows over the cache
+ * of a layer. Token j of row i stands at position pos = lens[i] - t + j and sees the
+ * keys 0 .. pos, of those the last `window` if window > 0. With query head h and KV
+ * head h / (q_heads / kv_heads):
+ *   s[k] = scale * sum_c q[c] K[k, c];  p[k] = exp(s[k] - max s)
+ *   out  = bf16_rn( sum_k p[k] V[k, :] / sum_k p[k] );  lse = max s + log sum_k p[k]
+ * A token that sees nothing (pos < 0, a row of length 0, missing pages) gets zeros
+ * and lse -inf. What the cache holds in places that no token sees does not matter,
+ * be it scales that are no numbers.
+ *   q      BF16 [b, t, q_heads, head_dim]; q_stride: values from a token to the next
+ *   cache  the layer's;  table int32 [b, width], lens int32 [b]
+ *   out    BF16 [b, t, q_heads, head_dim], contiguous: the rows of the o_proj
+ *   lse    FP32 [b, t, q_heads] or NULL
+ *   workspace: at least sk_attn_nvfp4_workspace(...) bytes, 256-byte aligned, in any
+ *   state; scratch for this call alone (calls that may run at the same time need
+ *   one each)
+ *   q_heads a multiple of kv_heads, at most 4096; b t <= 2^24, b t q_heads <= 2^30;
+ *   scale finite; q, cache and out 16-byte, the rest 4-byte aligned.
+ * Scores and sums are FP32, K and V exact; p enters the product with V in FP16 (of
+ * 2^7 to 2^15 at its largest), with a rounding of at most 2^-11 of itself.
+ * Results depend on the inputs alone: the work is cut by the lengths, in a fixed
+ * order.
+ */
+sk_status sk_attn_nvfp4(const void *q, const float *k_global_scale, const float *v_global_scale,
+                        const uint8_t *cache, const int32_t *table, const int32_t *lens, void *out,
+                        float *lse, void *workspace, size_t workspace_bytes, int b, int t,
+                        int q_heads, int kv_heads, int head_dim, int page_size, int pages, int width,
+                        int64_t q_stride, float scale, int window, void *stream);
+
+/* Size in bytes of the workspace sk_kv_resize needs; 0 for sizes that it rejects. */
+size_t sk_kv_resize_workspace(int rows, int pages);
+
+/*
+ * sk_kv_resize -- gives every row the length new_lens[i]; a negative one leaves row
+ * i as it is. In the order of rows:
+ *   longer   pages are added, the free ones with the lowest numbers first. If the
+ *            row's last page is partly filled and others hold it too, it is first
+ *            replaced by a copy, in all layers; who holds it alone by then keeps it.
+ *   shorter  the pages behind the new end are given back (0: all). They are free
+ *            after the call, not within it.
+ *   status[i]  0; 1 where the free pages do not suffice: from the first such row on,
+ *            every row that needs a page is refused; 2 for a length beyond
+ *            width * page_size, or a row whose own lens is out of range. A refused
+ *            row keeps its pages and its length.
+ * Entries of the table behind a row's new end become -1.
+ *   new_lens int32 [rows]; cache: all layers'; table, lens, refs: read and written;
+ *   status int32 [rows]
+ *   workspace: at least sk_kv_resize_workspace(...) bytes, 256-byte aligned, in any
+ *   state, for this call alone
+ *   rows <= 4096, pages <= 2^30, layers <= 65536, kv_heads <= 1024; cache 16-byte, the
+ *   rest 4-byte aligned.
+ */
+sk_status sk_kv_resize(const int32_t *new_lens, uint8_t *cache, int32_t *table, int32_t *lens,
+                       int32_t *refs, int32_t *status, void *workspace, size_t workspace_bytes,
+                       int rows, int width, int pages, int layers, int kv_heads, int head_dim,
+                       int page_size, void *stream);
+
+/*
+ * sk_kv_fork -- row i becomes what row parents[i] was before the call (all rows at
+ * once, so beams may change places); a negative parent, or i itself, leaves it as it
+ * is. Nothing is copied: the rows share their pages, refs counts them, and the pages
+ * that a row held before are given back.
+ *   parents int32 [rows]; table, lens, refs: read and written
+ *   status int32 [rows]: 0, or 2 for a parent beyond the last row (left as it is)
+ *   rows <= 4096; all 4-byte aligned.
+ */
+sk_status sk_kv_fork(const int32_t *parents, int32_t *table, int32_t *lens, int32_t *refs,
+                     int32_t *status, int rows, int width, int pages, int page_size, void *stream);
+
+/* Size in bytes of the workspace sk_kv_compact needs; 0 for sizes that it rejects. */
+size_t sk_kv_compact_workspace(int pages);
+
+/*
+ * sk_kv_compact -- moves the pages in use together: of L pages with refs > 0, those
+ * numbered L and up move to the free ones below L, in ascending order, in all layers;
+ * table and refs follow.
+ *   page_map int32 [pages]: the new number of each page, -1 of a free one (for who
+ *            holds pages outside the table)
+ *   workspace: at least sk_kv_compact_workspace(pages) bytes, 256-byte aligned, in any
+ *   state, for this call alone; the rest as for sk_kv_resize.
+ */
+sk_status sk_kv_compact(uint8_t *cache, int32_t *table, const int32_t *lens, int32_t *refs,
+                        int32_t *page_map, void *workspace, size_t workspace_bytes, int rows,
+                        int width, int pages, int layers, int kv_heads, int head_dim, int page_size,
+                        void *stream);
+
 /*
  * sk_wait_probe -- diagnostic of the bounded-wait path: launches one CTA that
  * waits on an mbarrier that nothing completes, through the same bounded wait

@@ -61,6 +61,7 @@ def lib() -> ctypes.CDLL:
                 "(python -c 'import __graft_entry__ as g; g.build()')")
         L = ctypes.CDLL(LIB_PATH)
         vp, i, f, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+        i64 = ctypes.c_int64
         sig = {
             "sk_last_error": ([], ctypes.c_char_p),
             "sk_version": ([], i),
@@ -88,6 +89,15 @@ def lib() -> ctypes.CDLL:
             "sk_gemm_int8_supported": ([i, i, i, i], i),
             "sk_experts_int8_workspace": ([i, i, i, i], sz),
             "sk_experts_int8": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, i, i, i, i, i, vp], i),
+            "sk_kv_block_bytes": ([i, i], sz),
+            "sk_kv_append": ([vp] * 7 + [i] * 7 + [i64, i64, vp], i),
+            "sk_attn_nvfp4_workspace": ([i] * 5, sz),
+            "sk_attn_nvfp4": ([vp] * 9 + [sz] + [i] * 8 + [i64, f, i, vp], i),
+            "sk_kv_resize_workspace": ([i, i], sz),
+            "sk_kv_resize": ([vp] * 7 + [sz] + [i] * 7 + [vp], i),
+            "sk_kv_fork": ([vp] * 5 + [i] * 4 + [vp], i),
+            "sk_kv_compact_workspace": ([i], sz),
+            "sk_kv_compact": ([vp] * 6 + [sz] + [i] * 7 + [vp], i),
             "sk_device_status": ([ctypes.POINTER(ctypes.c_uint32), i], i),
             "sk_convert_probe": ([i, vp, vp, i, vp], i),
             "sk_wait_probe": ([ctypes.c_uint, vp], i),
@@ -570,6 +580,218 @@ def experts_int8(xq, x_scale, w13, s13, w2, s2, ids, weights, out=None, workspac
         s2.data_ptr(), ids.data_ptr(), weights.data_ptr(), out.data_ptr(), workspace.data_ptr(),
         workspace.numel(), m, n_experts, top_k, hidden, inter, s))
     return out, workspace
+
+
+# ------------------------------------------- key/value cache held in 4 bits ----
+MAX_CACHE_ROWS = 4096
+
+
+def kv_block_bytes(page_size: int, head_dim: int) -> int:
+    """Bytes of a KV head's part of a page (page_size 16, 32 or 64 tokens,
+    head_dim 64 or 128): the last dimension of a cache."""
+    if _misfit(page_size=page_size, head_dim=head_dim):
+        return 0
+    return int(lib().sk_kv_block_bytes(page_size, head_dim))
+
+
+def _token_stride(x, name):
+    """Values from a token of x [b, t, heads, d] to the next: the tokens' rows may
+    be parts of longer ones."""
+    b, t, heads, d = x.shape
+    sb, st, sh, sd = x.stride()
+    step = st if t > 1 else sb if b > 1 else heads * d
+    if not x.is_cuda or sd != 1 or (heads > 1 and sh != d) or (b > 1 and t > 1 and sb != t * st):
+        raise ValueError(f"{name}: needs a CUDA tensor of contiguous token rows a fixed stride apart")
+    return step
+
+
+def _want_cache(cache, dims, page_size, head_dim, kv_heads):
+    """Pages of a cache uint8 [(layers,) pages, kv_heads, block]."""
+    if cache.dim() != dims:
+        raise ValueError(f"cache: {cache.dim()} dimensions, needs {dims}")
+    pages = cache.shape[-3]
+    block = page_size * head_dim * 9 // 8
+    _want(cache, torch.uint8, (*cache.shape[: dims - 2], kv_heads, block), "cache")
+    return pages
+
+
+def kv_append(k, v, k_global_scale, v_global_scale, cache, table, lens, page_size: int, stream=None):
+    """Quantizes the last t tokens of each row, k and v BF16 [b, t, kv_heads, d], into
+    a layer's cache uint8 [pages, kv_heads, block], in place: token j of row i at
+    position lens[i] - t + j of the pages that table int32 [b, width] names. k and v
+    may be parts of longer rows (sk_kv_append)."""
+    b, t, heads, d = k.shape
+    if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16:
+        raise ValueError(f"k, v: dtypes {k.dtype}, {v.dtype}, need torch.bfloat16")
+    if v.shape != k.shape:
+        raise ValueError(f"v: shape {tuple(v.shape)}, needs {tuple(k.shape)}")
+    ks, vs = _token_stride(k, "k"), _token_stride(v, "v")
+    width = table.shape[-1]
+    if (b | t | width | page_size) >> 31 or cache.shape[0] >> 31:
+        _fits(b=b, t=t, width=width, page_size=page_size, pages=cache.shape[0])
+    _want(k_global_scale, torch.float32, (1,), "k_global_scale")
+    _want(v_global_scale, torch.float32, (1,), "v_global_scale")
+    pages = _want_cache(cache, 3, page_size, d, heads)
+    _want(table, torch.int32, (b, width), "table")
+    _want(lens, torch.int32, (b,), "lens")
+    s = _launch_on(stream, k.get_device(), v, k_global_scale, v_global_scale, cache, table, lens)
+    _check(lib().sk_kv_append(k.data_ptr(), v.data_ptr(), k_global_scale.data_ptr(),
+                              v_global_scale.data_ptr(), cache.data_ptr(), table.data_ptr(),
+                              lens.data_ptr(), b, t, heads, d, page_size, pages, width, ks, vs, s))
+
+
+def attn_nvfp4_workspace(b: int, t: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    if _misfit(b=b, t=t, q_heads=q_heads, kv_heads=kv_heads, head_dim=head_dim):
+        return 0
+    return int(lib().sk_attn_nvfp4_workspace(b, t, q_heads, kv_heads, head_dim))
+
+
+_attn_workspace = functools.lru_cache(maxsize=256)(attn_nvfp4_workspace)
+
+
+def attn_nvfp4(q, k_global_scale, v_global_scale, cache, table, lens, page_size: int, scale=None,
+               window: int = 0, out=None, lse=None, workspace=None, stream=None):
+    """(out BF16 [b, t, q_heads, d], lse, workspace): attention of the last t tokens of
+    each row, q BF16 [b, t, q_heads, d], over a layer's cache uint8 [pages, kv_heads,
+    block]; token j of row i sees the keys up to its position lens[i] - t + j, with
+    ``window`` the last that many of them. ``scale`` is 1 / sqrt(d) if None; ``lse``
+    (FP32 [b, t, q_heads]) may be a tensor, True (allocate) or None (not stored)
+    (sk_attn_nvfp4)."""
+    b, t, heads, d = q.shape
+    if q.dtype is not torch.bfloat16:
+        raise ValueError(f"q: dtype {q.dtype}, needs torch.bfloat16")
+    stride = _token_stride(q, "q")
+    width, kv_heads = table.shape[-1], cache.shape[-2]
+    if (b | t | width | page_size | window) >> 31 or cache.shape[0] >> 31:
+        _fits(b=b, t=t, width=width, page_size=page_size, window=window, pages=cache.shape[0])
+    _want(k_global_scale, torch.float32, (1,), "k_global_scale")
+    _want(v_global_scale, torch.float32, (1,), "v_global_scale")
+    pages = _want_cache(cache, 3, page_size, d, kv_heads)
+    _want(table, torch.int32, (b, width), "table")
+    _want(lens, torch.int32, (b,), "lens")
+    if out is None:
+        out = _new((b, t, heads, d), torch.bfloat16, q.device, stream)
+    else:
+        _want(out, torch.bfloat16, (b, t, heads, d), "out")
+    if lse is True:
+        lse = _new((b, t, heads), torch.float32, q.device, stream)
+    elif lse is not None:
+        _want(lse, torch.float32, (b, t, heads), "lse")
+    if workspace is None:
+        workspace = _new((_attn_workspace(b, t, heads, kv_heads, d),), torch.uint8, q.device, stream)
+    else:
+        _want(workspace, torch.uint8, (workspace.numel(),), "workspace")
+    s = _launch_on(stream, q.get_device(), k_global_scale, v_global_scale, cache, table, lens, out, lse,
+                   workspace)
+    _check(lib().sk_attn_nvfp4(
+        q.data_ptr(), k_global_scale.data_ptr(), v_global_scale.data_ptr(), cache.data_ptr(),
+        table.data_ptr(), lens.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), b, t, heads, kv_heads, d, page_size, pages, width,
+        stride, d ** -0.5 if scale is None else scale, window, s))
+    return out, lse, workspace
+
+
+def kv_resize_workspace(rows: int, pages: int) -> int:
+    if _misfit(rows=rows, pages=pages):
+        return 0
+    return int(lib().sk_kv_resize_workspace(rows, pages))
+
+
+def kv_compact_workspace(pages: int) -> int:
+    if _misfit(pages=pages):
+        return 0
+    return int(lib().sk_kv_compact_workspace(pages))
+
+
+def _pages_sizes(cache, table, lens, refs, page_size):
+    """(layers, pages, kv_heads, head_dim, rows, width) of a cache's bookkeeping."""
+    if cache.dim() != 4:
+        raise ValueError(f"cache: {cache.dim()} dimensions, needs 4")
+    layers, pages, heads, block = cache.shape
+    rows, width = table.shape
+    if (layers | pages | heads | rows | width | page_size) >> 31:
+        _fits(layers=layers, pages=pages, kv_heads=heads, rows=rows, width=width, page_size=page_size)
+    d = block * 8 // (9 * page_size) if page_size > 0 else 0
+    if page_size > 0 and d * page_size * 9 != block * 8:
+        raise ValueError(f"cache: blocks of {block} bytes, not of {page_size} tokens")
+    _want(cache, torch.uint8, (layers, pages, heads, block), "cache")
+    _want_pages(table, lens, refs, pages, rows, width)
+    return layers, pages, heads, d, rows, width
+
+
+def _want_pages(table, lens, refs, pages, rows, width):
+    _want(table, torch.int32, (rows, width), "table")
+    _want(lens, torch.int32, (rows,), "lens")
+    _want(refs, torch.int32, (pages,), "refs")
+
+
+def kv_resize(new_lens, cache, table, lens, refs, page_size: int, status=None, workspace=None,
+              stream=None):
+    """(status int32 [rows], workspace): gives each row of table int32 [rows, width] the
+    length new_lens[i] (negative: as it is), adding pages from the free ones or giving
+    them back; a partly filled last page that others hold too is copied first, in all
+    layers of cache uint8 [layers, pages, kv_heads, block]. table, lens and refs int32
+    [pages] (how many rows hold a page) are updated in place; status is 1 for a row
+    refused for want of pages, 2 for a length out of range (sk_kv_resize)."""
+    layers, pages, heads, d, rows, width = _pages_sizes(cache, table, lens, refs, page_size)
+    _want(new_lens, torch.int32, (rows,), "new_lens")
+    if status is None:
+        status = _new((rows,), torch.int32, table.device, stream)
+    else:
+        _want(status, torch.int32, (rows,), "status")
+    if workspace is None:
+        workspace = _new((_resize_workspace(rows, pages),), torch.uint8, table.device, stream)
+    else:
+        _want(workspace, torch.uint8, (workspace.numel(),), "workspace")
+    s = _launch_on(stream, table.get_device(), new_lens, cache, lens, refs, status, workspace)
+    _check(lib().sk_kv_resize(new_lens.data_ptr(), cache.data_ptr(), table.data_ptr(), lens.data_ptr(),
+                              refs.data_ptr(), status.data_ptr(), workspace.data_ptr(),
+                              workspace.numel(), rows, width, pages, layers, heads, d, page_size, s))
+    return status, workspace
+
+
+_resize_workspace = functools.lru_cache(maxsize=256)(kv_resize_workspace)
+_compact_workspace = functools.lru_cache(maxsize=256)(kv_compact_workspace)
+
+
+def kv_fork(parents, table, lens, refs, page_size: int, status=None, stream=None):
+    """status int32 [rows]: row i of table becomes what row parents[i] was before the
+    call (negative, or i: as it is); the rows share their pages. table, lens and refs are
+    updated in place; status is 2 for a parent that is no row (sk_kv_fork)."""
+    rows, width = table.shape
+    pages, = refs.shape
+    if (rows | width | pages | page_size) >> 31:
+        _fits(rows=rows, width=width, pages=pages, page_size=page_size)
+    _want_pages(table, lens, refs, pages, rows, width)
+    _want(parents, torch.int32, (rows,), "parents")
+    if status is None:
+        status = _new((rows,), torch.int32, table.device, stream)
+    else:
+        _want(status, torch.int32, (rows,), "status")
+    s = _launch_on(stream, table.get_device(), parents, lens, refs, status)
+    _check(lib().sk_kv_fork(parents.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
+                            status.data_ptr(), rows, width, pages, page_size, s))
+    return status
+
+
+def kv_compact(cache, table, lens, refs, page_size: int, page_map=None, workspace=None, stream=None):
+    """(page_map int32 [pages], workspace): moves the pages in use to the lowest numbers, in
+    all layers of cache uint8 [layers, pages, kv_heads, block]; table and refs follow, in
+    place. page_map is the new number of each page, -1 of a free one (sk_kv_compact)."""
+    layers, pages, heads, d, rows, width = _pages_sizes(cache, table, lens, refs, page_size)
+    if page_map is None:
+        page_map = _new((pages,), torch.int32, table.device, stream)
+    else:
+        _want(page_map, torch.int32, (pages,), "page_map")
+    if workspace is None:
+        workspace = _new((_compact_workspace(pages),), torch.uint8, table.device, stream)
+    else:
+        _want(workspace, torch.uint8, (workspace.numel(),), "workspace")
+    s = _launch_on(stream, table.get_device(), cache, lens, refs, page_map, workspace)
+    _check(lib().sk_kv_compact(cache.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
+                               page_map.data_ptr(), workspace.data_ptr(), workspace.numel(), rows,
+                               width, pages, layers, heads, d, page_size, s))
+    return page_map, workspace
 
 
 # ----------------------------------------------------------- diagnostics ----

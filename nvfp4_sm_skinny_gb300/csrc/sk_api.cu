@@ -674,10 +674,11 @@ sk_status sk_device_status(uint32_t *out, int clear) {
   sk_status st;
   if ((st = current_device(&info)) != SK_OK) return st;
   cudaError_t e = sk::read_device_status(out, clear != 0);
-  uint32_t core = 0;
+  uint32_t core = 0, cache = 0;
   if (e == cudaSuccess) e = sk::read_core_status(&core, clear != 0);
+  if (e == cudaSuccess) e = sk::read_cache_status(&cache, clear != 0);
   if (e != cudaSuccess) return fail(SK_ERR_CUDA, "device status read failed: %s", cudaGetErrorString(e));
-  *out |= core;
+  *out |= core | cache;
   return ok();
 }
 

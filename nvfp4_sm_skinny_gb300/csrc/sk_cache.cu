@@ -1,0 +1,1196 @@
+// Device code of the key/value cache held in 4 bits: appending to it
+// (sk_kv_append), attention over it (sk_attn_nvfp4) and its pages
+// (sk_kv_resize, sk_kv_fork, sk_kv_compact). include/sk.h has the formulas and
+// the cache's layout.
+#include <math_constants.h>
+
+#include <type_traits>
+
+#include "sk.h"
+#include "sk_internal.h"
+#include "sk_ptx.cuh"
+
+namespace sk {
+namespace {
+
+__device__ uint32_t g_cache_status;                // OR of SK_DEVICE_WAIT_* bits
+constexpr uint64_t kCacheWaitNs = 2000000000ull;   // 2 s of wall time per wait
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+
+template <typename... Args>
+cudaError_t launch(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                   bool pdl, typename std::remove_reference<Args>::type... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+__host__ __device__ __forceinline__ int ceil_div(int a, int b) { return a / b + (a % b != 0); }
+
+// Untiled bulk copy global -> shared, completion counted on `bar` in bytes.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Eight e2m1 codes of a word as four FP16 pairs, byte i in o[i], its low nibble
+// in the low half.
+__device__ __forceinline__ void widen_e2m1(uint32_t w, uint32_t (&o)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+      : "r"(w));
+}
+
+// Two e4m3 bytes as an FP16 pair, exact.
+__device__ __forceinline__ uint32_t widen_e4m3(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
+  return r;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The transpose of an 8 x 8 matrix of 16-bit values, row l / 4, columns 2 (l % 4)
+// and the next in lane l's register.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// ---------------------------------------------------------------- attention
+// out = sum_k p_k v_k / sum_k p_k, p = exp(scale q . k - max): one pass over the
+// keys with a running maximum and sum.
+//
+// A warp works by itself on chunks of 64 tokens of one KV head, which bulk copies
+// bring into its own ring in shared memory (a block of the cache is one run of
+// bytes). The rows of a KV head, group query heads times t tokens, are the
+// tensor instruction's N (8 each, up to 32 a tile); keys and values are its 16-row
+// operand, widened in registers from the codes: one conversion and one product
+// with the scale per pair, both exact in FP16. So every code that is read is
+// widened once, whatever the number of rows:
+//   S^T [16 tokens, rows] = K [16 tokens, d] Q^T, then
+//   O^T [16 channels, rows] += V^T [16 channels, 16 tokens] P^T.
+// The order of an inner product is free, so lanes take what lies together in
+// memory: of K, lane (g, j) of the instruction (g = lane / 4, j = lane % 4) the j-th
+// quarter of a token's d columns; of V, the g-th eighth of the columns of the 16
+// tokens [16 j, 16 j + 16). Row r = 2 j + e (+ 8 h) of token tile mt is therefore
+// token 16 j + 4 mt + ((2 h + e) ^ f(j)); f = 0, 2, 1, 3 keeps the lanes of a
+// shared-memory access apart.
+//
+// The work is cut evenly whatever the lengths: units of 256 tokens of an item (a
+// sequence, a KV head, a tile of rows), item after item, in as many equal parts as
+// CTAs fit on the GPU. An item that falls into several parts is joined by
+// attn_join_kernel, in the order of its tokens.
+constexpr int kChunk = 64;
+constexpr int kAttnWarps = 4;
+constexpr int kAttnThreads = 32 * kAttnWarps;
+// Scores are kept as powers of two relative to a base that is at most 15 and after
+// an update 7 below the largest, so that P fits FP16 and what is 2^31 times smaller
+// than the largest still counts; the base moves (and the sums are scaled) only
+// when a score exceeds it by 2^15.
+constexpr float kTop = 15.0f, kAim = 7.0f;
+
+__host__ __device__ constexpr int attn_per_sm(int nt) { return nt == 4 ? 2 : 3; }
+
+template <int D, int NT>
+struct AttnShared {
+  static constexpr int kStageBytes = kChunk * D * 9 / 8;
+  static constexpr int kStages = (D == 128 ? 1 : 2) * (NT == 4 ? 3 : 2);
+  alignas(128) uint8_t ring[kAttnWarps][kStages * kStageBytes];
+  uint64_t full[kAttnWarps][kStages];
+  float2 stat[kAttnWarps][8 * NT];  // base and sum of each row
+  long long at;                     // where the part starts: offset in its sequence
+  int seq;
+  long long sums[kAttnWarps];
+};
+
+// Registers of O^T per thread, and floats of a part's result: a base and a sum per
+// row, then register r of lane l at 32 r + l.
+__host__ __device__ constexpr int attn_regs(int d, int nt) { return d / 16 * nt * 4; }
+__host__ __device__ constexpr int attn_part_floats(int d, int nt) { return 16 * nt + 32 * attn_regs(d, nt); }
+
+struct Keys {
+  int c0, c1;  // chunks [c0, c1) of a sequence that some of its tokens see
+  int units;
+};
+
+__device__ __forceinline__ Keys keys_of(const AttnArgs &a, int len) {
+  Keys k;
+  const int hi = min(max(len, 0), a.width * a.ps);
+  const int lo = a.window ? max(0, len - a.t - a.window + 1) : 0;
+  k.c0 = lo / kChunk;
+  k.c1 = ceil_div(hi, kChunk);
+  k.units = k.c1 > k.c0 ? ceil_div(k.c1 - k.c0, kAttnWarps) : 0;
+  return k;
+}
+
+// Sum over the CTA of one value per thread.
+__device__ __forceinline__ long long cta_sum(long long v, long long *sums) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0;
+  for (int w = 0; w < kAttnWarps; ++w) v += sums[w];
+  __syncthreads();
+  return v;
+}
+
+// Part c of U units in G parts starts here: equal parts, the first U % G one longer.
+__device__ __forceinline__ long long part_start(long long U, int G, long long c) {
+  const long long q = U / G, rest = U % G;
+  return c * q + min(c, rest);
+}
+__device__ __forceinline__ long long part_of(long long U, int G, long long u) {
+  const long long q = U / G, rest = U % G;
+  return u < rest * (q + 1) ? u / (q + 1) : rest + (u - rest * (q + 1)) / q;
+}
+
+// Stores a finished item's output: acc[nt][c] of this warp's share of the channels
+// (two neighbouring ones per row and half), base and sum of the row.
+template <int D, int NT>
+__device__ __forceinline__ void attn_store(const AttnArgs &a, int seq, int h, int r0,
+                                           const float (&acc)[D / 64][NT][4], const float2 (&st)[NT][2],
+                                           float v_inv) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, j = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = r0 + 8 * nt + 2 * j + e;
+      if (r >= a.rows) continue;
+      const int token = r / a.group, head = h * a.group + r % a.group;
+      const size_t row = (static_cast<size_t>(seq) * a.t + token) * a.hq + head;
+      const float l = st[nt][e].y, f = l == 0.0f ? 0.0f : v_inv / l;
+      uint16_t *o = a.out + row * D;
+      auto two = [&](int at, float x, float y) {
+        *reinterpret_cast<uint32_t *>(o + at) =
+            bf16_store_bits(x * f) | static_cast<uint32_t>(bf16_store_bits(y * f)) << 16;
+      };
+      if constexpr (D == 128) {
+        two(16 * g + 2 * w, acc[0][nt][e], acc[1][nt][e]);
+        two(16 * g + 8 + 2 * w, acc[0][nt][2 + e], acc[1][nt][2 + e]);
+      } else {
+        two(8 * g + 2 * w, acc[0][nt][e], acc[0][nt][2 + e]);
+      }
+      if (a.lse && w == 0 && g == 0)
+        a.lse[row] = l == 0.0f ? -CUDART_INF_F : (st[nt][e].x + log2f(l)) * 0.693147180559945f;
+    }
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kAttnThreads, attn_per_sm(NT)) attn_kernel(const __grid_constant__ AttnArgs a) {
+  using Sh = AttnShared<D, NT>;
+  constexpr int kMt = D / 16, kSub = D == 128 && NT == 4 ? 2 : 4, kSteps = D / 16;
+  extern __shared__ __align__(128) uint8_t raw[];
+  Sh &sh = *reinterpret_cast<Sh *>(raw);
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
+  griddep_launch_dependents();
+  if (lane == 0) {
+    for (int s = 0; s < Sh::kStages; ++s) mbar_init(smem_u32(&sh.full[w][s]), 1);
+    fence_barrier_init();
+  }
+  griddep_wait();
+
+  // This CTA's part [u, end) of all units, and the sequence it starts in.
+  const int per = a.hk * a.tiles;
+  long long U = 0;
+  for (int s = tid; s < a.b; s += kAttnThreads) U += static_cast<long long>(keys_of(a, a.lens[s]).units) * per;
+  U = cta_sum(U, sh.sums);
+  long long u = part_start(U, gridDim.x, blockIdx.x);
+  const long long end = part_start(U, gridDim.x, blockIdx.x + 1ll);
+  if (u >= end) return;
+  long long before = 0;
+  for (int base = 0;; base += kAttnThreads) {
+    const int s = base + tid;
+    const long long n = s < a.b ? static_cast<long long>(keys_of(a, a.lens[s]).units) * per : 0;
+    long long upto = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(kAll, upto, d);
+      if (lane >= d) upto += o;
+    }
+    if (lane == 31) sh.sums[w] = upto;
+    __syncthreads();
+    long long tile = 0;
+    for (int i = 0; i < kAttnWarps; ++i) {
+      if (i < w) upto += sh.sums[i];
+      tile += sh.sums[i];
+    }
+    upto += before;
+    if (upto - n <= u && u < upto) {
+      sh.seq = s;
+      sh.at = u - (upto - n);
+    }
+    __syncthreads();
+    before += tile;
+    if (before > u) break;
+  }
+  int seq = sh.seq;
+  long long at = sh.at;
+
+  // Addresses of this lane within a chunk: tokens [16 i, 16 i + 16) lie in piece
+  // 16 i / ps of it. swap = f(j).
+  const int blk = a.ps * D * 9 / 8, pieces = kChunk / a.ps, codes = a.ps * (D / 2);
+  const int gj = g >> 1, ge = g & 1;
+  const int fk = (gj & 1) << 1 | gj >> 1, fv = (j & 1) << 1 | j >> 1;
+  const int k_piece = 16 * gj / a.ps * blk, k_in = 16 * gj % a.ps;
+  const int v_piece = 16 * j / a.ps * blk, v_in = 16 * j % a.ps;
+  const int k_at0 = k_piece + (k_in + (ge ^ fk)) * (D / 2) + j * (D / 8);
+  const int k_at1 = k_piece + (k_in + ((2 + ge) ^ fk)) * (D / 2) + j * (D / 8);
+  const int ks_at0 = k_piece + 2 * codes + (k_in + (ge ^ fk)) * (D / 16) + j * (D / 64);
+  const int ks_at1 = k_piece + 2 * codes + (k_in + ((2 + ge) ^ fk)) * (D / 16) + j * (D / 64);
+  const int v_at = v_piece + codes + v_in * (D / 2) + g * (D / 16);
+  const int vs_at = v_piece + 2 * codes + a.ps * (D / 16) + (D == 128 ? g : g >> 1) * a.ps + v_in;
+  const uint32_t vs_order = fv == 0 ? 0x3210u : fv == 1 ? 0x2301u : fv == 2 ? 0x1032u : 0x0123u;
+  uint8_t *const ring = sh.ring[w];
+  const float c_all = __fmul_rn(a.scale, 1.44269504088896f) / *a.k_gs;
+  const float v_inv = 1.0f / *a.v_gs;
+
+  int slot = 0, phase = 0;  // the next stage to consume
+  int held = 0;             // 4 bits per stage: the pieces that it holds
+  bool first = true, lost = false;
+
+  while (u < end) {
+    const int len = a.lens[seq];
+    const Keys keys = keys_of(a, len);
+    const int item = static_cast<int>(at / keys.units), uo = static_cast<int>(at % keys.units);
+    const int h = item / a.tiles, r0 = item % a.tiles * 8 * NT;
+    const int take = static_cast<int>(min(static_cast<long long>(keys.units - uo), end - u));
+    const int c_first = keys.c0 + kAttnWarps * uo + w;
+    const int c_end = min(keys.c1, keys.c0 + kAttnWarps * (uo + take));
+    const int count = c_first < c_end ? (c_end - c_first + kAttnWarps - 1) / kAttnWarps : 0;
+    const int32_t *const table = a.table + static_cast<size_t>(seq) * a.width;
+    const uint8_t *const cache = a.cache + static_cast<size_t>(h) * blk;
+
+    // The page of this lane's piece of chunk i (-1: none), and the copy of a chunk.
+    auto page_of = [&](int i) {
+      const int token = (c_first + kAttnWarps * i) * kChunk + lane * a.ps;
+      return i < count && lane < pieces && token < len && token < a.width * a.ps ? table[token / a.ps] : -1;
+    };
+    auto issue = [&](int page, int s) {
+      const bool real = page >= 0 && page < a.pages;
+      const uint32_t bar = smem_u32(&sh.full[w][s]);
+      const uint32_t mask = __ballot_sync(kAll, real);
+      if (lane == 0) mbar_arrive_expect_tx(bar, __popc(mask) * blk);
+      __syncwarp();
+      if (real)
+        bulk_load(smem_u32(ring + s * Sh::kStageBytes + lane * blk),
+                  cache + static_cast<size_t>(page) * a.hk * blk, blk, bar);
+      held = (held & ~(15 << 4 * s)) | static_cast<int>(mask) << 4 * s;
+    };
+    int ahead = slot;  // the stage of the next copy
+#pragma unroll
+    for (int i = 0; i < Sh::kStages; ++i) {
+      if (i < count) {
+        issue(page_of(i), ahead);
+        ahead = ahead + 1 == Sh::kStages ? 0 : ahead + 1;
+      }
+    }
+    int page = page_of(Sh::kStages);
+
+    // Queries as FP16, each row times a power of two that brings its largest value
+    // to [2^14, 2^15): exact but for values 2^38 times smaller than that one. Lane
+    // (g, j) holds row g of each N tile, the j-th quarter of the columns.
+    uint32_t qf[NT][kSteps][2];
+    float c[NT][2];  // what a score is multiplied with, rows 2 j and 2 j + 1
+    int last[NT][2];  // one past the last key that a row sees
+    uint32_t unseen = 0;  // rows (bit 2 nt + e) without any key so far
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = r0 + 8 * nt + g;
+      uint4 v[D / 32];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) v[i] = make_uint4(0, 0, 0, 0);
+      if (r < a.rows) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            a.q + (static_cast<size_t>(seq) * a.t + r / a.group) * a.q_stride +
+            (h * a.group + r % a.group) * D + j * (D / 4));
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) v[i] = src[i];
+      }
+      uint32_t most = 0;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) most = max(most, max(x[q] & 0x7FFFu, x[q] >> 16 & 0x7FFFu));
+      }
+      most = max(most, __shfl_xor_sync(kAll, most, 1));
+      most = max(most, __shfl_xor_sync(kAll, most, 2));
+      const int shift = 14 - max(static_cast<int>(most >> 7) - 127, -126);
+      // two factors, as 2^shift alone may not be an FP32 number
+      const float f0 = __uint_as_float((127 + shift / 2) << 23), f1 = __uint_as_float((127 + shift - shift / 2) << 23);
+      const float back = c_all * __uint_as_float((127 - shift / 2) << 23) * __uint_as_float((127 - shift + shift / 2) << 23);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          qf[nt][2 * i + q / 2][q & 1] = cvt_f16x2(__uint_as_float(x[q] << 16) * f0 * f1,
+                                                   __uint_as_float(x[q] & 0xFFFF0000u) * f0 * f1);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        c[nt][e] = __shfl_sync(kAll, back, 4 * (2 * j + e));
+        const int row = r0 + 8 * nt + 2 * j + e;
+        last[nt][e] = row < a.rows ? min(len - a.t + row / a.group + 1, a.width * a.ps) : 0;
+        if (last[nt][e] > 0) unseen |= 1u << (2 * nt + e);
+      }
+    }
+
+    float o[kMt][NT][4], base[NT][2], sum[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < kMt; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[i][nt][q] = 0.0f;
+      base[nt][0] = base[nt][1] = sum[nt][0] = sum[nt][1] = 0.0f;
+    }
+
+    for (int i = 0; i < count && !lost; ++i) {
+      const int from = (c_first + kAttnWarps * i) * kChunk;
+      if (!mbar_wait_bounded(smem_u32(&sh.full[w][slot]), phase, kCacheWaitNs)) {
+        if (lane == 0) atomicOr(&g_cache_status, SK_DEVICE_WAIT_PRODUCER);
+        lost = true;
+      }
+      lost = __any_sync(kAll, lost);
+      if (lost) break;
+      const uint8_t *const st = ring + slot * Sh::kStageBytes;
+      const int have = held >> 4 * slot & 15;
+      // every token of the chunk is there and seen by every row
+      const bool whole = have == (1 << pieces) - 1 && from + kChunk <= len - a.t + 1 &&
+                         from + kChunk <= a.width * a.ps && (!a.window || from >= len - a.window);
+#pragma unroll
+      for (int part = 0; part < 4 / kSub; ++part) {
+        float s[kSub][NT][4];
+#pragma unroll
+        for (int m = 0; m < kSub; ++m) {
+          const int mt = part * kSub + m;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) s[m][nt][q] = 0.0f;
+          uint32_t k0[D / 32], k1[D / 32];
+          uint32_t sc0[D / 64], sc1[D / 64];
+          if constexpr (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(st + k_at0 + mt * 4 * (D / 2));
+            const uint4 y = *reinterpret_cast<const uint4 *>(st + k_at1 + mt * 4 * (D / 2));
+            k0[0] = x.x, k0[1] = x.y, k0[2] = x.z, k0[3] = x.w;
+            k1[0] = y.x, k1[1] = y.y, k1[2] = y.z, k1[3] = y.w;
+            const uint32_t p = widen_e4m3(*reinterpret_cast<const uint16_t *>(st + ks_at0 + mt * 4 * (D / 16)));
+            const uint32_t q = widen_e4m3(*reinterpret_cast<const uint16_t *>(st + ks_at1 + mt * 4 * (D / 16)));
+            sc0[0] = __byte_perm(p, 0, 0x1010), sc0[1] = __byte_perm(p, 0, 0x3232);
+            sc1[0] = __byte_perm(q, 0, 0x1010), sc1[1] = __byte_perm(q, 0, 0x3232);
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2 *>(st + k_at0 + mt * 4 * (D / 2));
+            const uint2 y = *reinterpret_cast<const uint2 *>(st + k_at1 + mt * 4 * (D / 2));
+            k0[0] = x.x, k0[1] = x.y;
+            k1[0] = y.x, k1[1] = y.y;
+            const uint32_t p = widen_e4m3(st[ks_at0 + mt * 4 * (D / 16)]);
+            const uint32_t q = widen_e4m3(st[ks_at1 + mt * 4 * (D / 16)]);
+            sc0[0] = __byte_perm(p, 0, 0x1010);
+            sc1[0] = __byte_perm(q, 0, 0x1010);
+          }
+#pragma unroll
+          for (int wd = 0; wd < D / 32; ++wd) {
+            uint32_t x[4], y[4];
+            widen_e2m1(k0[wd], x);
+            widen_e2m1(k1[wd], y);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              x[q] = mul_f16x2(x[q], sc0[wd / 2]);
+              y[q] = mul_f16x2(y[q], sc1[wd / 2]);
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_f16(s[m][nt], x[2 * q], y[2 * q], x[2 * q + 1], y[2 * q + 1], qf[nt][2 * wd + q][0],
+                        qf[nt][2 * wd + q][1]);
+          }
+        }
+
+        // scores relative to the base of their row, as powers of two
+#pragma unroll
+        for (int m = 0; m < kSub; ++m)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              s[m][nt][q] = fmaf(s[m][nt][q], c[nt][q & 1], -base[nt][q & 1]);
+        if (!whole) {
+          const bool there = have >> (16 * gj / a.ps) & 1;
+#pragma unroll
+          for (int m = 0; m < kSub; ++m)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int token = from + 16 * gj + 4 * (part * kSub + m) + (((q & 2) + ge) ^ fk);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                if (!there || token >= last[nt][q & 1] || (a.window && token < last[nt][q & 1] - a.window))
+                  s[m][nt][q] = -CUDART_INF_F;
+            }
+        }
+        float most = -CUDART_INF_F;
+#pragma unroll
+        for (int m = 0; m < kSub; ++m)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) most = fmaxf(most, s[m][nt][q]);
+        if (__any_sync(kAll, unseen != 0 || most > kTop)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = -CUDART_INF_F;
+#pragma unroll
+              for (int m = 0; m < kSub; ++m) x = fmaxf(x, fmaxf(s[m][nt][e], s[m][nt][2 + e]));
+              x = fmaxf(x, __shfl_xor_sync(kAll, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(kAll, x, 8));
+              x = fmaxf(x, __shfl_xor_sync(kAll, x, 16));
+              const uint32_t bit = 1u << (2 * nt + e);
+              float by = x > kAim ? x - kAim : 0.0f, f = ex2(-by);
+              if (unseen & bit) {  // the row's first keys set its base
+                by = x == -CUDART_INF_F ? 0.0f : x - kAim;
+                f = 1.0f;
+                if (x != -CUDART_INF_F) unseen &= ~bit;
+              }
+              base[nt][e] += by;
+              sum[nt][e] *= f;
+#pragma unroll
+              for (int m = 0; m < kSub; ++m) {
+                s[m][nt][e] -= by;
+                s[m][nt][2 + e] -= by;
+              }
+#pragma unroll
+              for (int i2 = 0; i2 < kMt; ++i2) {
+                o[i2][nt][e] *= f;
+                o[i2][nt][2 + e] *= f;
+              }
+            }
+        }
+        uint32_t p[kSub][NT][2];
+#pragma unroll
+        for (int m = 0; m < kSub; ++m)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              s[m][nt][q] = ex2(s[m][nt][q]);
+              sum[nt][q & 1] += s[m][nt][q];
+            }
+            p[m][nt][0] = transpose8(cvt_f16x2(s[m][nt][0], s[m][nt][1]));
+            p[m][nt][1] = transpose8(cvt_f16x2(s[m][nt][2], s[m][nt][3]));
+          }
+
+        // this lane's scales of V for its 16 tokens, in the order of the rows
+        uint32_t vs[kSub];
+        if constexpr (kSub == 4) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(st + vs_at);
+          vs[0] = x.x, vs[1] = x.y, vs[2] = x.z, vs[3] = x.w;
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2 *>(st + vs_at + 8 * part);
+          vs[0] = x.x, vs[1] = x.y;
+        }
+#pragma unroll
+        for (int m = 0; m < kSub; ++m) {
+          const int mt = part * kSub + m;
+          if (!whole) {  // what is not seen weighs 0, but its scale may be no number
+            const bool there = have >> (16 * j / a.ps) & 1;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int token = from + 16 * j + 4 * mt + q;
+              if (!there || token >= len || token >= a.width * a.ps) vs[m] &= ~(0xFFu << 8 * q);
+            }
+          }
+          const uint32_t order = __byte_perm(vs[m], 0, vs_order);
+          const uint32_t f0 = widen_e4m3(order & 0xFFFFu), f1 = widen_e4m3(order >> 16);
+          constexpr int kWords = D / 64;
+          uint32_t v[4][kWords];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint8_t *src = st + v_at + (4 * mt + (q ^ fv)) * (D / 2);
+            if constexpr (D == 128) {
+              const uint2 x = *reinterpret_cast<const uint2 *>(src);
+              v[q][0] = x.x, v[q][1] = x.y;
+            } else {
+              v[q][0] = *reinterpret_cast<const uint32_t *>(src);
+            }
+          }
+          // bytes of (code of one token, code of the next) for the even and odd columns
+          auto even = [](uint32_t x, uint32_t y) { return (x & 0x0F0F0F0Fu) | (y << 4 & 0xF0F0F0F0u); };
+          auto odd = [](uint32_t x, uint32_t y) { return (x >> 4 & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u); };
+          if constexpr (D == 128) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t x[4][4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const uint32_t l = v[q & 2][q & 1], r = v[(q & 2) + 1][q & 1];
+                widen_e2m1(half ? odd(l, r) : even(l, r), x[q]);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) x[q][y] = mul_f16x2(x[q][y], q & 2 ? f1 : f0);
+              }
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_f16(o[4 * half + y][nt], x[0][y], x[1][y], x[2][y], x[3][y], p[m][nt][0], p[m][nt][1]);
+            }
+          } else {
+            uint32_t x[4][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t l = v[q & 2][0], r = v[(q & 2) + 1][0];
+              widen_e2m1(q & 1 ? odd(l, r) : even(l, r), x[q]);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) x[q][y] = mul_f16x2(x[q][y], q & 2 ? f1 : f0);
+            }
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_f16(o[y][nt], x[0][y], x[1][y], x[2][y], x[3][y], p[m][nt][0], p[m][nt][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (i + Sh::kStages < count) {
+        issue(page, slot);
+        page = page_of(i + Sh::kStages + 1);
+      }
+      if (++slot == Sh::kStages) {
+        slot = 0;
+        phase ^= 1;
+      }
+    }
+
+    // The four warps' sums, joined: each leaves its own in its ring, and warp w
+    // finishes two channels of every 16.
+    float *const mine = reinterpret_cast<float *>(ring);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float l = sum[nt][e];
+        l += __shfl_xor_sync(kAll, l, 4);
+        l += __shfl_xor_sync(kAll, l, 8);
+        l += __shfl_xor_sync(kAll, l, 16);
+        if (g == 0) sh.stat[w][8 * nt + 2 * j + e] = make_float2(l == 0.0f ? -CUDART_INF_F : base[nt][e], l);
+      }
+    if (!lost) {
+#pragma unroll
+      for (int i = 0; i < kMt; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mine[((i * NT + nt) * 4 + q) * 32 + lane] = o[i][nt][q];
+    }
+    if (__syncthreads_or(lost)) {
+      // a copy never landed: wait for those in flight, within the same limit, and leave
+      for (int s = 0; lost && s < Sh::kStages; ++s)
+        mbar_wait_bounded(smem_u32(&sh.full[w][s]), phase ^ (s < slot), kCacheWaitNs);
+      return;
+    }
+    float2 st[NT][2];
+    float f[kAttnWarps][NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * nt + 2 * j + e;
+        float top = -CUDART_INF_F, l = 0.0f;
+#pragma unroll
+        for (int x = 0; x < kAttnWarps; ++x) top = fmaxf(top, sh.stat[x][r].x);
+#pragma unroll
+        for (int x = 0; x < kAttnWarps; ++x) {
+          const float2 v = sh.stat[x][r];
+          f[x][nt][e] = v.x == -CUDART_INF_F ? 0.0f : ex2(v.x - top);
+          l = fmaf(f[x][nt][e], v.y, l);
+        }
+        st[nt][e] = make_float2(top, l);
+      }
+    float acc[D / 64][NT][4];
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int at32 = (((w + 4 * k) * NT + nt) * 4 + q) * 32 + lane;
+          float v = 0.0f;
+#pragma unroll
+          for (int x = 0; x < kAttnWarps; ++x)
+            v = fmaf(f[x][nt][q & 1], reinterpret_cast<const float *>(sh.ring[x])[at32], v);
+          acc[k][nt][q] = v;
+        }
+    if (take == keys.units) {
+      attn_store<D, NT>(a, seq, h, r0, acc, st, v_inv);
+    } else {
+      float *part = a.parts + (2 * static_cast<size_t>(blockIdx.x) + (first ? 0 : 1)) * attn_part_floats(D, NT);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (w == 0 && g == 0) reinterpret_cast<float2 *>(part)[8 * nt + 2 * j + e] = st[nt][e];
+#pragma unroll
+      for (int k = 0; k < D / 64; ++k)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            part[16 * NT + (((w + 4 * k) * NT + nt) * 4 + q) * 32 + lane] = acc[k][nt][q];
+    }
+    fence_proxy_async_smem();
+    __syncthreads();  // the rings are free again
+    first = false;
+    u += take;
+    at += take;
+    while (u < end && at >= static_cast<long long>(keys_of(a, a.lens[seq]).units) * per) {
+      at = 0;
+      ++seq;
+    }
+  }
+}
+
+// Joins the items that fell into several parts, and writes the zeros of those that
+// see nothing. A CTA per item.
+template <int D, int NT>
+__global__ void __launch_bounds__(kAttnThreads) attn_join_kernel(const __grid_constant__ AttnArgs a, int G) {
+  __shared__ long long sums[kAttnWarps];
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, j = lane & 3;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int per = a.hk * a.tiles, seq = blockIdx.x / per, item = blockIdx.x % per;
+  long long U = 0, before = 0;
+  for (int s = tid; s < a.b; s += kAttnThreads) {
+    const int n = keys_of(a, a.lens[s]).units;
+    U += static_cast<long long>(n) * per;
+    if (s < seq) before += static_cast<long long>(n) * per;
+  }
+  U = cta_sum(U, sums);
+  before = cta_sum(before, sums);
+  const int n = keys_of(a, a.lens[seq]).units;
+  long long c0 = 0, c1 = 0;
+  bool inside = true;  // the item starts within part c0, not with it
+  if (n) {
+    const long long u0 = before + static_cast<long long>(item) * n;
+    c0 = part_of(U, G, u0), c1 = part_of(U, G, u0 + n - 1);
+    if (c0 == c1) return;  // written where it was computed
+    inside = part_start(U, G, c0) < u0;
+  } else {
+    c1 = -1;
+  }
+  float2 st[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) st[nt][e] = make_float2(-CUDART_INF_F, 0.0f);
+  auto part = [&](long long c) {
+    return a.parts + static_cast<size_t>(2 * c + (c == c0 && inside ? 1 : 0)) * attn_part_floats(D, NT);
+  };
+  for (long long c = c0; c <= c1; ++c) {
+    const float2 *p = reinterpret_cast<const float2 *>(part(c));
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) st[nt][e].x = fmaxf(st[nt][e].x, p[8 * nt + 2 * j + e].x);
+  }
+  float acc[D / 64][NT][4] = {};
+  for (long long c = c0; c <= c1; ++c) {
+    const float *p = part(c);
+    float f[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float2 v = reinterpret_cast<const float2 *>(p)[8 * nt + 2 * j + e];
+        f[nt][e] = v.x == -CUDART_INF_F ? 0.0f : ex2(v.x - st[nt][e].x);
+        st[nt][e].y = fmaf(f[nt][e], v.y, st[nt][e].y);
+      }
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          acc[k][nt][q] = fmaf(f[nt][q & 1], p[16 * NT + (((w + 4 * k) * NT + nt) * 4 + q) * 32 + lane], acc[k][nt][q]);
+  }
+  attn_store<D, NT>(a, seq, item / a.tiles, item % a.tiles * 8 * NT, acc, st, 1.0f / *a.v_gs);
+}
+
+// ------------------------------------------------------------------- append
+// A thread per 16 columns of a token's K or V head.
+constexpr int kAppendThreads = 256;
+
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int blocks = a.d / 16;
+  const long long i = static_cast<long long>(blockIdx.x) * kAppendThreads + threadIdx.x;
+  const int block = static_cast<int>(i % blocks);
+  const int h = static_cast<int>(i / blocks % a.hk);
+  const long long token = i / blocks / a.hk;
+  if (token >= static_cast<long long>(a.b) * a.t) return;
+  const int seq = static_cast<int>(token / a.t);
+  const long long pos = static_cast<long long>(a.lens[seq]) - a.t + token % a.t;
+  if (pos < 0 || pos >= static_cast<long long>(a.width) * a.ps) return;
+  const int page = a.table[static_cast<size_t>(seq) * a.width + pos / a.ps];
+  if (page < 0 || page >= a.pages) return;
+  const int at = static_cast<int>(pos % a.ps);
+  const bool value = blockIdx.y;
+  const uint16_t *src = value ? a.v + token * a.v_stride : a.k + token * a.k_stride;
+  const uint4 *sp = reinterpret_cast<const uint4 *>(src + h * a.d + 16 * block);
+  const uint4 x = sp[0], y = sp[1];
+  const uint32_t words[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  uint16_t z[16];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    z[2 * q] = static_cast<uint16_t>(words[q]);
+    z[2 * q + 1] = static_cast<uint16_t>(words[q] >> 16);
+  }
+  uint2 packed;
+  const uint32_t sf = nvfp4_block16(z, value ? *a.v_gs : *a.k_gs, packed);
+  const int codes = a.ps * a.d / 2, scales = a.ps * blocks;
+  uint8_t *base = a.cache + (static_cast<size_t>(page) * a.hk + h) * (2 * codes + 2 * scales);
+  *reinterpret_cast<uint2 *>(base + (value ? codes : 0) + at * (a.d / 2) + 8 * block) = packed;
+  base[2 * codes + (value ? scales + block * a.ps + at : at * blocks + block)] = static_cast<uint8_t>(sf);
+}
+
+// -------------------------------------------------------------------- pages
+constexpr int kPageThreads = 1024;
+
+// Exclusive prefix sum over a CTA of kPageThreads threads; total in `all`.
+__device__ __forceinline__ int cta_scan(int v, int *warps, int &all) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int upto = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(kAll, upto, d);
+    if (lane >= d) upto += o;
+  }
+  if (lane == 31) warps[w] = upto;
+  __syncthreads();
+  if (w == 0) {
+    int x = warps[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(kAll, x, d);
+      if (lane >= d) x += o;
+    }
+    warps[lane] = x;
+  }
+  __syncthreads();
+  all = warps[31];
+  const int before = upto - v + (w ? warps[w - 1] : 0);
+  __syncthreads();
+  return before;
+}
+
+// What becomes of a row: its length before and after, the first of its fresh
+// pages, and whether that one is a copy of its last page.
+struct RowPlan {
+  int old_len, new_len, first, copy;
+};
+
+struct ResizeShared {
+  int need[SK_MAX_CACHE_ROWS];    // fresh pages of each row, then the sum before it
+  int page[SK_MAX_CACHE_ROWS];    // rows that grow from a page that others hold too:
+  int who[SK_MAX_CACHE_ROWS];     //   the page, the row,
+  int before[SK_MAX_CACHE_ROWS];  //   the copying row before it (-1: none), -2: this one copies
+  int warps[32];
+};
+
+__global__ void __launch_bounds__(kPageThreads) kv_resize_plan_kernel(const __grid_constant__ ResizeArgs a) {
+  extern __shared__ __align__(128) uint8_t raw[];
+  ResizeShared &sh = *reinterpret_cast<ResizeShared *>(raw);
+  const int tid = threadIdx.x;
+  griddep_launch_dependents();
+  griddep_wait();
+  RowPlan *plan = reinterpret_cast<RowPlan *>(a.plan);
+  const int most = a.width * a.ps;
+  int sharers = 0, all;
+  for (int base = 0; base < a.rows; base += kPageThreads) {
+    const int row = base + tid;
+    bool shared = false;
+    int page = -1;
+    if (row < a.rows) {
+      const int old = a.lens[row], want = a.new_lens[row];
+      const bool bad = old < 0 || old > most || want > most;
+      const int next = bad || want < 0 ? old : want;
+      const int have = bad ? 0 : ceil_div(old, a.ps);
+      if (!bad && next > old && old % a.ps) {
+        page = a.table[static_cast<size_t>(row) * a.width + have - 1];
+        shared = page >= 0 && page < a.pages && a.refs[page] > 1;
+      }
+      sh.need[row] = !bad && next > old ? ceil_div(next, a.ps) - have : 0;
+      a.status[row] = bad ? 2 : 0;
+    }
+    const int at = sharers + cta_scan(shared, sh.warps, all);
+    if (shared) {
+      sh.page[at] = page;
+      sh.who[at] = row;
+    }
+    sharers += all;
+  }
+  __syncthreads();
+  // In the order of rows, who holds a page as its last keeps it; the others copy it.
+  for (int i = tid; i < sharers; i += kPageThreads) {
+    int rank = 0, latest = -1;
+    for (int k = 0; k < i; ++k)
+      if (sh.page[k] == sh.page[i]) {
+        ++rank;
+        latest = sh.who[k];
+      }
+    const bool copies = rank < a.refs[sh.page[i]] - 1;
+    sh.before[i] = copies ? -2 : latest;
+    if (copies) ++sh.need[sh.who[i]];
+  }
+  __syncthreads();
+  int total = 0;
+  for (int base = 0; base < a.rows; base += kPageThreads) {
+    const int row = base + tid;
+    const int need = row < a.rows ? sh.need[row] : 0;
+    const int at = total + cta_scan(need, sh.warps, all);
+    if (row < a.rows) plan[row] = {a.lens[row], need, at, 0};
+    total += all;
+  }
+  // The free pages, lowest number first, as many as are needed.
+  int got = 0;
+  for (int base = 0; base < a.pages && got < total; base += 4 * kPageThreads) {
+    const int p = base + 4 * tid;
+    int4 r = make_int4(1, 1, 1, 1);
+    if (p + 3 < a.pages && a.refs_vector) {
+      r = *reinterpret_cast<const int4 *>(a.refs + p);
+    } else {
+      if (p < a.pages) r.x = a.refs[p];
+      if (p + 1 < a.pages) r.y = a.refs[p + 1];
+      if (p + 2 < a.pages) r.z = a.refs[p + 2];
+      if (p + 3 < a.pages) r.w = a.refs[p + 3];
+    }
+    const int n = (r.x <= 0) + (r.y <= 0) + (r.z <= 0) + (r.w <= 0);
+    int at = got + cta_scan(n, sh.warps, all);
+    if (r.x <= 0 && at < total) a.fresh[at] = p;
+    at += r.x <= 0;
+    if (r.y <= 0 && at < total) a.fresh[at] = p + 1;
+    at += r.y <= 0;
+    if (r.z <= 0 && at < total) a.fresh[at] = p + 2;
+    at += r.z <= 0;
+    if (r.w <= 0 && at < total) a.fresh[at] = p + 3;
+    got += all;
+  }
+  __syncthreads();
+  // Rows whose pages are not there are refused, and one that was to keep a page
+  // which a refused row before it still holds.
+  for (int row = tid; row < a.rows; row += kPageThreads) {
+    const RowPlan r = plan[row];
+    const bool bad = a.status[row] != 0, refused = !bad && r.new_len > 0 && r.first + r.new_len > got;
+    const int want = a.new_lens[row];
+    if (refused) a.status[row] = 1;
+    sh.need[row] = refused;
+    plan[row] = {r.old_len, bad || refused || want < 0 ? r.old_len : want, r.first, 0};
+  }
+  __syncthreads();
+  int copies = 0;
+  for (int base = 0; base < sharers; base += kPageThreads) {
+    const int i = base + tid;
+    bool copy = false;
+    if (i < sharers) {
+      const int row = sh.who[i];
+      copy = sh.before[i] == -2 && !sh.need[row];
+      if (copy) plan[row].copy = 1;
+      if (sh.before[i] >= 0 && sh.need[sh.before[i]]) {
+        a.status[row] = 1;
+        plan[row].new_len = plan[row].old_len;
+      }
+    }
+    const int at = copies + cta_scan(copy, sh.warps, all);
+    if (copy) a.copies[at] = make_int2(sh.page[i], a.fresh[plan[sh.who[i]].first]);
+    copies += all;
+  }
+  if (tid == 0) *a.count = copies;
+}
+
+// Copies pages (source, destination) of every layer: runs of page_bytes, in pieces
+// of kCopyBytes spread over the grid.
+constexpr int kCopyThreads = 256;
+constexpr int kCopyUnroll = 8;
+constexpr int kCopyBytes = 16 * kCopyThreads * kCopyUnroll;
+
+template <typename Pair>
+__device__ __forceinline__ void copy_pages(uint8_t *cache, int layers, size_t layer_bytes, int page_bytes, int count,
+                                           Pair pair) {
+  const int pieces = ceil_div(page_bytes, kCopyBytes);
+  const long long all = static_cast<long long>(count) * layers * pieces;
+  for (long long i = blockIdx.x; i < all; i += gridDim.x) {
+    const int2 move = pair(static_cast<int>(i / pieces / layers));
+    uint8_t *layer = cache + static_cast<size_t>(i / pieces % layers) * layer_bytes;
+    const int at = static_cast<int>(i % pieces) * kCopyBytes + 16 * threadIdx.x;
+    const uint8_t *from = layer + static_cast<size_t>(move.x) * page_bytes;
+    uint8_t *to = layer + static_cast<size_t>(move.y) * page_bytes;
+    uint4 v[kCopyUnroll];
+#pragma unroll
+    for (int k = 0; k < kCopyUnroll; ++k)
+      if (at + k * 16 * kCopyThreads < page_bytes)
+        v[k] = *reinterpret_cast<const uint4 *>(from + at + k * 16 * kCopyThreads);
+#pragma unroll
+    for (int k = 0; k < kCopyUnroll; ++k)
+      if (at + k * 16 * kCopyThreads < page_bytes)
+        *reinterpret_cast<uint4 *>(to + at + k * 16 * kCopyThreads) = v[k];
+  }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) kv_resize_apply_kernel(const __grid_constant__ ResizeArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const RowPlan *plan = reinterpret_cast<const RowPlan *>(a.plan);
+  for (int row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const RowPlan r = plan[row];
+    if (r.new_len == r.old_len) continue;
+    int32_t *table = a.table + static_cast<size_t>(row) * a.width;
+    const int have = ceil_div(r.old_len, a.ps), after = ceil_div(r.new_len, a.ps);
+    if (threadIdx.x == 0) {
+      a.lens[row] = r.new_len;
+      if (r.copy) {
+        const int page = a.fresh[r.first];
+        atomicSub(a.refs + table[have - 1], 1);
+        a.refs[page] = 1;
+        table[have - 1] = page;
+      }
+    }
+    for (int c = have + threadIdx.x; c < after; c += kCopyThreads) {
+      const int page = a.fresh[r.first + r.copy + c - have];
+      table[c] = page;
+      a.refs[page] = 1;
+    }
+    for (int c = after + threadIdx.x; c < have; c += kCopyThreads) {
+      const int page = table[c];
+      if (page >= 0 && page < a.pages) atomicSub(a.refs + page, 1);
+      table[c] = -1;
+    }
+  }
+  copy_pages(a.cache, a.layers, a.layer_bytes, a.page_bytes, *a.count, [&](int i) { return a.copies[i]; });
+}
+
+// A CTA takes eight columns of the table, of all rows: what a row becomes depends on
+// other rows in these columns alone, which it reads before it writes.
+constexpr int kForkCols = 8;
+constexpr int kForkThreads = 512;
+
+__global__ void __launch_bounds__(kForkThreads) kv_fork_kernel(const __grid_constant__ ForkArgs a) {
+  extern __shared__ __align__(128) uint8_t raw[];
+  int32_t *old = reinterpret_cast<int32_t *>(raw);  // [rows][kForkCols]; -1 where a row has no page
+  griddep_launch_dependents();
+  griddep_wait();
+  const int c0 = blockIdx.x * kForkCols, n = a.rows * kForkCols;
+  for (int i = threadIdx.x; i < n; i += kForkThreads) {
+    const int row = i / kForkCols, c = c0 + i % kForkCols;
+    const int len = min(max(a.lens[row], 0), a.width * a.ps);
+    old[i] = c < ceil_div(len, a.ps) ? a.table[static_cast<size_t>(row) * a.width + c] : -1;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kForkThreads) {
+    const int row = i / kForkCols, c = c0 + i % kForkCols, p = a.parents[row];
+    if (c >= a.width || p < 0 || p >= a.rows || p == row) continue;
+    const int gone = old[i], got = old[p * kForkCols + i % kForkCols];
+    if (gone != got) {
+      if (gone >= 0 && gone < a.pages) atomicSub(a.refs + gone, 1);
+      if (got >= 0 && got < a.pages) atomicAdd(a.refs + got, 1);
+    }
+    a.table[static_cast<size_t>(row) * a.width + c] = got;
+  }
+}
+
+// The lengths of forked rows, after their tables: one CTA, which reads all before it writes.
+__global__ void __launch_bounds__(kPageThreads) kv_fork_lens_kernel(const __grid_constant__ ForkArgs a) {
+  __shared__ int32_t old[SK_MAX_CACHE_ROWS];
+  griddep_launch_dependents();
+  griddep_wait();
+  for (int row = threadIdx.x; row < a.rows; row += kPageThreads) old[row] = a.lens[row];
+  __syncthreads();
+  for (int row = threadIdx.x; row < a.rows; row += kPageThreads) {
+    const int p = a.parents[row];
+    a.status[row] = p >= a.rows ? 2 : 0;
+    if (p >= 0 && p < a.rows && p != row) a.lens[row] = old[p];
+  }
+}
+
+// Of L pages in use, those numbered L and up move to the free ones below L, k-th to
+// k-th, so no page is both source and destination.
+__global__ void __launch_bounds__(kPageThreads) kv_compact_plan_kernel(const __grid_constant__ CompactArgs a) {
+  __shared__ int warps[32];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int tid = threadIdx.x;
+  int used = 0, all;
+  for (int p = tid; p < a.pages; p += kPageThreads) used += a.refs[p] > 0;
+  cta_scan(used, warps, used);
+  int holes = 0, moved = 0;
+  for (int base = 0; base < a.pages; base += kPageThreads) {
+    const int p = base + tid;
+    const bool in = p < a.pages, live = in && a.refs[p] > 0;
+    const bool hole = in && !live && p < used, moves = live && p >= used;
+    const int h = holes + cta_scan(hole, warps, all);
+    holes += all;
+    const int m = moved + cta_scan(moves, warps, all);
+    moved += all;
+    if (hole) a.holes[h] = p;
+    if (moves) a.moves[m] = p;
+    if (in) a.page_map[p] = live ? p : -1;
+  }
+  __syncthreads();
+  for (int m = tid; m < moved; m += kPageThreads) a.page_map[a.moves[m]] = a.holes[m];
+  if (tid == 0) *a.count = moved;
+}
+
+__global__ void __launch_bounds__(kCopyThreads) kv_compact_apply_kernel(const __grid_constant__ CompactArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int count = *a.count;
+  const long long step = static_cast<long long>(gridDim.x) * kCopyThreads;
+  const long long first = static_cast<long long>(blockIdx.x) * kCopyThreads + threadIdx.x;
+  for (long long m = first; m < count; m += step) {
+    a.refs[a.holes[m]] = a.refs[a.moves[m]];
+    a.refs[a.moves[m]] = 0;
+  }
+  const long long entries = static_cast<long long>(a.rows) * a.width;
+  for (long long i = first; i < entries; i += step) {
+    const int row = static_cast<int>(i / a.width), c = static_cast<int>(i % a.width);
+    const int len = min(max(a.lens[row], 0), a.width * a.ps);
+    if (c >= ceil_div(len, a.ps)) continue;
+    const int page = a.table[i];
+    if (page >= 0 && page < a.pages) a.table[i] = a.page_map[page];
+  }
+  copy_pages(a.cache, a.layers, a.layer_bytes, a.page_bytes, count,
+             [&](int m) { return make_int2(a.moves[m], a.holes[m]); });
+}
+
+// Calls f with the attention kernels' instance for a head size and rows per tile.
+template <typename F>
+cudaError_t with_attn(int d, int nt, F f) {
+  auto at = [&](auto dim) {
+    constexpr int D = decltype(dim)::value;
+    if (nt == 1) return f(std::integral_constant<int, D>(), std::integral_constant<int, 1>());
+    if (nt == 2) return f(std::integral_constant<int, D>(), std::integral_constant<int, 2>());
+    return f(std::integral_constant<int, D>(), std::integral_constant<int, 4>());
+  };
+  return d == 64 ? at(std::integral_constant<int, 64>()) : at(std::integral_constant<int, 128>());
+}
+
+}  // namespace
+
+int attn_row_tiles(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+
+size_t attn_part_bytes(int d, int nt) { return sizeof(float) * attn_part_floats(d, nt); }
+
+int attn_max_parts(int nt, int sm_count) { return attn_per_sm(nt) * sm_count; }
+
+cudaError_t launch_attn(const AttnArgs &a, int d, int sm_count, cudaStream_t stream, bool pdl) {
+  const int nt = attn_row_tiles(a.rows);
+  return with_attn(d, nt, [&](auto dim, auto tiles) {
+    constexpr int D = decltype(dim)::value, NT = decltype(tiles)::value;
+    // no more parts than there can be units
+    const long long units = static_cast<long long>(ceil_div(a.width * a.ps, kChunk * kAttnWarps) + 1) * a.b * a.hk * a.tiles;
+    const long long most = attn_max_parts(NT, sm_count);
+    const int grid = static_cast<int>(units < most ? units : most);
+    cudaError_t e = launch(attn_kernel<D, NT>, dim3(grid), dim3(kAttnThreads), sizeof(AttnShared<D, NT>), stream,
+                           pdl, a);
+    if (e != cudaSuccess) return e;
+    return launch(attn_join_kernel<D, NT>, dim3(static_cast<unsigned>(a.b) * a.hk * a.tiles), dim3(kAttnThreads), 0,
+                  stream, pdl, a, grid);
+  });
+}
+
+cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream, bool pdl) {
+  const long long threads = static_cast<long long>(a.b) * a.t * a.hk * (a.d / 16);
+  return launch(kv_append_kernel, dim3(static_cast<unsigned>((threads + kAppendThreads - 1) / kAppendThreads), 2),
+                dim3(kAppendThreads), 0, stream, pdl, a);
+}
+
+cudaError_t launch_kv_resize(const ResizeArgs &a, int sm_count, cudaStream_t stream, bool pdl) {
+  cudaError_t e = launch(kv_resize_plan_kernel, dim3(1), dim3(kPageThreads), sizeof(ResizeShared), stream, pdl, a);
+  if (e != cudaSuccess) return e;
+  return launch(kv_resize_apply_kernel, dim3(4 * sm_count), dim3(kCopyThreads), 0, stream, pdl, a);
+}
+
+cudaError_t launch_kv_fork(const ForkArgs &a, cudaStream_t stream, bool pdl) {
+  cudaError_t e = launch(kv_fork_kernel, dim3(ceil_div(a.width, kForkCols)), dim3(kForkThreads),
+                         sizeof(int32_t) * kForkCols * a.rows, stream, pdl, a);
+  if (e != cudaSuccess) return e;
+  return launch(kv_fork_lens_kernel, dim3(1), dim3(kPageThreads), 0, stream, pdl, a);
+}
+
+cudaError_t launch_kv_compact(const CompactArgs &a, int sm_count, cudaStream_t stream, bool pdl) {
+  cudaError_t e = launch(kv_compact_plan_kernel, dim3(1), dim3(kPageThreads), 0, stream, pdl, a);
+  if (e != cudaSuccess) return e;
+  return launch(kv_compact_apply_kernel, dim3(4 * sm_count), dim3(kCopyThreads), 0, stream, pdl, a);
+}
+
+cudaError_t cache_setup() {
+  cudaError_t e;
+  for (int d : {64, 128})
+    for (int nt : {1, 2, 4})
+      if ((e = with_attn(d, nt, [&](auto dim, auto tiles) {
+             constexpr int D = decltype(dim)::value, NT = decltype(tiles)::value;
+             return cudaFuncSetAttribute(attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(sizeof(AttnShared<D, NT>)));
+           })))
+        return e;
+  if ((e = cudaFuncSetAttribute(kv_resize_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(sizeof(ResizeShared)))))
+    return e;
+  return cudaFuncSetAttribute(kv_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(sizeof(int32_t) * kForkCols * SK_MAX_CACHE_ROWS));
+}
+
+cudaError_t read_cache_status(uint32_t *out, bool clear) {
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_cache_status, sizeof(uint32_t));
+  if (e != cudaSuccess || !clear) return e;
+  const uint32_t zero = 0;
+  return cudaMemcpyToSymbol(g_cache_status, &zero, sizeof zero);
+}
+
+}  // namespace sk

@@ -256,6 +256,74 @@ cudaError_t launch_experts_int8(const ExpertsArgs &a, int sm_count, cudaStream_t
 cudaError_t experts_setup();
 cudaError_t read_core_status(uint32_t *out, bool clear);
 
+// ------------------------------------------ the key/value cache held in 4 bits
+// Attention over it (sk_attn_nvfp4): rows = group * t rows per KV head, in `tiles`
+// tiles; parts is the caller's workspace, two results per CTA.
+struct AttnArgs {
+  const uint16_t *q;
+  const uint8_t *cache;
+  const float *k_gs, *v_gs;
+  const int32_t *table, *lens;
+  uint16_t *out;
+  float *lse;  // or null
+  float *parts;
+  int b, t, hq, hk, ps, pages, width, window;
+  int group, rows, tiles;
+  long long q_stride;  // values between tokens
+  float scale;
+};
+int attn_row_tiles(int rows);                   // tiles of 8 rows that a CTA takes at once
+int attn_max_parts(int nt, int sm_count);       // CTAs of such a launch, at most
+size_t attn_part_bytes(int d, int nt);          // bytes of a CTA's unfinished result
+cudaError_t launch_attn(const AttnArgs &a, int d, int sm_count, cudaStream_t stream, bool pdl);
+
+struct AppendArgs {
+  const uint16_t *k, *v;
+  const float *k_gs, *v_gs;
+  uint8_t *cache;
+  const int32_t *table, *lens;
+  int b, t, hk, d, ps, pages, width;
+  long long k_stride, v_stride;  // values between tokens
+};
+cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream, bool pdl);
+
+// Pages: the arrays from `plan` on are parts of the caller's workspace.
+struct ResizeArgs {
+  const int32_t *new_lens;
+  uint8_t *cache;
+  int32_t *table, *lens, *refs, *status;
+  int rows, width, pages, ps, layers, page_bytes;
+  size_t layer_bytes;
+  bool refs_vector;  // refs is 16-byte aligned
+  int4 *plan;        // [rows]
+  int2 *copies;      // [rows]
+  int32_t *fresh;    // [pages]
+  int32_t *count;    // copies made
+};
+cudaError_t launch_kv_resize(const ResizeArgs &a, int sm_count, cudaStream_t stream, bool pdl);
+
+struct ForkArgs {
+  const int32_t *parents;
+  int32_t *table, *lens, *refs, *status;
+  int rows, width, pages, ps;
+};
+cudaError_t launch_kv_fork(const ForkArgs &a, cudaStream_t stream, bool pdl);
+
+struct CompactArgs {
+  uint8_t *cache;
+  int32_t *table;
+  const int32_t *lens;
+  int32_t *refs, *page_map;
+  int rows, width, pages, ps, layers, page_bytes;
+  size_t layer_bytes;
+  int32_t *holes, *moves;  // [pages]
+  int32_t *count;          // pages moved
+};
+cudaError_t launch_kv_compact(const CompactArgs &a, int sm_count, cudaStream_t stream, bool pdl);
+
+cudaError_t cache_setup();
+cudaError_t read_cache_status(uint32_t *out, bool clear);
+
 // The current device, checked to be compute capability 10.3, set up.
 sk_status checked_device(DeviceInfo *info, int *device);
 bool pdl_on();

@@ -434,4 +434,28 @@ __device__ __forceinline__ float bf16_bits_to_f32(uint32_t b) {
   return __uint_as_float(b << 16);
 }
 
+// NVFP4 of one 16-element block of BF16 values (cutedsl/moe/pooler_gather:
+// module docstring and nvfp4_compute_output_scale; the block-scale formula is
+// our reading, (amax / 6) * gs, since the pages print only its inverse).
+// Writes the 8 packed code bytes (column 2c in the low nibble) and returns the
+// e4m3 scale byte. Every step is an IEEE FP32 operation.
+__device__ __forceinline__ uint32_t nvfp4_block16(const uint16_t (&z)[16], float gs,
+                                                  uint2 &packed) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(bf16_bits_to_f32(z[j])));
+  const float t = __fmul_rn(__fdiv_rn(amax, 6.0f), gs);
+  const uint32_t sf = cvt_f32_e4m3(t);
+  const float sff = cvt_e4m3_f32(sf);
+  const float os = (sff == 0.0f) ? 0.0f : __fdiv_rn(1.0f, __fmul_rn(sff, __fdiv_rn(1.0f, gs)));
+  uint32_t b[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    b[c] = cvt_f32x2_e2m1x2(__fmul_rn(bf16_bits_to_f32(z[2 * c]), os),
+                            __fmul_rn(bf16_bits_to_f32(z[2 * c + 1]), os));
+  packed.x = b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
+  packed.y = b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24);
+  return sf;
+}
+
 }  // namespace sk
