@@ -117,41 +117,40 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 // token 16 j + 4 mt + ((2 h + e) ^ f(j)); f = 0, 2, 1, 3 keeps the lanes of a
 // shared-memory access apart.
 //
-// The work is cut evenly whatever the lengths: units of 256 tokens of an item (a
-// sequence, a KV head, a tile of rows), item after item, in as many equal parts as
-// CTAs fit on the GPU. An item that falls into several parts is joined by
-// attn_join_kernel, in the order of its tokens.
+// The work is cut evenly whatever the lengths: the chunks of an item (a sequence, a
+// KV head, a tile of rows), item after item, in as many equal parts as the GPU holds
+// warps, an item's beginning counting like kItemCost chunks more. An item that falls
+// into several parts is joined by attn_join_kernel, in the order of its tokens. Warps
+// share nothing, and a CTA is all that fit on an SM: three CTAs of four did not always
+// fit beside the last CTAs of the kernel before (b64 d128, 5400 tokens on average:
+// 114 us, 85 where the kernel ran alone), and four warps that join their sums in
+// shared memory item by item waited for one another (93 us).
 constexpr int kChunk = 64;
-constexpr int kAttnWarps = 4;
-constexpr int kAttnThreads = 32 * kAttnWarps;
+constexpr int kItemCost = 1;
 // Scores are kept as powers of two relative to a base that is at most 15 and after
 // an update 7 below the largest, so that P fits FP16 and what is 2^31 times smaller
 // than the largest still counts; the base moves (and the sums are scaled) only
 // when a score exceeds it by 2^15.
 constexpr float kTop = 15.0f, kAim = 7.0f;
 
-__host__ __device__ constexpr int attn_per_sm(int nt) { return nt == 4 ? 2 : 3; }
+__host__ __device__ constexpr int attn_warps(int nt) { return nt == 4 ? 8 : 12; }
 
 template <int D, int NT>
-struct AttnShared {
+struct AttnWarp {
   static constexpr int kStageBytes = kChunk * D * 9 / 8;
   static constexpr int kStages = (D == 128 ? 1 : 2) * (NT == 4 ? 3 : 2);
-  alignas(128) uint8_t ring[kAttnWarps][kStages * kStageBytes];
-  uint64_t full[kAttnWarps][kStages];
-  float2 stat[kAttnWarps][8 * NT];  // base and sum of each row
-  long long at;                     // where the part starts: offset in its sequence
-  int seq;
-  long long sums[kAttnWarps];
+  alignas(128) uint8_t ring[kStages * kStageBytes];
+  uint64_t full[kStages];
 };
 
-// Registers of O^T per thread, and floats of a part's result: a base and a sum per
-// row, then register r of lane l at 32 r + l.
-__host__ __device__ constexpr int attn_regs(int d, int nt) { return d / 16 * nt * 4; }
-__host__ __device__ constexpr int attn_part_floats(int d, int nt) { return 16 * nt + 32 * attn_regs(d, nt); }
+// Floats of a part's result: a base and a sum per row, then the rows.
+__host__ __device__ constexpr int attn_part_floats(int d, int nt) { return 16 * nt + 8 * nt * d; }
 
 struct Keys {
   int c0, c1;  // chunks [c0, c1) of a sequence that some of its tokens see
-  int units;
+  __device__ int count() const { return max(c1 - c0, 0); }
+  // what an item of the sequence counts for
+  __device__ int cost() const { return c1 > c0 ? c1 - c0 + kItemCost : 0; }
 };
 
 __device__ __forceinline__ Keys keys_of(const AttnArgs &a, int len) {
@@ -160,114 +159,125 @@ __device__ __forceinline__ Keys keys_of(const AttnArgs &a, int len) {
   const int lo = a.window ? max(0, len - a.t - a.window + 1) : 0;
   k.c0 = lo / kChunk;
   k.c1 = ceil_div(hi, kChunk);
-  k.units = k.c1 > k.c0 ? ceil_div(k.c1 - k.c0, kAttnWarps) : 0;
   return k;
 }
 
-// Sum over the CTA of one value per thread.
-__device__ __forceinline__ long long cta_sum(long long v, long long *sums) {
+// What four sequences from s on count for, with all their items.
+__device__ __forceinline__ long long cost_of4(const AttnArgs &a, int s, long long (&n)[4]) {
+  int len[4];
 #pragma unroll
-  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0;
-  for (int w = 0; w < kAttnWarps; ++w) v += sums[w];
-  __syncthreads();
-  return v;
+  for (int k = 0; k < 4; ++k) len[k] = s + k < a.b ? a.lens[s + k] : 0;
+  long long sum = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    n[k] = static_cast<long long>(keys_of(a, len[k]).cost()) * (a.hk * a.tiles);
+    sum += n[k];
+  }
+  return sum;
 }
 
-// Part c of U units in G parts starts here: equal parts, the first U % G one longer.
-__device__ __forceinline__ long long part_start(long long U, int G, long long c) {
-  const long long q = U / G, rest = U % G;
-  return c * q + min(c, rest);
-}
-__device__ __forceinline__ long long part_of(long long U, int G, long long u) {
-  const long long q = U / G, rest = U % G;
-  return u < rest * (q + 1) ? u / (q + 1) : rest + (u - rest * (q + 1)) / q;
-}
-
-// Stores a finished item's output: acc[nt][c] of this warp's share of the channels
-// (two neighbouring ones per row and half), base and sum of the row.
-template <int D, int NT>
-__device__ __forceinline__ void attn_store(const AttnArgs &a, int seq, int h, int r0,
-                                           const float (&acc)[D / 64][NT][4], const float2 (&st)[NT][2],
-                                           float v_inv) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, j = lane & 3;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = r0 + 8 * nt + 2 * j + e;
-      if (r >= a.rows) continue;
-      const int token = r / a.group, head = h * a.group + r % a.group;
-      const size_t row = (static_cast<size_t>(seq) * a.t + token) * a.hq + head;
-      const float l = st[nt][e].y, f = l == 0.0f ? 0.0f : v_inv / l;
-      uint16_t *o = a.out + row * D;
-      auto two = [&](int at, float x, float y) {
-        *reinterpret_cast<uint32_t *>(o + at) =
-            bf16_store_bits(x * f) | static_cast<uint32_t>(bf16_store_bits(y * f)) << 16;
-      };
-      if constexpr (D == 128) {
-        two(16 * g + 2 * w, acc[0][nt][e], acc[1][nt][e]);
-        two(16 * g + 8 + 2 * w, acc[0][nt][2 + e], acc[1][nt][2 + e]);
-      } else {
-        two(8 * g + 2 * w, acc[0][nt][e], acc[0][nt][2 + e]);
-      }
-      if (a.lse && w == 0 && g == 0)
-        a.lse[row] = l == 0.0f ? -CUDART_INF_F : (st[nt][e].x + log2f(l)) * 0.693147180559945f;
+// G equal parts of U, the first U % G one longer: where part c starts, and the part
+// of place u. 64-bit divisions take hundreds of instructions, and U rarely needs them.
+struct Parts {
+  long long q, rest;
+  __device__ Parts(long long U, int G) {
+    if (U >> 31) {
+      q = U / G;
+      rest = U % G;
+    } else {
+      q = static_cast<uint32_t>(U) / static_cast<uint32_t>(G);
+      rest = static_cast<uint32_t>(U) % static_cast<uint32_t>(G);
     }
+  }
+  __device__ long long start(int c) const { return c * q + min(static_cast<long long>(c), rest); }
+  __device__ int of(long long u) const {
+    const long long longer = rest * (q + 1);
+    if ((u | q) >> 31) return static_cast<int>(u < longer ? u / (q + 1) : rest + (u - longer) / q);
+    return static_cast<int>(u < longer ? static_cast<uint32_t>(u) / static_cast<uint32_t>(q + 1)
+                                       : rest + static_cast<uint32_t>(u - longer) / static_cast<uint32_t>(q));
+  }
+};
+
+__device__ __forceinline__ int token_of(const AttnArgs &a, int r) { return a.t == 1 ? 0 : r / a.group; }
+
+// Where row r of a KV head's rows stands in q and out (in rows of head_dim), and in lse.
+__device__ __forceinline__ size_t attn_row(const AttnArgs &a, int seq, int h, int r) {
+  const int token = token_of(a, r);
+  return (static_cast<size_t>(seq) * a.t + token) * a.hq + h * a.group + r - token * a.group;
+}
+
+__device__ __forceinline__ float row_lse(float base, float sum) {
+  return sum == 0.0f ? -CUDART_INF_F : (base + log2f(sum)) * 0.693147180559945f;
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float x, float y) {
+  return bf16_store_bits(x) | static_cast<uint32_t>(bf16_store_bits(y)) << 16;
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads, attn_per_sm(NT)) attn_kernel(const __grid_constant__ AttnArgs a) {
-  using Sh = AttnShared<D, NT>;
+__global__ void __launch_bounds__(32 * attn_warps(NT), 1) attn_kernel(const __grid_constant__ AttnArgs a) {
+  using Sh = AttnWarp<D, NT>;
   constexpr int kMt = D / 16, kSub = D == 128 && NT == 4 ? 2 : 4, kSteps = D / 16;
   extern __shared__ __align__(128) uint8_t raw[];
-  Sh &sh = *reinterpret_cast<Sh *>(raw);
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, j = lane & 3;
+  Sh &sh = reinterpret_cast<Sh *>(raw)[w];
   griddep_launch_dependents();
   if (lane == 0) {
-    for (int s = 0; s < Sh::kStages; ++s) mbar_init(smem_u32(&sh.full[w][s]), 1);
+    for (int s = 0; s < Sh::kStages; ++s) mbar_init(smem_u32(&sh.full[s]), 1);
     fence_barrier_init();
   }
   griddep_wait();
 
-  // This CTA's part [u, end) of all units, and the sequence it starts in.
-  const int per = a.hk * a.tiles;
-  long long U = 0;
-  for (int s = tid; s < a.b; s += kAttnThreads) U += static_cast<long long>(keys_of(a, a.lens[s]).units) * per;
-  U = cta_sum(U, sh.sums);
-  long long u = part_start(U, gridDim.x, blockIdx.x);
-  const long long end = part_start(U, gridDim.x, blockIdx.x + 1ll);
+  // This warp's part [u, end) of all, and the sequence it starts in. Few parts go to
+  // different SMs.
+  const int per = a.hk * a.tiles, G = gridDim.x * attn_warps(NT);
+  const int me = w * gridDim.x + blockIdx.x;
+  long long U = 0, n[4];
+  for (int s = 4 * lane; s < a.b; s += 128) U += cost_of4(a, s, n);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) U += __shfl_xor_sync(kAll, U, d);
+  const Parts parts(U, G);
+  long long u = parts.start(me);
+  const long long end = parts.start(me + 1);
+  if (me == 0 && lane == 0) *a.total = U;
+
+  // Sequences of which nothing is seen.
+  for (int s = me; s < a.b; s += G) {
+    if (keys_of(a, a.lens[s]).cost()) continue;
+    uint4 *o = reinterpret_cast<uint4 *>(a.out + static_cast<size_t>(s) * a.t * a.hq * D);
+    for (int i = lane; i < a.t * a.hq * (D / 8); i += 32) o[i] = make_uint4(0, 0, 0, 0);
+    for (int i = lane; a.lse && i < a.t * a.hq; i += 32) a.lse[static_cast<size_t>(s) * a.t * a.hq + i] = -CUDART_INF_F;
+    for (int i = lane; i < per; i += 32) a.joins[static_cast<size_t>(s) * per + i] = make_longlong2(0, -1);
+  }
   if (u >= end) return;
-  long long before = 0;
-  for (int base = 0;; base += kAttnThreads) {
-    const int s = base + tid;
-    const long long n = s < a.b ? static_cast<long long>(keys_of(a, a.lens[s]).units) * per : 0;
-    long long upto = n;
+
+  int seq = 0;
+  long long at = 0;  // place of u within its sequence
+  for (int base = 0;; base += 128) {
+    const long long mine = cost_of4(a, base + 4 * lane, n);
+    long long upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const long long o = __shfl_up_sync(kAll, upto, d);
       if (lane >= d) upto += o;
     }
-    if (lane == 31) sh.sums[w] = upto;
-    __syncthreads();
-    long long tile = 0;
-    for (int i = 0; i < kAttnWarps; ++i) {
-      if (i < w) upto += sh.sums[i];
-      tile += sh.sums[i];
+    const uint32_t behind = __ballot_sync(kAll, at + upto > u);
+    if (behind) {
+      const int from = __ffs(behind) - 1;
+      long long off = u - at - (upto - mine);  // from this lane's first sequence
+      int s = base + 4 * lane;
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        if (s == base + 4 * lane + k && off >= n[k]) {
+          off -= n[k];
+          ++s;
+        }
+      seq = __shfl_sync(kAll, s, from);
+      at = __shfl_sync(kAll, off, from);
+      break;
     }
-    upto += before;
-    if (upto - n <= u && u < upto) {
-      sh.seq = s;
-      sh.at = u - (upto - n);
-    }
-    __syncthreads();
-    before += tile;
-    if (before > u) break;
+    at += __shfl_sync(kAll, upto, 31);
   }
-  int seq = sh.seq;
-  long long at = sh.at;
 
   // Addresses of this lane within a chunk: tokens [16 i, 16 i + 16) lie in piece
   // 16 i / ps of it. swap = f(j).
@@ -283,34 +293,44 @@ __global__ void __launch_bounds__(kAttnThreads, attn_per_sm(NT)) attn_kernel(con
   const int v_at = v_piece + codes + v_in * (D / 2) + g * (D / 16);
   const int vs_at = v_piece + 2 * codes + a.ps * (D / 16) + (D == 128 ? g : g >> 1) * a.ps + v_in;
   const uint32_t vs_order = fv == 0 ? 0x3210u : fv == 1 ? 0x2301u : fv == 2 ? 0x1032u : 0x0123u;
-  uint8_t *const ring = sh.ring[w];
+  uint8_t *const ring = sh.ring;
   const float c_all = __fmul_rn(a.scale, 1.44269504088896f) / *a.k_gs;
   const float v_inv = 1.0f / *a.v_gs;
 
   int slot = 0, phase = 0;  // the next stage to consume
   int held = 0;             // 4 bits per stage: the pieces that it holds
-  bool first = true, lost = false;
 
   while (u < end) {
     const int len = a.lens[seq];
     const Keys keys = keys_of(a, len);
-    const int item = static_cast<int>(at / keys.units), uo = static_cast<int>(at % keys.units);
+    const int cost = keys.cost();
+    if (at >= static_cast<long long>(cost) * per) {
+      at = 0;
+      ++seq;
+      continue;
+    }
+    const int item = at >> 31 ? static_cast<int>(at / cost) : static_cast<int>(at) / cost;
+    // of its cost, [x, x + take) is this part's; the first kItemCost are no chunks
+    const int x = static_cast<int>(at - static_cast<long long>(item) * cost);
+    const int take = static_cast<int>(min(static_cast<long long>(cost - x), end - u));
+    const int from_chunk = max(x - kItemCost, 0), count = x + take - kItemCost - from_chunk;
+    const long long item_at = u - x;
+    u += take;
+    at += take;
+    if (count <= 0) continue;
     const int h = item / a.tiles, r0 = item % a.tiles * 8 * NT;
-    const int take = static_cast<int>(min(static_cast<long long>(keys.units - uo), end - u));
-    const int c_first = keys.c0 + kAttnWarps * uo + w;
-    const int c_end = min(keys.c1, keys.c0 + kAttnWarps * (uo + take));
-    const int count = c_first < c_end ? (c_end - c_first + kAttnWarps - 1) / kAttnWarps : 0;
+    const int c_first = keys.c0 + from_chunk;
     const int32_t *const table = a.table + static_cast<size_t>(seq) * a.width;
     const uint8_t *const cache = a.cache + static_cast<size_t>(h) * blk;
 
     // The page of this lane's piece of chunk i (-1: none), and the copy of a chunk.
     auto page_of = [&](int i) {
-      const int token = (c_first + kAttnWarps * i) * kChunk + lane * a.ps;
+      const int token = (c_first + i) * kChunk + lane * a.ps;
       return i < count && lane < pieces && token < len && token < a.width * a.ps ? table[token / a.ps] : -1;
     };
     auto issue = [&](int page, int s) {
       const bool real = page >= 0 && page < a.pages;
-      const uint32_t bar = smem_u32(&sh.full[w][s]);
+      const uint32_t bar = smem_u32(&sh.full[s]);
       const uint32_t mask = __ballot_sync(kAll, real);
       if (lane == 0) mbar_arrive_expect_tx(bar, __popc(mask) * blk);
       __syncwarp();
@@ -344,8 +364,8 @@ __global__ void __launch_bounds__(kAttnThreads, attn_per_sm(NT)) attn_kernel(con
       for (int i = 0; i < D / 32; ++i) v[i] = make_uint4(0, 0, 0, 0);
       if (r < a.rows) {
         const uint4 *src = reinterpret_cast<const uint4 *>(
-            a.q + (static_cast<size_t>(seq) * a.t + r / a.group) * a.q_stride +
-            (h * a.group + r % a.group) * D + j * (D / 4));
+            a.q + (static_cast<size_t>(seq) * a.t + token_of(a, r)) * a.q_stride +
+            (h * a.group + r - token_of(a, r) * a.group) * D + j * (D / 4));
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) v[i] = src[i];
       }
@@ -374,7 +394,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_per_sm(NT)) attn_kernel(con
       for (int e = 0; e < 2; ++e) {
         c[nt][e] = __shfl_sync(kAll, back, 4 * (2 * j + e));
         const int row = r0 + 8 * nt + 2 * j + e;
-        last[nt][e] = row < a.rows ? min(len - a.t + row / a.group + 1, a.width * a.ps) : 0;
+        last[nt][e] = row < a.rows ? min(len - a.t + token_of(a, row) + 1, a.width * a.ps) : 0;
         if (last[nt][e] > 0) unseen |= 1u << (2 * nt + e);
       }
     }
@@ -389,14 +409,15 @@ __global__ void __launch_bounds__(kAttnThreads, attn_per_sm(NT)) attn_kernel(con
       base[nt][0] = base[nt][1] = sum[nt][0] = sum[nt][1] = 0.0f;
     }
 
-    for (int i = 0; i < count && !lost; ++i) {
-      const int from = (c_first + kAttnWarps * i) * kChunk;
-      if (!mbar_wait_bounded(smem_u32(&sh.full[w][slot]), phase, kCacheWaitNs)) {
+    for (int i = 0; i < count; ++i) {
+      const int from = (c_first + i) * kChunk;
+      if (__any_sync(kAll, !mbar_wait_bounded(smem_u32(&sh.full[slot]), phase, kCacheWaitNs))) {
+        // a copy never landed: wait for those in flight, within the same limit, and leave
         if (lane == 0) atomicOr(&g_cache_status, SK_DEVICE_WAIT_PRODUCER);
-        lost = true;
+        for (int s = 0; s < Sh::kStages; ++s)
+          mbar_wait_bounded(smem_u32(&sh.full[s]), phase ^ (s < slot), kCacheWaitNs);
+        return;
       }
-      lost = __any_sync(kAll, lost);
-      if (lost) break;
       const uint8_t *const st = ring + slot * Sh::kStageBytes;
       const int have = held >> 4 * slot & 15;
       // every token of the chunk is there and seen by every row
@@ -608,9 +629,10 @@ __global__ void __launch_bounds__(kAttnThreads, attn_per_sm(NT)) attn_kernel(con
       }
     }
 
-    // The four warps' sums, joined: each leaves its own in its ring, and warp w
-    // finishes two channels of every 16.
-    float *const mine = reinterpret_cast<float *>(ring);
+    // The whole item's output, or the result of a part: of one that the item began
+    // before in slot 2 me, of one that it begins in in slot 2 me + 1.
+    const bool whole = from_chunk == 0 && count == keys.count();
+    float *part = a.parts + (2 * static_cast<size_t>(me) + (from_chunk ? 0 : 1)) * attn_part_floats(D, NT);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -619,147 +641,138 @@ __global__ void __launch_bounds__(kAttnThreads, attn_per_sm(NT)) attn_kernel(con
         l += __shfl_xor_sync(kAll, l, 4);
         l += __shfl_xor_sync(kAll, l, 8);
         l += __shfl_xor_sync(kAll, l, 16);
-        if (g == 0) sh.stat[w][8 * nt + 2 * j + e] = make_float2(l == 0.0f ? -CUDART_INF_F : base[nt][e], l);
-      }
-    if (!lost) {
+        const int rt = 8 * nt + 2 * j + e, r = r0 + rt;
+        if (r >= a.rows) continue;
+        // a lane's channels: 16 of its own, or 8
+        constexpr int C = D / 8;
+        float v[C];
 #pragma unroll
-      for (int i = 0; i < kMt; ++i)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) mine[((i * NT + nt) * 4 + q) * 32 + lane] = o[i][nt][q];
-    }
-    if (__syncthreads_or(lost)) {
-      // a copy never landed: wait for those in flight, within the same limit, and leave
-      for (int s = 0; lost && s < Sh::kStages; ++s)
-        mbar_wait_bounded(smem_u32(&sh.full[w][s]), phase ^ (s < slot), kCacheWaitNs);
-      return;
-    }
-    float2 st[NT][2];
-    float f[kAttnWarps][NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 8 * nt + 2 * j + e;
-        float top = -CUDART_INF_F, l = 0.0f;
-#pragma unroll
-        for (int x = 0; x < kAttnWarps; ++x) top = fmaxf(top, sh.stat[x][r].x);
-#pragma unroll
-        for (int x = 0; x < kAttnWarps; ++x) {
-          const float2 v = sh.stat[x][r];
-          f[x][nt][e] = v.x == -CUDART_INF_F ? 0.0f : ex2(v.x - top);
-          l = fmaf(f[x][nt][e], v.y, l);
+        for (int k = 0; k < C; ++k) {
+          if constexpr (D == 128) v[k] = o[k % 8 / 2 + k % 2 * 4][nt][k / 8 * 2 + e];
+          else v[k] = o[k / 2][nt][k % 2 * 2 + e];
         }
-        st[nt][e] = make_float2(top, l);
-      }
-    float acc[D / 64][NT][4];
+        if (whole) {
+          const size_t row = attn_row(a, seq, h, r);
+          const float f = l == 0.0f ? 0.0f : v_inv / l;
+          uint4 *dst = reinterpret_cast<uint4 *>(a.out + row * D + C * g);
 #pragma unroll
-    for (int k = 0; k < D / 64; ++k)
+          for (int k = 0; k < C; k += 8)
+            dst[k / 8] = make_uint4(bf16_pair(v[k] * f, v[k + 1] * f), bf16_pair(v[k + 2] * f, v[k + 3] * f),
+                                    bf16_pair(v[k + 4] * f, v[k + 5] * f), bf16_pair(v[k + 6] * f, v[k + 7] * f));
+          if (a.lse && g == 0) a.lse[row] = row_lse(base[nt][e], l);
+        } else {
+          float4 *dst = reinterpret_cast<float4 *>(part + 16 * NT + rt * D + C * g);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int at32 = (((w + 4 * k) * NT + nt) * 4 + q) * 32 + lane;
-          float v = 0.0f;
-#pragma unroll
-          for (int x = 0; x < kAttnWarps; ++x)
-            v = fmaf(f[x][nt][q & 1], reinterpret_cast<const float *>(sh.ring[x])[at32], v);
-          acc[k][nt][q] = v;
+          for (int k = 0; k < C; k += 4) dst[k / 4] = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+          if (g == 0) reinterpret_cast<float2 *>(part)[rt] = make_float2(l == 0.0f ? -CUDART_INF_F : base[nt][e], l);
         }
-    if (take == keys.units) {
-      attn_store<D, NT>(a, seq, h, r0, acc, st, v_inv);
-    } else {
-      float *part = a.parts + (2 * static_cast<size_t>(blockIdx.x) + (first ? 0 : 1)) * attn_part_floats(D, NT);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (w == 0 && g == 0) reinterpret_cast<float2 *>(part)[8 * nt + 2 * j + e] = st[nt][e];
-#pragma unroll
-      for (int k = 0; k < D / 64; ++k)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            part[16 * NT + (((w + 4 * k) * NT + nt) * 4 + q) * 32 + lane] = acc[k][nt][q];
-    }
-    fence_proxy_async_smem();
-    __syncthreads();  // the rings are free again
-    first = false;
-    u += take;
-    at += take;
-    while (u < end && at >= static_cast<long long>(keys_of(a, a.lens[seq]).units) * per) {
-      at = 0;
-      ++seq;
-    }
+      }
+    // the part that an item ends in says where it lies, for attn_join_kernel
+    if (lane == 0 && x + take == cost)
+      a.joins[static_cast<size_t>(seq) * per + item] = make_longlong2(item_at, whole ? -1 : me);
   }
 }
 
-// Joins the items that fell into several parts, and writes the zeros of those that
-// see nothing. A CTA per item.
+// Joins the items that fell into several parts. A CTA takes rows of an item, and as
+// many of its 16 warps take a row together as leave each about eight results, whose
+// loads do not wait for one another (b64 d128: 512 items of five results, with all
+// warps on one row after another 25 us, a warp per row 3).
+constexpr int kJoinWarps = 16;
+constexpr int kJoinThreads = 32 * kJoinWarps;
+
 template <int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads) attn_join_kernel(const __grid_constant__ AttnArgs a, int G) {
-  __shared__ long long sums[kAttnWarps];
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, j = lane & 3;
-  griddep_launch_dependents();
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnArgs a, int G) {
+  constexpr int V = D / 32;  // neighbouring channels per lane
+  constexpr int kBatch = 8;
+  __shared__ float2 stat[kJoinWarps];
+  __shared__ float sums[kJoinWarps][D];
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_wait();
+  const longlong2 join = a.joins[blockIdx.x];  // where the item lies, and the part that it ends in
+  const long long U = *a.total;
+  const float v_inv = 1.0f / *a.v_gs;
+  if (join.y < 0) return;
   const int per = a.hk * a.tiles, seq = blockIdx.x / per, item = blockIdx.x % per;
-  long long U = 0, before = 0;
-  for (int s = tid; s < a.b; s += kAttnThreads) {
-    const int n = keys_of(a, a.lens[s]).units;
-    U += static_cast<long long>(n) * per;
-    if (s < seq) before += static_cast<long long>(n) * per;
-  }
-  U = cta_sum(U, sums);
-  before = cta_sum(before, sums);
-  const int n = keys_of(a, a.lens[seq]).units;
-  long long c0 = 0, c1 = 0;
-  bool inside = true;  // the item starts within part c0, not with it
-  if (n) {
-    const long long u0 = before + static_cast<long long>(item) * n;
-    c0 = part_of(U, G, u0), c1 = part_of(U, G, u0 + n - 1);
-    if (c0 == c1) return;  // written where it was computed
-    inside = part_start(U, G, c0) < u0;
-  } else {
-    c1 = -1;
-  }
-  float2 st[NT][2];
+  const int h = item / a.tiles, r0 = item % a.tiles * 8 * NT;
+  const int p0 = Parts(U, G).of(join.x + kItemCost), results = static_cast<int>(join.y) - p0 + 1;
+  int S = 1;  // warps of a row
+  while (S < kJoinWarps && S * kBatch < results) S *= 2;
+  const int sub = w % S;
+  for (int first = blockIdx.y * (kJoinWarps / S); first < 8 * NT && r0 + first < a.rows;
+       first += gridDim.y * (kJoinWarps / S)) {
+    const int rt = first + w / S, r = r0 + rt;
+    const bool mine = rt < 8 * NT && r < a.rows;
+    float top = -CUDART_INF_F, l = 0.0f, acc[V] = {};
+    for (int i0 = sub; mine && i0 < results; i0 += kBatch * S) {
+      float2 st[kBatch];
+      float v[kBatch][V];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) st[nt][e] = make_float2(-CUDART_INF_F, 0.0f);
-  auto part = [&](long long c) {
-    return a.parts + static_cast<size_t>(2 * c + (c == c0 && inside ? 1 : 0)) * attn_part_floats(D, NT);
-  };
-  for (long long c = c0; c <= c1; ++c) {
-    const float2 *p = reinterpret_cast<const float2 *>(part(c));
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) st[nt][e].x = fmaxf(st[nt][e].x, p[8 * nt + 2 * j + e].x);
-  }
-  float acc[D / 64][NT][4] = {};
-  for (long long c = c0; c <= c1; ++c) {
-    const float *p = part(c);
-    float f[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 v = reinterpret_cast<const float2 *>(p)[8 * nt + 2 * j + e];
-        f[nt][e] = v.x == -CUDART_INF_F ? 0.0f : ex2(v.x - st[nt][e].x);
-        st[nt][e].y = fmaf(f[nt][e], v.y, st[nt][e].y);
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * S;
+        st[k] = make_float2(-CUDART_INF_F, 0.0f);
+        if (i < results) {
+          const float *p = a.parts + (2 * static_cast<size_t>(p0 + i) + (i == 0)) * attn_part_floats(D, NT);
+          st[k] = reinterpret_cast<const float2 *>(p)[rt];
+          if constexpr (V == 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(p + 16 * NT + rt * D + V * lane);
+            v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2 *>(p + 16 * NT + rt * D + V * lane);
+            v[k][0] = x.x, v[k][1] = x.y;
+          }
+        }
       }
+      float most = top;
 #pragma unroll
-    for (int k = 0; k < D / 64; ++k)
+      for (int k = 0; k < kBatch; ++k) most = fmaxf(most, st[k].x);
+      const float f0 = top == -CUDART_INF_F ? 0.0f : ex2(top - most);
+      l *= f0;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int c = 0; c < V; ++c) acc[c] *= f0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          acc[k][nt][q] = fmaf(f[nt][q & 1], p[16 * NT + (((w + 4 * k) * NT + nt) * 4 + q) * 32 + lane], acc[k][nt][q]);
+      for (int k = 0; k < kBatch; ++k) {
+        if (st[k].x == -CUDART_INF_F) continue;
+        const float f = ex2(st[k].x - most);
+        l = fmaf(f, st[k].y, l);
+#pragma unroll
+        for (int c = 0; c < V; ++c) acc[c] = fmaf(f, v[k][c], acc[c]);
+      }
+      top = most;
+    }
+    if (S > 1) {
+      if (lane == 0) stat[w] = make_float2(top, l);
+#pragma unroll
+      for (int c = 0; c < V; ++c) sums[w][V * lane + c] = acc[c];
+      __syncthreads();
+      if (sub == 0) {
+        const float own = top;
+        for (int k = 1; k < S; ++k) top = fmaxf(top, stat[w + k].x);
+        const float f0 = own == -CUDART_INF_F ? 0.0f : ex2(own - top);
+        l *= f0;
+#pragma unroll
+        for (int c = 0; c < V; ++c) acc[c] *= f0;
+        for (int k = 1; k < S; ++k) {
+          const float2 x = stat[w + k];
+          if (x.x == -CUDART_INF_F) continue;
+          const float f = ex2(x.x - top);
+          l = fmaf(f, x.y, l);
+#pragma unroll
+          for (int c = 0; c < V; ++c) acc[c] = fmaf(f, sums[w + k][V * lane + c], acc[c]);
+        }
+      }
+      __syncthreads();
+    }
+    if (mine && sub == 0) {
+      const float f = l == 0.0f ? 0.0f : v_inv / l;
+      const size_t row = attn_row(a, seq, h, r);
+      uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + row * D + V * lane);
+#pragma unroll
+      for (int c = 0; c < V; c += 2) dst[c / 2] = bf16_pair(acc[c] * f, acc[c + 1] * f);
+      if (a.lse && lane == 0) a.lse[row] = row_lse(top, l);
+    }
   }
-  attn_store<D, NT>(a, seq, item / a.tiles, item % a.tiles * 8 * NT, acc, st, 1.0f / *a.v_gs);
+  // Not earlier: CTAs of the next kernel would take their places between these.
+  griddep_launch_dependents();
 }
 
 // ------------------------------------------------------------------- append
@@ -1126,21 +1139,25 @@ int attn_row_tiles(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
 size_t attn_part_bytes(int d, int nt) { return sizeof(float) * attn_part_floats(d, nt); }
 
-int attn_max_parts(int nt, int sm_count) { return attn_per_sm(nt) * sm_count; }
+int attn_max_parts(int nt, int sm_count) { return attn_warps(nt) * sm_count; }
 
 cudaError_t launch_attn(const AttnArgs &a, int d, int sm_count, cudaStream_t stream, bool pdl) {
   const int nt = attn_row_tiles(a.rows);
   return with_attn(d, nt, [&](auto dim, auto tiles) {
     constexpr int D = decltype(dim)::value, NT = decltype(tiles)::value;
-    // no more parts than there can be units
-    const long long units = static_cast<long long>(ceil_div(a.width * a.ps, kChunk * kAttnWarps) + 1) * a.b * a.hk * a.tiles;
-    const long long most = attn_max_parts(NT, sm_count);
-    const int grid = static_cast<int>(units < most ? units : most);
-    cudaError_t e = launch(attn_kernel<D, NT>, dim3(grid), dim3(kAttnThreads), sizeof(AttnShared<D, NT>), stream,
-                           pdl, a);
+    // no more SMs than there can be chunks
+    const long long items = static_cast<long long>(a.b) * a.hk * a.tiles;
+    const long long chunks = (ceil_div(a.width * a.ps, kChunk) + 1 + kItemCost) * items;
+    const int grid = static_cast<int>(chunks < sm_count ? chunks : sm_count);
+    cudaError_t e = launch(attn_kernel<D, NT>, dim3(grid), dim3(32 * attn_warps(NT)),
+                           attn_warps(NT) * sizeof(AttnWarp<D, NT>), stream, pdl, a);
     if (e != cudaSuccess) return e;
-    return launch(attn_join_kernel<D, NT>, dim3(static_cast<unsigned>(a.b) * a.hk * a.tiles), dim3(kAttnThreads), 0,
-                  stream, pdl, a, grid);
+    // rows of few items are spread over the SMs
+    const int rows = a.rows < 8 * NT ? a.rows : 8 * NT;
+    const long long spread = 4ll * sm_count / items;
+    const int y = spread < 1 ? 1 : spread < rows ? static_cast<int>(spread) : rows;
+    return launch(attn_join_kernel<D, NT>, dim3(static_cast<unsigned>(items), y), dim3(kJoinThreads), 0, stream, pdl,
+                  a, grid * attn_warps(NT));
   });
 }
 
@@ -1176,7 +1193,7 @@ cudaError_t cache_setup() {
       if ((e = with_attn(d, nt, [&](auto dim, auto tiles) {
              constexpr int D = decltype(dim)::value, NT = decltype(tiles)::value;
              return cudaFuncSetAttribute(attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(sizeof(AttnShared<D, NT>)));
+                                         static_cast<int>(attn_warps(NT) * sizeof(AttnWarp<D, NT>)));
            })))
         return e;
   if ((e = cudaFuncSetAttribute(kv_resize_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

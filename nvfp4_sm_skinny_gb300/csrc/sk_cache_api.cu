@@ -104,6 +104,22 @@ sk_status check_layers(int layers, int kv_heads, int page_size, int head_dim, in
   return SK_OK;
 }
 
+struct AttnWorkspace {
+  int nt, tiles;
+  size_t joins, parts, total;
+};
+
+AttnWorkspace attn_workspace(int b, int t, int q_heads, int kv_heads, int head_dim) {
+  AttnWorkspace w;
+  const int rows = q_heads / kv_heads * t;
+  w.nt = sk::attn_row_tiles(rows);
+  w.tiles = (rows + 8 * w.nt - 1) / (8 * w.nt);
+  w.joins = 256;  // behind the total
+  w.parts = w.joins + round256(16 * static_cast<size_t>(b) * kv_heads * w.tiles);
+  w.total = w.parts + round256(2 * sk::attn_max_parts(w.nt, SK_MAX_SMS) * sk::attn_part_bytes(head_dim, w.nt));
+  return w;
+}
+
 struct ResizeWorkspace {
   size_t plan, copies, fresh, count, total;
 };
@@ -155,8 +171,7 @@ sk_status sk_kv_append(const void *k, const void *v, const float *k_global_scale
 size_t sk_attn_nvfp4_workspace(int b, int t, int q_heads, int kv_heads, int head_dim) {
   if (check_attn(b, t, q_heads, kv_heads, head_dim) != SK_OK) return 0;
   ok();
-  const int nt = sk::attn_row_tiles(q_heads / kv_heads * t);
-  return round256(2 * sk::attn_max_parts(nt, SK_MAX_SMS) * sk::attn_part_bytes(head_dim, nt));
+  return attn_workspace(b, t, q_heads, kv_heads, head_dim).total;
 }
 
 sk_status sk_attn_nvfp4(const void *q, const float *k_global_scale, const float *v_global_scale,
@@ -178,18 +193,19 @@ sk_status sk_attn_nvfp4(const void *q, const float *k_global_scale, const float 
     return st;
   if (lse && (st = check_ptrs("sk_attn_nvfp4", 4, {{"lse", lse}})) != SK_OK) return st;
   if ((st = check_ptrs("sk_attn_nvfp4", 256, {{"workspace", workspace}})) != SK_OK) return st;
-  const size_t need = sk_attn_nvfp4_workspace(b, t, q_heads, kv_heads, head_dim);
-  if (workspace_bytes < need)
-    return fail(SK_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes, need);
+  const AttnWorkspace w = attn_workspace(b, t, q_heads, kv_heads, head_dim);
+  if (workspace_bytes < w.total)
+    return fail(SK_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes, w.total);
   sk::DeviceInfo info;
   int dev = 0;
   if ((st = sk::checked_device(&info, &dev)) != SK_OK) return st;
-  const int group = q_heads / kv_heads, rows = group * t, nt = sk::attn_row_tiles(rows);
+  const int group = q_heads / kv_heads;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
   // a window beyond the last position hides nothing
   sk::AttnArgs a{static_cast<const uint16_t *>(q), cache, k_global_scale, v_global_scale, table, lens,
-                 static_cast<uint16_t *>(out), lse, static_cast<float *>(workspace), b, t, q_heads,
-                 kv_heads, page_size, pages, width, window > (1 << 30) ? 0 : window, group, rows,
-                 (rows + 8 * nt - 1) / (8 * nt), q_stride, scale};
+                 static_cast<uint16_t *>(out), lse, reinterpret_cast<long long *>(ws), reinterpret_cast<longlong2 *>(ws + w.joins),
+                 reinterpret_cast<float *>(ws + w.parts), b, t, q_heads, kv_heads, page_size, pages,
+                 width, window > (1 << 30) ? 0 : window, group, group * t, w.tiles, q_stride, scale};
   const int sms = info.sm_count < SK_MAX_SMS ? info.sm_count : SK_MAX_SMS;
   return launch_status(sk::launch_attn(a, head_dim, sms, as_stream(stream), sk::pdl_on()), "attn_nvfp4");
 }
