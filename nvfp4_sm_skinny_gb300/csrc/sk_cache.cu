@@ -81,12 +81,43 @@ __device__ __forceinline__ uint32_t widen_e4m3(uint32_t two) {
   return r;
 }
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                        uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float &c0, float &c1, float &c2, float &c3, uint32_t a0, uint32_t a1,
+                                        uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "+f"(c0), "+f"(c1), "+f"(c2), "+f"(c3)
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// As mma_f16, into a sum that starts at 0.
+__device__ __forceinline__ void mma_f16_first(float &c0, float &c1, float &c2, float &c3, uint32_t a0, uint32_t a1,
+                                              uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c0), "=f"(c1), "=f"(c2), "=f"(c3)
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// Two FP32 operations in one instruction: (x, y) = (x, y) * (cx, cy) + (dx, dy), and + (dx, dy).
+__device__ __forceinline__ void fma_f32x2(float &x, float &y, float cx, float cy, float dx, float dy) {
+  asm("{\n\t.reg .b64 v, c, d;\n\t"
+      "mov.b64 v, {%0, %1};\n\tmov.b64 c, {%2, %3};\n\tmov.b64 d, {%4, %5};\n\t"
+      "fma.rn.f32x2 v, v, c, d;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(cx), "f"(cy), "f"(dx), "f"(dy));
+}
+__device__ __forceinline__ void add_f32x2(float &x, float &y, float dx, float dy) {
+  asm("{\n\t.reg .b64 v, d;\n\t"
+      "mov.b64 v, {%0, %1};\n\tmov.b64 d, {%2, %3};\n\t"
+      "add.rn.f32x2 v, v, d;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(dx), "f"(dy));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // The transpose of an 8 x 8 matrix of 16-bit values, row l / 4, columns 2 (l % 4)
@@ -103,17 +134,18 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 //
 // A warp works by itself on chunks of 64 tokens of one KV head, which bulk copies
 // bring into its own ring in shared memory (a block of the cache is one run of
-// bytes). The rows of a KV head, group query heads times t tokens, are the
-// tensor instruction's N (8 each, up to 32 a tile); keys and values are its 16-row
-// operand, widened in registers from the codes: one conversion and one product
-// with the scale per pair, both exact in FP16. So every code that is read is
-// widened once, whatever the number of rows:
-//   S^T [16 tokens, rows] = K [16 tokens, d] Q^T, then
-//   O^T [16 channels, rows] += V^T [16 channels, 16 tokens] P^T.
+// bytes). Codes are widened in registers into operands of the tensor instruction (16 x
+// 8 x 16): one conversion and one product with the scale per pair, both exact in FP16.
+// The rows of a KV head, group query heads times t tokens, are taken 8 or 16 at a time,
+// and every code is widened once for them:
+//   8 rows:   S^T [16 tokens, 8 rows] = K [16 tokens, d] Q^T
+//   16 rows:  S [16 rows, 8 tokens] = Q [16 rows, d] K^T, for two sets of tokens
+//   O^T [16 channels, 8 rows] += V^T [16 channels, 16 tokens] P^T, for 8 rows each
+// What S holds is P^T's operand as it stands with 16 rows, transposed with 8.
 // The order of an inner product is free, so lanes take what lies together in
 // memory: of K, lane (g, j) of the instruction (g = lane / 4, j = lane % 4) the j-th
 // quarter of a token's d columns; of V, the g-th eighth of the columns of the 16
-// tokens [16 j, 16 j + 16). Row r = 2 j + e (+ 8 h) of token tile mt is therefore
+// tokens [16 j, 16 j + 16). Row r = 2 j + e + 8 h of token tile mt is therefore
 // token 16 j + 4 mt + ((2 h + e) ^ f(j)); f = 0, 2, 1, 3 keeps the lanes of a
 // shared-memory access apart.
 //
@@ -133,22 +165,28 @@ constexpr int kItemCost = 1;
 // when a score exceeds it by 2^15.
 constexpr float kTop = 15.0f, kAim = 7.0f;
 
-__host__ __device__ constexpr int attn_warps(int nt) { return nt == 4 ? 8 : 12; }
+constexpr int kAttnWarps = 12;  // of a CTA: their sums and queries fill the registers
 
 template <int D, int NT>
 struct AttnWarp {
   static constexpr int kStageBytes = kChunk * D * 9 / 8;
-  static constexpr int kStages = (D == 128 ? 1 : 2) * (NT == 4 ? 3 : 2);
-  alignas(128) uint8_t ring[kStages * kStageBytes];
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  alignas(256) uint8_t ring[kStages * kStageBytes];
   uint64_t full[kStages];
+  // What the loop over chunks does not need, kept here as registers are short (b16 of
+  // 8192 tokens, d128, 16 rows: 63 us with them).
+  struct Place {
+    long long u, end, at;
+    int seq, item, flags, first, h, r0;  // first: the part that the item begins in
+  } place;
 };
+constexpr int kBegins = 1, kEnds = 2;  // the part holds the first, the last chunk of the item
 
 // Floats of a part's result: a base and a sum per row, then the rows.
 __host__ __device__ constexpr int attn_part_floats(int d, int nt) { return 16 * nt + 8 * nt * d; }
 
 struct Keys {
   int c0, c1;  // chunks [c0, c1) of a sequence that some of its tokens see
-  __device__ int count() const { return max(c1 - c0, 0); }
   // what an item of the sequence counts for
   __device__ int cost() const { return c1 > c0 ? c1 - c0 + kItemCost : 0; }
 };
@@ -215,9 +253,11 @@ __device__ __forceinline__ uint32_t bf16_pair(float x, float y) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * attn_warps(NT), 1) attn_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_constant__ AttnArgs a) {
   using Sh = AttnWarp<D, NT>;
-  constexpr int kMt = D / 16, kSub = D == 128 && NT == 4 ? 2 : 4, kSteps = D / 16;
+  constexpr int kMt = D / 16, kSub = NT == 2 ? 2 : 4, kSteps = D / 16;
+  constexpr bool kWide = NT == 2;       // 16 rows: they are the instruction's M in Q K^T
+  constexpr int R = kWide ? 1 : 2;      // rows per N tile whose statistics a lane holds
   extern __shared__ __align__(128) uint8_t raw[];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, j = lane & 3;
   Sh &sh = reinterpret_cast<Sh *>(raw)[w];
@@ -230,7 +270,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NT), 1) attn_kernel(const __gr
 
   // This warp's part [u, end) of all, and the sequence it starts in. Few parts go to
   // different SMs.
-  const int per = a.hk * a.tiles, G = gridDim.x * attn_warps(NT);
+  const int per = a.hk * a.tiles, G = gridDim.x * kAttnWarps;
   const int me = w * gridDim.x + blockIdx.x;
   long long U = 0, n[4];
   for (int s = 4 * lane; s < a.b; s += 128) U += cost_of4(a, s, n);
@@ -238,8 +278,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NT), 1) attn_kernel(const __gr
   for (int d = 16; d; d >>= 1) U += __shfl_xor_sync(kAll, U, d);
   const Parts parts(U, G);
   long long u = parts.start(me);
-  const long long end = parts.start(me + 1);
-  if (me == 0 && lane == 0) *a.total = U;
+  long long end = parts.start(me + 1);
 
   // Sequences of which nothing is seen.
   for (int s = me; s < a.b; s += G) {
@@ -247,7 +286,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NT), 1) attn_kernel(const __gr
     uint4 *o = reinterpret_cast<uint4 *>(a.out + static_cast<size_t>(s) * a.t * a.hq * D);
     for (int i = lane; i < a.t * a.hq * (D / 8); i += 32) o[i] = make_uint4(0, 0, 0, 0);
     for (int i = lane; a.lse && i < a.t * a.hq; i += 32) a.lse[static_cast<size_t>(s) * a.t * a.hq + i] = -CUDART_INF_F;
-    for (int i = lane; i < per; i += 32) a.joins[static_cast<size_t>(s) * per + i] = make_longlong2(0, -1);
+    for (int i = lane; i < per; i += 32) a.joins[static_cast<size_t>(s) * per + i] = make_int2(0, -1);
   }
   if (u >= end) return;
 
@@ -279,23 +318,25 @@ __global__ void __launch_bounds__(32 * attn_warps(NT), 1) attn_kernel(const __gr
     at += __shfl_sync(kAll, upto, 31);
   }
 
-  // Addresses of this lane within a chunk: tokens [16 i, 16 i + 16) lie in piece
-  // 16 i / ps of it. swap = f(j).
+  // Row e of those of N tile nt that this lane holds statistics of.
+  auto row_at = [&](int nt, int e) { return 8 * nt + (kWide ? g : 2 * j + e); };
+
+  // Places of this lane's values within a chunk, whose tokens [16 i, 16 i + 16) lie in
+  // piece 16 i / ps: of K and its scales for row h = 0, of V for e = h = 0. The others
+  // differ in the bits of the token alone, which no other term has: they follow by
+  // exclusive or, where more addresses would take more registers.
+  const int ps_bits = 31 - __clz(a.ps);
   const int blk = a.ps * D * 9 / 8, pieces = kChunk / a.ps, codes = a.ps * (D / 2);
   const int gj = g >> 1, ge = g & 1;
   const int fk = (gj & 1) << 1 | gj >> 1, fv = (j & 1) << 1 | j >> 1;
   const int k_piece = 16 * gj / a.ps * blk, k_in = 16 * gj % a.ps;
   const int v_piece = 16 * j / a.ps * blk, v_in = 16 * j % a.ps;
-  const int k_at0 = k_piece + (k_in + (ge ^ fk)) * (D / 2) + j * (D / 8);
-  const int k_at1 = k_piece + (k_in + ((2 + ge) ^ fk)) * (D / 2) + j * (D / 8);
-  const int ks_at0 = k_piece + 2 * codes + (k_in + (ge ^ fk)) * (D / 16) + j * (D / 64);
-  const int ks_at1 = k_piece + 2 * codes + (k_in + ((2 + ge) ^ fk)) * (D / 16) + j * (D / 64);
-  const int v_at = v_piece + codes + v_in * (D / 2) + g * (D / 16);
+  const int k_at = k_piece + (k_in + (ge ^ fk)) * (D / 2) + j * (D / 8);
+  const int ks_at = k_piece + 2 * codes + (k_in + (ge ^ fk)) * (D / 16) + j * (D / 64);
+  const int v_at = v_piece + codes + (v_in + fv) * (D / 2) + g * (D / 16);
   const int vs_at = v_piece + 2 * codes + a.ps * (D / 16) + (D == 128 ? g : g >> 1) * a.ps + v_in;
   const uint32_t vs_order = fv == 0 ? 0x3210u : fv == 1 ? 0x2301u : fv == 2 ? 0x1032u : 0x0123u;
   uint8_t *const ring = sh.ring;
-  const float c_all = __fmul_rn(a.scale, 1.44269504088896f) / *a.k_gs;
-  const float v_inv = 1.0f / *a.v_gs;
 
   int slot = 0, phase = 0;  // the next stage to consume
   int held = 0;             // 4 bits per stage: the pieces that it holds
@@ -314,19 +355,25 @@ __global__ void __launch_bounds__(32 * attn_warps(NT), 1) attn_kernel(const __gr
     const int x = static_cast<int>(at - static_cast<long long>(item) * cost);
     const int take = static_cast<int>(min(static_cast<long long>(cost - x), end - u));
     const int from_chunk = max(x - kItemCost, 0), count = x + take - kItemCost - from_chunk;
-    const long long item_at = u - x;
+    __syncwarp();  // the last item's is read
+    if (count > 0 && lane == 0)
+      sh.place = {u + take, end, at + take, seq, item, (from_chunk ? 0 : kBegins) | (x + take == cost ? kEnds : 0),
+                  from_chunk && x + take == cost ? parts.of(u - x + kItemCost) : me, item / a.tiles,
+                  item % a.tiles * 8 * NT};
+    __syncwarp();
     u += take;
     at += take;
     if (count <= 0) continue;
-    const int h = item / a.tiles, r0 = item % a.tiles * 8 * NT;
-    const int c_first = keys.c0 + from_chunk;
-    const int32_t *const table = a.table + static_cast<size_t>(seq) * a.width;
-    const uint8_t *const cache = a.cache + static_cast<size_t>(h) * blk;
+    const volatile typename Sh::Place &place = sh.place;
+    int from = (keys.c0 + from_chunk) * kChunk;  // first token of the chunk at hand
+    const int to = from + count * kChunk;
 
-    // The page of this lane's piece of chunk i (-1: none), and the copy of a chunk.
-    auto page_of = [&](int i) {
-      const int token = (c_first + i) * kChunk + lane * a.ps;
-      return i < count && lane < pieces && token < len && token < a.width * a.ps ? table[token / a.ps] : -1;
+    // The page of this lane's piece of a chunk (-1: none), and the copy of a chunk.
+    auto page_of = [&](int chunk) {
+      const int token = chunk + lane * a.ps;
+      return chunk < to && lane < pieces && token < len && token < a.width * a.ps
+                 ? a.table[static_cast<size_t>(place.seq) * a.width + (token >> ps_bits)]
+                 : -1;
     };
     auto issue = [&](int page, int s) {
       const bool real = page >= 0 && page < a.pages;
@@ -336,36 +383,39 @@ __global__ void __launch_bounds__(32 * attn_warps(NT), 1) attn_kernel(const __gr
       __syncwarp();
       if (real)
         bulk_load(smem_u32(ring + s * Sh::kStageBytes + lane * blk),
-                  cache + static_cast<size_t>(page) * a.hk * blk, blk, bar);
+                  a.cache + (static_cast<size_t>(page) * a.hk + place.h) * blk, blk, bar);
       held = (held & ~(15 << 4 * s)) | static_cast<int>(mask) << 4 * s;
     };
     int ahead = slot;  // the stage of the next copy
 #pragma unroll
     for (int i = 0; i < Sh::kStages; ++i) {
-      if (i < count) {
-        issue(page_of(i), ahead);
+      if (from + i * kChunk < to) {
+        issue(page_of(from + i * kChunk), ahead);
         ahead = ahead + 1 == Sh::kStages ? 0 : ahead + 1;
       }
     }
-    int page = page_of(Sh::kStages);
+    int page = page_of(from + Sh::kStages * kChunk);
+
+    // one past the last key that a row sees
+    auto keys_end = [&](int r) { return r < a.rows ? min(len - a.t + token_of(a, r) + 1, a.width * a.ps) : 0; };
 
     // Queries as FP16, each row times a power of two that brings its largest value
     // to [2^14, 2^15): exact but for values 2^38 times smaller than that one. Lane
     // (g, j) holds row g of each N tile, the j-th quarter of the columns.
+    const float c_all = __fmul_rn(a.scale, 1.44269504088896f) / *a.k_gs;
     uint32_t qf[NT][kSteps][2];
-    float c[NT][2];  // what a score is multiplied with, rows 2 j and 2 j + 1
-    int last[NT][2];  // one past the last key that a row sees
-    uint32_t unseen = 0;  // rows (bit 2 nt + e) without any key so far
+    float c[NT][R];       // what a score is multiplied with
+    uint32_t unseen = 0;  // rows (bit R nt + e) without any key so far
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = r0 + 8 * nt + g;
+      const int r = place.r0 + 8 * nt + g;
       uint4 v[D / 32];
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) v[i] = make_uint4(0, 0, 0, 0);
       if (r < a.rows) {
         const uint4 *src = reinterpret_cast<const uint4 *>(
-            a.q + (static_cast<size_t>(seq) * a.t + token_of(a, r)) * a.q_stride +
-            (h * a.group + r - token_of(a, r) * a.group) * D + j * (D / 4));
+            a.q + (static_cast<size_t>(place.seq) * a.t + token_of(a, r)) * a.q_stride +
+            (place.h * a.group + r - token_of(a, r) * a.group) * D + j * (D / 4));
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) v[i] = src[i];
       }
@@ -387,30 +437,28 @@ __global__ void __launch_bounds__(32 * attn_warps(NT), 1) attn_kernel(const __gr
         const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          qf[nt][2 * i + q / 2][q & 1] = cvt_f16x2(__uint_as_float(x[q] << 16) * f0 * f1,
-                                                   __uint_as_float(x[q] & 0xFFFF0000u) * f0 * f1);
+          qf[nt][2 * i + q / 2][q & 1] =
+              cvt_f16x2(__uint_as_float(x[q] << 16) * f0 * f1, __uint_as_float(x[q] & 0xFFFF0000u) * f0 * f1);
       }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        c[nt][e] = __shfl_sync(kAll, back, 4 * (2 * j + e));
-        const int row = r0 + 8 * nt + 2 * j + e;
-        last[nt][e] = row < a.rows ? min(len - a.t + token_of(a, row) + 1, a.width * a.ps) : 0;
-        if (last[nt][e] > 0) unseen |= 1u << (2 * nt + e);
+      for (int e = 0; e < R; ++e) {
+        c[nt][e] = kWide ? back : __shfl_sync(kAll, back, 4 * (2 * j + e));
+        if (keys_end(place.r0 + row_at(nt, e)) > 0) unseen |= 1u << (R * nt + e);
       }
     }
 
-    float o[kMt][NT][4], base[NT][2], sum[NT][2];
+    float o[kMt][NT][4], base[NT][R];  // the base with its sign changed
+    float sum[NT][2];                  // of rows 2 j and 2 j + 1, or of row g in two parts
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int i = 0; i < kMt; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) o[i][nt][q] = 0.0f;
-      base[nt][0] = base[nt][1] = sum[nt][0] = sum[nt][1] = 0.0f;
+      base[nt][0] = base[nt][R - 1] = sum[nt][0] = sum[nt][1] = 0.0f;
     }
 
-    for (int i = 0; i < count; ++i) {
-      const int from = (c_first + i) * kChunk;
+    for (; from < to; from += kChunk) {
       if (__any_sync(kAll, !mbar_wait_bounded(smem_u32(&sh.full[slot]), phase, kCacheWaitNs))) {
         // a copy never landed: wait for those in flight, within the same limit, and leave
         if (lane == 0) atomicOr(&g_cache_status, SK_DEVICE_WAIT_PRODUCER);
@@ -418,7 +466,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NT), 1) attn_kernel(const __gr
           mbar_wait_bounded(smem_u32(&sh.full[s]), phase ^ (s < slot), kCacheWaitNs);
         return;
       }
-      const uint8_t *const st = ring + slot * Sh::kStageBytes;
+      const int stage = w * static_cast<int>(sizeof(Sh)) + slot * Sh::kStageBytes;  // within raw
       const int have = held >> 4 * slot & 15;
       // every token of the chunk is there and seen by every row
       const bool whole = have == (1 << pieces) - 1 && from + kChunk <= len - a.t + 1 &&
@@ -426,34 +474,30 @@ __global__ void __launch_bounds__(32 * attn_warps(NT), 1) attn_kernel(const __gr
 #pragma unroll
       for (int part = 0; part < 4 / kSub; ++part) {
         float s[kSub][NT][4];
+        const int k0_at = stage + k_at, s0_at = stage + ks_at;
 #pragma unroll
         for (int m = 0; m < kSub; ++m) {
           const int mt = part * kSub + m;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) s[m][nt][q] = 0.0f;
           uint32_t k0[D / 32], k1[D / 32];
           uint32_t sc0[D / 64], sc1[D / 64];
           if constexpr (D == 128) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(st + k_at0 + mt * 4 * (D / 2));
-            const uint4 y = *reinterpret_cast<const uint4 *>(st + k_at1 + mt * 4 * (D / 2));
+            const uint4 x = *reinterpret_cast<const uint4 *>(raw + k0_at + mt * 4 * (D / 2));
+            const uint4 y = *reinterpret_cast<const uint4 *>(raw + (k0_at ^ D) + mt * 4 * (D / 2));
             k0[0] = x.x, k0[1] = x.y, k0[2] = x.z, k0[3] = x.w;
             k1[0] = y.x, k1[1] = y.y, k1[2] = y.z, k1[3] = y.w;
-            const uint32_t p = widen_e4m3(*reinterpret_cast<const uint16_t *>(st + ks_at0 + mt * 4 * (D / 16)));
-            const uint32_t q = widen_e4m3(*reinterpret_cast<const uint16_t *>(st + ks_at1 + mt * 4 * (D / 16)));
+            const uint32_t p = widen_e4m3(*reinterpret_cast<const uint16_t *>(raw + s0_at + mt * 4 * (D / 16)));
+            const uint32_t q = widen_e4m3(*reinterpret_cast<const uint16_t *>(raw + (s0_at ^ D / 8) + mt * 4 * (D / 16)));
             sc0[0] = __byte_perm(p, 0, 0x1010), sc0[1] = __byte_perm(p, 0, 0x3232);
             sc1[0] = __byte_perm(q, 0, 0x1010), sc1[1] = __byte_perm(q, 0, 0x3232);
           } else {
-            const uint2 x = *reinterpret_cast<const uint2 *>(st + k_at0 + mt * 4 * (D / 2));
-            const uint2 y = *reinterpret_cast<const uint2 *>(st + k_at1 + mt * 4 * (D / 2));
+            const uint2 x = *reinterpret_cast<const uint2 *>(raw + k0_at + mt * 4 * (D / 2));
+            const uint2 y = *reinterpret_cast<const uint2 *>(raw + (k0_at ^ D) + mt * 4 * (D / 2));
             k0[0] = x.x, k0[1] = x.y;
             k1[0] = y.x, k1[1] = y.y;
-            const uint32_t p = widen_e4m3(st[ks_at0 + mt * 4 * (D / 16)]);
-            const uint32_t q = widen_e4m3(st[ks_at1 + mt * 4 * (D / 16)]);
-            sc0[0] = __byte_perm(p, 0, 0x1010);
-            sc1[0] = __byte_perm(q, 0, 0x1010);
+            sc0[0] = __byte_perm(widen_e4m3(raw[s0_at + mt * 4 * (D / 16)]), 0, 0x1010);
+            sc1[0] = __byte_perm(widen_e4m3(raw[(s0_at ^ D / 8) + mt * 4 * (D / 16)]), 0, 0x1010);
           }
+          float(&t)[NT][4] = s[m];
 #pragma unroll
           for (int wd = 0; wd < D / 32; ++wd) {
             uint32_t x[4], y[4];
@@ -465,33 +509,51 @@ __global__ void __launch_bounds__(32 * attn_warps(NT), 1) attn_kernel(const __gr
               y[q] = mul_f16x2(y[q], sc1[wd / 2]);
             }
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_f16(s[m][nt], x[2 * q], y[2 * q], x[2 * q + 1], y[2 * q + 1], qf[nt][2 * wd + q][0],
-                        qf[nt][2 * wd + q][1]);
+            for (int q = 0; q < 2; ++q) {
+              auto go = [&](float &s0, float &s1, float &s2, float &s3, uint32_t a0, uint32_t a1, uint32_t a2,
+                            uint32_t a3, uint32_t b0, uint32_t b1) {
+                if (wd == 0 && q == 0) mma_f16_first(s0, s1, s2, s3, a0, a1, a2, a3, b0, b1);
+                else mma_f16(s0, s1, s2, s3, a0, a1, a2, a3, b0, b1);
+              };
+              const int k = 2 * wd + q;
+              if constexpr (kWide) {
+                go(t[0][0], t[0][1], t[1][0], t[1][1], qf[0][k][0], qf[1][k][0], qf[0][k][1], qf[1][k][1], x[2 * q],
+                   x[2 * q + 1]);
+                go(t[0][2], t[0][3], t[1][2], t[1][3], qf[0][k][0], qf[1][k][0], qf[0][k][1], qf[1][k][1], y[2 * q],
+                   y[2 * q + 1]);
+              } else {
+                go(t[0][0], t[0][1], t[0][2], t[0][3], x[2 * q], y[2 * q], x[2 * q + 1], y[2 * q + 1], qf[0][k][0],
+                   qf[0][k][1]);
+              }
+            }
           }
         }
 
-        // scores relative to the base of their row, as powers of two
+        // scores relative to the base of their row, as powers of two; s[m][nt][2 h + e] is
+        // that of row 2 j + e with the token that row g + 8 h of tile m stands for, or if
+        // wide, of row g with the token of row 2 j + e + 8 h
 #pragma unroll
         for (int m = 0; m < kSub; ++m)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              s[m][nt][q] = fmaf(s[m][nt][q], c[nt][q & 1], -base[nt][q & 1]);
+            for (int q = 0; q < 4; q += 2)
+              fma_f32x2(s[m][nt][q], s[m][nt][q + 1], c[nt][0], c[nt][R - 1], base[nt][0], base[nt][R - 1]);
         if (!whole) {
-          const bool there = have >> (16 * gj / a.ps) & 1;
+          const bool there = have >> (16 * (kWide ? j : gj) / a.ps) & 1;
 #pragma unroll
-          for (int m = 0; m < kSub; ++m)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int token = from + 16 * gj + 4 * (part * kSub + m) + (((q & 2) + ge) ^ fk);
+            for (int e = 0; e < 2; ++e) {
+              const int hi = there ? keys_end(place.r0 + row_at(nt, e)) : 0, lo = a.window ? hi - a.window : 0;
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                if (!there || token >= last[nt][q & 1] || (a.window && token < last[nt][q & 1] - a.window))
-                  s[m][nt][q] = -CUDART_INF_F;
+              for (int m = 0; m < kSub; ++m)
+#pragma unroll
+                for (int half = 0; half < 4; half += 2) {
+                  const int token = from + 4 * (part * kSub + m) +
+                                    (kWide ? 16 * j + ((half + e) ^ fv) : 16 * gj + ((half + ge) ^ fk));
+                  if (token >= hi || token < lo) s[m][nt][half + e] = -CUDART_INF_F;
+                }
             }
         }
         float most = -CUDART_INF_F;
@@ -500,60 +562,66 @@ __global__ void __launch_bounds__(32 * attn_warps(NT), 1) attn_kernel(const __gr
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) most = fmaxf(most, s[m][nt][q]);
+            for (int q = 0; q < 4; q += 2) most = max3(most, s[m][nt][q], s[m][nt][q + 1]);
         if (__any_sync(kAll, unseen != 0 || most > kTop)) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt) {
+            float f[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < R; ++e) {
               float x = -CUDART_INF_F;
 #pragma unroll
-              for (int m = 0; m < kSub; ++m) x = fmaxf(x, fmaxf(s[m][nt][e], s[m][nt][2 + e]));
-              x = fmaxf(x, __shfl_xor_sync(kAll, x, 4));
-              x = fmaxf(x, __shfl_xor_sync(kAll, x, 8));
-              x = fmaxf(x, __shfl_xor_sync(kAll, x, 16));
-              const uint32_t bit = 1u << (2 * nt + e);
-              float by = x > kAim ? x - kAim : 0.0f, f = ex2(-by);
+              for (int m = 0; m < kSub; ++m) {
+                x = max3(x, s[m][nt][e], s[m][nt][2 + e]);
+                if (kWide) x = max3(x, s[m][nt][1], s[m][nt][3]);
+              }
+#pragma unroll
+              for (int d = kWide ? 1 : 4; d < (kWide ? 4 : 32); d <<= 1) x = fmaxf(x, __shfl_xor_sync(kAll, x, d));
+              const uint32_t bit = 1u << (R * nt + e);
+              float by = x > kAim ? x - kAim : 0.0f;
+              f[e] = ex2(-by);
               if (unseen & bit) {  // the row's first keys set its base
                 by = x == -CUDART_INF_F ? 0.0f : x - kAim;
-                f = 1.0f;
+                f[e] = 1.0f;
                 if (x != -CUDART_INF_F) unseen &= ~bit;
               }
-              base[nt][e] += by;
-              sum[nt][e] *= f;
+              base[nt][e] -= by;
+              sum[nt][e] *= f[e];
+              if (kWide) sum[nt][1] *= f[e];
 #pragma unroll
-              for (int m = 0; m < kSub; ++m) {
-                s[m][nt][e] -= by;
-                s[m][nt][2 + e] -= by;
-              }
+              for (int m = 0; m < kSub; ++m)
 #pragma unroll
-              for (int i2 = 0; i2 < kMt; ++i2) {
-                o[i2][nt][e] *= f;
-                o[i2][nt][2 + e] *= f;
-              }
+                for (int q = e; q < 4; q += R) s[m][nt][q] -= by;
             }
+            if (kWide) {  // O^T has rows 2 j and 2 j + 1 here
+              f[1] = __shfl_sync(kAll, f[0], 4 * (2 * j + 1));
+              f[0] = __shfl_sync(kAll, f[0], 4 * (2 * j));
+            }
+#pragma unroll
+            for (int i = 0; i < kMt; ++i)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) o[i][nt][q] *= f[q & 1];
+          }
         }
-        uint32_t p[kSub][NT][2];
+        uint32_t p[kSub][NT][2];  // P^T: rows 2 j, 2 j + 1 (+ 8) of tile m by row g
 #pragma unroll
         for (int m = 0; m < kSub; ++m)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              s[m][nt][q] = ex2(s[m][nt][q]);
-              sum[nt][q & 1] += s[m][nt][q];
+            for (int h = 0; h < 2; ++h) {
+              const float x = ex2(s[m][nt][2 * h]), y = ex2(s[m][nt][2 * h + 1]);
+              add_f32x2(sum[nt][0], sum[nt][1], x, y);
+              p[m][nt][h] = kWide ? cvt_f16x2(x, y) : transpose8(cvt_f16x2(x, y));
             }
-            p[m][nt][0] = transpose8(cvt_f16x2(s[m][nt][0], s[m][nt][1]));
-            p[m][nt][1] = transpose8(cvt_f16x2(s[m][nt][2], s[m][nt][3]));
-          }
 
         // this lane's scales of V for its 16 tokens, in the order of the rows
         uint32_t vs[kSub];
         if constexpr (kSub == 4) {
-          const uint4 x = *reinterpret_cast<const uint4 *>(st + vs_at);
+          const uint4 x = *reinterpret_cast<const uint4 *>(raw + stage + vs_at);
           vs[0] = x.x, vs[1] = x.y, vs[2] = x.z, vs[3] = x.w;
         } else {
-          const uint2 x = *reinterpret_cast<const uint2 *>(st + vs_at + 8 * part);
+          const uint2 x = *reinterpret_cast<const uint2 *>(raw + stage + vs_at + 8 * part);
           vs[0] = x.x, vs[1] = x.y;
         }
 #pragma unroll
@@ -573,7 +641,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NT), 1) attn_kernel(const __gr
           uint32_t v[4][kWords];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const uint8_t *src = st + v_at + (4 * mt + (q ^ fv)) * (D / 2);
+            const uint8_t *src = raw + (stage + v_at ^ q * (D / 2)) + 4 * mt * (D / 2);
             if constexpr (D == 128) {
               const uint2 x = *reinterpret_cast<const uint2 *>(src);
               v[q][0] = x.x, v[q][1] = x.y;
@@ -599,7 +667,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NT), 1) attn_kernel(const __gr
               for (int y = 0; y < 4; ++y)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                  mma_f16(o[4 * half + y][nt], x[0][y], x[1][y], x[2][y], x[3][y], p[m][nt][0], p[m][nt][1]);
+                  mma_f16(o[4 * half + y][nt][0], o[4 * half + y][nt][1], o[4 * half + y][nt][2], o[4 * half + y][nt][3], x[0][y], x[1][y], x[2][y], x[3][y], p[m][nt][0], p[m][nt][1]);
             }
           } else {
             uint32_t x[4][4];
@@ -614,14 +682,14 @@ __global__ void __launch_bounds__(32 * attn_warps(NT), 1) attn_kernel(const __gr
             for (int y = 0; y < 4; ++y)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
-                mma_f16(o[y][nt], x[0][y], x[1][y], x[2][y], x[3][y], p[m][nt][0], p[m][nt][1]);
+                mma_f16(o[y][nt][0], o[y][nt][1], o[y][nt][2], o[y][nt][3], x[0][y], x[1][y], x[2][y], x[3][y], p[m][nt][0], p[m][nt][1]);
           }
         }
       }
       __syncwarp();
-      if (i + Sh::kStages < count) {
+      if (from + Sh::kStages * kChunk < to) {
         issue(page, slot);
-        page = page_of(i + Sh::kStages + 1);
+        page = page_of(from + (Sh::kStages + 1) * kChunk);
       }
       if (++slot == Sh::kStages) {
         slot = 0;
@@ -631,17 +699,36 @@ __global__ void __launch_bounds__(32 * attn_warps(NT), 1) attn_kernel(const __gr
 
     // The whole item's output, or the result of a part: of one that the item began
     // before in slot 2 me, of one that it begins in in slot 2 me + 1.
-    const bool whole = from_chunk == 0 && count == keys.count();
-    float *part = a.parts + (2 * static_cast<size_t>(me) + (from_chunk ? 0 : 1)) * attn_part_floats(D, NT);
+    u = place.u, end = place.end, at = place.at, seq = place.seq;
+    const int now = place.item, flags = place.flags;
+    const bool whole = flags == (kBegins | kEnds);
+    const float v_inv = 1.0f / *a.v_gs;
+    const int head = place.h, row0 = place.r0;
+    float *part = a.parts + (2 * static_cast<size_t>(me) + (flags & kBegins ? 1 : 0)) * attn_part_floats(D, NT);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      float l[2], top[2];  // of rows 2 j and 2 j + 1
+      if constexpr (kWide) {
+        float x = sum[nt][0] + sum[nt][1];
+        x += __shfl_xor_sync(kAll, x, 1);
+        x += __shfl_xor_sync(kAll, x, 2);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          l[e] = __shfl_sync(kAll, x, 4 * (2 * j + e));
+          top[e] = -__shfl_sync(kAll, base[nt][0], 4 * (2 * j + e));
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          l[e] = sum[nt][e];
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) l[e] += __shfl_xor_sync(kAll, l[e], d);
+          top[e] = -base[nt][e];
+        }
+      }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float l = sum[nt][e];
-        l += __shfl_xor_sync(kAll, l, 4);
-        l += __shfl_xor_sync(kAll, l, 8);
-        l += __shfl_xor_sync(kAll, l, 16);
-        const int rt = 8 * nt + 2 * j + e, r = r0 + rt;
+        const int rt = 8 * nt + 2 * j + e, r = row0 + rt;
         if (r >= a.rows) continue;
         // a lane's channels: 16 of its own, or 8
         constexpr int C = D / 8;
@@ -652,124 +739,117 @@ __global__ void __launch_bounds__(32 * attn_warps(NT), 1) attn_kernel(const __gr
           else v[k] = o[k / 2][nt][k % 2 * 2 + e];
         }
         if (whole) {
-          const size_t row = attn_row(a, seq, h, r);
-          const float f = l == 0.0f ? 0.0f : v_inv / l;
+          const size_t row = attn_row(a, seq, head, r);
+          const float f = l[e] == 0.0f ? 0.0f : v_inv / l[e];
           uint4 *dst = reinterpret_cast<uint4 *>(a.out + row * D + C * g);
 #pragma unroll
           for (int k = 0; k < C; k += 8)
             dst[k / 8] = make_uint4(bf16_pair(v[k] * f, v[k + 1] * f), bf16_pair(v[k + 2] * f, v[k + 3] * f),
                                     bf16_pair(v[k + 4] * f, v[k + 5] * f), bf16_pair(v[k + 6] * f, v[k + 7] * f));
-          if (a.lse && g == 0) a.lse[row] = row_lse(base[nt][e], l);
+          if (a.lse && g == 0) a.lse[row] = row_lse(top[e], l[e]);
         } else {
           float4 *dst = reinterpret_cast<float4 *>(part + 16 * NT + rt * D + C * g);
 #pragma unroll
           for (int k = 0; k < C; k += 4) dst[k / 4] = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-          if (g == 0) reinterpret_cast<float2 *>(part)[rt] = make_float2(l == 0.0f ? -CUDART_INF_F : base[nt][e], l);
+          if (g == 0) reinterpret_cast<float2 *>(part)[rt] = make_float2(l[e] == 0.0f ? -CUDART_INF_F : top[e], l[e]);
         }
       }
+    }
     // the part that an item ends in says where it lies, for attn_join_kernel
-    if (lane == 0 && x + take == cost)
-      a.joins[static_cast<size_t>(seq) * per + item] = make_longlong2(item_at, whole ? -1 : me);
+    if (lane == 0 && flags & kEnds)
+      a.joins[static_cast<size_t>(seq) * per + now] = make_int2(place.first, whole ? -1 : me);
   }
 }
 
-// Joins the items that fell into several parts. A CTA takes rows of an item, and as
-// many of its 16 warps take a row together as leave each about eight results, whose
-// loads do not wait for one another (b64 d128: 512 items of five results, with all
-// warps on one row after another 25 us, a warp per row 3).
-constexpr int kJoinWarps = 16;
-constexpr int kJoinThreads = 32 * kJoinWarps;
+// Joins the items that fell into several parts. S warps of a CTA take a row of an item
+// together, as many as leave each about four results, whose loads do not wait for one
+// another (b64 d128: 512 items of five results, with 16 warps on one row after another
+// 25 us, a warp per row 5).
+constexpr int kJoinWarps = 16;  // of a row, at most
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnArgs a, int G) {
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ AttnArgs a, int S) {
   constexpr int V = D / 32;  // neighbouring channels per lane
-  constexpr int kBatch = 8;
+  constexpr int kBatch = 4;
   __shared__ float2 stat[kJoinWarps];
   __shared__ float sums[kJoinWarps][D];
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, rows = (blockDim.x >> 5) / S;
   griddep_wait();
-  const longlong2 join = a.joins[blockIdx.x];  // where the item lies, and the part that it ends in
-  const long long U = *a.total;
-  const float v_inv = 1.0f / *a.v_gs;
+  const int2 join = a.joins[blockIdx.x];  // the parts that the item begins and ends in
   if (join.y < 0) return;
+  const float v_inv = 1.0f / *a.v_gs;
   const int per = a.hk * a.tiles, seq = blockIdx.x / per, item = blockIdx.x % per;
   const int h = item / a.tiles, r0 = item % a.tiles * 8 * NT;
-  const int p0 = Parts(U, G).of(join.x + kItemCost), results = static_cast<int>(join.y) - p0 + 1;
-  int S = 1;  // warps of a row
-  while (S < kJoinWarps && S * kBatch < results) S *= 2;
+  const int p0 = join.x, results = join.y - p0 + 1;
   const int sub = w % S;
-  for (int first = blockIdx.y * (kJoinWarps / S); first < 8 * NT && r0 + first < a.rows;
-       first += gridDim.y * (kJoinWarps / S)) {
-    const int rt = first + w / S, r = r0 + rt;
-    const bool mine = rt < 8 * NT && r < a.rows;
-    float top = -CUDART_INF_F, l = 0.0f, acc[V] = {};
-    for (int i0 = sub; mine && i0 < results; i0 += kBatch * S) {
-      float2 st[kBatch];
-      float v[kBatch][V];
+  const int rt = blockIdx.y * rows + w / S, r = r0 + rt;
+  const bool mine = rt < 8 * NT && r < a.rows;
+  float top = -CUDART_INF_F, l = 0.0f, acc[V] = {};
+  for (int i0 = sub; mine && i0 < results; i0 += kBatch * S) {
+    float2 st[kBatch];
+    float v[kBatch][V];
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int i = i0 + k * S;
-        st[k] = make_float2(-CUDART_INF_F, 0.0f);
-        if (i < results) {
-          const float *p = a.parts + (2 * static_cast<size_t>(p0 + i) + (i == 0)) * attn_part_floats(D, NT);
-          st[k] = reinterpret_cast<const float2 *>(p)[rt];
-          if constexpr (V == 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(p + 16 * NT + rt * D + V * lane);
-            v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
-          } else {
-            const float2 x = *reinterpret_cast<const float2 *>(p + 16 * NT + rt * D + V * lane);
-            v[k][0] = x.x, v[k][1] = x.y;
-          }
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * S;
+      st[k] = make_float2(-CUDART_INF_F, 0.0f);
+      if (i < results) {
+        const float *p = a.parts + (2 * static_cast<size_t>(p0 + i) + (i == 0)) * attn_part_floats(D, NT);
+        st[k] = reinterpret_cast<const float2 *>(p)[rt];
+        if constexpr (V == 4) {
+          const float4 x = *reinterpret_cast<const float4 *>(p + 16 * NT + rt * D + V * lane);
+          v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2 *>(p + 16 * NT + rt * D + V * lane);
+          v[k][0] = x.x, v[k][1] = x.y;
         }
       }
-      float most = top;
+    }
+    float most = top;
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) most = fmaxf(most, st[k].x);
-      const float f0 = top == -CUDART_INF_F ? 0.0f : ex2(top - most);
+    for (int k = 0; k < kBatch; ++k) most = fmaxf(most, st[k].x);
+    const float f0 = top == -CUDART_INF_F ? 0.0f : ex2(top - most);
+    l *= f0;
+#pragma unroll
+    for (int c = 0; c < V; ++c) acc[c] *= f0;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (st[k].x == -CUDART_INF_F) continue;
+      const float f = ex2(st[k].x - most);
+      l = fmaf(f, st[k].y, l);
+#pragma unroll
+      for (int c = 0; c < V; ++c) acc[c] = fmaf(f, v[k][c], acc[c]);
+    }
+    top = most;
+  }
+  if (S > 1) {
+    if (lane == 0) stat[w] = make_float2(top, l);
+#pragma unroll
+    for (int c = 0; c < V; ++c) sums[w][V * lane + c] = acc[c];
+    __syncthreads();
+    if (sub == 0) {
+      const float own = top;
+      for (int k = 1; k < S; ++k) top = fmaxf(top, stat[w + k].x);
+      const float f0 = own == -CUDART_INF_F ? 0.0f : ex2(own - top);
       l *= f0;
 #pragma unroll
       for (int c = 0; c < V; ++c) acc[c] *= f0;
+      for (int k = 1; k < S; ++k) {
+        const float2 x = stat[w + k];
+        if (x.x == -CUDART_INF_F) continue;
+        const float f = ex2(x.x - top);
+        l = fmaf(f, x.y, l);
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        if (st[k].x == -CUDART_INF_F) continue;
-        const float f = ex2(st[k].x - most);
-        l = fmaf(f, st[k].y, l);
-#pragma unroll
-        for (int c = 0; c < V; ++c) acc[c] = fmaf(f, v[k][c], acc[c]);
+        for (int c = 0; c < V; ++c) acc[c] = fmaf(f, sums[w + k][V * lane + c], acc[c]);
       }
-      top = most;
     }
-    if (S > 1) {
-      if (lane == 0) stat[w] = make_float2(top, l);
+  }
+  if (mine && sub == 0) {
+    const float f = l == 0.0f ? 0.0f : v_inv / l;
+    const size_t row = attn_row(a, seq, h, r);
+    uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + row * D + V * lane);
 #pragma unroll
-      for (int c = 0; c < V; ++c) sums[w][V * lane + c] = acc[c];
-      __syncthreads();
-      if (sub == 0) {
-        const float own = top;
-        for (int k = 1; k < S; ++k) top = fmaxf(top, stat[w + k].x);
-        const float f0 = own == -CUDART_INF_F ? 0.0f : ex2(own - top);
-        l *= f0;
-#pragma unroll
-        for (int c = 0; c < V; ++c) acc[c] *= f0;
-        for (int k = 1; k < S; ++k) {
-          const float2 x = stat[w + k];
-          if (x.x == -CUDART_INF_F) continue;
-          const float f = ex2(x.x - top);
-          l = fmaf(f, x.y, l);
-#pragma unroll
-          for (int c = 0; c < V; ++c) acc[c] = fmaf(f, sums[w + k][V * lane + c], acc[c]);
-        }
-      }
-      __syncthreads();
-    }
-    if (mine && sub == 0) {
-      const float f = l == 0.0f ? 0.0f : v_inv / l;
-      const size_t row = attn_row(a, seq, h, r);
-      uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + row * D + V * lane);
-#pragma unroll
-      for (int c = 0; c < V; c += 2) dst[c / 2] = bf16_pair(acc[c] * f, acc[c + 1] * f);
-      if (a.lse && lane == 0) a.lse[row] = row_lse(top, l);
-    }
+    for (int c = 0; c < V; c += 2) dst[c / 2] = bf16_pair(acc[c] * f, acc[c + 1] * f);
+    if (a.lse && lane == 0) a.lse[row] = row_lse(top, l);
   }
   // Not earlier: CTAs of the next kernel would take their places between these.
   griddep_launch_dependents();
@@ -1127,19 +1207,20 @@ cudaError_t with_attn(int d, int nt, F f) {
   auto at = [&](auto dim) {
     constexpr int D = decltype(dim)::value;
     if (nt == 1) return f(std::integral_constant<int, D>(), std::integral_constant<int, 1>());
-    if (nt == 2) return f(std::integral_constant<int, D>(), std::integral_constant<int, 2>());
-    return f(std::integral_constant<int, D>(), std::integral_constant<int, 4>());
+    return f(std::integral_constant<int, D>(), std::integral_constant<int, 2>());
   };
   return d == 64 ? at(std::integral_constant<int, 64>()) : at(std::integral_constant<int, 128>());
 }
 
 }  // namespace
 
-int attn_row_tiles(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+// Tiles of 8 rows, or of 16: of 32 the sums alone take 128 registers (d128, b16 of 8192
+// tokens, 32 rows: 121 us, in two tiles of 16, which read and widen all twice, 80).
+int attn_row_tiles(int rows) { return rows <= 8 ? 1 : 2; }
 
 size_t attn_part_bytes(int d, int nt) { return sizeof(float) * attn_part_floats(d, nt); }
 
-int attn_max_parts(int nt, int sm_count) { return attn_warps(nt) * sm_count; }
+int attn_max_parts(int sm_count) { return kAttnWarps * sm_count; }
 
 cudaError_t launch_attn(const AttnArgs &a, int d, int sm_count, cudaStream_t stream, bool pdl) {
   const int nt = attn_row_tiles(a.rows);
@@ -1149,15 +1230,17 @@ cudaError_t launch_attn(const AttnArgs &a, int d, int sm_count, cudaStream_t str
     const long long items = static_cast<long long>(a.b) * a.hk * a.tiles;
     const long long chunks = (ceil_div(a.width * a.ps, kChunk) + 1 + kItemCost) * items;
     const int grid = static_cast<int>(chunks < sm_count ? chunks : sm_count);
-    cudaError_t e = launch(attn_kernel<D, NT>, dim3(grid), dim3(32 * attn_warps(NT)),
-                           attn_warps(NT) * sizeof(AttnWarp<D, NT>), stream, pdl, a);
+    cudaError_t e = launch(attn_kernel<D, NT>, dim3(grid), dim3(32 * kAttnWarps),
+                           kAttnWarps * sizeof(AttnWarp<D, NT>), stream, pdl, a);
     if (e != cudaSuccess) return e;
-    // rows of few items are spread over the SMs
+    // warps of a row: a quarter of the results that an item has on average
     const int rows = a.rows < 8 * NT ? a.rows : 8 * NT;
-    const long long spread = 4ll * sm_count / items;
-    const int y = spread < 1 ? 1 : spread < rows ? static_cast<int>(spread) : rows;
-    return launch(attn_join_kernel<D, NT>, dim3(static_cast<unsigned>(items), y), dim3(kJoinThreads), 0, stream, pdl,
-                  a, grid * attn_warps(NT));
+    const long long results = grid * kAttnWarps / items + 2;
+    int S = 1;
+    while (S < kJoinWarps && 4 * S < results) S *= 2;
+    const int warps = S < 4 ? 4 : S;
+    return launch(attn_join_kernel<D, NT>, dim3(static_cast<unsigned>(items), ceil_div(rows * S, warps)),
+                  dim3(32 * warps), 0, stream, pdl, a, S);
   });
 }
 
@@ -1189,11 +1272,11 @@ cudaError_t launch_kv_compact(const CompactArgs &a, int sm_count, cudaStream_t s
 cudaError_t cache_setup() {
   cudaError_t e;
   for (int d : {64, 128})
-    for (int nt : {1, 2, 4})
+    for (int nt : {1, 2})
       if ((e = with_attn(d, nt, [&](auto dim, auto tiles) {
              constexpr int D = decltype(dim)::value, NT = decltype(tiles)::value;
              return cudaFuncSetAttribute(attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(attn_warps(NT) * sizeof(AttnWarp<D, NT>)));
+                                         static_cast<int>(kAttnWarps * sizeof(AttnWarp<D, NT>)));
            })))
         return e;
   if ((e = cudaFuncSetAttribute(kv_resize_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

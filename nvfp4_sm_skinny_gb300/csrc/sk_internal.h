@@ -258,9 +258,8 @@ cudaError_t read_core_status(uint32_t *out, bool clear);
 
 // ------------------------------------------ the key/value cache held in 4 bits
 // Attention over it (sk_attn_nvfp4): rows = group * t rows per KV head, in `tiles`
-// tiles. Parts of the caller's workspace: total, what the work counts for; joins, for
-// each of b hk tiles items where it lies in it, and the part of the work that it ends
-// in (-1: it is finished); parts, two results per part.
+// tiles. Parts of the caller's workspace: joins, the parts of the work that each of
+// b hk tiles items begins and ends in (-1: it is finished); parts, two results per part.
 struct AttnArgs {
   const uint16_t *q;
   const uint8_t *cache;
@@ -268,8 +267,7 @@ struct AttnArgs {
   const int32_t *table, *lens;
   uint16_t *out;
   float *lse;  // or null
-  long long *total;
-  longlong2 *joins;
+  int2 *joins;
   float *parts;
   int b, t, hq, hk, ps, pages, width, window;
   int group, rows, tiles;
@@ -277,7 +275,7 @@ struct AttnArgs {
   float scale;
 };
 int attn_row_tiles(int rows);                   // tiles of 8 rows that a CTA takes at once
-int attn_max_parts(int nt, int sm_count);       // parts of such a launch, at most
+int attn_max_parts(int sm_count);               // parts of such a launch, at most
 size_t attn_part_bytes(int d, int nt);          // bytes of an unfinished result
 cudaError_t launch_attn(const AttnArgs &a, int d, int sm_count, cudaStream_t stream, bool pdl);
 
