@@ -386,15 +386,35 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
                   a.cache + (static_cast<size_t>(page) * a.hk + place.h) * blk, blk, bar);
       held = (held & ~(15 << 4 * s)) | static_cast<int>(mask) << 4 * s;
     };
+    // The first pages' numbers and the queries are on their way before the copies, which
+    // would hold them up (b1 of 131,071 tokens: the queries came 5 us after the copies).
+    int pages_at[Sh::kStages];
+#pragma unroll
+    for (int i = 0; i < Sh::kStages; ++i) pages_at[i] = page_of(from + i * kChunk);
+    int page = page_of(from + Sh::kStages * kChunk);
+    uint4 raw_q[NT][D / 32];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = place.r0 + 8 * nt + g;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) raw_q[nt][i] = make_uint4(0, 0, 0, 0);
+      if (r < a.rows) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            a.q + (static_cast<size_t>(place.seq) * a.t + token_of(a, r)) * a.q_stride +
+            (place.h * a.group + r - token_of(a, r) * a.group) * D + j * (D / 4));
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) raw_q[nt][i] = src[i];
+      }
+    }
+    const float c_all = __fmul_rn(a.scale, 1.44269504088896f) / *a.k_gs;
     int ahead = slot;  // the stage of the next copy
 #pragma unroll
     for (int i = 0; i < Sh::kStages; ++i) {
       if (from + i * kChunk < to) {
-        issue(page_of(from + i * kChunk), ahead);
+        issue(pages_at[i], ahead);
         ahead = ahead + 1 == Sh::kStages ? 0 : ahead + 1;
       }
     }
-    int page = page_of(from + Sh::kStages * kChunk);
 
     // one past the last key that a row sees
     auto keys_end = [&](int r) { return r < a.rows ? min(len - a.t + token_of(a, r) + 1, a.width * a.ps) : 0; };
@@ -402,23 +422,12 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
     // Queries as FP16, each row times a power of two that brings its largest value
     // to [2^14, 2^15): exact but for values 2^38 times smaller than that one. Lane
     // (g, j) holds row g of each N tile, the j-th quarter of the columns.
-    const float c_all = __fmul_rn(a.scale, 1.44269504088896f) / *a.k_gs;
     uint32_t qf[NT][kSteps][2];
     float c[NT][R];       // what a score is multiplied with
     uint32_t unseen = 0;  // rows (bit R nt + e) without any key so far
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = place.r0 + 8 * nt + g;
-      uint4 v[D / 32];
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) v[i] = make_uint4(0, 0, 0, 0);
-      if (r < a.rows) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(
-            a.q + (static_cast<size_t>(place.seq) * a.t + token_of(a, r)) * a.q_stride +
-            (place.h * a.group + r - token_of(a, r) * a.group) * D + j * (D / 4));
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) v[i] = src[i];
-      }
+      const uint4(&v)[D / 32] = raw_q[nt];
       uint32_t most = 0;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
@@ -765,7 +774,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
 // together, as many as leave each about four results, whose loads do not wait for one
 // another (b64 d128: 512 items of five results, with 16 warps on one row after another
 // 25 us, a warp per row 5).
-constexpr int kJoinWarps = 16;  // of a row, at most
+constexpr int kJoinWarps = 32;  // of a row, at most
 
 template <int D, int NT>
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ AttnArgs a, int S) {
@@ -1228,14 +1237,14 @@ cudaError_t launch_attn(const AttnArgs &a, int d, int sm_count, cudaStream_t str
     constexpr int D = decltype(dim)::value, NT = decltype(tiles)::value;
     // no more SMs than there can be chunks
     const long long items = static_cast<long long>(a.b) * a.hk * a.tiles;
-    const long long chunks = (ceil_div(a.width * a.ps, kChunk) + 1 + kItemCost) * items;
-    const int grid = static_cast<int>(chunks < sm_count ? chunks : sm_count);
+    const long long chunks = ceil_div(a.width * a.ps, kChunk);  // of an item, at most
+    const int grid = static_cast<int>((chunks + kItemCost) * items < sm_count ? (chunks + kItemCost) * items : sm_count);
     cudaError_t e = launch(attn_kernel<D, NT>, dim3(grid), dim3(32 * kAttnWarps),
                            kAttnWarps * sizeof(AttnWarp<D, NT>), stream, pdl, a);
     if (e != cudaSuccess) return e;
     // warps of a row: a quarter of the results that an item has on average
     const int rows = a.rows < 8 * NT ? a.rows : 8 * NT;
-    const long long results = grid * kAttnWarps / items + 2;
+    const long long most = grid * kAttnWarps / items + 2, results = most < chunks ? most : chunks;
     int S = 1;
     while (S < kJoinWarps && 4 * S < results) S *= 2;
     const int warps = S < 4 ? 4 : S;
