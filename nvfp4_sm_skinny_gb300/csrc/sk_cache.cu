@@ -61,17 +61,18 @@ __device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
   return r;
 }
 
-// Eight e2m1 codes of a word as four FP16 pairs, byte i in o[i], its low nibble
-// in the low half.
-__device__ __forceinline__ void widen_e2m1(uint32_t w, uint32_t (&o)[4]) {
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "mov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
-      : "r"(w));
+// The two e2m1 codes of byte i of a word as an FP16 pair, the low nibble in the low half.
+__device__ __forceinline__ uint32_t widen_e2m1(uint32_t w, int i) {
+  uint32_t r;
+  if (i == 0)
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(r) : "r"(w));
+  else if (i == 1)
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(r) : "r"(w));
+  else if (i == 2)
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}" : "=r"(r) : "r"(w));
+  else
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, d;\n\t}" : "=r"(r) : "r"(w));
+  return r;
 }
 
 // Two e4m3 bytes as an FP16 pair, exact.
@@ -510,12 +511,10 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
 #pragma unroll
           for (int wd = 0; wd < D / 32; ++wd) {
             uint32_t x[4], y[4];
-            widen_e2m1(k0[wd], x);
-            widen_e2m1(k1[wd], y);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              x[q] = mul_f16x2(x[q], sc0[wd / 2]);
-              y[q] = mul_f16x2(y[q], sc1[wd / 2]);
+              x[q] = mul_f16x2(widen_e2m1(k0[wd], q), sc0[wd / 2]);
+              y[q] = mul_f16x2(widen_e2m1(k1[wd], q), sc1[wd / 2]);
             }
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -661,37 +660,35 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
           // bytes of (code of one token, code of the next) for the even and odd columns
           auto even = [](uint32_t x, uint32_t y) { return (x & 0x0F0F0F0Fu) | (y << 4 & 0xF0F0F0F0u); };
           auto odd = [](uint32_t x, uint32_t y) { return (x >> 4 & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u); };
+          // channel tiles i to i + 3, of their operand's four registers one in each word
+          auto add_pv = [&](int i, const uint32_t(&both)[4]) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              uint32_t x[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) x[q] = mul_f16x2(widen_e2m1(both[q], y), q & 2 ? f1 : f0);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float(&t)[4] = o[i + y][nt];
+                mma_f16(t[0], t[1], t[2], t[3], x[0], x[1], x[2], x[3], p[m][nt][0], p[m][nt][1]);
+              }
+            }
+          };
           if constexpr (D == 128) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              uint32_t x[4][4];
+              uint32_t both[4];
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const uint32_t l = v[q & 2][q & 1], r = v[(q & 2) + 1][q & 1];
-                widen_e2m1(half ? odd(l, r) : even(l, r), x[q]);
-#pragma unroll
-                for (int y = 0; y < 4; ++y) x[q][y] = mul_f16x2(x[q][y], q & 2 ? f1 : f0);
-              }
-#pragma unroll
-              for (int y = 0; y < 4; ++y)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                  mma_f16(o[4 * half + y][nt][0], o[4 * half + y][nt][1], o[4 * half + y][nt][2], o[4 * half + y][nt][3], x[0][y], x[1][y], x[2][y], x[3][y], p[m][nt][0], p[m][nt][1]);
+              for (int q = 0; q < 4; ++q)
+                both[q] = half ? odd(v[q & 2][q & 1], v[(q & 2) + 1][q & 1]) : even(v[q & 2][q & 1], v[(q & 2) + 1][q & 1]);
+              add_pv(4 * half, both);
             }
           } else {
-            uint32_t x[4][4];
+            uint32_t both[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t l = v[q & 2][0], r = v[(q & 2) + 1][0];
-              widen_e2m1(q & 1 ? odd(l, r) : even(l, r), x[q]);
-#pragma unroll
-              for (int y = 0; y < 4; ++y) x[q][y] = mul_f16x2(x[q][y], q & 2 ? f1 : f0);
-            }
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_f16(o[y][nt][0], o[y][nt][1], o[y][nt][2], o[y][nt][3], x[0][y], x[1][y], x[2][y], x[3][y], p[m][nt][0], p[m][nt][1]);
+            for (int q = 0; q < 4; ++q)
+              both[q] = q & 1 ? odd(v[q & 2][0], v[(q & 2) + 1][0]) : even(v[q & 2][0], v[(q & 2) + 1][0]);
+            add_pv(0, both);
           }
         }
       }
@@ -865,41 +862,93 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
 }
 
 // ------------------------------------------------------------------- append
-// A thread per 16 columns of a token's K or V head.
+// A thread takes 16 columns of a token's head, of K and of V. What a block of 16 costs is
+// instructions (a thread per block with three IEEE divisions: 51 us for 32,768 tokens
+// of 8 heads, d128, twice what its bytes take), so the divisions go: that by 6 becomes a
+// product and two fused steps, which are exact for every BF16 value, and 1 / (scale / gs)
+// is looked up by the scale's byte.
 constexpr int kAppendThreads = 256;
 
+struct AppendShared {
+  float step[2][256];  // of K and V: what a scale byte's values are multiplied with
+};
+
+__device__ __forceinline__ void append_steps(AppendShared &sh, const AppendArgs &a) {
+  for (int i = threadIdx.x; i < 512; i += kAppendThreads) {
+    const float gs = i < 256 ? *a.k_gs : *a.v_gs, sf = cvt_e4m3_f32(i & 255);
+    sh.step[i >> 8][i & 255] = sf == 0.0f ? 0.0f : __fdiv_rn(1.0f, __fmul_rn(sf, __fdiv_rn(1.0f, gs)));
+  }
+}
+
+// As nvfp4_block16, with 1 / (scale / gs) from a table: the scale byte of 16 BF16 values,
+// their codes in `packed`.
+__device__ __forceinline__ uint32_t append_block(const uint4 &x, const uint4 &y, float gs, const float *step,
+                                                 uint2 &packed) {
+  const uint32_t z[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    asm("{\n\t.reg .b32 t;\n\tabs.bf16x2 t, %1;\n\tmax.bf16x2 %0, %0, t;\n\t}" : "+r"(most) : "r"(z[i]));
+  const float amax = fmaxf(bf16_bits_to_f32(most & 0xFFFFu), __uint_as_float(most & 0xFFFF0000u));
+  const float sixth = 0.166666666666666667f, q = amax * sixth;
+  const float by6 = amax < CUDART_INF_F ? fmaf(fmaf(-6.0f, q, amax), sixth, q) : amax;
+  const uint32_t sf = cvt_f32_e4m3(__fmul_rn(by6, gs));
+  const float os = step[sf];
+  uint32_t b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    b[i] = cvt_f32x2_e2m1x2(__fmul_rn(__uint_as_float(z[i] << 16), os),
+                            __fmul_rn(__uint_as_float(z[i] & 0xFFFF0000u), os));
+  packed.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+  packed.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+  return sf;
+}
+
+// A CTA takes a.tile tokens at a time.
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+  __shared__ AppendShared sh;
   griddep_launch_dependents();
   griddep_wait();
-  const int blocks = a.d / 16;
-  const long long i = static_cast<long long>(blockIdx.x) * kAppendThreads + threadIdx.x;
-  const int block = static_cast<int>(i % blocks);
-  const int h = static_cast<int>(i / blocks % a.hk);
-  const long long token = i / blocks / a.hk;
-  if (token >= static_cast<long long>(a.b) * a.t) return;
-  const int seq = static_cast<int>(token / a.t);
-  const long long pos = static_cast<long long>(a.lens[seq]) - a.t + token % a.t;
-  if (pos < 0 || pos >= static_cast<long long>(a.width) * a.ps) return;
-  const int page = a.table[static_cast<size_t>(seq) * a.width + pos / a.ps];
-  if (page < 0 || page >= a.pages) return;
-  const int at = static_cast<int>(pos % a.ps);
-  const bool value = blockIdx.y;
-  const uint16_t *src = value ? a.v + token * a.v_stride : a.k + token * a.k_stride;
-  const uint4 *sp = reinterpret_cast<const uint4 *>(src + h * a.d + 16 * block);
-  const uint4 x = sp[0], y = sp[1];
-  const uint32_t words[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-  uint16_t z[16];
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    z[2 * q] = static_cast<uint16_t>(words[q]);
-    z[2 * q + 1] = static_cast<uint16_t>(words[q] >> 16);
+  const int bits = a.d == 128 ? 3 : 2, blocks = 1 << bits, per = a.hk << bits;  // blocks of a token
+  const int codes = a.ps * a.d / 2, scales = a.ps * blocks, blk = 2 * (codes + scales);
+  const int tokens = a.b * a.t;
+  bool ready = false;
+  for (int first = blockIdx.x * a.tile; first < tokens; first += gridDim.x * a.tile) {
+    const int units = min(a.tile, tokens - first) * per;
+    for (int u0 = 0; u0 < units; u0 += kAppendThreads) {
+      const int u = u0 + threadIdx.x;
+      const bool mine = u < units;
+      const int in = mine ? u / per : 0, token = first + in, r = u - in * per, h = r >> bits, block = r & (blocks - 1);
+      uint4 x[2], y[2];
+      uint8_t *base = nullptr;
+      int at = 0;
+      if (mine) {
+        const uint4 *k = reinterpret_cast<const uint4 *>(a.k + token * a.k_stride + h * a.d + 16 * block);
+        const uint4 *v = reinterpret_cast<const uint4 *>(a.v + token * a.v_stride + h * a.d + 16 * block);
+        x[0] = k[0], y[0] = k[1], x[1] = v[0], y[1] = v[1];
+        const int seq = token / a.t;
+        const long long pos = static_cast<long long>(a.lens[seq]) - a.t + (token - seq * a.t);
+        if (pos >= 0 && pos < a.width * a.ps) {
+          const int page = a.table[static_cast<size_t>(seq) * a.width + static_cast<int>(pos) / a.ps];
+          at = static_cast<int>(pos) % a.ps;
+          if (page >= 0 && page < a.pages) base = a.cache + (static_cast<size_t>(page) * a.hk + h) * blk;
+        }
+      }
+      if (!ready) {  // the first values are on their way
+        append_steps(sh, a);
+        __syncthreads();
+        ready = true;
+      }
+      if (!base) continue;
+      uint2 packed;
+      uint32_t sf = append_block(x[0], y[0], *a.k_gs, sh.step[0], packed);
+      *reinterpret_cast<uint2 *>(base + at * (a.d / 2) + 8 * block) = packed;
+      base[2 * codes + at * blocks + block] = static_cast<uint8_t>(sf);
+      sf = append_block(x[1], y[1], *a.v_gs, sh.step[1], packed);
+      *reinterpret_cast<uint2 *>(base + codes + at * (a.d / 2) + 8 * block) = packed;
+      base[2 * codes + scales + block * a.ps + at] = static_cast<uint8_t>(sf);
+    }
   }
-  uint2 packed;
-  const uint32_t sf = nvfp4_block16(z, value ? *a.v_gs : *a.k_gs, packed);
-  const int codes = a.ps * a.d / 2, scales = a.ps * blocks;
-  uint8_t *base = a.cache + (static_cast<size_t>(page) * a.hk + h) * (2 * codes + 2 * scales);
-  *reinterpret_cast<uint2 *>(base + (value ? codes : 0) + at * (a.d / 2) + 8 * block) = packed;
-  base[2 * codes + (value ? scales + block * a.ps + at : at * blocks + block)] = static_cast<uint8_t>(sf);
 }
 
 // -------------------------------------------------------------------- pages
@@ -1253,10 +1302,14 @@ cudaError_t launch_attn(const AttnArgs &a, int d, int sm_count, cudaStream_t str
   });
 }
 
-cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream, bool pdl) {
-  const long long threads = static_cast<long long>(a.b) * a.t * a.hk * (a.d / 16);
-  return launch(kv_append_kernel, dim3(static_cast<unsigned>((threads + kAppendThreads - 1) / kAppendThreads), 2),
-                dim3(kAppendThreads), 0, stream, pdl, a);
+cudaError_t launch_kv_append(AppendArgs a, int sm_count, cudaStream_t stream, bool pdl) {
+  // two rounds of a CTA's threads per tile, or one token where that leaves SMs idle
+  const int per = a.hk * (a.d / 16), tokens = a.b * a.t;
+  a.tile = 2 * kAppendThreads / per;
+  if (a.tile < 1 || tokens / a.tile < sm_count) a.tile = 1;
+  const int tiles = ceil_div(tokens, a.tile);
+  return launch(kv_append_kernel, dim3(tiles < 8 * sm_count ? tiles : 8 * sm_count), dim3(kAppendThreads), 0, stream,
+                pdl, a);
 }
 
 cudaError_t launch_kv_resize(const ResizeArgs &a, int sm_count, cudaStream_t stream, bool pdl) {

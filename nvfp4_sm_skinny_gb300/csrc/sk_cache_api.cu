@@ -164,8 +164,8 @@ sk_status sk_kv_append(const void *k, const void *v, const float *k_global_scale
   if ((st = sk::checked_device(&info, &dev)) != SK_OK) return st;
   sk::AppendArgs a{static_cast<const uint16_t *>(k), static_cast<const uint16_t *>(v), k_global_scale,
                    v_global_scale, cache, table, lens, b, t, kv_heads, head_dim, page_size, pages, width,
-                   k_stride, v_stride};
-  return launch_status(sk::launch_kv_append(a, as_stream(stream), sk::pdl_on()), "kv_append");
+                   k_stride, v_stride, 1};
+  return launch_status(sk::launch_kv_append(a, info.sm_count, as_stream(stream), sk::pdl_on()), "kv_append");
 }
 
 size_t sk_attn_nvfp4_workspace(int b, int t, int q_heads, int kv_heads, int head_dim) {

@@ -286,8 +286,9 @@ struct AppendArgs {
   const int32_t *table, *lens;
   int b, t, hk, d, ps, pages, width;
   long long k_stride, v_stride;  // values between tokens
+  int tile;                      // tokens that a CTA takes at a time, set by the launch
 };
-cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream, bool pdl);
+cudaError_t launch_kv_append(AppendArgs a, int sm_count, cudaStream_t stream, bool pdl);
 
 // Pages: the arrays from `plan` on are parts of the caller's workspace.
 struct ResizeArgs {

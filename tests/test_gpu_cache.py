@@ -94,6 +94,26 @@ def test_append_from_the_rows_of_one_product(sk):
         sk.kv_append(kd.transpose(0, 1), vd.transpose(0, 1), one, one, c, gpu(table[:2], I32), gpu(lens[:2], I32), ps)
 
 
+def test_append_of_every_largest_value(sk):
+    # a block for each finite BF16 magnitude, which its scale's division by 6 starts from
+    ps, d, hk, t = 64, 128, 2, 2048
+    mag = np.arange(t * hk * d // 16, dtype=np.uint16)  # 32,768 bit patterns, the last 128 not finite
+    mag[mag >= 0x7F80] = 0
+    rng = np.random.default_rng(5)
+    z = (rng.random((len(mag), 16)) * mag[:, None]).astype(np.uint16)  # smaller patterns are smaller values
+    z[:, 7] = mag
+    z |= (rng.integers(0, 2, z.shape) << 15).astype(np.uint16)
+    k = torch.as_tensor(z.view(np.int16)).view(BF16).view(1, t, hk, d)
+    table = rng.permutation(32)[None].astype(np.int32)
+    cache = np.zeros((32, hk, ps * d * 9 // 8), np.uint8)
+    for k_gs, v_gs in ((1.0, 448.0), (3e-30, 7e30)):
+        c = gpu(cache, U8)
+        sk.kv_append(k.to(DEV), k.flip(1).to(DEV), gpu([k_gs], F32), gpu([v_gs], F32), c, gpu(table, I32),
+                     gpu([t], I32), ps)
+        want = oc.append(bits(k), bits(k.flip(1)), k_gs, v_gs, cache, table, np.array([t]), ps)
+        assert np.array_equal(host(c), want)
+
+
 def test_append_leaves_out_what_has_no_place(sk):
     # pages outside the cache, positions before the row and beyond the table
     rng = np.random.default_rng(4)
