@@ -955,30 +955,58 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
 constexpr int kPageThreads = 1024;
 
 // Exclusive prefix sum over a CTA of kPageThreads threads; total in `all`.
-__device__ __forceinline__ int cta_scan(int v, int *warps, int &all) {
+template <typename T>
+__device__ __forceinline__ T cta_scan(T v, T *warps, T &all) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  int upto = v;
+  T upto = v;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(kAll, upto, d);
+    const T o = __shfl_up_sync(kAll, upto, d);
     if (lane >= d) upto += o;
   }
   if (lane == 31) warps[w] = upto;
   __syncthreads();
   if (w == 0) {
-    int x = warps[lane];
+    T x = warps[lane];
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(kAll, x, d);
+      const T o = __shfl_up_sync(kAll, x, d);
       if (lane >= d) x += o;
     }
     warps[lane] = x;
   }
   __syncthreads();
   all = warps[31];
-  const int before = upto - v + (w ? warps[w - 1] : 0);
+  const T before = upto - v + (w ? warps[w - 1] : 0);
   __syncthreads();
   return before;
+}
+
+// Which of pages [p, p + 16) are in use, and which there are. A scan of the CTA is a
+// microsecond whatever it scans, so a thread takes 16 pages at a time.
+constexpr int kPagesEach = 16;
+
+__device__ __forceinline__ uint32_t pages_in_use(const int32_t *refs, int p, int pages, bool vectors, uint32_t &there) {
+  int r[kPagesEach];
+  if (vectors && p + kPagesEach <= pages) {
+#pragma unroll
+    for (int i = 0; i < kPagesEach; i += 4) {
+      const int4 v = *reinterpret_cast<const int4 *>(refs + p + i);
+      r[i] = v.x, r[i + 1] = v.y, r[i + 2] = v.z, r[i + 3] = v.w;
+    }
+    there = 0xFFFF;
+  } else {
+    there = 0;
+#pragma unroll
+    for (int i = 0; i < kPagesEach; ++i) {
+      r[i] = p + i < pages ? refs[p + i] : 0;
+      there |= (p + i < pages) << i;
+    }
+  }
+  uint32_t used = 0;
+#pragma unroll
+  for (int i = 0; i < kPagesEach; ++i) used |= (r[i] > 0) << i;
+  return used;
 }
 
 // What becomes of a row: its length before and after, the first of its fresh
@@ -1020,7 +1048,7 @@ __global__ void __launch_bounds__(kPageThreads) kv_resize_plan_kernel(const __gr
       sh.need[row] = !bad && next > old ? ceil_div(next, a.ps) - have : 0;
       a.status[row] = bad ? 2 : 0;
     }
-    const int at = sharers + cta_scan(shared, sh.warps, all);
+    const int at = sharers + cta_scan<int>(shared, sh.warps, all);
     if (shared) {
       sh.page[at] = page;
       sh.who[at] = row;
@@ -1051,26 +1079,12 @@ __global__ void __launch_bounds__(kPageThreads) kv_resize_plan_kernel(const __gr
   }
   // The free pages, lowest number first, as many as are needed.
   int got = 0;
-  for (int base = 0; base < a.pages && got < total; base += 4 * kPageThreads) {
-    const int p = base + 4 * tid;
-    int4 r = make_int4(1, 1, 1, 1);
-    if (p + 3 < a.pages && a.refs_vector) {
-      r = *reinterpret_cast<const int4 *>(a.refs + p);
-    } else {
-      if (p < a.pages) r.x = a.refs[p];
-      if (p + 1 < a.pages) r.y = a.refs[p + 1];
-      if (p + 2 < a.pages) r.z = a.refs[p + 2];
-      if (p + 3 < a.pages) r.w = a.refs[p + 3];
-    }
-    const int n = (r.x <= 0) + (r.y <= 0) + (r.z <= 0) + (r.w <= 0);
-    int at = got + cta_scan(n, sh.warps, all);
-    if (r.x <= 0 && at < total) a.fresh[at] = p;
-    at += r.x <= 0;
-    if (r.y <= 0 && at < total) a.fresh[at] = p + 1;
-    at += r.y <= 0;
-    if (r.z <= 0 && at < total) a.fresh[at] = p + 2;
-    at += r.z <= 0;
-    if (r.w <= 0 && at < total) a.fresh[at] = p + 3;
+  for (int base = 0; base < a.pages && got < total; base += kPagesEach * kPageThreads) {
+    const int p = base + kPagesEach * tid;
+    uint32_t there, free = pages_in_use(a.refs, p, a.pages, a.refs_vector, there);
+    free = there & ~free;
+    int at = got + cta_scan(__popc(free), sh.warps, all);
+    for (; free && at < total; free &= free - 1) a.fresh[at++] = p + __ffs(free) - 1;
     got += all;
   }
   __syncthreads();
@@ -1098,7 +1112,7 @@ __global__ void __launch_bounds__(kPageThreads) kv_resize_plan_kernel(const __gr
         plan[row].new_len = plan[row].old_len;
       }
     }
-    const int at = copies + cta_scan(copy, sh.warps, all);
+    const int at = copies + cta_scan<int>(copy, sh.warps, all);
     if (copy) a.copies[at] = make_int2(sh.page[i], a.fresh[plan[sh.who[i]].first]);
     copies += all;
   }
@@ -1166,32 +1180,42 @@ __global__ void __launch_bounds__(kCopyThreads) kv_resize_apply_kernel(const __g
   copy_pages(a.cache, a.layers, a.layer_bytes, a.page_bytes, *a.count, [&](int i) { return a.copies[i]; });
 }
 
-// A CTA takes eight columns of the table, of all rows: what a row becomes depends on
-// other rows in these columns alone, which it reads before it writes.
-constexpr int kForkCols = 8;
-constexpr int kForkThreads = 512;
+// A CTA takes four columns of the table, of all rows: what a row becomes depends on
+// other rows in these columns alone, which it reads before it writes. A thread takes a
+// row, whose four loads wait for nothing.
+constexpr int kForkCols = 4;
 
-__global__ void __launch_bounds__(kForkThreads) kv_fork_kernel(const __grid_constant__ ForkArgs a) {
+__global__ void __launch_bounds__(kPageThreads) kv_fork_kernel(const __grid_constant__ ForkArgs a) {
   extern __shared__ __align__(128) uint8_t raw[];
-  int32_t *old = reinterpret_cast<int32_t *>(raw);  // [rows][kForkCols]; -1 where a row has no page
+  int4 *old = reinterpret_cast<int4 *>(raw);  // [rows]; -1 where a row has no page
   griddep_launch_dependents();
   griddep_wait();
-  const int c0 = blockIdx.x * kForkCols, n = a.rows * kForkCols;
-  for (int i = threadIdx.x; i < n; i += kForkThreads) {
-    const int row = i / kForkCols, c = c0 + i % kForkCols;
-    const int len = min(max(a.lens[row], 0), a.width * a.ps);
-    old[i] = c < ceil_div(len, a.ps) ? a.table[static_cast<size_t>(row) * a.width + c] : -1;
+  const int c0 = blockIdx.x * kForkCols;
+  for (int row = threadIdx.x; row < a.rows; row += kPageThreads) {
+    const int32_t *t = a.table + static_cast<size_t>(row) * a.width + c0;
+    int v[kForkCols];
+#pragma unroll
+    for (int c = 0; c < kForkCols; ++c) v[c] = c0 + c < a.width ? t[c] : -1;
+    const int used = ceil_div(min(max(a.lens[row], 0), a.width * a.ps), a.ps) - c0;
+    old[row] = make_int4(used > 0 ? v[0] : -1, used > 1 ? v[1] : -1, used > 2 ? v[2] : -1, used > 3 ? v[3] : -1);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kForkThreads) {
-    const int row = i / kForkCols, c = c0 + i % kForkCols, p = a.parents[row];
-    if (c >= a.width || p < 0 || p >= a.rows || p == row) continue;
-    const int gone = old[i], got = old[p * kForkCols + i % kForkCols];
-    if (gone != got) {
-      if (gone >= 0 && gone < a.pages) atomicSub(a.refs + gone, 1);
-      if (got >= 0 && got < a.pages) atomicAdd(a.refs + got, 1);
-    }
-    a.table[static_cast<size_t>(row) * a.width + c] = got;
+  for (int row = threadIdx.x; row < a.rows; row += kPageThreads) {
+    const int p = a.parents[row];
+    if (p < 0 || p >= a.rows || p == row) continue;
+    int32_t *t = a.table + static_cast<size_t>(row) * a.width + c0;
+    const int4 gone = old[row], got = old[p];
+    auto change = [&](int c, int from, int to) {
+      if (c0 + c >= a.width) return;
+      t[c] = to;
+      if (from == to) return;
+      if (from >= 0 && from < a.pages) atomicSub(a.refs + from, 1);
+      if (to >= 0 && to < a.pages) atomicAdd(a.refs + to, 1);
+    };
+    change(0, gone.x, got.x);
+    change(1, gone.y, got.y);
+    change(2, gone.z, got.z);
+    change(3, gone.w, got.w);
   }
 }
 
@@ -1212,27 +1236,43 @@ __global__ void __launch_bounds__(kPageThreads) kv_fork_lens_kernel(const __grid
 // Of L pages in use, those numbered L and up move to the free ones below L, k-th to
 // k-th, so no page is both source and destination.
 __global__ void __launch_bounds__(kPageThreads) kv_compact_plan_kernel(const __grid_constant__ CompactArgs a) {
-  __shared__ int warps[32];
+  __shared__ unsigned long long warps[32];
   griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x;
-  int used = 0, all;
-  for (int p = tid; p < a.pages; p += kPageThreads) used += a.refs[p] > 0;
-  cta_scan(used, warps, used);
-  int holes = 0, moved = 0;
-  for (int base = 0; base < a.pages; base += kPageThreads) {
-    const int p = base + tid;
-    const bool in = p < a.pages, live = in && a.refs[p] > 0;
-    const bool hole = in && !live && p < used, moves = live && p >= used;
-    const int h = holes + cta_scan(hole, warps, all);
-    holes += all;
-    const int m = moved + cta_scan(moves, warps, all);
-    moved += all;
-    if (hole) a.holes[h] = p;
-    if (moves) a.moves[m] = p;
-    if (in) a.page_map[p] = live ? p : -1;
+  unsigned long long all, mine = 0;
+  for (int p = kPagesEach * tid; p < a.pages; p += kPagesEach * kPageThreads) {
+    uint32_t there;
+    mine += __popc(pages_in_use(a.refs, p, a.pages, a.refs_vector, there));
+  }
+  cta_scan(mine, warps, all);
+  const int used = static_cast<int>(all);
+  unsigned long long sum = 0;  // holes in the low half, pages to move in the high one
+  for (int base = 0; base < a.pages; base += kPagesEach * kPageThreads) {
+    const int p = base + kPagesEach * tid;
+    uint32_t there = 0, live = 0;
+    if (p < a.pages) live = pages_in_use(a.refs, p, a.pages, a.refs_vector, there);
+    const uint32_t below = used <= p ? 0 : used - p >= kPagesEach ? 0xFFFF : (1u << (used - p)) - 1;
+    uint32_t holes = there & ~live & below, moves = live & ~below;
+    const unsigned long long at =
+        sum + cta_scan<unsigned long long>(__popc(holes) | static_cast<unsigned long long>(__popc(moves)) << 32, warps, all);
+    sum += all;
+    int h = static_cast<int>(at), m = static_cast<int>(at >> 32);
+    for (; holes; holes &= holes - 1) a.holes[h++] = p + __ffs(holes) - 1;
+    for (; moves; moves &= moves - 1) a.moves[m++] = p + __ffs(moves) - 1;
+    if (there == 0xFFFF && a.map_vector) {
+#pragma unroll
+      for (int i = 0; i < kPagesEach; i += 4)
+        *reinterpret_cast<int4 *>(a.page_map + p + i) =
+            make_int4(live >> i & 1 ? p + i : -1, live >> i & 2 ? p + i + 1 : -1, live >> i & 4 ? p + i + 2 : -1,
+                      live >> i & 8 ? p + i + 3 : -1);
+    } else {
+      for (int i = 0; i < kPagesEach; ++i)
+        if (there >> i & 1) a.page_map[p + i] = live >> i & 1 ? p + i : -1;
+    }
   }
   __syncthreads();
+  const int moved = static_cast<int>(sum >> 32);
   for (int m = tid; m < moved; m += kPageThreads) a.page_map[a.moves[m]] = a.holes[m];
   if (tid == 0) *a.count = moved;
 }
@@ -1319,8 +1359,8 @@ cudaError_t launch_kv_resize(const ResizeArgs &a, int sm_count, cudaStream_t str
 }
 
 cudaError_t launch_kv_fork(const ForkArgs &a, cudaStream_t stream, bool pdl) {
-  cudaError_t e = launch(kv_fork_kernel, dim3(ceil_div(a.width, kForkCols)), dim3(kForkThreads),
-                         sizeof(int32_t) * kForkCols * a.rows, stream, pdl, a);
+  cudaError_t e = launch(kv_fork_kernel, dim3(ceil_div(a.width, kForkCols)), dim3(kPageThreads),
+                         sizeof(int4) * a.rows, stream, pdl, a);
   if (e != cudaSuccess) return e;
   return launch(kv_fork_lens_kernel, dim3(1), dim3(kPageThreads), 0, stream, pdl, a);
 }
@@ -1345,7 +1385,7 @@ cudaError_t cache_setup() {
                                 static_cast<int>(sizeof(ResizeShared)))))
     return e;
   return cudaFuncSetAttribute(kv_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(sizeof(int32_t) * kForkCols * SK_MAX_CACHE_ROWS));
+                              static_cast<int>(sizeof(int4) * SK_MAX_CACHE_ROWS));
 }
 
 cudaError_t read_cache_status(uint32_t *out, bool clear) {

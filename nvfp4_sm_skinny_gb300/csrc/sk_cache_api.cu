@@ -289,7 +289,8 @@ sk_status sk_kv_compact(uint8_t *cache, int32_t *table, const int32_t *lens, int
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   const size_t list = round256(4 * static_cast<size_t>(pages));
   sk::CompactArgs a{cache, table, lens, refs, page_map, rows, width, pages, page_size, layers, page_bytes,
-                    static_cast<size_t>(pages) * page_bytes, reinterpret_cast<int32_t *>(ws),
+                    static_cast<size_t>(pages) * page_bytes, (reinterpret_cast<uintptr_t>(refs) & 15) == 0,
+                    (reinterpret_cast<uintptr_t>(page_map) & 15) == 0, reinterpret_cast<int32_t *>(ws),
                     reinterpret_cast<int32_t *>(ws + list), reinterpret_cast<int32_t *>(ws + 2 * list)};
   return launch_status(sk::launch_kv_compact(a, info.sm_count, as_stream(stream), sk::pdl_on()), "kv_compact");
 }

@@ -319,6 +319,7 @@ struct CompactArgs {
   int32_t *refs, *page_map;
   int rows, width, pages, ps, layers, page_bytes;
   size_t layer_bytes;
+  bool refs_vector, map_vector;  // refs, page_map are 16-byte aligned
   int32_t *holes, *moves;  // [pages]
   int32_t *count;          // pages moved
 };
