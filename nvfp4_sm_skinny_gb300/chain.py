@@ -19,7 +19,21 @@ routed experts in int8 on z:
     zq, zs  = int8 codes of z's rows                                  (sk_int8_quantize)
     e       = sum_j g_j W2(silu(W1 z) * W3 z)  [E, 2 I, 4096], [E, 4096, I] (sk_experts_int8)
 
-and the unpooler reads e; the NVFP4 codes a and a_sf have no reader then. This
+and the unpooler reads e; the NVFP4 codes a and a_sf have no reader then.
+
+The attention stands before the o_proj (attention width 128 heads of 64, H). The
+pages start at its output, and so does the chain by default: the o_proj reads h in
+its place. With ``context`` > 0 each layer runs it on h, one token of each of the m
+rows per pass, with kv_heads KV heads and a key/value cache held in 4 bits, of
+``context`` tokens per row:
+
+    q, k, v = h_l @ W_qkv^T               qkv   [8192 + 2 kv_heads 64, 8192]  (sk_gemm_bf16)
+    cache  <- k, v                        at the last position of each row    (sk_kv_append)
+    o       = attention of q over it                                          (sk_attn_nvfp4)
+
+and the o_proj reads o. A pass starts by giving the rows the lengths in ``want``
+(sk_kv_resize), which the caller sets before it, each row's tokens so far and one
+more (0: a row without a sequence). This
 module only allocates buffers and calls the binding; every step runs in libsk's
 kernels. ``capture()`` records one pass into a CUDA graph (the calls allocate
 nothing and are capturable).
@@ -35,6 +49,7 @@ from nvfp4_sm_skinny_gb300 import synth
 
 H = synth.HIDDEN
 P = synth.POOLED
+HEAD = 64  # columns of a query, key or value head
 
 
 def layer_bytes(m: int) -> dict:
@@ -60,7 +75,7 @@ class DecodeChain:
     def __init__(self, layers: int = 48, m: int = 16, device="cuda", eps: float = synth.EPS,
                  gain_center: float = synth.GAIN_CENTER, splits: int = 0,
                  prefetch_next: bool = True, experts: int = 0, top_k: int = 8,
-                 inter: int = 1024):
+                 inter: int = 1024, context: int = 0, kv_heads: int = 8, page_size: int = 64):
         self.L, self.m, self.device = layers, m, torch.device(device)
         self.experts, self.top_k, self.inter = experts, top_k, inter
         # each GEMM starts the next GEMM's first weight stages towards L2
@@ -90,8 +105,30 @@ class DecodeChain:
         self.ws_p = torch.zeros(layers, sk.gemm_rmsnorm_nvfp4_workspace(m, P), dtype=torch.uint8,
                                 device=dev)
 
+        self.context = context
+        if context:
+            self._add_attention(bf, kv_heads, page_size)
         if experts:
             self._add_experts(bf)
+
+    def _add_attention(self, bf, kv_heads, page_size) -> None:
+        L, m, dev, d = self.L, self.m, self.device, HEAD
+        self.kv_heads, self.page_size = kv_heads, page_size
+        self.heads = [H, kv_heads * d, kv_heads * d]           # columns of q, k and v
+        self.w_qkv = [synth.chain_weight(l, 11, (sum(self.heads), H), device=dev) for l in range(L)]
+        self.k_gs = torch.full((L, 1), 448.0, dtype=torch.float32, device=dev)
+        self.v_gs = torch.full((L, 1), 448.0, dtype=torch.float32, device=dev)
+        self.qkv = torch.zeros(L, m, sum(self.heads), **bf)
+        self.o = torch.zeros(L, m, H, **bf)                    # attention outputs
+        width = -(-self.context // page_size)
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.cache = torch.zeros(L, m * width, kv_heads, sk.kv_block_bytes(page_size, d), dtype=torch.uint8,
+                                 device=dev)
+        self.table = torch.full((m, width), -1, **i32)
+        self.lens, self.want, self.row_status = (torch.zeros(m, **i32) for _ in range(3))
+        self.refs = torch.zeros(m * width, **i32)
+        self.ws_a = torch.zeros(sk.attn_nvfp4_workspace(m, 1, H // d, kv_heads, d), dtype=torch.uint8, device=dev)
+        self.ws_r = torch.zeros(sk.kv_resize_workspace(m, m * width), dtype=torch.uint8, device=dev)
 
     def _add_experts(self, bf) -> None:
         L, m, E, I, dev = self.L, self.m, self.experts, self.inter, self.device
@@ -122,6 +159,8 @@ class DecodeChain:
         names = ("h", "s", "u", "z", "a", "a_sf", "ws_o", "ws_p")
         if self.experts:
             names += ("logits", "ids", "gates", "zq", "zs", "e", "ws_e")
+        if self.context:
+            names += ("qkv", "o", "cache", "table", "lens", "want", "row_status", "refs", "ws_a", "ws_r")
         for name in names:
             setattr(t, name, torch.zeros_like(getattr(self, name)))
         return t
@@ -134,7 +173,8 @@ class DecodeChain:
         """One of the layer's three calls: 0 o_proj + dual norm, 1 pooler +
         RMSNorm + NVFP4, 2 unpooler."""
         if op == 0:
-            sk.gemm_dual_norm(self.h[l], self.w_o[l], self.s, self.post_w[l], self.alpha,
+            x = self.o[l] if self.context else self.h[l]
+            sk.gemm_dual_norm(x, self.w_o[l], self.s, self.post_w[l], self.alpha,
                               self.beta[l], self.pre_w[l], out=self.u[l], eps_post=self.eps,
                               eps_pre=self.eps, workspace=self.ws_o[l], splits=self.splits,
                               stream=stream)
@@ -156,15 +196,35 @@ class DecodeChain:
                         self.ids[l], self.gates[l], out=self.e[l], workspace=self.ws_e,
                         stream=stream)
 
+    def rows(self, stream=None) -> None:
+        """The rows take the lengths in ``want`` (a chain with attention)."""
+        sk.kv_resize(self.want, self.cache, self.table, self.lens, self.refs, self.page_size,
+                     status=self.row_status, workspace=self.ws_r, stream=stream)
+
+    def attend(self, l: int, stream=None) -> None:
+        """The attention of layer l: h[l] to o[l] (a chain with attention)."""
+        m, d = self.m, HEAD
+        if self.prefetch_next:
+            sk.gemm_prefetch_next(self.w_o[l])
+        sk.gemm_bf16(self.h[l], self.w_qkv[l], out=self.qkv[l], splits=self.splits, stream=stream)
+        q, k, v = (x.unflatten(1, (1, -1, d)) for x in self.qkv[l].split(self.heads, 1))
+        sk.kv_append(k, v, self.k_gs[l], self.v_gs[l], self.cache[l], self.table, self.lens, self.page_size,
+                     stream=stream)
+        sk.attn_nvfp4(q, self.k_gs[l], self.v_gs[l], self.cache[l], self.table, self.lens, self.page_size,
+                      out=self.o[l].view(m, 1, H // d, d), workspace=self.ws_a, stream=stream)
+
     def next_weight(self, l: int, op: int):
         """The weight of the GEMM after layer l's call `op` (None after the last)."""
         if op == 0:
             return self.w_p[l]
         if op == 1:
             return self.w_r[l] if self.experts else self.w_u[l]
-        return self.w_o[l + 1] if l + 1 < self.L else None
+        first = self.w_qkv if self.context else self.w_o
+        return first[l + 1] if l + 1 < self.L else None
 
     def layer(self, l: int, stream=None) -> None:
+        if self.context:
+            self.attend(l, stream)
         for op in range(3):
             if self.prefetch_next:
                 sk.gemm_prefetch_next(self.next_weight(l, op))
@@ -173,6 +233,8 @@ class DecodeChain:
                 self.routed(l, stream)
 
     def forward(self, stream=None) -> None:
+        if self.context:
+            self.rows(stream)
         for l in range(self.L):
             self.layer(l, stream)
 
@@ -187,19 +249,31 @@ class DecodeChain:
             hint(self.w_u[l])  # next here, routed experts or not
             sk.gemm_bf16(self.u[l], self.w_p[l], out=self.ws_p[l][: self.m * P * 2].view(
                 torch.bfloat16).view(self.m, P), splits=self.splits, stream=stream)
-            hint(self.next_weight(l, 2))
+            hint(self.w_o[l + 1] if l + 1 < self.L else None)  # next here, attention or not
             sk.gemm_bf16(self.z[l], self.w_u[l], out=self.h[l + 1], splits=self.splits,
                          stream=stream)
 
     def calibrate(self, x_cal: torch.Tensor, s_cal: torch.Tensor) -> None:
         """Sets each layer's NVFP4 global scale to 448 * 6 / amax(z) of one
-        calibration pass (set-up, outside any timed region)."""
+        calibration pass (set-up, outside any timed region). With attention also
+        those of K and V; the pass takes one token of each row, the rows' first, and
+        leaves them without any."""
         self.set_input(x_cal, s_cal)
         self.gs.fill_(1.0)
+        if self.context:
+            self.want.fill_(1)
+            self.rows()
         for l in range(self.L):
             self.layer(l)
             amax = self.z[l].float().abs().amax()
             self.gs[l].copy_(2688.0 / amax.clamp_min(1e-30))
+            if self.context:
+                _, k, v = self.qkv[l].float().abs().split(self.heads, 1)
+                self.k_gs[l].copy_(2688.0 / k.amax().clamp_min(1e-30))
+                self.v_gs[l].copy_(2688.0 / v.amax().clamp_min(1e-30))
+        if self.context:
+            self.want.fill_(0)
+            self.rows()
         torch.cuda.synchronize(self.device)
 
     def capture(self, fn=None) -> torch.cuda.CUDAGraph:
@@ -216,5 +290,5 @@ class DecodeChain:
         torch.cuda.synchronize(self.device)
         return g
 
-    launches_per_layer = 5          # without experts, which add 7
+    launches_per_layer = 5          # without experts, which add 7, and attention, which adds 4
     gemm_launches_per_layer = 3
