@@ -202,14 +202,15 @@ __device__ __forceinline__ Keys keys_of(const AttnArgs &a, int len) {
 }
 
 // What four sequences from s on count for, with all their items.
-__device__ __forceinline__ long long cost_of4(const AttnArgs &a, int s, long long (&n)[4]) {
+template <typename T>
+__device__ __forceinline__ T cost_of4(const AttnArgs &a, int s, T (&n)[4]) {
   int len[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) len[k] = s + k < a.b ? a.lens[s + k] : 0;
-  long long sum = 0;
+  T sum = 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    n[k] = static_cast<long long>(keys_of(a, len[k]).cost()) * (a.hk * a.tiles);
+    n[k] = static_cast<T>(keys_of(a, len[k]).cost()) * (a.hk * a.tiles);
     sum += n[k];
   }
   return sum;
@@ -273,13 +274,50 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
   // different SMs.
   const int per = a.hk * a.tiles, G = gridDim.x * kAttnWarps;
   const int me = w * gridDim.x + blockIdx.x;
-  long long U = 0, n[4];
-  for (int s = 4 * lane; s < a.b; s += 128) U += cost_of4(a, s, n);
+  long long u, end, at = 0;  // at: the place of u within its sequence
+  int seq = 0;
+  Parts parts(0, 1);
+  // A warp finds its part by itself, a lane for four sequences, in 32 bits where the sum
+  // of all fits.
+  auto find = [&](auto zero) {
+    using T = decltype(zero);
+    T U = 0, n[4], mine = 0;
+    for (int s = 4 * lane; s < a.b; s += 128) U += mine = cost_of4(a, s, n);
 #pragma unroll
-  for (int d = 16; d; d >>= 1) U += __shfl_xor_sync(kAll, U, d);
-  const Parts parts(U, G);
-  long long u = parts.start(me);
-  long long end = parts.start(me + 1);
+    for (int d = 16; d; d >>= 1) U += __shfl_xor_sync(kAll, U, d);
+    parts = Parts(U, G);
+    u = parts.start(me);
+    end = parts.start(me + 1);
+    if (u >= end) return;
+    const T from = static_cast<T>(u);
+    T before = 0;
+    for (int base = 0;; base += 128) {
+      if (a.b > 128) mine = cost_of4(a, base + 4 * lane, n);  // else still at hand
+      T upto = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const T o = __shfl_up_sync(kAll, upto, d);
+        if (lane >= d) upto += o;
+      }
+      const uint32_t behind = __ballot_sync(kAll, before + upto > from);
+      if (behind) {
+        T off = from - before - (upto - mine);  // from this lane's first sequence
+        int s = base + 4 * lane;
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          if (s == base + 4 * lane + k && off >= n[k]) {
+            off -= n[k];
+            ++s;
+          }
+        seq = __shfl_sync(kAll, s, __ffs(behind) - 1);
+        at = __shfl_sync(kAll, off, __ffs(behind) - 1);
+        return;
+      }
+      before += __shfl_sync(kAll, upto, 31);
+    }
+  };
+  if (a.small) find(0);
+  else find(0ll);
 
   // Sequences of which nothing is seen.
   for (int s = me; s < a.b; s += G) {
@@ -290,34 +328,6 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
     for (int i = lane; i < per; i += 32) a.joins[static_cast<size_t>(s) * per + i] = make_int2(0, -1);
   }
   if (u >= end) return;
-
-  int seq = 0;
-  long long at = 0;  // place of u within its sequence
-  for (int base = 0;; base += 128) {
-    const long long mine = cost_of4(a, base + 4 * lane, n);
-    long long upto = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long o = __shfl_up_sync(kAll, upto, d);
-      if (lane >= d) upto += o;
-    }
-    const uint32_t behind = __ballot_sync(kAll, at + upto > u);
-    if (behind) {
-      const int from = __ffs(behind) - 1;
-      long long off = u - at - (upto - mine);  // from this lane's first sequence
-      int s = base + 4 * lane;
-#pragma unroll
-      for (int k = 0; k < 3; ++k)
-        if (s == base + 4 * lane + k && off >= n[k]) {
-          off -= n[k];
-          ++s;
-        }
-      seq = __shfl_sync(kAll, s, from);
-      at = __shfl_sync(kAll, off, from);
-      break;
-    }
-    at += __shfl_sync(kAll, upto, 31);
-  }
 
   // Row e of those of N tile nt that this lane holds statistics of.
   auto row_at = [&](int nt, int e) { return 8 * nt + (kWide ? g : 2 * j + e); };
@@ -832,20 +842,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
 #pragma unroll
     for (int c = 0; c < V; ++c) sums[w][V * lane + c] = acc[c];
     __syncthreads();
-    if (sub == 0) {
-      const float own = top;
-      for (int k = 1; k < S; ++k) top = fmaxf(top, stat[w + k].x);
-      const float f0 = own == -CUDART_INF_F ? 0.0f : ex2(own - top);
-      l *= f0;
+    if (sub == 0) {  // a lane per warp of the row weighs its sums
+      const float2 x = lane < S ? stat[w + lane] : make_float2(-CUDART_INF_F, 0.0f);
+      top = x.x;
 #pragma unroll
-      for (int c = 0; c < V; ++c) acc[c] *= f0;
-      for (int k = 1; k < S; ++k) {
-        const float2 x = stat[w + k];
-        if (x.x == -CUDART_INF_F) continue;
-        const float f = ex2(x.x - top);
-        l = fmaf(f, x.y, l);
+      for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
+      const float f = x.x == -CUDART_INF_F ? 0.0f : ex2(x.x - top);
+      l = f * x.y;
 #pragma unroll
-        for (int c = 0; c < V; ++c) acc[c] = fmaf(f, sums[w + k][V * lane + c], acc[c]);
+      for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(kAll, l, d);
+#pragma unroll
+      for (int c = 0; c < V; ++c) acc[c] = 0.0f;
+#pragma unroll 4
+      for (int k = 0; k < S; ++k) {
+        const float fk = __shfl_sync(kAll, f, k);
+#pragma unroll
+        for (int c = 0; c < V; ++c) acc[c] = fmaf(fk, sums[w + k][V * lane + c], acc[c]);
       }
     }
   }
@@ -1320,13 +1332,14 @@ size_t attn_part_bytes(int d, int nt) { return sizeof(float) * attn_part_floats(
 
 int attn_max_parts(int sm_count) { return kAttnWarps * sm_count; }
 
-cudaError_t launch_attn(const AttnArgs &a, int d, int sm_count, cudaStream_t stream, bool pdl) {
+cudaError_t launch_attn(AttnArgs a, int d, int sm_count, cudaStream_t stream, bool pdl) {
   const int nt = attn_row_tiles(a.rows);
   return with_attn(d, nt, [&](auto dim, auto tiles) {
     constexpr int D = decltype(dim)::value, NT = decltype(tiles)::value;
     // no more SMs than there can be chunks
     const long long items = static_cast<long long>(a.b) * a.hk * a.tiles;
     const long long chunks = ceil_div(a.width * a.ps, kChunk);  // of an item, at most
+    a.small = (chunks + kItemCost) * items < (1ll << 31);
     const int grid = static_cast<int>((chunks + kItemCost) * items < sm_count ? (chunks + kItemCost) * items : sm_count);
     cudaError_t e = launch(attn_kernel<D, NT>, dim3(grid), dim3(32 * kAttnWarps),
                            kAttnWarps * sizeof(AttnWarp<D, NT>), stream, pdl, a);

@@ -273,11 +273,12 @@ struct AttnArgs {
   int group, rows, tiles;
   long long q_stride;  // values between tokens
   float scale;
+  bool small;  // the work counts for less than 2^31, set by the launch
 };
 int attn_row_tiles(int rows);                   // tiles of 8 rows that a CTA takes at once
 int attn_max_parts(int sm_count);               // parts of such a launch, at most
 size_t attn_part_bytes(int d, int nt);          // bytes of an unfinished result
-cudaError_t launch_attn(const AttnArgs &a, int d, int sm_count, cudaStream_t stream, bool pdl);
+cudaError_t launch_attn(AttnArgs a, int d, int sm_count, cudaStream_t stream, bool pdl);
 
 struct AppendArgs {
   const uint16_t *k, *v;
