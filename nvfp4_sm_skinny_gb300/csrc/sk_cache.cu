@@ -159,7 +159,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 // 114 us, 85 where the kernel ran alone), and four warps that join their sums in
 // shared memory item by item waited for one another (93 us).
 constexpr int kChunk = 64;
-constexpr int kItemCost = 1;
+constexpr int kItemCost = 3;
 // Scores are kept as powers of two relative to a base that is at most 15 and after
 // an update 7 below the largest, so that P fits FP16 and what is 2^31 times smaller
 // than the largest still counts; the base moves (and the sums are scaled) only
@@ -778,15 +778,15 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
 }
 
 // Joins the items that fell into several parts. S warps of a CTA take a row of an item
-// together, as many as leave each about four results, whose loads do not wait for one
-// another (b64 d128: 512 items of five results, with 16 warps on one row after another
-// 25 us, a warp per row 5).
+// together, so that each has few results, whose loads do not wait for one another (b64
+// d128: 512 items of five results, with 16 warps on one row after another 25 us, a
+// warp per row 5).
 constexpr int kJoinWarps = 32;  // of a row, at most
 
 template <int D, int NT>
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ AttnArgs a, int S) {
   constexpr int V = D / 32;  // neighbouring channels per lane
-  constexpr int kBatch = 4;
+  constexpr int kBatch = 8;
   __shared__ float2 stat[kJoinWarps];
   __shared__ float sums[kJoinWarps][D];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, rows = (blockDim.x >> 5) / S;
@@ -1344,12 +1344,14 @@ cudaError_t launch_attn(AttnArgs a, int d, int sm_count, cudaStream_t stream, bo
     cudaError_t e = launch(attn_kernel<D, NT>, dim3(grid), dim3(32 * kAttnWarps),
                            kAttnWarps * sizeof(AttnWarp<D, NT>), stream, pdl, a);
     if (e != cudaSuccess) return e;
-    // warps of a row: a quarter of the results that an item has on average
+    // Warps of a row: as many as take eight results each on average, or four where the
+    // GPU holds them all at once (b16 t4 of 512 items: 32.7 us with four, 30.6 with
+    // eight; b1 of 2048 tokens: 11.0 and 11.9).
     const int rows = a.rows < 8 * NT ? a.rows : 8 * NT;
     const long long most = grid * kAttnWarps / items + 2, results = most < chunks ? most : chunks;
     int S = 1;
-    while (S < kJoinWarps && 4 * S < results) S *= 2;
-    const int warps = S < 4 ? 4 : S;
+    while (S < kJoinWarps && (8 * S < results || (4 * S < results && 2 * S * items * rows <= 32 * sm_count))) S *= 2;
+    const int warps = S > 8 ? S : rows * S < 8 ? rows * S : 8;
     return launch(attn_join_kernel<D, NT>, dim3(static_cast<unsigned>(items), ceil_div(rows * S, warps)),
                   dim3(32 * warps), 0, stream, pdl, a, S);
   });
