@@ -35,11 +35,14 @@ cudaError_t launch(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, 
 
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return a / b + (a % b != 0); }
 
-// Untiled bulk copy global -> shared, completion counted on `bar` in bytes.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+// Untiled bulk copy global -> shared, completion counted on `bar` in bytes. What is
+// copied leaves L2 first: the cache is read once, and table, queries and unfinished
+// results stay (b64 d128: 66.2 us without, 64.0 with).
+__device__ __forceinline__ void bulk_load_once(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar), "l"(l2_policy_evict_first())
       : "memory");
 }
 
@@ -393,7 +396,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
       if (lane == 0) mbar_arrive_expect_tx(bar, __popc(mask) * blk);
       __syncwarp();
       if (real)
-        bulk_load(smem_u32(ring + s * Sh::kStageBytes + lane * blk),
+        bulk_load_once(smem_u32(ring + s * Sh::kStageBytes + lane * blk),
                   a.cache + (static_cast<size_t>(page) * a.hk + place.h) * blk, blk, bar);
       held = (held & ~(15 << 4 * s)) | static_cast<int>(mask) << 4 * s;
     };
@@ -790,6 +793,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
   __shared__ float2 stat[kJoinWarps];
   __shared__ float sums[kJoinWarps][D];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, rows = (blockDim.x >> 5) / S;
+  griddep_launch_dependents();
   griddep_wait();
   const int2 join = a.joins[blockIdx.x];  // the parts that the item begins and ends in
   if (join.y < 0) return;
@@ -869,8 +873,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
     for (int c = 0; c < V; c += 2) dst[c / 2] = bf16_pair(acc[c] * f, acc[c + 1] * f);
     if (a.lse && lane == 0) a.lse[row] = row_lse(top, l);
   }
-  // Not earlier: CTAs of the next kernel would take their places between these.
-  griddep_launch_dependents();
 }
 
 // ------------------------------------------------------------------- append
