@@ -514,7 +514,8 @@ size_t sk_attn_nvfp4_workspace(int b, int t, int q_heads, int kv_heads, int head
  *   state; scratch for this call alone (calls that may run at the same time need
  *   one each)
  *   q_heads a multiple of kv_heads, at most 4096; b t <= 2^24, b t q_heads <= 2^30;
- *   scale finite; q, cache and out 16-byte, the rest 4-byte aligned.
+ *   scale finite; q, cache and out 16-byte, the rest 4-byte aligned; out and lse
+ *   overlap nothing that is read.
  * Scores and sums are FP32, K and V exact; p enters the product with V in FP16 (of
  * 2^7 to 2^15 at its largest), with a rounding of at most 2^-11 of itself.
  * Results depend on the inputs alone: the work is cut by the lengths, in a fixed

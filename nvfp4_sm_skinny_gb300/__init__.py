@@ -605,14 +605,24 @@ def _token_stride(x, name):
     return step
 
 
-def _want_cache(cache, dims, page_size, head_dim, kv_heads):
-    """Pages of a cache uint8 [(layers,) pages, kv_heads, block]."""
-    if cache.dim() != dims:
-        raise ValueError(f"cache: {cache.dim()} dimensions, needs {dims}")
-    pages = cache.shape[-3]
-    block = page_size * head_dim * 9 // 8
-    _want(cache, torch.uint8, (*cache.shape[: dims - 2], kv_heads, block), "cache")
-    return pages
+def _sizes(t, dims, name):
+    """The shape of t, which has that many dimensions."""
+    shape = t.shape
+    if len(shape) != dims:
+        raise ValueError(f"{name}: shape {tuple(shape)}, needs {dims} dimensions")
+    return shape
+
+
+def _layer_sizes(cache, table, page_size, head_dim, b, t):
+    """(pages, kv_heads, width) of a layer's cache uint8 [pages, kv_heads, block] and
+    the table int32 [b, width]."""
+    pages, heads, _ = _sizes(cache, 3, "cache")
+    _, width = _sizes(table, 2, "table")
+    if (b | t | pages | heads | width | page_size) >> 31:
+        _fits(b=b, t=t, pages=pages, kv_heads=heads, width=width, page_size=page_size)
+    _want(cache, torch.uint8, (pages, heads, page_size * head_dim * 9 // 8), "cache")
+    _want(table, torch.int32, (b, width), "table")
+    return pages, heads, width
 
 
 def kv_append(k, v, k_global_scale, v_global_scale, cache, table, lens, page_size: int, stream=None):
@@ -620,19 +630,17 @@ def kv_append(k, v, k_global_scale, v_global_scale, cache, table, lens, page_siz
     a layer's cache uint8 [pages, kv_heads, block], in place: token j of row i at
     position lens[i] - t + j of the pages that table int32 [b, width] names. k and v
     may be parts of longer rows (sk_kv_append)."""
-    b, t, heads, d = k.shape
+    b, t, heads, d = _sizes(k, 4, "k")
     if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16:
         raise ValueError(f"k, v: dtypes {k.dtype}, {v.dtype}, need torch.bfloat16")
     if v.shape != k.shape:
         raise ValueError(f"v: shape {tuple(v.shape)}, needs {tuple(k.shape)}")
     ks, vs = _token_stride(k, "k"), _token_stride(v, "v")
-    width = table.shape[-1]
-    if (b | t | width | page_size) >> 31 or cache.shape[0] >> 31:
-        _fits(b=b, t=t, width=width, page_size=page_size, pages=cache.shape[0])
+    pages, kv_heads, width = _layer_sizes(cache, table, page_size, d, b, t)
+    if kv_heads != heads:
+        raise ValueError(f"k: {heads} heads, needs the cache's {kv_heads}")
     _want(k_global_scale, torch.float32, (1,), "k_global_scale")
     _want(v_global_scale, torch.float32, (1,), "v_global_scale")
-    pages = _want_cache(cache, 3, page_size, d, heads)
-    _want(table, torch.int32, (b, width), "table")
     _want(lens, torch.int32, (b,), "lens")
     s = _launch_on(stream, k.get_device(), v, k_global_scale, v_global_scale, cache, table, lens)
     _check(lib().sk_kv_append(k.data_ptr(), v.data_ptr(), k_global_scale.data_ptr(),
@@ -657,17 +665,15 @@ def attn_nvfp4(q, k_global_scale, v_global_scale, cache, table, lens, page_size:
     ``window`` the last that many of them. ``scale`` is 1 / sqrt(d) if None; ``lse``
     (FP32 [b, t, q_heads]) may be a tensor, True (allocate) or None (not stored)
     (sk_attn_nvfp4)."""
-    b, t, heads, d = q.shape
+    b, t, heads, d = _sizes(q, 4, "q")
     if q.dtype is not torch.bfloat16:
         raise ValueError(f"q: dtype {q.dtype}, needs torch.bfloat16")
     stride = _token_stride(q, "q")
-    width, kv_heads = table.shape[-1], cache.shape[-2]
-    if (b | t | width | page_size | window) >> 31 or cache.shape[0] >> 31:
-        _fits(b=b, t=t, width=width, page_size=page_size, window=window, pages=cache.shape[0])
+    if window >> 31:
+        _fits(window=window)
+    pages, kv_heads, width = _layer_sizes(cache, table, page_size, d, b, t)
     _want(k_global_scale, torch.float32, (1,), "k_global_scale")
     _want(v_global_scale, torch.float32, (1,), "v_global_scale")
-    pages = _want_cache(cache, 3, page_size, d, kv_heads)
-    _want(table, torch.int32, (b, width), "table")
     _want(lens, torch.int32, (b,), "lens")
     if out is None:
         out = _new((b, t, heads, d), torch.bfloat16, q.device, stream)
@@ -705,10 +711,8 @@ def kv_compact_workspace(pages: int) -> int:
 
 def _pages_sizes(cache, table, lens, refs, page_size):
     """(layers, pages, kv_heads, head_dim, rows, width) of a cache's bookkeeping."""
-    if cache.dim() != 4:
-        raise ValueError(f"cache: {cache.dim()} dimensions, needs 4")
-    layers, pages, heads, block = cache.shape
-    rows, width = table.shape
+    layers, pages, heads, block = _sizes(cache, 4, "cache")
+    rows, width = _sizes(table, 2, "table")
     if (layers | pages | heads | rows | width | page_size) >> 31:
         _fits(layers=layers, pages=pages, kv_heads=heads, rows=rows, width=width, page_size=page_size)
     d = block * 8 // (9 * page_size) if page_size > 0 else 0
@@ -758,8 +762,8 @@ def kv_fork(parents, table, lens, refs, page_size: int, status=None, stream=None
     """status int32 [rows]: row i of table becomes what row parents[i] was before the
     call (negative, or i: as it is); the rows share their pages. table, lens and refs are
     updated in place; status is 2 for a parent that is no row (sk_kv_fork)."""
-    rows, width = table.shape
-    pages, = refs.shape
+    rows, width = _sizes(table, 2, "table")
+    pages, = _sizes(refs, 1, "refs")
     if (rows | width | pages | page_size) >> 31:
         _fits(rows=rows, width=width, pages=pages, page_size=page_size)
     _want_pages(table, lens, refs, pages, rows, width)

@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
     if (u >= end) return;
     const T from = static_cast<T>(u);
     T before = 0;
-    for (int base = 0;; base += 128) {
+    for (int base = 0; base < a.b; base += 128) {
       if (a.b > 128) mine = cost_of4(a, base + 4 * lane, n);  // else still at hand
       T upto = mine;
 #pragma unroll
@@ -318,6 +318,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
       }
       before += __shfl_sync(kAll, upto, 31);
     }
+    u = end;  // lengths that somebody changes meanwhile are no reason to search on
   };
   if (a.small) find(0);
   else find(0ll);
@@ -326,8 +327,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
   for (int s = me; s < a.b; s += G) {
     if (keys_of(a, a.lens[s]).cost()) continue;
     uint4 *o = reinterpret_cast<uint4 *>(a.out + static_cast<size_t>(s) * a.t * a.hq * D);
-    for (int i = lane; i < a.t * a.hq * (D / 8); i += 32) o[i] = make_uint4(0, 0, 0, 0);
-    for (int i = lane; a.lse && i < a.t * a.hq; i += 32) a.lse[static_cast<size_t>(s) * a.t * a.hq + i] = -CUDART_INF_F;
+    const long long rows = static_cast<long long>(a.t) * a.hq;
+    for (long long i = lane; i < rows * (D / 8); i += 32) o[i] = make_uint4(0, 0, 0, 0);
+    for (long long i = lane; a.lse && i < rows; i += 32) a.lse[s * rows + i] = -CUDART_INF_F;
     for (int i = lane; i < per; i += 32) a.joins[static_cast<size_t>(s) * per + i] = make_int2(0, -1);
   }
   if (u >= end) return;
@@ -361,7 +363,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
     const int cost = keys.cost();
     if (at >= static_cast<long long>(cost) * per) {
       at = 0;
-      ++seq;
+      if (++seq >= a.b) break;  // as above
       continue;
     }
     const int item = at >> 31 ? static_cast<int>(at / cost) : static_cast<int>(at) / cost;
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
       __syncwarp();
       if (real)
         bulk_load_once(smem_u32(ring + s * Sh::kStageBytes + lane * blk),
-                  a.cache + (static_cast<size_t>(page) * a.hk + place.h) * blk, blk, bar);
+                       a.cache + (static_cast<size_t>(page) * a.hk + place.h) * blk, blk, bar);
       held = (held & ~(15 << 4 * s)) | static_cast<int>(mask) << 4 * s;
     };
     // The first pages' numbers and the queries are on their way before the copies, which
@@ -430,8 +432,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
       }
     }
 
-    // one past the last key that a row sees
-    auto keys_end = [&](int r) { return r < a.rows ? min(len - a.t + token_of(a, r) + 1, a.width * a.ps) : 0; };
+    // one past the position of a row's token
+    auto row_end = [&](int r) { return r < a.rows ? len - a.t + token_of(a, r) + 1 : 0; };
 
     // Queries as FP16, each row times a power of two that brings its largest value
     // to [2^14, 2^15): exact but for values 2^38 times smaller than that one. Lane
@@ -466,7 +468,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
 #pragma unroll
       for (int e = 0; e < R; ++e) {
         c[nt][e] = kWide ? back : __shfl_sync(kAll, back, 4 * (2 * j + e));
-        if (keys_end(place.r0 + row_at(nt, e)) > 0) unseen |= 1u << (R * nt + e);
+        if (row_end(place.r0 + row_at(nt, e)) > 0) unseen |= 1u << (R * nt + e);
       }
     }
 
@@ -566,7 +568,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int hi = there ? keys_end(place.r0 + row_at(nt, e)) : 0, lo = a.window ? hi - a.window : 0;
+              const int last = row_end(place.r0 + row_at(nt, e)), lo = a.window ? last - a.window : 0;
+              const int hi = there ? min(last, a.width * a.ps) : 0;
 #pragma unroll
               for (int m = 0; m < kSub; ++m)
 #pragma unroll
@@ -787,7 +790,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
 constexpr int kJoinWarps = 32;  // of a row, at most
 
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ AttnArgs a, int S) {
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ AttnArgs a, int S, int G) {
   constexpr int V = D / 32;  // neighbouring channels per lane
   constexpr int kBatch = 8;
   __shared__ float2 stat[kJoinWarps];
@@ -796,7 +799,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
   griddep_launch_dependents();
   griddep_wait();
   const int2 join = a.joins[blockIdx.x];  // the parts that the item begins and ends in
-  if (join.y < 0) return;
+  if (join.x < 0 || join.y < join.x || join.y >= G) return;
   const float v_inv = 1.0f / *a.v_gs;
   const int per = a.hk * a.tiles, seq = blockIdx.x / per, item = blockIdx.x % per;
   const int h = item / a.tiles, r0 = item % a.tiles * 8 * NT;
@@ -1198,7 +1201,8 @@ __global__ void __launch_bounds__(kCopyThreads) kv_resize_apply_kernel(const __g
       a.lens[row] = r.new_len;
       if (r.copy) {
         const int page = a.fresh[r.first];
-        atomicSub(a.refs + table[have - 1], 1);
+        const int old = table[have - 1];
+        if (old >= 0 && old < a.pages) atomicSub(a.refs + old, 1);
         a.refs[page] = 1;
         table[have - 1] = page;
       }
@@ -1309,7 +1313,7 @@ __global__ void __launch_bounds__(kPageThreads) kv_compact_plan_kernel(const __g
     }
   }
   __syncthreads();
-  const int moved = static_cast<int>(sum >> 32);
+  const int moved = min(static_cast<int>(sum >> 32), static_cast<int>(sum));  // as many as there are holes
   for (int m = tid; m < moved; m += kPageThreads) a.page_map[a.moves[m]] = a.holes[m];
   if (tid == 0) *a.count = moved;
 }
@@ -1378,7 +1382,7 @@ cudaError_t launch_attn(AttnArgs a, int d, int sm_count, cudaStream_t stream, bo
     while (S < kJoinWarps && (8 * S < results || (4 * S < results && 2 * S * items * rows <= 32 * sm_count))) S *= 2;
     const int warps = S > 8 ? S : rows * S < 8 ? rows * S : 8;
     return launch(attn_join_kernel<D, NT>, dim3(static_cast<unsigned>(items), ceil_div(rows * S, warps)),
-                  dim3(32 * warps), 0, stream, pdl, a, S);
+                  dim3(32 * warps), 0, stream, pdl, a, S, grid * kAttnWarps);
   });
 }
 

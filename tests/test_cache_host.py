@@ -124,7 +124,7 @@ def test_binding_refuses_other_tensors(sk):
         sk.attn_nvfp4(k.half(), gs, gs, cache, table, lens, 64)
     whole = cache[None]
     refs = torch.zeros(10, dtype=i32)
-    with pytest.raises(ValueError, match="cache: 3 dimensions"):
+    with pytest.raises(ValueError, match="cache: shape .*needs 4 dimensions"):
         sk.kv_resize(lens, cache, table, lens, refs, 64)
     with pytest.raises(ValueError, match="cache: blocks"):
         sk.kv_compact(whole[..., :4600], table, lens, refs, 64)
@@ -132,3 +132,9 @@ def test_binding_refuses_other_tensors(sk):
         sk.kv_resize(lens, whole, table, lens, refs, 64)
     with pytest.raises(ValueError, match="table"):
         sk.kv_fork(lens, table, lens, refs, 64)
+    for bad, name in (((k[0], k, gs, gs, cache, table, lens), "k"), ((k, k, gs, gs, whole, table, lens), "cache"),
+                      ((k, k, gs, gs, cache, lens, lens), "table")):
+        with pytest.raises(ValueError, match="k|cache|table"):
+            sk.kv_append(*bad, 64)
+    with pytest.raises(ValueError, match="refs: shape"):
+        sk.kv_fork(lens, table, lens, table, 64)

@@ -233,6 +233,9 @@ def test_lengths_out_of_range(sk):
     q = rng.normal(size=(3, 2, 2, 64))
     out, lse = check_attn(sk, q, 5.0, 5.0, cache, table, [-7, 80, 2 ** 31 - 1], 16)
     assert not host(out)[0].any() and (host(lse)[0] == -np.inf).all()
+    # a window counts from the position, whatever of it the table names
+    check_attn(sk, q, 5.0, 5.0, cache, table, [66, 80, 2 ** 31 - 1], 16, window=10)
+    check_attn(sk, q, 5.0, 5.0, cache, table, [65, 100, 73], 16, window=40)
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.3, 1.0, 8.0])
