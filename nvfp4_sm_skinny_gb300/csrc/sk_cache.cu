@@ -656,7 +656,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const int token = from + 16 * j + 4 * mt + q;
-              if (!there || token >= len || token >= a.width * a.ps) vs[m] &= ~(0xFFu << 8 * q);
+              if (!there || token >= len || token >= a.width * a.ps || (a.window && token <= len - a.t - a.window))
+                vs[m] &= ~(0xFFu << 8 * q);
             }
           }
           const uint32_t order = __byte_perm(vs[m], 0, vs_order);

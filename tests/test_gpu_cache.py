@@ -213,6 +213,26 @@ def test_what_no_token_sees_does_not_matter(sk, d, ps):
     assert torch.equal(clean, dirty)
 
 
+@pytest.mark.parametrize("t,hq,d,ps,window", [(1, 4, 64, 16, 70), (1, 4, 128, 64, 1), (2, 16, 128, 32, 100), (4, 32, 64, 64, 33),
+                                              (8, 32, 128, 16, 150)])
+def test_what_lies_before_the_window_does_not_matter(sk, t, hq, d, ps, window):
+    # scales that are no number before the first key that a row's first token sees
+    rng = np.random.default_rng(window)
+    lens = np.array([300, 130, 64, 9])
+    table = random_table(rng, lens, -(-300 // ps), 60, ps)
+    cache = random_cache(rng, 60, 2, ps, d)
+    q = rng.normal(size=(4, t, hq, d))
+    clean, _ = check_attn(sk, q, 9.0, 9.0, cache, table, lens, ps, window=window)
+    _, _, ks, vs = oc.parts(cache, ps, d)
+    for i, n in enumerate(lens):
+        for p in range(n - t - window + 1):
+            ks[table[i, p // ps], :, p % ps] = 0x7F
+            vs[table[i, p // ps], :, :, p % ps] = 0xFF
+    dirty = sk.attn_nvfp4(torch.as_tensor(q).to(BF16).to(DEV), gpu([9.0], F32), gpu([9.0], F32),
+                          gpu(cache, U8), gpu(table, I32), gpu(lens, I32), ps, window=window)[0]
+    assert torch.equal(clean, dirty)
+
+
 def test_missing_pages_are_left_out(sk):
     rng = np.random.default_rng(8)
     ps, d = 16, 64
