@@ -20,8 +20,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsk.so")
 
 SOURCES = ["sk_api.cu", "sk_kernels.cu", "sk_static_scratch.cu", "sk_experts_api.cu",
-           "sk_experts.cu", "sk_cache_api.cu", "sk_cache.cu"]
-HEADERS = ["sk_internal.h", "sk_ptx.cuh"]
+           "sk_experts.cu", "sk_cache_api.cu", "sk_cache.cu", "sk_attn_tile.cu"]
+HEADERS = ["sk_internal.h", "sk_ptx.cuh", "sk_attn.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          f"-I{INCLUDE}", f"-I{CSRC}"]

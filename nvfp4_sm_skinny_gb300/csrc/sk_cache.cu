@@ -2,128 +2,12 @@
 // (sk_kv_append), attention over it (sk_attn_nvfp4) and its pages
 // (sk_kv_resize, sk_kv_fork, sk_kv_compact). include/sk.h has the formulas and
 // the cache's layout.
-#include <math_constants.h>
-
-#include <type_traits>
-
-#include "sk.h"
-#include "sk_internal.h"
-#include "sk_ptx.cuh"
+#include "sk_attn.cuh"
 
 namespace sk {
 namespace {
 
 __device__ uint32_t g_cache_status;                // OR of SK_DEVICE_WAIT_* bits
-constexpr uint64_t kCacheWaitNs = 2000000000ull;   // 2 s of wall time per wait
-constexpr uint32_t kAll = 0xFFFFFFFFu;
-
-template <typename... Args>
-cudaError_t launch(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                   bool pdl, typename std::remove_reference<Args>::type... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-__host__ __device__ __forceinline__ int ceil_div(int a, int b) { return a / b + (a % b != 0); }
-
-// Untiled bulk copy global -> shared, completion counted on `bar` in bytes. What is
-// copied leaves L2 first: the cache is read once, and table, queries and unfinished
-// results stay (b64 d128: 66.2 us without, 64.0 with).
-__device__ __forceinline__ void bulk_load_once(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
-          dst),
-      "l"(src), "r"(bytes), "r"(bar), "l"(l2_policy_evict_first())
-      : "memory");
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// The two e2m1 codes of byte i of a word as an FP16 pair, the low nibble in the low half.
-__device__ __forceinline__ uint32_t widen_e2m1(uint32_t w, int i) {
-  uint32_t r;
-  if (i == 0)
-    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(r) : "r"(w));
-  else if (i == 1)
-    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(r) : "r"(w));
-  else if (i == 2)
-    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}" : "=r"(r) : "r"(w));
-  else
-    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, d;\n\t}" : "=r"(r) : "r"(w));
-  return r;
-}
-
-// Two e4m3 bytes as an FP16 pair, exact.
-__device__ __forceinline__ uint32_t widen_e4m3(uint32_t two) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
-  return r;
-}
-
-__device__ __forceinline__ void mma_f16(float &c0, float &c1, float &c2, float &c3, uint32_t a0, uint32_t a1,
-                                        uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c0), "+f"(c1), "+f"(c2), "+f"(c3)
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// As mma_f16, into a sum that starts at 0.
-__device__ __forceinline__ void mma_f16_first(float &c0, float &c1, float &c2, float &c3, uint32_t a0, uint32_t a1,
-                                              uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %10, %10, %10};"
-      : "=f"(c0), "=f"(c1), "=f"(c2), "=f"(c3)
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
-}
-
-// Two FP32 operations in one instruction: (x, y) = (x, y) * (cx, cy) + (dx, dy), and + (dx, dy).
-__device__ __forceinline__ void fma_f32x2(float &x, float &y, float cx, float cy, float dx, float dy) {
-  asm("{\n\t.reg .b64 v, c, d;\n\t"
-      "mov.b64 v, {%0, %1};\n\tmov.b64 c, {%2, %3};\n\tmov.b64 d, {%4, %5};\n\t"
-      "fma.rn.f32x2 v, v, c, d;\n\tmov.b64 {%0, %1}, v;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(cx), "f"(cy), "f"(dx), "f"(dy));
-}
-__device__ __forceinline__ void add_f32x2(float &x, float &y, float dx, float dy) {
-  asm("{\n\t.reg .b64 v, d;\n\t"
-      "mov.b64 v, {%0, %1};\n\tmov.b64 d, {%2, %3};\n\t"
-      "add.rn.f32x2 v, v, d;\n\tmov.b64 {%0, %1}, v;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(dx), "f"(dy));
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 // The transpose of an 8 x 8 matrix of 16-bit values, row l / 4, columns 2 (l % 4)
 // and the next in lane l's register.
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
@@ -163,12 +47,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 // shared memory item by item waited for one another (93 us).
 constexpr int kChunk = 64;
 constexpr int kItemCost = 3;
-// Scores are kept as powers of two relative to a base that is at most 15 and after
-// an update 7 below the largest, so that P fits FP16 and what is 2^31 times smaller
-// than the largest still counts; the base moves (and the sums are scaled) only
-// when a score exceeds it by 2^15.
-constexpr float kTop = 15.0f, kAim = 7.0f;
-
 constexpr int kAttnWarps = 12;  // of a CTA: their sums and queries fill the registers
 
 template <int D, int NT>
@@ -184,10 +62,6 @@ struct AttnWarp {
     int seq, item, flags, first, h, r0;  // first: the part that the item begins in
   } place;
 };
-constexpr int kBegins = 1, kEnds = 2;  // the part holds the first, the last chunk of the item
-
-// Floats of a part's result: a base and a sum per row, then the rows.
-__host__ __device__ constexpr int attn_part_floats(int d, int nt) { return 16 * nt + 8 * nt * d; }
 
 struct Keys {
   int c0, c1;  // chunks [c0, c1) of a sequence that some of its tokens see
@@ -217,44 +91,6 @@ __device__ __forceinline__ T cost_of4(const AttnArgs &a, int s, T (&n)[4]) {
     sum += n[k];
   }
   return sum;
-}
-
-// G equal parts of U, the first U % G one longer: where part c starts, and the part
-// of place u. 64-bit divisions take hundreds of instructions, and U rarely needs them.
-struct Parts {
-  long long q, rest;
-  __device__ Parts(long long U, int G) {
-    if (U >> 31) {
-      q = U / G;
-      rest = U % G;
-    } else {
-      q = static_cast<uint32_t>(U) / static_cast<uint32_t>(G);
-      rest = static_cast<uint32_t>(U) % static_cast<uint32_t>(G);
-    }
-  }
-  __device__ long long start(int c) const { return c * q + min(static_cast<long long>(c), rest); }
-  __device__ int of(long long u) const {
-    const long long longer = rest * (q + 1);
-    if ((u | q) >> 31) return static_cast<int>(u < longer ? u / (q + 1) : rest + (u - longer) / q);
-    return static_cast<int>(u < longer ? static_cast<uint32_t>(u) / static_cast<uint32_t>(q + 1)
-                                       : rest + static_cast<uint32_t>(u - longer) / static_cast<uint32_t>(q));
-  }
-};
-
-__device__ __forceinline__ int token_of(const AttnArgs &a, int r) { return a.t == 1 ? 0 : r / a.group; }
-
-// Where row r of a KV head's rows stands in q and out (in rows of head_dim), and in lse.
-__device__ __forceinline__ size_t attn_row(const AttnArgs &a, int seq, int h, int r) {
-  const int token = token_of(a, r);
-  return (static_cast<size_t>(seq) * a.t + token) * a.hq + h * a.group + r - token * a.group;
-}
-
-__device__ __forceinline__ float row_lse(float base, float sum) {
-  return sum == 0.0f ? -CUDART_INF_F : (base + log2f(sum)) * 0.693147180559945f;
-}
-
-__device__ __forceinline__ uint32_t bf16_pair(float x, float y) {
-  return bf16_store_bits(x) | static_cast<uint32_t>(bf16_store_bits(y)) << 16;
 }
 
 template <int D, int NT>
@@ -799,12 +635,21 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, rows = (blockDim.x >> 5) / S;
   griddep_launch_dependents();
   griddep_wait();
-  const int2 join = a.joins[blockIdx.x];  // the parts that the item begins and ends in
-  if (join.x < 0 || join.y < join.x || join.y >= G) return;
+  // the parts that the item begins and ends in; with NT = 16 the part that an item of
+  // several ends in says which it is and where it begins
+  const int2 join = a.joins[blockIdx.x];
+  const int p0 = join.x, ends = NT == 16 ? blockIdx.x : join.y;
+  if (p0 < 0 || ends < p0 || ends >= G) return;
   const float v_inv = 1.0f / *a.v_gs;
-  const int per = a.hk * a.tiles, seq = blockIdx.x / per, item = blockIdx.x % per;
-  const int h = item / a.tiles, r0 = item % a.tiles * 8 * NT;
-  const int p0 = join.x, results = join.y - p0 + 1;
+  int seq, h, tile;
+  if constexpr (NT == 16) {
+    const int pair = join.y / a.hk;
+    h = join.y % a.hk, seq = pair / a.tiles, tile = pair % a.tiles;
+  } else {
+    const int per = a.hk * a.tiles, item = blockIdx.x % per;
+    seq = blockIdx.x / per, h = item / a.tiles, tile = item % a.tiles;
+  }
+  const int r0 = tile * 8 * NT, results = ends - p0 + 1;
   const int sub = w % S;
   const int rt = blockIdx.y * rows + w / S, r = r0 + rt;
   const bool mine = rt < 8 * NT && r < a.rows;
@@ -1355,15 +1200,38 @@ cudaError_t with_attn(int d, int nt, F f) {
 }  // namespace
 
 // Tiles of 8 rows, or of 16: of 32 the sums alone take 128 registers (d128, b16 of 8192
-// tokens, 32 rows: 121 us, in two tiles of 16, which read and widen all twice, 80).
-int attn_row_tiles(int rows) { return rows <= 8 ? 1 : 2; }
+// tokens, 32 rows: 121 us, in two tiles of 16, which read and widen all twice, 80). From
+// 33 rows on attn_tile_kernel's 128 (b16 of 8192 tokens; d128, 32 rows: 76 us here, 78
+// there; 64 rows: 136 and 93; d64, 32 rows: 49 and 56; 64 rows: 84 and 64).
+int attn_row_tiles(int rows) { return rows <= 8 ? 1 : rows <= 32 ? 2 : attn_tile_nt(); }
 
 size_t attn_part_bytes(int d, int nt) { return sizeof(float) * attn_part_floats(d, nt); }
 
-int attn_max_parts(int sm_count) { return kAttnWarps * sm_count; }
+int attn_max_parts(int sm_count, int nt) { return nt == attn_tile_nt() ? sm_count : kAttnWarps * sm_count; }
+
+size_t attn_joins(int nt, size_t items, int sm_count) { return nt == attn_tile_nt() ? sm_count : items; }
 
 cudaError_t launch_attn(AttnArgs a, int d, int sm_count, cudaStream_t stream, bool pdl) {
   const int nt = attn_row_tiles(a.rows);
+  // Warps of a row: as many as take eight results each on average, or four where the
+  // GPU holds them all at once (b16 t4 of 512 items: 32.7 us with four, 30.6 with
+  // eight; b1 of 2048 tokens: 11.0 and 11.9).
+  auto join = [&](auto kernel, long long joins, long long results, int G) {
+    const int rows = a.rows < 8 * nt ? a.rows : 8 * nt;
+    int S = 1;
+    while (S < kJoinWarps && (8 * S < results || (4 * S < results && 2 * S * joins * rows <= 32 * sm_count))) S *= 2;
+    const int warps = S > 8 ? S : rows * S < 8 ? rows * S : 8;
+    return launch(kernel, dim3(static_cast<unsigned>(joins), ceil_div(rows * S, warps)), dim3(32 * warps), 0, stream,
+                  pdl, a, S, G);
+  };
+  if (nt == attn_tile_nt()) {
+    int parts = 0;
+    cudaError_t e = launch_attn_tile(a, d, sm_count, stream, pdl, &parts);
+    if (e != cudaSuccess) return e;
+    const long long items = static_cast<long long>(a.b) * a.hk * a.tiles, results = parts / items + 2;
+    return d == 64 ? join(attn_join_kernel<64, 16>, parts, results, parts)
+                   : join(attn_join_kernel<128, 16>, parts, results, parts);
+  }
   return with_attn(d, nt, [&](auto dim, auto tiles) {
     constexpr int D = decltype(dim)::value, NT = decltype(tiles)::value;
     // no more SMs than there can be chunks
@@ -1374,16 +1242,8 @@ cudaError_t launch_attn(AttnArgs a, int d, int sm_count, cudaStream_t stream, bo
     cudaError_t e = launch(attn_kernel<D, NT>, dim3(grid), dim3(32 * kAttnWarps),
                            kAttnWarps * sizeof(AttnWarp<D, NT>), stream, pdl, a);
     if (e != cudaSuccess) return e;
-    // Warps of a row: as many as take eight results each on average, or four where the
-    // GPU holds them all at once (b16 t4 of 512 items: 32.7 us with four, 30.6 with
-    // eight; b1 of 2048 tokens: 11.0 and 11.9).
-    const int rows = a.rows < 8 * NT ? a.rows : 8 * NT;
-    const long long most = grid * kAttnWarps / items + 2, results = most < chunks ? most : chunks;
-    int S = 1;
-    while (S < kJoinWarps && (8 * S < results || (4 * S < results && 2 * S * items * rows <= 32 * sm_count))) S *= 2;
-    const int warps = S > 8 ? S : rows * S < 8 ? rows * S : 8;
-    return launch(attn_join_kernel<D, NT>, dim3(static_cast<unsigned>(items), ceil_div(rows * S, warps)),
-                  dim3(32 * warps), 0, stream, pdl, a, S, grid * kAttnWarps);
+    const long long most = grid * kAttnWarps / items + 2;
+    return join(attn_join_kernel<D, NT>, items, most < chunks ? most : chunks, grid * kAttnWarps);
   });
 }
 
@@ -1416,7 +1276,8 @@ cudaError_t launch_kv_compact(const CompactArgs &a, int sm_count, cudaStream_t s
 }
 
 cudaError_t cache_setup() {
-  cudaError_t e;
+  cudaError_t e = attn_tile_setup();
+  if (e != cudaSuccess) return e;
   for (int d : {64, 128})
     for (int nt : {1, 2})
       if ((e = with_attn(d, nt, [&](auto dim, auto tiles) {
@@ -1433,7 +1294,10 @@ cudaError_t cache_setup() {
 }
 
 cudaError_t read_cache_status(uint32_t *out, bool clear) {
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_cache_status, sizeof(uint32_t));
+  uint32_t tile = 0;
+  cudaError_t e = read_tile_status(&tile, clear);
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(out, g_cache_status, sizeof(uint32_t));
+  *out |= tile;
   if (e != cudaSuccess || !clear) return e;
   const uint32_t zero = 0;
   return cudaMemcpyToSymbol(g_cache_status, &zero, sizeof zero);

@@ -115,8 +115,9 @@ AttnWorkspace attn_workspace(int b, int t, int q_heads, int kv_heads, int head_d
   w.nt = sk::attn_row_tiles(rows);
   w.tiles = (rows + 8 * w.nt - 1) / (8 * w.nt);
   w.joins = 0;
-  w.parts = w.joins + round256(8 * static_cast<size_t>(b) * kv_heads * w.tiles);
-  w.total = w.parts + round256(2 * sk::attn_max_parts(SK_MAX_SMS) * sk::attn_part_bytes(head_dim, w.nt));
+  const size_t items = static_cast<size_t>(b) * kv_heads * w.tiles;
+  w.parts = w.joins + round256(8 * sk::attn_joins(w.nt, items, SK_MAX_SMS));
+  w.total = w.parts + round256(2 * sk::attn_max_parts(SK_MAX_SMS, w.nt) * sk::attn_part_bytes(head_dim, w.nt));
   return w;
 }
 
@@ -205,7 +206,7 @@ sk_status sk_attn_nvfp4(const void *q, const float *k_global_scale, const float 
   sk::AttnArgs a{static_cast<const uint16_t *>(q), cache, k_global_scale, v_global_scale, table, lens,
                  static_cast<uint16_t *>(out), lse, reinterpret_cast<int2 *>(ws + w.joins),
                  reinterpret_cast<float *>(ws + w.parts), b, t, q_heads, kv_heads, page_size, pages,
-                 width, window > (1 << 30) ? 0 : window, group, group * t, w.tiles, q_stride, scale, false};
+                 width, window > (1 << 30) ? 0 : window, group, group * t, w.tiles, q_stride, scale, false, 1};
   const int sms = info.sm_count < SK_MAX_SMS ? info.sm_count : SK_MAX_SMS;
   return launch_status(sk::launch_attn(a, head_dim, sms, as_stream(stream), sk::pdl_on()), "attn_nvfp4");
 }

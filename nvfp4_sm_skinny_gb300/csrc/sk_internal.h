@@ -274,10 +274,16 @@ struct AttnArgs {
   long long q_stride;  // values between tokens
   float scale;
   bool small;  // the work counts for less than 2^31, set by the launch
+  int copies;  // of a row, set by the launch
 };
-int attn_row_tiles(int rows);                   // tiles of 8 rows that a CTA takes at once
-int attn_max_parts(int sm_count);               // parts of such a launch, at most
-size_t attn_part_bytes(int d, int nt);          // bytes of an unfinished result
+int attn_row_tiles(int rows);                              // tiles of 8 rows that are taken at once
+int attn_max_parts(int sm_count, int nt);                  // parts of such a launch, at most
+size_t attn_joins(int nt, size_t items, int sm_count);     // its records for the joining kernel
+size_t attn_part_bytes(int d, int nt);                     // bytes of an unfinished result
+int attn_tile_nt();                                        // attn_row_tiles for many rows
+cudaError_t launch_attn_tile(AttnArgs a, int d, int sm_count, cudaStream_t stream, bool pdl, int *parts);
+cudaError_t attn_tile_setup();
+cudaError_t read_tile_status(uint32_t *out, bool clear);
 cudaError_t launch_attn(AttnArgs a, int d, int sm_count, cudaStream_t stream, bool pdl);
 
 struct AppendArgs {

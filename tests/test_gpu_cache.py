@@ -322,6 +322,111 @@ def test_many_parts_and_many_rows(sk, b, hq, hk, d, ps, n):
     check_attn(sk, rng.normal(size=(b, 1, hq, d)), 30.0, 9.0, cache, table, lens, ps)
 
 
+# More than 32 rows per KV head, in tiles of 128: up to 64 rows, up to 128, several tiles,
+# rows before the first token, windows that end within a chunk of 128.
+MANY = [  # t, hq, hk, d, ps, lens
+    (3, 12, 1, 64, 16, [5, 200, 129, 0]), (4, 16, 1, 128, 64, [128, 127, 1, 0, 2, 256]), (1, 64, 1, 64, 32, [300]),
+    (5, 13, 1, 128, 16, [700]), (8, 16, 1, 64, 64, [513, 3, 8]), (8, 32, 2, 128, 32, [640, 1000]),
+    (130, 1, 1, 64, 16, [130, 200, 40]), (70, 4, 2, 128, 64, [70, 333]), (300, 2, 1, 64, 64, [300, 777]),
+    (40, 9, 3, 128, 16, [90] * 5), (1, 33, 1, 64, 64, [1, 2500]),
+]
+
+
+@pytest.mark.parametrize("window", [0, 1, 100, 129])
+@pytest.mark.parametrize("t,hq,hk,d,ps,lens", MANY)
+def test_many_rows(sk, t, hq, hk, d, ps, lens, window):
+    rng = np.random.default_rng(t + hq)
+    width = -(-max(lens) // ps) + 1
+    pages = sum(-(-n // ps) for n in lens) + 2
+    table = random_table(rng, lens, width, pages, ps, spare=pages + 5)
+    cache = random_cache(rng, pages, hk, ps, d)
+    q = rng.normal(size=(len(lens), t, hq, d)) * np.exp2(rng.integers(-3, 2, (len(lens), t, hq, 1)))
+    check_attn(sk, q, 30.0, 7.0, cache, table, lens, ps, window=window)
+
+
+@pytest.mark.parametrize("d,t,hq", [(64, 4, 10), (64, 9, 10), (128, 4, 10), (128, 9, 10)])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1.0, 8.0])
+def test_many_rows_with_scores_that_move_the_base(sk, scale, d, t, hq):
+    # scales of keys that grow from page to page, and queries of every size and sign
+    rng = np.random.default_rng(16)
+    n = 1400
+    table = np.arange(24)[None]
+    cache = random_cache(rng, 24, 1, 64, d)
+    kc, _, ks, _ = oc.parts(cache, 64, d)
+    kc[:, :, :, :4] = 0x22                                   # 1.0
+    ks[...] = (0x20 + np.arange(24) * 2)[:, None, None, None]
+    q = rng.normal(size=(1, t, hq, d)) * np.exp2(rng.integers(-12, 3, (1, t, hq, 1)))
+    q[0, 0, 0] = 0.0
+    q[0, 1, 1] = 1e-39
+    q[0, 2, 2, 1:] *= 2.0 ** -20
+    check_attn(sk, q, 40.0, 1.0, cache, table, [n], 64, scale=scale)
+
+
+@pytest.mark.parametrize("d,ps", [(64, 16), (128, 32), (128, 64)])
+def test_many_rows_with_missing_pages_and_strange_lengths(sk, d, ps):
+    rng = np.random.default_rng(17)
+    width = 320 // ps
+    lens = [300, 300, 20, 320, -7, 400, 2 ** 31 - 1]
+    table = random_table(rng, [320] * 7, width, 7 * width, ps)
+    table[0, [0, 3]] = -1, 7 * width
+    table[1] = -2 ** 31
+    table[2, 0] = 2 ** 31 - 1
+    cache = random_cache(rng, 7 * width, 1, ps, d)
+    q = rng.normal(size=(7, 12, 4, d))
+    check_attn(sk, q, 5.0, 5.0, cache, table, lens, ps)
+    check_attn(sk, q, 5.0, 5.0, cache, table, lens, ps, window=90)
+    # scales that are no number where nobody looks
+    _, _, ks, vs = oc.parts(cache, ps, d)
+    clean = sk.attn_nvfp4(torch.as_tensor(q).to(BF16).to(DEV), gpu([5.0], F32), gpu([5.0], F32), gpu(cache, U8),
+                          gpu(table, I32), gpu(lens, I32), ps)[0]
+    held = np.zeros((7 * width, ps), bool)
+    for i, n in enumerate(lens):
+        for p in range(min(max(n, 0), 320)):
+            if 0 <= table[i, p // ps] < 7 * width:
+                held[table[i, p // ps], p % ps] = True
+    ks[:] = np.where(held[:, None, :, None], ks, 0x7F)
+    vs[:] = np.where(held[:, None, None, :], vs, 0xFF)
+    dirty = sk.attn_nvfp4(torch.as_tensor(q).to(BF16).to(DEV), gpu([5.0], F32), gpu([5.0], F32), gpu(cache, U8),
+                          gpu(table, I32), gpu(lens, I32), ps)[0]
+    assert torch.equal(clean, dirty)
+
+
+@pytest.mark.parametrize("b,t,hq,hk,d,ps,n", [(1, 4, 10, 1, 128, 64, 20000), (1, 9, 10, 1, 64, 16, 9001),
+                                              (300, 5, 8, 1, 64, 64, 40), (150, 4, 20, 2, 128, 16, 33)])
+def test_many_rows_in_many_parts(sk, b, t, hq, hk, d, ps, n):
+    rng = np.random.default_rng(18)
+    lens = [n] if b == 1 else rng.integers(0, n, b)
+    width = -(-n // ps)
+    pages = sum(-(-int(x) // ps) for x in lens) + 1
+    table = random_table(rng, lens, width, pages, ps)
+    cache = random_cache(rng, pages, hk, ps, d)
+    check_attn(sk, rng.normal(size=(b, t, hq, d)), 30.0, 9.0, cache, table, lens, ps)
+
+
+def test_many_rows_of_longer_rows_and_captured(sk):
+    # queries as they lie in a product's rows; the same result from a replayed graph, with other lengths
+    rng = np.random.default_rng(19)
+    d, ps, t, hq, hk = 64, 32, 6, 16, 2
+    lens = np.array([100, 600])
+    table = random_table(rng, [700, 700], 22, 44, ps)
+    cache = random_cache(rng, 44, hk, ps, d)
+    rows = torch.as_tensor(rng.normal(size=(2 * t, hq * d + 256))).to(BF16).to(DEV)
+    q = rows[:, 128:128 + hq * d].unflatten(0, (2, t)).unflatten(2, (hq, d))
+    one, c, tb, ln = gpu([3.0], F32), gpu(cache, U8), gpu(table, I32), gpu(lens, I32)
+    out, _, ws = sk.attn_nvfp4(q, one, one, c, tb, ln, ps)
+    flat, _ = check_attn(sk, host(q), 3.0, 3.0, cache, table, lens, ps)
+    assert torch.equal(out, flat)
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=stream):
+        sk.attn_nvfp4(q, one, one, c, tb, ln, ps, out=out, workspace=ws, stream=stream)
+    for lens in ([700, 1], [129, 350]):
+        ln.copy_(gpu(lens, I32))
+        graph.replay()
+        want, _ = check_attn(sk, host(q), 3.0, 3.0, cache, table, lens, ps)
+        assert torch.equal(out, want)
+
+
 def test_cache_beyond_31_bits(sk):
     # the last pages of a cache of 2.4 GB
     ps, d, hk = 64, 128, 8
