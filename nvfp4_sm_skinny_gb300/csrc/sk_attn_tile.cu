@@ -310,6 +310,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     const uint32_t mine = tmem + (static_cast<uint32_t>(32 * (w & 3)) << 16);
     const uint32_t s_at = mine + col_s(g), p_at = mine + col_p<D>(g), o_at = mine + col_o<D>(g);
     const float c_all = __fmul_rn(a.scale, 1.44269504088896f) / *a.k_gs, v_inv = 1.0f / *a.v_gs;
+    // P of the tokens that are the other copy's, which with d64 stays 0
+    auto hide_others = [&] {
+      const uint32_t zero[8] = {};
+      for (int s = 0; s < 8; ++s)
+        if (s < s0 || s >= s1) tmem_st_x8(p_at + 8 * s, zero);
+    };
+    if (D == 64 && a.copies > 1) hide_others();
     int soft = 0;
     auto together = [&] {  // the threads of all rows
       arrive(sh.soft);
@@ -379,9 +386,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         const int have = sh.have[at_chunk % kHave];
         const bool whole = have == (1 << pieces) - 1 && from + kTileChunk <= t.all_hi && from >= t.all_lo;
         // Scores of tokens that the row does not see, of columns [16 s, 16 s + 16), are
-        // replaced; token i lies in column i ^ (i / 8 & kFlip).
-        auto hide = [&](int s, auto odd, float(&x)[16]) {
-          constexpr int kOdd = decltype(odd)::value;
+        // replaced; token i lies in column i ^ (i / 8 & kFlip). `step` is s % 4, known here.
+        auto hide = [&](int s, auto step, float(&x)[16]) {
+          constexpr int kOdd = decltype(step)::value & 1;
           const int at = from + 16 * (s - kOdd), over = hi - at, under = lo - at;
           uint32_t ok = over >= 32 ? kAll : over <= 0 ? 0 : (1u << over) - 1;
           if (under > 0) ok &= under >= 32 ? 0 : kAll << under;
@@ -392,17 +399,25 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             if (!(ok >> (col ^ (col >> 3 & kFlip)) & 1)) x[k] = -CUDART_INF_F;
           }
         };
-        // Goes over this copy's columns, 16 at a time, the next on their way meanwhile.
-        auto over_columns = [&](auto f) {
+        // Goes over this copy's columns, 16 at a time, the next on their way meanwhile; `end`
+        // follows each 64.
+        auto over_columns = [&](auto f, auto end) {
           float x[16], y[16];
           tmem_ld_x16(s_at + 16 * s0, x);
-          for (int s = s0; s < s1; s += 2) {
+          for (int s = s0; s < s1; s += 4) {
             tmem_ld_wait(x);
             tmem_ld_x16(s_at + 16 * (s + 1), y);
             f(s, std::integral_constant<int, 0>(), x);
             tmem_ld_wait(y);
-            if (s + 2 < s1) tmem_ld_x16(s_at + 16 * (s + 2), x);
+            tmem_ld_x16(s_at + 16 * (s + 2), x);
             f(s + 1, std::integral_constant<int, 1>(), y);
+            tmem_ld_wait(x);
+            tmem_ld_x16(s_at + 16 * (s + 3), y);
+            f(s + 2, std::integral_constant<int, 2>(), x);
+            tmem_ld_wait(y);
+            if (s + 4 < s1) tmem_ld_x16(s_at + 16 * (s + 4), x);
+            f(s + 3, std::integral_constant<int, 3>(), y);
+            end(s);
           }
         };
         bool waited = false;
@@ -418,11 +433,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         for (;;) {
           float top = -CUDART_INF_F;
           if (look) {
-            over_columns([&](int s, auto odd, float(&x)[16]) {
-              if (!whole) hide(s, odd, x);
+            over_columns(
+                [&](int s, auto step, float(&x)[16]) {
+                  if (!whole) hide(s, step, x);
 #pragma unroll
-              for (int k = 0; k < 16; k += 2) top = max3(top, x[k], x[k + 1]);
-            });
+                  for (int k = 0; k < 16; k += 2) top = max3(top, x[k], x[k + 1]);
+                },
+                [](int) {});
             // the largest score, relative to the base, moves the base if it has to
             top = top == -CUDART_INF_F ? top : fmaf(top, c, base);
             if (__any_sync(kAll, unseen || top > kTop)) {
@@ -451,30 +468,29 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           }
           sum0 = sum1 = 0.0f;
           top = -CUDART_INF_F;
-          over_columns([&](int s, auto odd, float(&x)[16]) {
+          uint32_t p[32];
+          over_columns(
+              [&](int s, auto step, float(&x)[16]) {
 #pragma unroll
-            for (int k = 0; k < 16; k += 2) fma_f32x2(x[k], x[k + 1], c, c, base, base);
-            if (!whole) hide(s, odd, x);
-            uint32_t p[8];
+                for (int k = 0; k < 16; k += 2) fma_f32x2(x[k], x[k + 1], c, c, base, base);
+                if (!whole) hide(s, step, x);
 #pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              if (D == 64) top = max3(top, x[k], x[k + 1]);
-              const float y = ex2(x[k]), z = ex2(x[k + 1]);
-              add_f32x2(sum0, sum1, y, z);
-              p[k / 2] = cvt_f16x2(y, z);
-            }
-            free_p();
-            tmem_st_x8(p_at + 8 * s, p);  // what it covers of S is read
-          });
+                for (int k = 0; k < 16; k += 2) {
+                  if (D == 64) top = max3(top, x[k], x[k + 1]);
+                  const float y = ex2(x[k]), z = ex2(x[k + 1]);
+                  add_f32x2(sum0, sum1, y, z);
+                  p[8 * decltype(step)::value + k / 2] = cvt_f16x2(y, z);
+                }
+              },
+              [&](int s) {  // P of 64 columns is written at once; what it covers of S is read
+                free_p();
+                tmem_st_32x32b_x32(p_at + 8 * s, p);
+              });
           if (look || !__any_sync(kAll, top > kTop)) break;
           look = true;
           tmem_st_wait();
         }
-        if (a.copies > 1) {
-          const uint32_t zero[8] = {};
-          for (int s = 0; s < 8; ++s)
-            if (s < s0 || s >= s1) tmem_st_x8(p_at + 8 * s, zero);
-        }
+        if (D == 128 && a.copies > 1) hide_others();
         tmem_st_wait();
         sum += sum0 + sum1;
         done = at_chunk;
