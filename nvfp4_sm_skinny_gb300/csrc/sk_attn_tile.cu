@@ -24,12 +24,17 @@ __device__ uint32_t g_tile_status;  // OR of SK_DEVICE_WAIT_* bits
 // The work is cut as in attn_kernel, in a part per CTA; the items of a tile of rows count
 // for the chunks that any of its rows sees, so a prompt's first tiles are cheap.
 //
-// b16 of 8192 tokens, 128 query heads: d64, 64 rows 64 us (84 in tiles of 16 rows), d128, 64
-// rows 93 (136), 128 rows 119 (261). A prompt of 2048 tokens behind 14,336, 64 query heads,
-// d128: 1370 us (4200). A chunk takes 1600 clocks with 64 rows of d64, 3100 with 128 of
-// d128, of which the products take 1000: instructions bound it, 62 % of the issue slots.
+// b16 of 8192 tokens, 128 query heads: d64, 64 rows 61 us (84 in tiles of 16 rows), d128, 64
+// rows 92 (136), 128 rows 114 (261). A prompt of 2048 tokens behind 14,336, 64 query heads,
+// d128: 1290 us (4200). A chunk takes 1430 clocks with 64 rows of d64, 2870 with 128 of d128,
+// of which the products take 770 and 1090 at their rate. What bounds it is instructions, at
+// 60 % of the issue slots with four or five warps to choose from: widening, P and
+// barriers in about equal parts.
 constexpr int kTileRows = 128, kTileChunk = 128;
-constexpr int kTileCost = 4;  // an item's beginning and end count for so many chunks
+// An item's beginning and end count for so many chunks (64 query heads: a prompt of 4096
+// tokens, d64, 495 us with 3, 423 with 4, 333 with 6, 329 with 8; b16 of 1024, 8 tokens, d128,
+// 43.0, 41.9, 39.7, 39.4).
+constexpr int kTileCost = 6;
 constexpr int kSoftWarps = 8, kWidenWarps = 8, kMmaWarp = kSoftWarps + kWidenWarps, kCopyWarp = kMmaWarp + 1;
 constexpr int kSoft = 32 * kSoftWarps, kSumStride = kSoft + 1;
 constexpr int kTileThreads = 32 * (kCopyWarp + 1);
