@@ -100,7 +100,7 @@ struct TileShared {
   uint64_t ring_full[kStages], ring_empty[kStages], k_full[2], v_full[2], qk_done[2], pv_done[2], p_full[2];
   uint64_t q_full, soft, drained, item_full[kItems];
   TileItem item[kItems];
-  int have[kHave], failed;
+  int have[kHave];
   uint32_t tmem;
 };
 
@@ -199,7 +199,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     mbar_init(smem_u32(&sh.soft), kSoftWarps);
     mbar_init(smem_u32(&sh.drained), 1);
     for (int i = 0; i < kItems; ++i) mbar_init(smem_u32(&sh.item_full[i]), 1);
-    sh.failed = 0;
     fence_barrier_init();
   }
   if (w == kMmaWarp) {
@@ -289,10 +288,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   // A wait of a whole warp, bounded: whoever waits in vain says so and leaves.
   auto wait = [&](uint64_t &bar, int parity, uint32_t bit) {
     if (__all_sync(kAll, mbar_wait_bounded(smem_u32(&bar), parity & 1, kCacheWaitNs))) return true;
-    if (lane == 0) {
-      atomicOr(&g_tile_status, bit);
-      sh.failed = 1;
-    }
+    if (lane == 0) atomicOr(&g_tile_status, bit);
     return false;
   };
   auto arrive = [&](uint64_t &bar) {
@@ -352,7 +348,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       top = max(top, sh.top[threadIdx.x ^ 128]);
       const int shift = 14 - max(static_cast<int>(top >> 7) - 127, -126);
       // two factors, as 2^shift alone may not be an FP32 number
-      const float f0 = copysignf(__uint_as_float((127 + shift / 2) << 23), a.scale);
+      const float f0 = copysignf(__uint_as_float((127 + shift / 2) << 23), c_all);
       const float f1 = __uint_as_float((127 + shift - shift / 2) << 23);
       c = fabsf(c_all) * __uint_as_float((127 - shift / 2) << 23) * __uint_as_float((127 - shift + shift / 2) << 23);
       auto two = [&](uint32_t x) {
