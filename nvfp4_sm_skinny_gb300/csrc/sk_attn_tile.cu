@@ -27,9 +27,9 @@ __device__ uint32_t g_tile_status;  // OR of SK_DEVICE_WAIT_* bits
 // b16 of 8192 tokens, 128 query heads: d64, 64 rows 61 us (84 in tiles of 16 rows), d128, 64
 // rows 92 (136), 128 rows 114 (261). A prompt of 2048 tokens behind 14,336, 64 query heads,
 // d128: 1290 us (4200). A chunk takes 1430 clocks with 64 rows of d64, 2870 with 128 of d128,
-// of which the products take 770 and 1090 at their rate. What bounds it is instructions, at
-// 60 % of the issue slots with four or five warps to choose from: widening, P and
-// barriers in about equal parts.
+// of which the products take 770 and 1090 at their rate. What bounds it is latency: of the
+// issue slots 40 % are used and of no pipe more than a third, with four or five warps per
+// scheduler that wait for tensor memory, for one another and for instructions.
 constexpr int kTileRows = 128, kTileChunk = 128;
 // An item's beginning and end count for so many chunks (64 query heads: a prompt of 4096
 // tokens, d64, 495 us with 3, 423 with 4, 333 with 6, 329 with 8; b16 of 1024, 8 tokens, d128,

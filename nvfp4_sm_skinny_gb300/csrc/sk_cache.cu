@@ -1214,7 +1214,7 @@ size_t attn_joins(int nt, size_t items, int sm_count) { return nt == attn_tile_n
 cudaError_t launch_attn(AttnArgs a, int d, int sm_count, cudaStream_t stream, bool pdl) {
   const int nt = attn_row_tiles(a.rows);
   // Warps of a row: as many as take eight results each on average, or four where the
-  // GPU holds them all at once (b16 t4 of 512 items: 32.7 us with four, 30.6 with
+  // GPU holds them all at once (512 items of 16 rows: 32.7 us with four, 30.6 with
   // eight; b1 of 2048 tokens: 11.0 and 11.9).
   auto join = [&](auto kernel, long long joins, long long results, int G) {
     const int rows = a.rows < 8 * nt ? a.rows : 8 * nt;
