@@ -182,7 +182,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   extern __shared__ uint8_t raw[];
   Sh &sh = *reinterpret_cast<Sh *>(raw + (1024 - (smem_u32(raw) & 1023)) % 1024);
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, G = gridDim.x, me = blockIdx.x;
-  griddep_launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&sh.ring_full[s]), 1);
@@ -201,11 +200,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     for (int i = 0; i < kItems; ++i) mbar_init(smem_u32(&sh.item_full[i]), 1);
     fence_barrier_init();
   }
+  griddep_wait();
+  // All of tensor memory: not before the kernels ahead are done, and before those behind
+  // start, as either might hold a part of it and wait for the other.
   if (w == kMmaWarp) {
     tmem_alloc(smem_u32(&sh.tmem), kCols);
     tmem_relinquish();
   }
-  griddep_wait();
 
   const int pairs = a.b * a.tiles;
   // This CTA's part [u, end) of all, and the pair it starts in, for the warp of the copies;
@@ -283,6 +284,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  griddep_launch_dependents();
   const uint32_t tmem = sh.tmem;
 
   // A wait of a whole warp, bounded: whoever waits in vain says so and leaves.

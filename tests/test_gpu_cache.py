@@ -427,6 +427,38 @@ def test_many_rows_of_longer_rows_and_captured(sk):
         assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_rows_between_products(sk, d):
+    # products before and after, which hold tensor memory too, one launch overlapping the next
+    rng = np.random.default_rng(20)
+    b, t, hk, ps = 4, 4, 2, 64
+    hq, lens = 32, np.array([500, 64, 300, 129])
+    table = random_table(rng, lens, 8, 32, ps)
+    cache = random_cache(rng, 32, hk, ps, d)
+    def bf16(*shape):
+        return torch.as_tensor(rng.normal(size=shape) * 0.1).to(BF16).to(DEV)
+    x, w_in, w_out = bf16(b * t, 1024), bf16((hq + 2 * hk) * d, 1024), bf16(1024, hq * d)
+    one, c, tb, ln = gpu([3.0], F32), gpu(cache, U8), gpu(table, I32), gpu(lens, I32)
+    def step():
+        qkv = sk.gemm_bf16(x, w_in).view(b, t, hq + 2 * hk, d)
+        q, k, v = qkv.split([hq, hk, hk], 2)
+        sk.kv_append(k, v, one, one, c, tb, ln, ps)
+        out, _, _ = sk.attn_nvfp4(q, one, one, c, tb, ln, ps)
+        return q, out, sk.gemm_bf16(out.view(b * t, hq * d), w_out)
+    q, first, y = step()
+    ref = oc.attn(host(q), 3.0, 3.0, host(c), table, lens, ps)
+    assert np.all(np.abs(host(first) - ref[0]) <= attn_bounds(ref, d, lens.max())[0])
+    assert torch.equal(y, sk.gemm_bf16(first.view(b * t, hq * d), w_out))
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=stream):
+        results = [step() for _ in range(8)]
+    for _ in range(5):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, first) and torch.equal(z, y) for _, out, z in results)
+
+
 def test_cache_beyond_31_bits(sk):
     # the last pages of a cache of 2.4 GB
     ps, d, hk = 64, 128, 8
