@@ -128,6 +128,14 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, float (&v)[16]) {
       : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld_wait(float (&v)[16]);
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, float (&v)[32]) {
+  float(&x)[2][16] = reinterpret_cast<float(&)[2][16]>(v);
+  tmem_ld_x16(taddr, x[0]);
+  tmem_ld_x16(taddr + 16, x[1]);
+  tmem_ld_wait(x[0]);
+  tmem_ld_wait(x[1]);
+}
 // Names the registers, so that no use is scheduled before it.
 __device__ __forceinline__ void tmem_ld_wait(float (&v)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -312,7 +320,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     const int s0 = m / R * (8 / a.copies), s1 = s0 + 8 / a.copies;  // this copy's tokens, 16 at a time
     const uint32_t mine = tmem + (static_cast<uint32_t>(32 * (w & 3)) << 16);
     const uint32_t s_at = mine + col_s(g), p_at = mine + col_p<D>(g), o_at = mine + col_o<D>(g);
-    const float c_all = __fmul_rn(a.scale, 1.44269504088896f) / *a.k_gs, v_inv = 1.0f / *a.v_gs;
+    const float c_all = __fmul_rn(a.scale, 1.44269504088896f) / *a.k_gs;
     // P of the tokens that are the other copy's, which with d64 stays 0
     auto hide_others = [&] {
       const uint32_t zero[8] = {};
@@ -353,6 +361,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       const float f0 = copysignf(__uint_as_float((127 + shift / 2) << 23), c_all);
       const float f1 = __uint_as_float((127 + shift - shift / 2) << 23);
       c = fabsf(c_all) * __uint_as_float((127 - shift / 2) << 23) * __uint_as_float((127 - shift + shift / 2) << 23);
+      // not 0, as that times the -inf of what is not seen is no number; S is below 2^34
+      c = c < 1e-30f ? 1e-30f : c;
       auto two = [&](uint32_t x) {
         return cvt_f16x2(__uint_as_float(x << 16) * f0 * f1, __uint_as_float(x & 0xFFFF0000u) * f0 * f1);
       };
@@ -388,20 +398,26 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         tc_fence_after_sync();
         const int have = sh.have[at_chunk % kHave];
         const bool whole = have == (1 << pieces) - 1 && from + kTileChunk <= t.all_hi && from >= t.all_lo;
-        // Scores of tokens that the row does not see, of columns [16 s, 16 s + 16), are
-        // replaced; token i lies in column i ^ (i / 8 & kFlip). `step` is s % 4, known here.
-        auto hide = [&](int s, auto step, float(&x)[16]) {
-          constexpr int kOdd = decltype(step)::value & 1;
-          const int at = from + 16 * (s - kOdd), over = hi - at, under = lo - at;
-          uint32_t ok = over >= 32 ? kAll : over <= 0 ? 0 : (1u << over) - 1;
-          if (under > 0) ok &= under >= 32 ? 0 : kAll << under;
-          if (!(have >> (16 * s >> ps_bits) & 1)) ok = 0;
+        // Scores of tokens that the row does not see are replaced where they lie; token i of 32
+        // lies in column i ^ (i / 8 & kFlip).
+        if (!whole) {
+#pragma unroll 1
+          for (int s = s0; s < s1; s += 2) {
+            const int at = from + 16 * s, over = hi - at, under = lo - at;
+            uint32_t ok = over >= 32 ? kAll : over <= 0 ? 0 : (1u << over) - 1;
+            if (under > 0) ok &= under >= 32 ? 0 : kAll << under;
+            if (!(have >> (16 * s >> ps_bits) & 1)) ok &= a.ps == 16 ? 0xFFFF0000u : 0;
+            if (a.ps == 16 && !(have >> (s + 1) & 1)) ok &= 0xFFFFu;
+            float x[32];
+            tmem_ld_x32(s_at + 16 * s, x);
+            uint32_t y[32];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int col = 16 * kOdd + k;
-            if (!(ok >> (col ^ (col >> 3 & kFlip)) & 1)) x[k] = -CUDART_INF_F;
+            for (int k = 0; k < 32; ++k)
+              y[k] = ok >> (k ^ (k >> 3 & kFlip)) & 1 ? __float_as_uint(x[k]) : 0xFF800000u;  // -inf
+            tmem_st_32x32b_x32(s_at + 16 * s, y);
           }
-        };
+          tmem_st_wait();
+        }
         // Goes over this copy's columns, 16 at a time, the next on their way meanwhile; `end`
         // follows each 64.
         auto over_columns = [&](auto f, auto end) {
@@ -410,16 +426,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           for (int s = s0; s < s1; s += 4) {
             tmem_ld_wait(x);
             tmem_ld_x16(s_at + 16 * (s + 1), y);
-            f(s, std::integral_constant<int, 0>(), x);
+            f(std::integral_constant<int, 0>(), x);
             tmem_ld_wait(y);
             tmem_ld_x16(s_at + 16 * (s + 2), x);
-            f(s + 1, std::integral_constant<int, 1>(), y);
+            f(std::integral_constant<int, 1>(), y);
             tmem_ld_wait(x);
             tmem_ld_x16(s_at + 16 * (s + 3), y);
-            f(s + 2, std::integral_constant<int, 2>(), x);
+            f(std::integral_constant<int, 2>(), x);
             tmem_ld_wait(y);
             if (s + 4 < s1) tmem_ld_x16(s_at + 16 * (s + 4), x);
-            f(s + 3, std::integral_constant<int, 3>(), y);
+            f(std::integral_constant<int, 3>(), y);
             end(s);
           }
         };
@@ -437,8 +453,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           float top = -CUDART_INF_F;
           if (look) {
             over_columns(
-                [&](int s, auto step, float(&x)[16]) {
-                  if (!whole) hide(s, step, x);
+                [&](auto, float(&x)[16]) {
 #pragma unroll
                   for (int k = 0; k < 16; k += 2) top = max3(top, x[k], x[k + 1]);
                 },
@@ -473,10 +488,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           top = -CUDART_INF_F;
           uint32_t p[32];
           over_columns(
-              [&](int s, auto step, float(&x)[16]) {
+              [&](auto step, float(&x)[16]) {
 #pragma unroll
                 for (int k = 0; k < 16; k += 2) fma_f32x2(x[k], x[k + 1], c, c, base, base);
-                if (!whole) hide(s, step, x);
 #pragma unroll
                 for (int k = 0; k < 16; k += 2) {
                   if (D == 64) top = max3(top, x[k], x[k + 1]);
@@ -539,7 +553,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           if (!whole) reinterpret_cast<float2 *>(part)[rt] = make_float2(top, l);
           else if (a.lse) a.lse[row] = row_lse(top, l);
         }
-        sh.out_f[rt] = l == 0.0f ? 0.0f : v_inv / l;
+        sh.out_f[rt] = l == 0.0f ? 0.0f : 1.0f / *a.v_gs / l;
         sh.out_at[rt] = !real ? -1 : whole ? static_cast<long long>(row) * D : 2 * kTileRows + rt * D;
       }
       // Four channels of a row per thread, so that a warp writes runs of 128 bytes; channel
