@@ -24,9 +24,9 @@ __device__ uint32_t g_tile_status;  // OR of SK_DEVICE_WAIT_* bits
 // The work is cut as in attn_kernel, in a part per CTA; the items of a tile of rows count
 // for the chunks that any of its rows sees, so a prompt's first tiles are cheap.
 //
-// b16 of 8192 tokens, 128 query heads: d64, 64 rows 61 us (84 in tiles of 16 rows), d128, 64
-// rows 92 (136), 128 rows 114 (261). A prompt of 2048 tokens behind 14,336, 64 query heads,
-// d128: 1290 us (4200). A chunk takes 1430 clocks with 64 rows of d64, 2870 with 128 of d128,
+// b16 of 8192 tokens, 128 query heads: d64, 64 rows 59 us (84 in tiles of 16 rows), d128, 64
+// rows 83 (136), 128 rows 100 (261). A prompt of 2048 tokens behind 14,336, 64 query heads,
+// d128: 1090 us (4200). A chunk takes 1400 clocks with 64 rows of d64, 2400 with 128 of d128,
 // of which the products take 770 and 1090 at their rate. What bounds it is latency: of the
 // issue slots 40 % are used and of no pipe more than a third, with four or five warps per
 // scheduler that wait for tensor memory, for one another and for instructions.
@@ -42,6 +42,7 @@ constexpr int kTileThreads = 32 * (kCopyWarp + 1);
 // the chunks whose pieces, and the items, that are remembered.
 constexpr int kHave = 8, kItems = 16;
 constexpr int kTileNt = kTileRows / 8;
+constexpr float kMost = 32768.0f;  // 2^kTop
 
 // Columns of tensor memory, of even and odd chunks: S, O and P, which with d128 takes the
 // place of the S that it is made of.
@@ -446,12 +447,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           waited = true;
         };
         // With d64 S outlives P: it is assumed that the base need not move, and done again
-        // if it has to.
+        // if it has to, which the sums tell: no p is above 2^kTop if they are not.
         bool look = D == 128 || __any_sync(kAll, unseen);
         float sum0, sum1;
         for (;;) {
-          float top = -CUDART_INF_F;
           if (look) {
+            float top = -CUDART_INF_F;
             over_columns(
                 [&](auto, float(&x)[16]) {
 #pragma unroll
@@ -485,7 +486,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             }
           }
           sum0 = sum1 = 0.0f;
-          top = -CUDART_INF_F;
           uint32_t p[32];
           over_columns(
               [&](auto step, float(&x)[16]) {
@@ -493,7 +493,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
                 for (int k = 0; k < 16; k += 2) fma_f32x2(x[k], x[k + 1], c, c, base, base);
 #pragma unroll
                 for (int k = 0; k < 16; k += 2) {
-                  if (D == 64) top = max3(top, x[k], x[k + 1]);
                   const float y = ex2(x[k]), z = ex2(x[k + 1]);
                   add_f32x2(sum0, sum1, y, z);
                   p[8 * decltype(step)::value + k / 2] = cvt_f16x2(y, z);
@@ -503,7 +502,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
                 free_p();
                 tmem_st_32x32b_x32(p_at + 8 * s, p);
               });
-          if (look || !__any_sync(kAll, top > kTop)) break;
+          if (look || !__any_sync(kAll, !(sum0 <= kMost && sum1 <= kMost))) break;
           look = true;
           tmem_st_wait();
         }
