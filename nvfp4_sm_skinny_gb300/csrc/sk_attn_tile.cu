@@ -32,9 +32,9 @@ __device__ uint32_t g_tile_status;  // OR of SK_DEVICE_WAIT_* bits
 // scheduler that wait for tensor memory, for one another and for instructions.
 constexpr int kTileRows = 128, kTileChunk = 128;
 // An item's beginning and end count for so many chunks (64 query heads: a prompt of 4096
-// tokens, d64, 495 us with 3, 423 with 4, 333 with 6, 329 with 8; b16 of 1024, 8 tokens, d128,
-// 43.0, 41.9, 39.7, 39.4).
-constexpr int kTileCost = 6;
+// tokens, d64, 423 us with 4, 333 with 6; when chunks had become cheaper, 290 with 6, 279
+// with 8; b16 of 1024, 8 tokens, d128, 41.9 and 39.7, 37.7 and 37.1).
+constexpr int kTileCost = 8;
 constexpr int kSoftWarps = 8, kWidenWarps = 8, kMmaWarp = kSoftWarps + kWidenWarps, kCopyWarp = kMmaWarp + 1;
 constexpr int kSoft = 32 * kSoftWarps, kSumStride = kSoft + 1;
 constexpr int kTileThreads = 32 * (kCopyWarp + 1);
