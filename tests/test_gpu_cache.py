@@ -459,6 +459,28 @@ def test_many_rows_between_products(sk, d):
     assert all(torch.equal(out, first) and torch.equal(z, y) for _, out, z in results)
 
 
+def test_many_rows_on_two_streams(sk):
+    # two calls at once, of head sizes that take different shares of an SM
+    rng = np.random.default_rng(21)
+    calls = []
+    for d, t in ((64, 5), (128, 40)):
+        lens = [2000, 700, 41]
+        table = random_table(rng, lens, 32, 96, 64)
+        q = torch.as_tensor(rng.normal(size=(3, t, 16, d))).to(BF16).to(DEV)
+        calls.append((q, gpu([9.0], F32), gpu([9.0], F32), gpu(random_cache(rng, 96, 2, 64, d), U8),
+                      gpu(table, I32), gpu(lens, I32), 64))
+    alone = [sk.attn_nvfp4(*a)[0] for a in calls]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    results = [[], []]
+    for _ in range(10):
+        for a, st, r in zip(calls, streams, results):
+            r.append(sk.attn_nvfp4(*a, stream=st)[0])
+    torch.cuda.synchronize()
+    for r, want in zip(results, alone):
+        assert all(torch.equal(x, want) for x in r)
+
+
 def test_cache_beyond_31_bits(sk):
     # the last pages of a cache of 2.4 GB
     ps, d, hk = 64, 128, 8
