@@ -24,9 +24,9 @@ __device__ uint32_t g_tile_status;  // OR of SK_DEVICE_WAIT_* bits
 // The work is cut as in attn_kernel, in a part per CTA; the items of a tile of rows count
 // for the chunks that any of its rows sees, so a prompt's first tiles are cheap.
 //
-// b16 of 8192 tokens, 128 query heads: d64, 64 rows 59 us (84 in tiles of 16 rows), d128, 64
-// rows 83 (136), 128 rows 100 (261). A prompt of 2048 tokens behind 14,336, 64 query heads,
-// d128: 1090 us (4200). A chunk takes 1400 clocks with 64 rows of d64, 2400 with 128 of d128,
+// b16 of 8192 tokens, 128 query heads: d64, 64 rows 61 us (84 in tiles of 16 rows), d128, 64
+// rows 83 (136), 128 rows 94 (261). A prompt of 2048 tokens behind 14,336, 64 query heads,
+// d128: 980 us (4200). A chunk takes 1450 clocks with 64 rows of d64, 2120 with 128 of d128,
 // of which the products take 770 and 1090 at their rate. What bounds it is latency: of the
 // issue slots 40 % are used and of no pipe more than a third, with four or five warps per
 // scheduler that wait for tensor memory, for one another and for instructions.
@@ -419,50 +419,33 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           }
           tmem_st_wait();
         }
-        // Goes over this copy's columns, 16 at a time, the next on their way meanwhile; `end`
-        // follows each 64.
-        auto over_columns = [&](auto f, auto end) {
-          float x[16], y[16];
-          tmem_ld_x16(s_at + 16 * s0, x);
-          for (int s = s0; s < s1; s += 4) {
-            tmem_ld_wait(x);
-            tmem_ld_x16(s_at + 16 * (s + 1), y);
-            f(std::integral_constant<int, 0>(), x);
-            tmem_ld_wait(y);
-            tmem_ld_x16(s_at + 16 * (s + 2), x);
-            f(std::integral_constant<int, 1>(), y);
-            tmem_ld_wait(x);
-            tmem_ld_x16(s_at + 16 * (s + 3), y);
-            f(std::integral_constant<int, 2>(), x);
-            tmem_ld_wait(y);
-            if (s + 4 < s1) tmem_ld_x16(s_at + 16 * (s + 4), x);
-            f(std::integral_constant<int, 3>(), y);
-            end(s);
-          }
-        };
         bool waited = false;
         auto free_p = [&] {  // the chunk before the last has been added to O, and its P read
           if (!waited && at_chunk >= 2) good = wait(sh.pv_done[g], (at_chunk >> 1) - 1, SK_DEVICE_WAIT_MMA);
           if (!waited) tc_fence_after_sync();
           waited = true;
         };
-        // With d64 S outlives P: it is assumed that the base need not move, and done again
+        // 64 columns at a time. It is assumed that the base need not move, and their P made again
         // if it has to, which the sums tell: no p is above 2^kTop if they are not.
-        bool look = D == 128 || __any_sync(kAll, unseen);
-        float sum0, sum1;
-        for (;;) {
-          if (look) {
-            float top = -CUDART_INF_F;
-            over_columns(
-                [&](auto, float(&x)[16]) {
+        for (int s = s0; s < s1; s += 4) {
+          float sum0, sum1;
+          uint32_t p[32];
+          bool look = __any_sync(kAll, unseen);
+          for (;;) {
+            if (look) {
+              float top = -CUDART_INF_F;
+#pragma unroll 1
+              for (int i = 0; i < 4; i += 2) {
+                float x[32];
+                tmem_ld_x32(s_at + 16 * (s + i), x);
 #pragma unroll
-                  for (int k = 0; k < 16; k += 2) top = max3(top, x[k], x[k + 1]);
-                },
-                [](int) {});
-            // the largest score, relative to the base, moves the base if it has to
-            top = top == -CUDART_INF_F ? top : fmaf(top, c, base);
-            if (__any_sync(kAll, unseen || top > kTop)) {
-              float by = top > kAim ? top - kAim : 0.0f, f = ex2(-by);
+                for (int k = 0; k < 32; k += 2) top = max3(top, x[k], x[k + 1]);
+              }
+              // the largest score, relative to the base, moves the base by a whole number, so
+              // that a power of two takes all before along: P loses nothing that it has
+              top = top == -CUDART_INF_F ? top : fmaf(top, c, base);
+              float by = top > kAim ? ceilf(top - kAim) : 0.0f;
+              float f = by < 127.0f ? __uint_as_float((127 - static_cast<int>(by)) << 23) : 0.0f;
               if (unseen) {  // the row's first keys set its base
                 by = top == -CUDART_INF_F ? 0.0f : top - kAim;
                 f = 1.0f;
@@ -470,45 +453,67 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
               }
               base -= by;
               sum *= f;
-              __syncwarp();
-              if (done >= 0 && __any_sync(kAll, f != 1.0f)) {
+              if (__any_sync(kAll, f != 1.0f)) {
                 free_p();
+                tmem_st_wait();
 #pragma unroll 1
-                for (int b = 0; b < D; b += 16) {
+                for (int k = 0; done >= 0 && k < D; k += 16) {
                   float y[16];
                   uint32_t z[16];
-                  tmem_ld_32x32b_x16(o_at + b, y);
+                  tmem_ld_32x32b_x16(o_at + k, y);
 #pragma unroll
-                  for (int k = 0; k < 16; ++k) z[k] = __float_as_uint(y[k] * f);
-                  tmem_st_x16(o_at + b, z);
+                  for (int i = 0; i < 16; ++i) z[i] = __float_as_uint(y[i] * f);
+                  tmem_st_x16(o_at + k, z);
+                }
+#pragma unroll 1
+                for (int k = 8 * s0; k < 8 * s; k += 16) {  // this chunk's
+                  float y[16];
+                  uint32_t z[16];
+                  tmem_ld_32x32b_x16(p_at + k, y);
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) {
+                    const uint32_t two = __float_as_uint(y[i]);
+                    z[i] = cvt_f16x2(__half2float(__ushort_as_half(two & 0xFFFFu)) * f,
+                                     __half2float(__ushort_as_half(two >> 16)) * f);
+                  }
+                  tmem_st_x16(p_at + k, z);
                 }
               }
             }
+            sum0 = sum1 = 0.0f;
+            auto make = [&](auto step, float(&x)[16]) {
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) fma_f32x2(x[k], x[k + 1], c, c, base, base);
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) {
+                const float y = ex2(x[k]), z = ex2(x[k + 1]);
+                add_f32x2(sum0, sum1, y, z);
+                p[8 * decltype(step)::value + k / 2] = cvt_f16x2(y, z);
+              }
+            };
+            // 16 columns at a time, the next on their way meanwhile
+            float x[16], y[16];
+            tmem_ld_x16(s_at + 16 * s, x);
+            tmem_ld_wait(x);
+            tmem_ld_x16(s_at + 16 * s + 16, y);
+            make(std::integral_constant<int, 0>(), x);
+            tmem_ld_wait(y);
+            tmem_ld_x16(s_at + 16 * s + 32, x);
+            make(std::integral_constant<int, 1>(), y);
+            tmem_ld_wait(x);
+            tmem_ld_x16(s_at + 16 * s + 48, y);
+            make(std::integral_constant<int, 2>(), x);
+            tmem_ld_wait(y);
+            make(std::integral_constant<int, 3>(), y);
+            if (look || !__any_sync(kAll, !(sum0 <= kMost && sum1 <= kMost))) break;
+            look = true;
           }
-          sum0 = sum1 = 0.0f;
-          uint32_t p[32];
-          over_columns(
-              [&](auto step, float(&x)[16]) {
-#pragma unroll
-                for (int k = 0; k < 16; k += 2) fma_f32x2(x[k], x[k + 1], c, c, base, base);
-#pragma unroll
-                for (int k = 0; k < 16; k += 2) {
-                  const float y = ex2(x[k]), z = ex2(x[k + 1]);
-                  add_f32x2(sum0, sum1, y, z);
-                  p[8 * decltype(step)::value + k / 2] = cvt_f16x2(y, z);
-                }
-              },
-              [&](int s) {  // P of 64 columns is written at once; what it covers of S is read
-                free_p();
-                tmem_st_32x32b_x32(p_at + 8 * s, p);
-              });
-          if (look || !__any_sync(kAll, !(sum0 <= kMost && sum1 <= kMost))) break;
-          look = true;
-          tmem_st_wait();
+          free_p();
+          tmem_st_32x32b_x32(p_at + 8 * s, p);  // at once; what it covers of S is read
+          sum += sum0 + sum1;
         }
         if (D == 128 && a.copies > 1) hide_others();
         tmem_st_wait();
-        sum += sum0 + sum1;
         done = at_chunk;
         tc_fence_before_sync();
         arrive(sh.p_full[g]);
