@@ -31,10 +31,10 @@ __device__ uint32_t g_tile_status;  // OR of SK_DEVICE_WAIT_* bits
 // issue slots 40 % are used and of no pipe more than a third, with four or five warps per
 // scheduler that wait for tensor memory, for one another and for instructions.
 constexpr int kTileRows = 128, kTileChunk = 128;
-// An item's beginning and end count for so many chunks (64 query heads: a prompt of 4096
-// tokens, d64, 423 us with 4, 333 with 6; when chunks had become cheaper, 290 with 6, 279
-// with 8; b16 of 1024, 8 tokens, d128, 41.9 and 39.7, 37.7 and 37.1).
-constexpr int kTileCost = 8;
+// An item's beginning and end count for so many chunks (64 query heads, a prompt of 4096
+// tokens, d64: 317 us with 5, 292 with 6, 286 with 7, 290 with 8; 128, 4 tokens of 16 rows of
+// 100 to 8192, window 4096, d64: 28.6, 27.7, 27.9, 28.7).
+constexpr int kTileCost = 7;
 constexpr int kSoftWarps = 8, kWidenWarps = 8, kMmaWarp = kSoftWarps + kWidenWarps, kCopyWarp = kMmaWarp + 1;
 constexpr int kSoft = 32 * kSoftWarps, kSumStride = kSoft + 1;
 constexpr int kTileThreads = 32 * (kCopyWarp + 1);
