@@ -181,7 +181,8 @@ __device__ __forceinline__ bool one_lane() {
   return one != 0;
 }
 
-template <int D>
+// C: how many times a row lies there.
+template <int D, int C>
 __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid_constant__ AttnArgs a) {
   using Sh = TileShared<D>;
   constexpr int kStages = Sh::kStages;
@@ -317,8 +318,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
 
   if (w < kSoftWarps) {
     // ------------------------------------------------- P of S, a thread per row
-    const int g = w >> 2, m = threadIdx.x & 127, R = kTileRows / a.copies, rt = m & (R - 1);
-    const int s0 = m / R * (8 / a.copies), s1 = s0 + 8 / a.copies;  // this copy's tokens, 16 at a time
+    const int g = w >> 2, m = threadIdx.x & 127, R = kTileRows / C, rt = m & (R - 1);
+    const int s0 = m / R * (8 / C), s1 = s0 + 8 / C;  // this copy's tokens, 16 at a time
     const uint32_t mine = tmem + (static_cast<uint32_t>(32 * (w & 3)) << 16);
     const uint32_t s_at = mine + col_s(g), p_at = mine + col_p<D>(g), o_at = mine + col_o<D>(g);
     const float c_all = __fmul_rn(a.scale, 1.44269504088896f) / *a.k_gs;
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       for (int s = 0; s < 8; ++s)
         if (s < s0 || s >= s1) tmem_st_x8(p_at + 8 * s, zero);
     };
-    if (D == 64 && a.copies > 1) hide_others();
+    if (D == 64 && C > 1) hide_others();
     int soft = 0;
     auto together = [&] {  // the threads of all rows
       arrive(sh.soft);
@@ -427,7 +428,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         };
         // 64 columns at a time. It is assumed that the base need not move, and their P made again
         // if it has to, which the sums tell: no p is above 2^kTop if they are not.
-        for (int s = s0; s < s1; s += 4) {
+        for (int s = s0; C == 1 ? s < s1 : s == s0; s += 4) {
           float sum0, sum1;
           uint32_t p[32];
           bool look = __any_sync(kAll, unseen);
@@ -466,7 +467,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
                   tmem_st_x16(o_at + k, z);
                 }
 #pragma unroll 1
-                for (int k = 8 * s0; k < 8 * s; k += 16) {  // this chunk's
+                for (int k = 8 * s0; C == 1 && k < 8 * s; k += 16) {  // this chunk's
                   float y[16];
                   uint32_t z[16];
                   tmem_ld_32x32b_x16(p_at + k, y);
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           tmem_st_32x32b_x32(p_at + 8 * s, p);  // at once; what it covers of S is read
           sum += sum0 + sum1;
         }
-        if (D == 128 && a.copies > 1) hide_others();
+        if (D == 128 && C > 1) hide_others();
         tmem_st_wait();
         done = at_chunk;
         tc_fence_before_sync();
@@ -542,11 +543,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       if (!(good = together())) break;
       float top = -CUDART_INF_F, l = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (k < 2 * a.copies) top = fmaxf(top, sh.stat[rt + k * R].x);
+      for (int k = 0; k < 2 * C; ++k) top = fmaxf(top, sh.stat[rt + k * R].x);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (k >= 2 * a.copies) break;
+      for (int k = 0; k < 2 * C; ++k) {
         const float2 x = sh.stat[rt + k * R];
         if (x.x != -CUDART_INF_F) l = fmaf(ex2(x.x - top), x.y, l);
       }
@@ -562,7 +561,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       }
       // Four channels of a row per thread, so that a warp writes runs of 128 bytes; channel
       // 8 i + k lies in column 8 i + (k ^ (i % 8)).
-      auto put = [&](auto results, int b) {
+      auto put = [&](int b) {
         const int q4 = threadIdx.x & 7, i = q4 >> 1;
         for (int row = threadIdx.x >> 3; row < R; row += kSoft / 8) {
           float x[4] = {};
@@ -570,7 +569,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           for (int k = 0; k < 4; ++k) {
             const float *src = sh.sums() + (8 * i + ((4 * (q4 & 1) + k) ^ ((4 * b + i) & 7))) * kSumStride + row;
 #pragma unroll
-            for (int j = 0; j < decltype(results)::value; ++j) x[k] += src[j * (kSoft / decltype(results)::value)];
+            for (int j = 0; j < 2 * C; ++j) x[k] += src[j * R];
           }
           const long long to = sh.out_at[row];
           const float g = sh.out_f[row];
@@ -593,8 +592,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             sh.sums()[(16 * s + i) * kSumStride + threadIdx.x] = f == 0.0f ? 0.0f : o[i] * f;
         }
         if (!(good = together())) break;
-        if (a.copies == 1) put(std::integral_constant<int, 2>(), b);
-        else put(std::integral_constant<int, 4>(), b);
+        put(b);
         good = together();
       }
       tc_fence_before_sync();
@@ -850,19 +848,26 @@ constexpr int tile_smem() {
 int attn_tile_nt() { return kTileNt; }
 
 cudaError_t launch_attn_tile(AttnArgs a, int d, int sm_count, cudaStream_t stream, bool pdl, int *parts) {
-  a.copies = a.rows <= 64 ? 2 : 1;
   const long long most = static_cast<long long>(ceil_div(a.width * a.ps, kTileChunk) + kTileCost) * a.b * a.hk * a.tiles;
   const int grid = static_cast<int>(most < sm_count ? most : sm_count);
   a.small = most < (1ll << 31);
   *parts = grid;
-  return d == 64 ? launch(attn_tile_kernel<64>, dim3(grid), dim3(kTileThreads), tile_smem<64>(), stream, pdl, a)
-                 : launch(attn_tile_kernel<128>, dim3(grid), dim3(kTileThreads), tile_smem<128>(), stream, pdl, a);
+  auto go = [&](auto kernel, int smem) {
+    return launch(kernel, dim3(grid), dim3(kTileThreads), smem, stream, pdl, a);
+  };
+  if (d == 64) return a.rows <= 64 ? go(attn_tile_kernel<64, 2>, tile_smem<64>()) : go(attn_tile_kernel<64, 1>, tile_smem<64>());
+  return a.rows <= 64 ? go(attn_tile_kernel<128, 2>, tile_smem<128>()) : go(attn_tile_kernel<128, 1>, tile_smem<128>());
 }
 
 cudaError_t attn_tile_setup() {
-  cudaError_t e = cudaFuncSetAttribute(attn_tile_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, tile_smem<64>());
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(attn_tile_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, tile_smem<128>());
+  auto set = [](auto kernel, int smem) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  };
+  cudaError_t e;
+  if ((e = set(attn_tile_kernel<64, 1>, tile_smem<64>()))) return e;
+  if ((e = set(attn_tile_kernel<64, 2>, tile_smem<64>()))) return e;
+  if ((e = set(attn_tile_kernel<128, 1>, tile_smem<128>()))) return e;
+  return set(attn_tile_kernel<128, 2>, tile_smem<128>());
 }
 
 cudaError_t read_tile_status(uint32_t *out, bool clear) {

@@ -206,7 +206,7 @@ sk_status sk_attn_nvfp4(const void *q, const float *k_global_scale, const float 
   sk::AttnArgs a{static_cast<const uint16_t *>(q), cache, k_global_scale, v_global_scale, table, lens,
                  static_cast<uint16_t *>(out), lse, reinterpret_cast<int2 *>(ws + w.joins),
                  reinterpret_cast<float *>(ws + w.parts), b, t, q_heads, kv_heads, page_size, pages,
-                 width, window > (1 << 30) ? 0 : window, group, group * t, w.tiles, q_stride, scale, false, 1};
+                 width, window > (1 << 30) ? 0 : window, group, group * t, w.tiles, q_stride, scale, false};
   const int sms = info.sm_count < SK_MAX_SMS ? info.sm_count : SK_MAX_SMS;
   return launch_status(sk::launch_attn(a, head_dim, sms, as_stream(stream), sk::pdl_on()), "attn_nvfp4");
 }

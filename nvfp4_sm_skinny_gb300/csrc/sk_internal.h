@@ -274,7 +274,6 @@ struct AttnArgs {
   long long q_stride;  // values between tokens
   float scale;
   bool small;  // the work counts for less than 2^31, set by the launch
-  int copies;  // of a row, set by the launch
 };
 int attn_row_tiles(int rows);                              // tiles of 8 rows that are taken at once
 int attn_max_parts(int sm_count, int nt);                  // parts of such a launch, at most
