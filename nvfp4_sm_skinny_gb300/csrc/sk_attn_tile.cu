@@ -24,16 +24,16 @@ __device__ uint32_t g_tile_status;  // OR of SK_DEVICE_WAIT_* bits
 // The work is cut as in attn_kernel, in a part per CTA; the items of a tile of rows count
 // for the chunks that any of its rows sees, so a prompt's first tiles are cheap.
 //
-// b16 of 8192 tokens, 128 query heads: d64, 64 rows 61 us (84 in tiles of 16 rows), d128, 64
-// rows 83 (136), 128 rows 94 (261). A prompt of 2048 tokens behind 14,336, 64 query heads,
-// d128: 980 us (4200). A chunk takes 1450 clocks with 64 rows of d64, 2120 with 128 of d128,
+// b16 of 8192 tokens, 128 query heads: d64, 64 rows 59 us (84 in tiles of 16 rows), d128, 64
+// rows 81 (136), 128 rows 91 (261). A prompt of 2048 tokens behind 14,336, 64 query heads,
+// d128: 950 us (4200). A chunk takes 1440 clocks with 64 rows of d64, 2090 with 128 of d128,
 // of which the products take 770 and 1090 at their rate. What bounds it is latency: of the
 // issue slots 40 % are used and of no pipe more than a third, with four or five warps per
 // scheduler that wait for tensor memory, for one another and for instructions.
 constexpr int kTileRows = 128, kTileChunk = 128;
 // An item's beginning and end count for so many chunks (64 query heads, a prompt of 4096
 // tokens, d64: 317 us with 5, 292 with 6, 286 with 7, 290 with 8; 128, 4 tokens of 16 rows of
-// 100 to 8192, window 4096, d64: 28.6, 27.7, 27.9, 28.7).
+// 100 to 8192, window 4096, d64: 28.6, 27.7, 27.9, 28.7; before the kernels were parted by C).
 constexpr int kTileCost = 7;
 constexpr int kSoftWarps = 8, kWidenWarps = 8, kMmaWarp = kSoftWarps + kWidenWarps, kCopyWarp = kMmaWarp + 1;
 constexpr int kSoft = 32 * kSoftWarps, kSumStride = kSoft + 1;

@@ -1202,7 +1202,7 @@ cudaError_t with_attn(int d, int nt, F f) {
 // Tiles of 8 rows, or of 16: of 32 the sums alone take 128 registers (d128, b16 of 8192
 // tokens, 32 rows: 121 us, in two tiles of 16, which read and widen all twice, 80). From
 // 33 rows on attn_tile_kernel's 128 (b16 of 8192 tokens; d128, 32 rows: 76 us here, 78
-// there; 64 rows: 136 and 83; d64, 32 rows: 49 and 56; 64 rows: 84 and 61).
+// there; 64 rows: 136 and 81; d64, 32 rows: 49 and 56; 64 rows: 84 and 59).
 int attn_row_tiles(int rows) { return rows <= 8 ? 1 : rows <= 32 ? 2 : attn_tile_nt(); }
 
 size_t attn_part_bytes(int d, int nt) { return sizeof(float) * attn_part_floats(d, nt); }
