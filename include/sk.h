@@ -464,7 +464,10 @@ sk_status sk_experts_int8(const int8_t *xq, const float *x_scale, const int8_t *
  * width * page_size at most 2^30.
  *
  * One step of a program that decodes t tokens of every row: sk_kv_resize to the
- * new lengths, once; then, for each layer, sk_kv_append and sk_attn_nvfp4.
+ * new lengths, once; then, for each layer, sk_kv_append_ex with the same new_lens and
+ * sk_attn_nvfp4. A row that the resize refused, or that waits, keeps its length and its
+ * last tokens; append leaves it out by new_lens. Attention of such a row's queries is
+ * that of its last t places, and of no use.
  * ------------------------------------------------------------------------ */
 
 #define SK_MAX_CACHE_ROWS 4096 /* rows of a table whose pages are managed */
@@ -476,21 +479,38 @@ size_t sk_kv_block_bytes(int page_size, int head_dim);
 /*
  * sk_kv_append -- quantizes the last t tokens of each of b rows into the cache of
  * a layer: token j of row i goes to position lens[i] - t + j. A token whose
- * position is negative or has no page is left out (a padded batch: put the tokens
- * last). All other bytes of the cache keep their values.
+ * position is negative or has no page is left out. All other bytes of the cache keep their values.
  *   k, v   BF16 [b, t, kv_heads, head_dim]; k_stride, v_stride: values from a token
  *          to the next (multiples of 8, at least kv_heads * head_dim), so that both
  *          may be parts of the rows of one product
  *   k_global_scale, v_global_scale  FP32 [1] on the device
  *   cache  the layer's, written;  table int32 [b, width], lens int32 [b]
  *   b t <= 2^24, kv_heads <= 1024; k, v and cache 16-byte, the rest 4-byte aligned.
- * No two tokens of a call may have the same place: pages that rows share are
- * parted by sk_kv_resize before anything is appended to them.
+ * Every row is appended to, whatever a resize said of it (sk_kv_append_ex leaves rows
+ * out). No two tokens of a call may have the same place. sk_kv_resize parts rows from
+ * the shared page that they grow out of; who brings more tokens than the resize added
+ * writes over what is there, also of rows that share it.
  */
 sk_status sk_kv_append(const void *k, const void *v, const float *k_global_scale,
                        const float *v_global_scale, uint8_t *cache, const int32_t *table,
                        const int32_t *lens, int b, int t, int kv_heads, int head_dim, int page_size,
                        int pages, int width, int64_t k_stride, int64_t v_stride, void *stream);
+
+/*
+ * sk_kv_append_ex -- as sk_kv_append, for rows of which some bring no tokens, or fewer
+ * than t. Both lists are read on the device, so a captured call takes what they hold
+ * when it runs.
+ *   new_lens  int32 [b] or NULL: the lengths that sk_kv_resize was given. Only rows that
+ *             have theirs are appended to (lens[i] == new_lens[i]): none that was
+ *             refused or that waits (a negative one)
+ *   fresh     int32 [b] or NULL: how many tokens row i brings, its last ones of the t;
+ *             the others are left out. Below 1: none; t and more: all
+ */
+sk_status sk_kv_append_ex(const void *k, const void *v, const float *k_global_scale,
+                          const float *v_global_scale, uint8_t *cache, const int32_t *table,
+                          const int32_t *lens, const int32_t *new_lens, const int32_t *fresh, int b,
+                          int t, int kv_heads, int head_dim, int page_size, int pages, int width,
+                          int64_t k_stride, int64_t v_stride, void *stream);
 
 /* Size in bytes of the workspace sk_attn_nvfp4 needs (whatever the lengths);
    0 for sizes that the call rejects. */

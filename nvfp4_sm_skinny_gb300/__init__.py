@@ -91,6 +91,7 @@ def lib() -> ctypes.CDLL:
             "sk_experts_int8": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, i, i, i, i, i, vp], i),
             "sk_kv_block_bytes": ([i, i], sz),
             "sk_kv_append": ([vp] * 7 + [i] * 7 + [i64, i64, vp], i),
+            "sk_kv_append_ex": ([vp] * 9 + [i] * 7 + [i64, i64, vp], i),
             "sk_attn_nvfp4_workspace": ([i] * 5, sz),
             "sk_attn_nvfp4": ([vp] * 9 + [sz] + [i] * 8 + [i64, f, i, vp], i),
             "sk_kv_resize_workspace": ([i, i], sz),
@@ -625,11 +626,14 @@ def _layer_sizes(cache, table, page_size, head_dim, b, t):
     return pages, heads, width
 
 
-def kv_append(k, v, k_global_scale, v_global_scale, cache, table, lens, page_size: int, stream=None):
+def kv_append(k, v, k_global_scale, v_global_scale, cache, table, lens, page_size: int, stream=None,
+              new_lens=None, fresh=None):
     """Quantizes the last t tokens of each row, k and v BF16 [b, t, kv_heads, d], into
     a layer's cache uint8 [pages, kv_heads, block], in place: token j of row i at
     position lens[i] - t + j of the pages that table int32 [b, width] names. k and v
-    may be parts of longer rows (sk_kv_append)."""
+    may be parts of longer rows (sk_kv_append). With ``new_lens`` int32 [b], what kv_resize
+    was given, rows that it refused or that wait are left out; with ``fresh`` int32 [b] row i
+    brings its last fresh[i] tokens alone (sk_kv_append_ex)."""
     b, t, heads, d = _sizes(k, 4, "k")
     if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16:
         raise ValueError(f"k, v: dtypes {k.dtype}, {v.dtype}, need torch.bfloat16")
@@ -642,10 +646,17 @@ def kv_append(k, v, k_global_scale, v_global_scale, cache, table, lens, page_siz
     _want(k_global_scale, torch.float32, (1,), "k_global_scale")
     _want(v_global_scale, torch.float32, (1,), "v_global_scale")
     _want(lens, torch.int32, (b,), "lens")
-    s = _launch_on(stream, k.get_device(), v, k_global_scale, v_global_scale, cache, table, lens)
-    _check(lib().sk_kv_append(k.data_ptr(), v.data_ptr(), k_global_scale.data_ptr(),
-                              v_global_scale.data_ptr(), cache.data_ptr(), table.data_ptr(),
-                              lens.data_ptr(), b, t, heads, d, page_size, pages, width, ks, vs, s))
+    if new_lens is not None:
+        _want(new_lens, torch.int32, (b,), "new_lens")
+    if fresh is not None:
+        _want(fresh, torch.int32, (b,), "fresh")
+    s = _launch_on(stream, k.get_device(), v, k_global_scale, v_global_scale, cache, table, lens, new_lens,
+                   fresh)
+    _check(lib().sk_kv_append_ex(k.data_ptr(), v.data_ptr(), k_global_scale.data_ptr(),
+                                 v_global_scale.data_ptr(), cache.data_ptr(), table.data_ptr(),
+                                 lens.data_ptr(), None if new_lens is None else new_lens.data_ptr(),
+                                 None if fresh is None else fresh.data_ptr(), b, t, heads, d, page_size,
+                                 pages, width, ks, vs, s))
 
 
 def attn_nvfp4_workspace(b: int, t: int, q_heads: int, kv_heads: int, head_dim: int) -> int:

@@ -33,7 +33,9 @@ rows per pass, with kv_heads KV heads and a key/value cache held in 4 bits, of
 
 and the o_proj reads o. A pass starts by giving the rows the lengths in ``want``
 (sk_kv_resize), which the caller sets before it, each row's tokens so far and one
-more (0: a row without a sequence). This
+more (0: a row without a sequence; negative: a row that waits). A row that waits, or for
+which there are no pages (``row_status``), keeps its cache as it is, and its outputs of
+the pass mean nothing. This
 module only allocates buffers and calls the binding; every step runs in libsk's
 kernels. ``capture()`` records one pass into a CUDA graph (the calls allocate
 nothing and are capturable).
@@ -209,7 +211,7 @@ class DecodeChain:
         sk.gemm_bf16(self.h[l], self.w_qkv[l], out=self.qkv[l], splits=self.splits, stream=stream)
         q, k, v = (x.unflatten(1, (1, -1, d)) for x in self.qkv[l].split(self.heads, 1))
         sk.kv_append(k, v, self.k_gs[l], self.v_gs[l], self.cache[l], self.table, self.lens, self.page_size,
-                     stream=stream)
+                     stream=stream, new_lens=self.want)
         sk.attn_nvfp4(q, self.k_gs[l], self.v_gs[l], self.cache[l], self.table, self.lens, self.page_size,
                       out=self.o[l].view(m, 1, H // d, d), workspace=self.ws_a, stream=stream)
 

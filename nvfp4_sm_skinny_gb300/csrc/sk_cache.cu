@@ -807,7 +807,11 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
   for (int token = first + in, step = 0; first + step < end; step += once, token += once) {
     const bool mine = in < once && token < end;
     const int seq = mine ? token / a.t : 0;
-    const int pos = mine ? a.lens[seq] - a.t + (token - seq * a.t) : -1;
+    const int len = mine ? a.lens[seq] : 0, from_end = a.t - (token - seq * a.t);
+    int pos = mine ? len - from_end : -1;
+    // rows without the length that they were to have, and what is not among a row's fresh tokens
+    if (mine && a.new_lens && (a.new_lens[seq] != len || len > most)) pos = -1;
+    if (mine && a.fresh && a.fresh[seq] < from_end) pos = -1;
     int page = -1;
     if (pos >= 0 && pos < most) page = a.table[static_cast<size_t>(seq) * a.width + (pos >> ps_bits)];
     for (int r = threadIdx.x - in * per, more = 0; more < per; more += kAppendThreads, r += kAppendThreads) {

@@ -149,6 +149,15 @@ sk_status sk_kv_append(const void *k, const void *v, const float *k_global_scale
                        const float *v_global_scale, uint8_t *cache, const int32_t *table,
                        const int32_t *lens, int b, int t, int kv_heads, int head_dim, int page_size,
                        int pages, int width, int64_t k_stride, int64_t v_stride, void *stream) {
+  return sk_kv_append_ex(k, v, k_global_scale, v_global_scale, cache, table, lens, nullptr, nullptr, b, t, kv_heads,
+                         head_dim, page_size, pages, width, k_stride, v_stride, stream);
+}
+
+sk_status sk_kv_append_ex(const void *k, const void *v, const float *k_global_scale,
+                          const float *v_global_scale, uint8_t *cache, const int32_t *table,
+                          const int32_t *lens, const int32_t *new_lens, const int32_t *fresh, int b,
+                          int t, int kv_heads, int head_dim, int page_size, int pages, int width,
+                          int64_t k_stride, int64_t v_stride, void *stream) {
   sk_status st;
   if ((st = check_block(page_size, head_dim)) != SK_OK) return st;
   if ((st = check_tokens(b, t, kv_heads)) != SK_OK) return st;
@@ -160,11 +169,13 @@ sk_status sk_kv_append(const void *k, const void *v, const float *k_global_scale
                        {{"k_global_scale", k_global_scale}, {"v_global_scale", v_global_scale},
                         {"table", table}, {"lens", lens}})) != SK_OK)
     return st;
+  if (new_lens && (st = check_ptrs("sk_kv_append", 4, {{"new_lens", new_lens}})) != SK_OK) return st;
+  if (fresh && (st = check_ptrs("sk_kv_append", 4, {{"fresh", fresh}})) != SK_OK) return st;
   sk::DeviceInfo info;
   int dev = 0;
   if ((st = sk::checked_device(&info, &dev)) != SK_OK) return st;
   sk::AppendArgs a{static_cast<const uint16_t *>(k), static_cast<const uint16_t *>(v), k_global_scale,
-                   v_global_scale, cache, table, lens, b, t, kv_heads, head_dim, page_size, pages, width,
+                   v_global_scale, cache, table, lens, new_lens, fresh, b, t, kv_heads, head_dim, page_size, pages, width,
                    k_stride, v_stride, 1};
   return launch_status(sk::launch_kv_append(a, info.sm_count, as_stream(stream), sk::pdl_on()), "kv_append");
 }

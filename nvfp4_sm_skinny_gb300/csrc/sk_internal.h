@@ -290,6 +290,7 @@ struct AppendArgs {
   const float *k_gs, *v_gs;
   uint8_t *cache;
   const int32_t *table, *lens;
+  const int32_t *new_lens, *fresh;  // or null
   int b, t, hk, d, ps, pages, width;
   long long k_stride, v_stride;  // values between tokens
   int tile;                      // tokens that a CTA takes at a time, set by the launch

@@ -33,14 +33,19 @@ def _split(v, shape):
     return np.lib.stride_tricks.as_strided(v, v.shape[:-1] + shape, s[:-1] + (shape[1] * s[-1], s[-1]))
 
 
-def append(k, v, k_gs, v_gs, cache, table, lens, ps):
-    """A copy of ``cache`` with the tokens k, v (BF16 bits [b, t, hk, d]) in it."""
+def append(k, v, k_gs, v_gs, cache, table, lens, ps, new_lens=None, fresh=None):
+    """A copy of ``cache`` with the tokens k, v (BF16 bits [b, t, hk, d]) in it: the last
+    fresh[i] of rows that have the length new_lens[i]."""
     b, t, hk, d = k.shape
     out = cache.copy()
     kc, vc, ks, vs = parts(out, ps, d)
     for i in range(b):
+        if new_lens is not None and (lens[i] != new_lens[i] or lens[i] > table.shape[1] * ps):
+            continue
         for j in range(t):
             pos = int(lens[i]) - t + j
+            if fresh is not None and t - j > fresh[i]:
+                continue
             if not 0 <= pos < table.shape[1] * ps:
                 continue
             page, at = int(table[i, pos // ps]), pos % ps
