@@ -911,6 +911,7 @@ struct ResizeShared {
   int who[SK_MAX_CACHE_ROWS];     //   the page, the row,
   int before[SK_MAX_CACHE_ROWS];  //   the copying row before it (-1: none), -2: this one copies
   int warps[32];
+  long long wide[32];
 };
 
 __global__ void __launch_bounds__(kPageThreads) kv_resize_plan_kernel(const __grid_constant__ ResizeArgs a) {
@@ -959,13 +960,15 @@ __global__ void __launch_bounds__(kPageThreads) kv_resize_plan_kernel(const __gr
     if (copies) ++sh.need[sh.who[i]];
   }
   __syncthreads();
-  int total = 0;
+  // 4096 rows may ask for 2^26 pages each: summed in 64 bits. Where more than all pages are
+  // taken by then, it does not matter how many more.
+  long long total = 0, sum;
   for (int base = 0; base < a.rows; base += kPageThreads) {
     const int row = base + tid;
     const int need = row < a.rows ? sh.need[row] : 0;
-    const int at = total + cta_scan(need, sh.warps, all);
-    if (row < a.rows) plan[row] = {a.lens[row], need, at, 0};
-    total += all;
+    const long long at = total + cta_scan<long long>(need, sh.wide, sum);
+    if (row < a.rows) plan[row] = {a.lens[row], need, static_cast<int>(min(at, a.pages + 1ll)), 0};
+    total += sum;
   }
   // The free pages, lowest number first, as many as are needed.
   int got = 0;

@@ -97,3 +97,24 @@ def test_resize_and_append_of_rows_that_share_pages(sk, free, seed):  # noqa: F8
                                   n1[i:i + 1], ps, fresh=grow[i:i + 1])
                 before = before + tokens(alone[None], own[i], n1[i])[lens[i]:]
             assert tokens(c1, t1[i], n1[i]) == before
+
+
+def test_rows_that_ask_for_more_pages_than_32_bits_count(sk):  # noqa: F811
+    # 70 rows, 66 of which want the 2^26 pages that a row of the table has places for: 2^32 and more
+    rows, width, ps, pages = 70, 2 ** 26, 16, 9
+    table = torch.full((rows, width), -1, dtype=I32, device=DEV)
+    table[3, 0] = 5
+    lens, refs = torch.zeros(rows, dtype=I32, device=DEV), torch.zeros(pages, dtype=I32, device=DEV)
+    lens[3], refs[5] = 7, 1
+    cache = torch.full((1, pages, 1, 1152), 9, dtype=U8, device=DEV)
+    new = torch.full((rows,), 2 ** 30, dtype=I32, device=DEV)
+    new[0], new[2], new[-1], new[-2] = 17, -1, 0, 1
+    status, _ = sk.kv_resize(new, cache, table, lens, refs, ps)
+    # served before the first refusal: row 0; rows that need no page: 2 and the last; row 68 needs one
+    want = torch.ones(rows, dtype=I32)
+    want[0] = want[2] = want[-1] = 0
+    assert torch.equal(status.cpu(), want)
+    assert lens.tolist() == [17, 0, 0, 7] + [0] * (rows - 4) and refs.tolist() == [1, 1, 0, 0, 0, 1, 0, 0, 0]
+    assert table[0, :2].tolist() == [0, 1] and int(table[3, 0]) == 5 and (cache == 9).all()
+    table[0, :2] = table[3, 0] = -1
+    assert all((table[i] == -1).all() for i in range(rows))
