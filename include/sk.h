@@ -537,7 +537,8 @@ size_t sk_attn_nvfp4_workspace(int b, int t, int q_heads, int kv_heads, int head
  *   scale finite; q, cache and out 16-byte, the rest 4-byte aligned; out and lse
  *   overlap nothing that is read.
  * Scores and sums are FP32, K and V exact; p enters the product with V in FP16 (of
- * 2^7 to 2^15 at its largest), with a rounding of at most 2^-11 of itself.
+ * 2^7 to 2^15 at its largest), off by at most 2^-11 of itself or 2^-31 of the row's
+ * largest p, whichever is more.
  * Results depend on the inputs alone: the work is cut by the lengths, in a fixed
  * order.
  */

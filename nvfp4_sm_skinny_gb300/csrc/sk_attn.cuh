@@ -125,9 +125,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // ---------------------------------------------------------------- attention
 // Scores are kept as powers of two relative to a base that is at most 15 and after
-// an update 7 below the largest, so that P fits FP16 and what is 2^31 times smaller
-// than the largest still counts; the base moves (and the sums are scaled) only
-// when a score exceeds it by 2^15.
+// an update 7 (in tiles of 128 rows, 7 to 8) below the largest, so that P fits FP16 and
+// what is 2^31 times smaller than the largest still counts: a p below 2^-14 is rounded to
+// the step of FP16's subnormal numbers, off by 2^-25, which is 2^-32 of 2^7. (What is scaled
+// in FP16 as the base moves is rounded twice, by 2^-26 at most the first time.) The base
+// moves, and the sums are scaled, only when a score exceeds it by 2^15, or where scores are
+// looked at for another reason.
 constexpr float kTop = 15.0f, kAim = 7.0f;
 
 constexpr int kBegins = 1, kEnds = 2;  // the part holds the first, the last chunk of the item

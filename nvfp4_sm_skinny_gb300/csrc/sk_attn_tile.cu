@@ -443,9 +443,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
                 for (int k = 0; k < 32; k += 2) top = max3(top, x[k], x[k + 1]);
               }
               // the largest score, relative to the base, moves the base by a whole number, so
-              // that a power of two takes all before along: P loses nothing that it has
+              // that a power of two takes all before along: P loses nothing that it has, and the
+              // largest p is in [2^kAim, 2^(kAim + 1)) then
               top = top == -CUDART_INF_F ? top : fmaf(top, c, base);
-              float by = top > kAim ? ceilf(top - kAim) : 0.0f;
+              float by = top > kAim ? floorf(top - kAim) : 0.0f;
               float f = by < 127.0f ? __uint_as_float((127 - static_cast<int>(by)) << 23) : 0.0f;
               if (unseen) {  // the row's first keys set its base
                 by = top == -CUDART_INF_F ? 0.0f : top - kAim;

@@ -1,0 +1,45 @@
+"""What attention over the 4-bit cache promises of its 16-bit operands: P's rounding after
+the base moved, against the 64-bit statement (oracle/cache.py) within attn_bounds
+(test_gpu_cache.py)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache as oc
+from test_gpu_cache import BF16, DEV, F32, I32, U8, attn_bounds, gpu, host, sk  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq", [4, 16, 40, 64, 100])
+def test_the_largest_p_stays_above_what_the_bound_says(sk, hq, d):  # noqa: F811
+    """Scores, in powers of two below the largest: 8.39 for the first key, 0 for one behind it,
+    31.45 for all others, of which the V of 64 behind these two alone is not 0. So the base moves,
+    in tiles of 128 rows by a whole number, and what is added up then is 2^-31.45 of the largest
+    p: lost if that is below 2^7 (0.48 steps of FP16's subnormal numbers with 2^6.39, 0.96 with
+    2^7.39)."""
+    ps, n, copies = 64, 640, 304
+    cache = np.zeros((4, 1, ps * d * 9 // 8), np.uint8)
+    kc, vc, ks, vs = oc.parts(cache, ps, d)
+    kc[..., 0] = 0x0F         # column 0 is -6 * 1.25
+    ks[...] = 0x3A
+    vs[...] = 0x38            # 1.0
+    kc[0, :, 0, 0] = 0x0C     # -2
+    ks[0, :, 0, 0] = 0x38
+    kc[1, :, 0, 0] = 0x00
+    vc[2] = 0x77              # 6.0
+    # chunks of 128 keys: the first, the next even one, and the one behind that, in their first halves
+    table = np.array([[0, 3, 3, 3, 1, 3, 3, 3, 2, 3]], np.int32)
+    lens = np.array([n - ps])
+    q = np.zeros((1, 1, hq, d))
+    q[..., 0] = 1.0
+    scale = 31.45 / 7.5 * np.log(2.0)
+    # so many rows of the same pages that most of them are not cut into parts
+    out, _, _ = sk.attn_nvfp4(torch.as_tensor(q).to(BF16).to(DEV).expand(copies, 1, hq, d).contiguous(), gpu([1.0], F32),
+                              gpu([1.0], F32), gpu(cache, U8), gpu(np.repeat(table, copies, 0), I32),
+                              gpu(np.repeat(lens, copies), I32), ps, scale=scale)
+    ref = oc.attn(q, 1.0, 1.0, cache, table, lens, ps, scale=scale)
+    off = np.abs(host(out) - ref[0])
+    bound = attn_bounds(ref, d, n)[0]
+    assert np.all(off <= bound), np.max(off / bound)
