@@ -538,7 +538,8 @@ size_t sk_attn_nvfp4_workspace(int b, int t, int q_heads, int kv_heads, int head
  *   overlap nothing that is read.
  * Scores and sums are FP32, K and V exact; p enters the product with V in FP16 (of
  * 2^7 to 2^15 at its largest), off by at most 2^-11 of itself or 2^-31 of the row's
- * largest p, whichever is more.
+ * largest p, whichever is more. Queries are exact down to 2^-31 of the largest value of
+ * their token's head, and off by at most 2^-39 of it below that.
  * Results depend on the inputs alone: the work is cut by the lengths, in a fixed
  * order.
  */

@@ -336,8 +336,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       return wait(sh.soft, soft++, SK_DEVICE_WAIT_EPILOGUE);
     };
     // Queries as FP16, each row times a power of two that brings its largest value to
-    // [2^14, 2^15): exact but for values 2^38 times smaller than that one. A negative scale
-    // changes their sign. Each group takes half of the columns.
+    // [2^14, 2^15): BF16's eight bits are exact in steps of 2^-24, down to 2^-31 of that value,
+    // and off by at most 2^-25, 2^-39 of it, below. A negative scale changes their sign. Each
+    // group takes half of the columns.
     uint4 half[D / 16];
     float c = 0.0f;  // what a score is multiplied with
     auto load_q = [&](const volatile TileItem &t) {

@@ -272,8 +272,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
     auto row_end = [&](int r) { return r < a.rows ? len - a.t + token_of(a, r) + 1 : 0; };
 
     // Queries as FP16, each row times a power of two that brings its largest value
-    // to [2^14, 2^15): exact but for values 2^38 times smaller than that one. Lane
-    // (g, j) holds row g of each N tile, the j-th quarter of the columns.
+    // to [2^14, 2^15): BF16's eight bits are exact in steps of 2^-24, down to 2^-31 of that
+    // value, and off by at most 2^-25, 2^-39 of it, below. Lane (g, j) holds row g of each N
+    // tile, the j-th quarter of the columns.
     uint32_t qf[NT][kSteps][2];
     float c[NT][R];       // what a score is multiplied with
     uint32_t unseen = 0;  // rows (bit R nt + e) without any key so far

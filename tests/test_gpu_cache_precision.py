@@ -1,12 +1,12 @@
-"""What attention over the 4-bit cache promises of its 16-bit operands: P's rounding after
-the base moved, against the 64-bit statement (oracle/cache.py) within attn_bounds
-(test_gpu_cache.py)."""
+"""What attention over the 4-bit cache promises of its 16-bit operands: P's rounding in
+tiles of 128 rows after the base moved, and the queries' range, against the 64-bit
+statement (oracle/cache.py) within attn_bounds (test_gpu_cache.py)."""
 import numpy as np
 import pytest
 import torch
 
 from oracle import cache as oc
-from test_gpu_cache import BF16, DEV, F32, I32, U8, attn_bounds, gpu, host, sk  # noqa: F401
+from test_gpu_cache import BF16, DEV, F32, I32, U8, attn_bounds, gpu, host, random_cache, random_table, sk  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +43,30 @@ def test_the_largest_p_stays_above_what_the_bound_says(sk, hq, d):  # noqa: F811
     off = np.abs(host(out) - ref[0])
     bound = attn_bounds(ref, d, n)[0]
     assert np.all(off <= bound), np.max(off / bound)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq", [3, 13, 40, 100])
+@pytest.mark.parametrize("below", [29, 30, 31, 32, 33])
+def test_queries_far_below_the_row_s_largest(sk, below, hq, d):  # noqa: F811
+    """A query's largest value meets keys of 0, so that its scores are those of values 2^below
+    smaller. Their eight significant bits are exact through 2^31; below that each is off by at
+    most half a step of FP16's subnormal numbers, 2^-25 where the largest is at least 2^14:
+    2^-39 of the largest."""
+    rng = np.random.default_rng(below)
+    n, ps = 300, 64
+    table = random_table(rng, [n], 5, 5, ps)
+    cache = random_cache(rng, 5, 1, ps, d)
+    kc = oc.parts(cache, ps, d)[0]
+    kc[..., 0] &= 0xF0                                          # column 0
+    q = rng.choice([-1.0, 1.0], (1, 1, hq, d)) * rng.integers(128, 256, (1, 1, hq, d)) / 128.0  # [1, 2)
+    q[..., 0] *= 2.0 ** below
+    scale = 0.02
+    out, lse, _ = sk.attn_nvfp4(torch.as_tensor(q).to(BF16).to(DEV), gpu([1.0], F32), gpu([9.0], F32), gpu(cache, U8),
+                                gpu(table, I32), gpu([n], I32), ps, scale=scale, lse=True)
+    out_ref, lse_ref, size, reach, mass = oc.attn(q, 1.0, 9.0, cache, table, np.array([n]), ps, scale=scale)
+    if below > 31:  # attn_bounds makes (d / 8 + 16) 2^-23 of `reach`, which is scale sum |q K|, |q| >= 1
+        reach = reach * (1 + 2.0 ** (below + 1 - 39) / ((d / 8 + 16) * 2.0 ** -23))
+    b_out, b_lse = attn_bounds((out_ref, lse_ref, size, reach, mass), d, n)
+    assert np.all(np.abs(host(out) - out_ref) <= b_out)
+    assert np.all(np.abs(host(lse) - lse_ref) <= b_lse)
