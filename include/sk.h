@@ -524,8 +524,8 @@ size_t sk_attn_nvfp4_workspace(int b, int t, int q_heads, int kv_heads, int head
  *   s[k] = scale * sum_c q[c] K[k, c];  p[k] = exp(s[k] - max s)
  *   out  = bf16_rn( sum_k p[k] V[k, :] / sum_k p[k] );  lse = max s + log sum_k p[k]
  * A token that sees nothing (pos < 0, a row of length 0, missing pages) gets zeros
- * and lse -inf. What the cache holds in places that no token sees does not matter,
- * be it scales that are no numbers.
+ * and lse -inf. What the cache holds in places that a token does not see does not matter
+ * to it, be it scales that are no numbers and other tokens of the call see them.
  *   q      BF16 [b, t, q_heads, head_dim]; q_stride: values from a token to the next
  *   cache  the layer's;  table int32 [b, width], lens int32 [b]
  *   out    BF16 [b, t, q_heads, head_dim], contiguous: the rows of the o_proj

@@ -168,6 +168,14 @@ __device__ __forceinline__ size_t attn_row(const AttnArgs &a, int seq, int h, in
   return (static_cast<size_t>(seq) * a.t + token) * a.hq + h * a.group + r - token * a.group;
 }
 
+// Of four scale bytes those that are no number: bit i of the result for byte i, which becomes 0.
+// (A key that a row does not see has p = 0 there, but 0 times what is no number is none.)
+__device__ __forceinline__ uint32_t take_nans(uint32_t &scales) {
+  const uint32_t ones = ((scales & 0x7F7F7F7Fu) + 0x01010101u) >> 7 & 0x01010101u;
+  scales &= ~(ones * 0xFFu);
+  return ones * 0x01020408u >> 24;
+}
+
 __device__ __forceinline__ float row_lse(float base, float sum) {
   return sum == 0.0f ? -CUDART_INF_F : (base + log2f(sum)) * 0.693147180559945f;
 }

@@ -102,6 +102,9 @@ struct TileShared {
   uint64_t q_full, soft, drained, item_full[kItems];
   TileItem item[kItems];
   int have[kHave];
+  // There was a scale of V that is no number in a chunk that not all rows see: it is left out
+  // of the product, which would bring it to all rows.
+  int any_nans;
   uint32_t tmem;
 };
 
@@ -181,6 +184,39 @@ __device__ __forceinline__ bool one_lane() {
   return one != 0;
 }
 
+// Makes a row's sums O no number in the blocks of 16 columns of which it sees a V with such a
+// scale, in chunks that not all rows see; [lo, hi) are the row's keys. Called where such scales
+// were met, which is rare: out of line, and reads them again.
+template <int D>
+__device__ __noinline__ void put_nans(const AttnArgs &a, const volatile TileItem &t, int lo, int hi, uint32_t o_at) {
+  const int end = min(t.from + kTileChunk * t.count, hi);
+  uint32_t lost = 0;
+  for (int at = max(t.from, lo); at < end; ++at) {
+    const int chunk = at & -kTileChunk;
+    if (chunk >= t.all_lo && chunk + kTileChunk <= t.all_hi) {
+      at = chunk + kTileChunk - 1;
+      continue;
+    }
+    const int page = a.table[static_cast<size_t>(t.seq) * a.width + at / a.ps];
+    if (page < 0 || page >= a.pages) continue;
+    const uint8_t *scales = a.cache + (static_cast<size_t>(page) * a.hk + t.h) * (a.ps * D * 9 / 8) +
+                            a.ps * D + a.ps * (D / 16) + at % a.ps;
+    for (int b = 0; b < D / 16; ++b) lost |= ((scales[b * a.ps] & 0x7F) == 0x7F) << b;
+  }
+#pragma unroll 1
+  for (int b = 0; b < D / 16; ++b) {
+    const bool none = lost >> b & 1;
+    if (!__any_sync(kAll, none)) continue;
+    float y[16];
+    uint32_t z[16];
+    tmem_ld_32x32b_x16(o_at + 16 * b, y);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] = none ? 0x7FFFFFFFu : __float_as_uint(y[i]);
+    tmem_st_x16(o_at + 16 * b, z);
+  }
+  tmem_st_wait();
+}
+
 // C: how many times a row lies there.
 template <int D, int C>
 __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid_constant__ AttnArgs a) {
@@ -193,6 +229,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   Sh &sh = *reinterpret_cast<Sh *>(raw + (1024 - (smem_u32(raw) & 1023)) % 1024);
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, G = gridDim.x, me = blockIdx.x;
   if (threadIdx.x == 0) {
+    sh.any_nans = 0;
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&sh.ring_full[s]), 1);
       mbar_init(smem_u32(&sh.ring_empty[s]), kWidenWarps);
@@ -535,6 +572,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       if (good && done >= 0) good = wait(sh.pv_done[g], done >> 1, SK_DEVICE_WAIT_EPILOGUE);
       if (!good) break;
       tc_fence_after_sync();
+      if (__any_sync(kAll, *static_cast<volatile int *>(&sh.any_nans) && done >= 0)) put_nans<D>(a, t, lo, hi, o_at);
 
       // The whole item's output, or the result of a part: of one that the item began
       // before in slot 2 me, of one that it begins in in slot 2 me + 1.
@@ -650,6 +688,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     for (int at_item = 0; good && item(at_item).count; ++at_item) {
       const volatile TileItem &t = item(at_item);
       const int seen_hi = min(t.len, most), seen_lo = a.window ? t.len - a.t - a.window + 1 : 0;
+      const int all_hi = t.all_hi, all_lo = t.all_lo;
       for (int from = t.from, to = from + kTileChunk * t.count; from < to; from += kTileChunk, ++n) {
         // K of the next chunk, of the next item's first after the last, goes before V
         const bool last = from + kTileChunk == to;
@@ -668,7 +707,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           for (int i = 0; i < 8; ++i) v[i] = lds32(src + (i ^ flip) * (D / 2));
           uint2 sc = lds64(stage + piece * blk + 2 * codes + a.ps * (D / 16) + (wd >> 1) * a.ps + in);
           const int have = sh.have[n % kHave];
-          if (have != (1 << pieces) - 1 || from + kTileChunk > seen_hi || from < seen_lo) {
+          const bool some = from + kTileChunk > all_hi || from < all_lo;  // rows do not see all
+          if (have != (1 << pieces) - 1 || some) {
             // what is not seen weighs 0, but its scale may be no number
             const bool there = have >> piece & 1;
 #pragma unroll
@@ -676,6 +716,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
               const int at = from + 8 * tg + q;
               if (!there || at >= seen_hi || at < seen_lo) sc.x &= ~(0xFFu << 8 * q);
               if (!there || at + 4 >= seen_hi || at + 4 < seen_lo) sc.y &= ~(0xFFu << 8 * q);
+            }
+            if (some) {
+              if (take_nans(sc.x) | take_nans(sc.y)) sh.any_nans = 1;
             }
           }
           const uint32_t order = flip == 0 ? 0x3210u : flip == 1 ? 0x2301u : flip == 2 ? 0x1032u : 0x0123u;

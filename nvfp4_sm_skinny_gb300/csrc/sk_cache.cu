@@ -93,6 +93,13 @@ __device__ __forceinline__ T cost_of4(const AttnArgs &a, int s, T (&n)[4]) {
   return sum;
 }
 
+// Bits i of 32 tokens from `token` on that lie in [lo, hi).
+__device__ __forceinline__ uint32_t tokens_in(int token, int lo, int hi) {
+  const int over = hi - token, under = lo - token;
+  const uint32_t below = over >= 32 ? kAll : over <= 0 ? 0 : (1u << over) - 1;
+  return under >= 32 ? 0 : under > 0 ? below & kAll << under : below;
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_constant__ AttnArgs a) {
   using Sh = AttnWarp<D, NT>;
@@ -485,18 +492,42 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
           const uint2 x = *reinterpret_cast<const uint2 *>(raw + stage + vs_at + 8 * part);
           vs[0] = x.x, vs[1] = x.y;
         }
+        if (!whole) {
+          // What is not seen weighs 0, but its scale may be no number. One that only some rows
+          // see is left out of the product, and makes the sums of these rows no number.
+          const bool there = have >> (16 * j / a.ps) & 1;
+          uint32_t nans = 0;
 #pragma unroll
-        for (int m = 0; m < kSub; ++m) {
-          const int mt = part * kSub + m;
-          if (!whole) {  // what is not seen weighs 0, but its scale may be no number
-            const bool there = have >> (16 * j / a.ps) & 1;
+          for (int m = 0; m < kSub; ++m) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const int token = from + 16 * j + 4 * mt + q;
+              const int token = from + 16 * j + 4 * (part * kSub + m) + q;
               if (!there || token >= len || token >= a.width * a.ps || (a.window && token <= len - a.t - a.window))
                 vs[m] &= ~(0xFFu << 8 * q);
             }
+            nans |= take_nans(vs[m]) << 4 * m;
           }
+          if (__any_sync(kAll, nans != 0)) {
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {  // the tokens of the lanes that share this one's columns
+              const uint32_t theirs = __shfl_sync(kAll, nans, (lane & ~3) | i);
+              const int token = from + 16 * i + 4 * kSub * part;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int last = row_end(place.r0 + 8 * nt + 2 * j + e), lo = a.window ? last - a.window : 0;
+                  if (theirs & tokens_in(token, lo, last)) {
+#pragma unroll
+                    for (int k = 0; k < kMt; ++k) o[k][nt][e] = o[k][nt][2 + e] = CUDART_NAN_F;
+                  }
+                }
+            }
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < kSub; ++m) {
+          const int mt = part * kSub + m;
           const uint32_t order = __byte_perm(vs[m], 0, vs_order);
           const uint32_t f0 = widen_e4m3(order & 0xFFFFu), f1 = widen_e4m3(order >> 16);
           constexpr int kWords = D / 64;
