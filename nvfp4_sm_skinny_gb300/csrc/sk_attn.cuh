@@ -142,7 +142,7 @@ __host__ __device__ constexpr int attn_part_floats(int d, int nt) { return 16 * 
 // of place u. 64-bit divisions take hundreds of instructions, and U rarely needs them.
 struct Parts {
   long long q, rest;
-  __device__ Parts(long long U, int G) {
+  __host__ __device__ Parts(long long U, int G) {
     if (U >> 31) {
       q = U / G;
       rest = U % G;
@@ -151,8 +151,8 @@ struct Parts {
       rest = static_cast<uint32_t>(U) % static_cast<uint32_t>(G);
     }
   }
-  __device__ long long start(int c) const { return c * q + min(static_cast<long long>(c), rest); }
-  __device__ int of(long long u) const {
+  __host__ __device__ long long start(int c) const { return c * q + (c < rest ? c : rest); }
+  __host__ __device__ int of(long long u) const {
     const long long longer = rest * (q + 1);
     if ((u | q) >> 31) return static_cast<int>(u < longer ? u / (q + 1) : rest + (u - longer) / q);
     return static_cast<int>(u < longer ? static_cast<uint32_t>(u) / static_cast<uint32_t>(q + 1)
