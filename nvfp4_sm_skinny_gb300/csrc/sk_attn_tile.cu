@@ -25,11 +25,12 @@ __device__ uint32_t g_tile_status;  // OR of SK_DEVICE_WAIT_* bits
 // for the chunks that any of its rows sees, so a prompt's first tiles are cheap.
 //
 // b16 of 8192 tokens, 128 query heads: d64, 64 rows 59 us (84 in tiles of 16 rows), d128, 64
-// rows 81 (136), 128 rows 91 (261). A prompt of 2048 tokens behind 14,336, 64 query heads,
-// d128: 950 us (4200). A chunk takes 1440 clocks with 64 rows of d64, 2090 with 128 of d128,
+// rows 79 (136), 128 rows 90 (261). A prompt of 2048 tokens behind 14,336, 64 query heads,
+// d128: 926 us (4200). A chunk takes 1440 clocks with 64 rows of d64, 2010 with 128 of d128,
 // of which the products take 770 and 1090 at their rate. What bounds it is latency: of the
-// issue slots 40 % are used and of no pipe more than a third, with four or five warps per
-// scheduler that wait for tensor memory, for one another and for instructions.
+// issue slots 39 to 42 % are used and of no pipe more than two fifths (in the long prompt 57 %,
+// the tensor pipe 47 %), with four or five warps per scheduler that wait for tensor memory, for
+// one another and for instructions.
 constexpr int kTileRows = 128, kTileChunk = 128;
 // An item's beginning and end count for so many chunks (64 query heads, a prompt of 4096
 // tokens, d64: 317 us with 5, 292 with 6, 286 with 7, 290 with 8; 128, 4 tokens of 16 rows of

@@ -759,9 +759,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
 // ------------------------------------------------------------------- append
 // A thread takes 16 columns of a token's head, of K and of V. What a block of 16 costs is
 // instructions (a thread per block with three IEEE divisions: 51 us for 32,768 tokens
-// of 8 heads, d128, twice what its bytes take), so the divisions go: that by 6 becomes a
-// product and two fused steps, which are exact for every BF16 value, and 1 / (scale / gs)
-// is looked up by the scale's byte.
+// of 8 heads, d128, twice what its bytes take), so the divisions go. That by 6 is
+// Markstein's: with y the FP32 number next to 1/6, q = a y is within a unit of a / 6, r = a - 6 q
+// is exact in one fused step, and q + r y in another is a / 6 correctly rounded (1990,
+// Computation of elementary functions on the IBM RISC System/6000 processor); every finite
+// BF16 magnitude is tested. 1 / (scale / gs) is looked up by the scale's byte.
 constexpr int kAppendThreads = 256;
 
 struct AppendShared {
