@@ -622,6 +622,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             *reinterpret_cast<float4 *>(part + to + 32 * b + 4 * q4) = make_float4(x[0], x[1], x[2], x[3]);
         }
       };
+      // (of a thread that saw no key O may hold anything; what is no number counts however small f is)
       for (int b = 0; good && b < D / 32; ++b) {
         __syncwarp();
 #pragma unroll
@@ -630,7 +631,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           tmem_ld_32x32b_x16(o_at + 32 * b + 16 * s, o);
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            sh.sums()[(16 * s + i) * kSumStride + threadIdx.x] = f == 0.0f ? 0.0f : o[i] * f;
+            sh.sums()[(16 * s + i) * kSumStride + threadIdx.x] = own == -CUDART_INF_F ? 0.0f : o[i] * f;
         }
         if (!(good = together())) break;
         put(b);

@@ -96,3 +96,23 @@ def test_keys_that_some_tokens_do_not_see_in_rows_that_are_not_cut(sk, d, hq, t)
     lost = torch.as_tensor(hurt).to(DEV)[:, :, None, :, None].expand(b, t, hq, d // 16, 16).reshape(b, t, hq, d)
     assert torch.equal(dirty.isnan(), lost) and torch.equal(dirty[~lost], clean[~lost])
     assert torch.equal(dirty_lse, clean_lse)
+
+
+@pytest.mark.parametrize("hq", [4, 16, 40, 100])
+@pytest.mark.parametrize("d", [64, 128])
+def test_what_is_no_number_counts_however_little_it_weighs(sk, d, hq):  # noqa: F811
+    # a V of that kind where p = exp(-400), 0 in FP32, in each chunk of the row in turn
+    ps, n, copies = 64, 640, 304
+    table = np.arange(10, dtype=np.int32)[None]
+    for where in range(10):
+        cache = np.zeros((10, 1, ps * d * 9 // 8), np.uint8)
+        kc, vc, ks, vs = oc.parts(cache, ps, d)
+        kc[..., 0] = 0x0F                       # column 0 is -6
+        kc[(where + 3) % 10, 0, 5, 0] = 0       # but of one key
+        vc[...], ks[...], vs[...] = 0x22, 0x38, 0x38
+        vs[where, 0, 1, 9] = 0x7F
+        q = torch.zeros(copies, 1, hq, d, dtype=BF16, device=DEV)
+        q[..., 0] = 1.0
+        out = sk.attn_nvfp4(q, gpu([1.0], F32), gpu([1.0], F32), gpu(cache, U8), gpu(np.repeat(table, copies, 0), I32),
+                            gpu(np.full(copies, n), I32), ps, scale=400 / 6)[0]
+        assert out[..., 16:32].isnan().all() and (out[..., :16] == 1).all() and (out[..., 32:] == 1).all()
