@@ -479,7 +479,8 @@ size_t sk_kv_block_bytes(int page_size, int head_dim);
 /*
  * sk_kv_append -- quantizes the last t tokens of each of b rows into the cache of
  * a layer: token j of row i goes to position lens[i] - t + j. A token whose
- * position is negative or has no page is left out. All other bytes of the cache keep their values.
+ * position is negative or has no page is left out. All other bytes of the cache keep
+ * their values.
  *   k, v   BF16 [b, t, kv_heads, head_dim]; k_stride, v_stride: values from a token
  *          to the next (multiples of 8, at least kv_heads * head_dim), so that both
  *          may be parts of the rows of one product
